@@ -2,7 +2,8 @@
  * specverify -- speculative-decoding verify-and-sample on one GPU (sm_103a).
  *
  * The library turns the target model's logit rows for a block of draft
- * positions into committed tokens and accept lengths.  Three modes:
+ * positions into committed tokens and accept lengths, and does the cache side
+ * of the forward pass that makes those rows.  Three verification modes:
  *
  *   greedy verification  -- "Decode Before You Hear: Speculative Listening for
  *       Chunk-Interleaved Full-Duplex Speech Language Models" (digest), section
@@ -65,8 +66,8 @@ enum {
     SV_ERR_DEVICE = -8       /* no usable CUDA device */
 };
 
-/* logit element types */
-enum { SV_BF16 = 0, SV_F32 = 1 };
+/* element types: logits are SV_BF16 or SV_F32, heads and caches SV_BF16 or SV_F16 */
+enum { SV_BF16 = 0, SV_F32 = 1, SV_F16 = 2 };
 
 /* per-request status bits, written to status[r] (0 = nothing to report) */
 enum {
@@ -77,7 +78,11 @@ enum {
     SV_ST_BAD_TEMP = 16,      /* temperature negative or NaN: greedy verification used */
     SV_ST_BAD_D2T = 32,       /* d2t holds an id outside [0, V) or a repeated id */
     SV_ST_TIMEOUT = 64,       /* a bounded device wait gave up; the request's outputs are invalid */
-    SV_ST_POOL_FULL = 128     /* sv_pool_append: the draft did not fit in the pool; nothing inserted */
+    SV_ST_POOL_FULL = 128,    /* sv_pool_append: the draft did not fit in the pool; nothing inserted */
+    SV_ST_NO_BLOCKS = 256,    /* sv_step_tables: no room for the request's tokens; it takes no part */
+    SV_ST_BAD_TREE = 512,     /* a parent, branch or path that is no tree of the request's tokens */
+    SV_ST_BAD_LENGTH = 1024,  /* a length that is negative or above what the tables can hold */
+    SV_ST_BAD_BLOCK = 2048    /* a block id outside the pool; the tokens in it have no slot */
 };
 
 /* limits */
@@ -88,6 +93,9 @@ enum {
 #define SV_MAX_NGRAM 64     /* emitted-suffix tokens matched by sv_pool_lookup */
 #define SV_MAX_POOL (1 << 24) /* pool capacity per request (tokens and separators) */
 #define SV_MAX_WIDTH (1 << 30)
+#define SV_MAX_HEAD_DIM 128   /* entries of a head (a multiple of 8) */
+#define SV_MAX_GROUP 128      /* query heads that share a key head */
+#define SV_MAX_TREE 2049      /* tokens of a drafted tree: the root and SV_MAX_BRANCHES * SV_MAX_K drafts */
 
 /* A matrix of logit rows: row i, entry x is at data + (i * row_stride + x)
  * elements.  `data` must be aligned to the element size.  Rows whose start
@@ -384,6 +392,189 @@ int sv_suffix_append(int32_t* suffix, int32_t N, int32_t R, const int32_t* token
  * ---------------------------------------------------------------------- */
 int sv_accept_scan(const uint8_t* accept, const int32_t* draft, const int32_t* fix, int32_t R,
                    int32_t k, int32_t* accept_len, int32_t* tokens, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The cache side of a verify step: the tokens of a step are laid out in a
+ * paged key/value cache (sv_step_tables), rotated and written into it
+ * (sv_rope_cache), attend over it as a drafted tree (sv_tree_attention), and
+ * after verification the accepted path is kept (sv_cache_commit).
+ * Source: "Decode Before You Hear ..." method steps 2 and 4: the main draft and
+ * the runner-up branch are verified in the same forward pass over the session's
+ * cache, of which the accepted prefix stays.
+ *
+ * A request r has seq_len[r] committed tokens in the cache and brings
+ * new_len[r] tokens, numbered 0, 1, ... in the order in which they lie behind
+ * the committed ones; token 0 is the last committed token whose keys are not
+ * cached yet (the root), the others are drafts.  The tokens of all requests are
+ * packed: request r's are cu_tokens[r] .. cu_tokens[r + 1) - 1.
+ *
+ * Paged cache: position p of a request lies in block block_table[r, p / block_size],
+ * at place p % block_size.  Entry (block, place, head, x) of K is at
+ * k + block * block_stride + place * token_stride + head * head_stride + x
+ * elements, V alike; a cache stacked over layers adds layer * layer_stride.  Any
+ * order of the axes goes, as long as x is contiguous.
+ * ---------------------------------------------------------------------- */
+typedef struct sv_kv_cache {
+    void* k;
+    void* v;
+    int32_t dtype;      /* SV_BF16 or SV_F16 */
+    int32_t num_blocks;
+    int32_t block_size; /* a multiple of 8 */
+    int32_t kv_heads;
+    int32_t head_dim;   /* a multiple of 8, <= SV_MAX_HEAD_DIM */
+    int32_t layers;     /* 1, or the layers of a stacked cache (sv_cache_commit) */
+    int64_t block_stride, token_stride, head_stride, layer_stride; /* elements, multiples of 8 */
+} sv_kv_cache;
+
+/* Heads of packed tokens: entry x of head h of token t is at
+ * data + t * token_stride + h * head_stride + x elements.  data is 16-byte
+ * aligned and the strides are multiples of 8: views of one fused projection do. */
+typedef struct sv_heads {
+    const void* data;
+    int32_t dtype; /* SV_BF16 or SV_F16 */
+    int32_t tokens, heads, head_dim;
+    int64_t token_stride, head_stride;
+} sv_heads;
+
+/* ------------------------------------------------------------------------
+ * sv_step_tables -- blocks, slots, positions and ancestor masks of a step.
+ *
+ *   seq_len     int32 [R]: committed tokens.  A request owns the blocks of its
+ *               first ceil(seq_len / block_size) table entries.
+ *   new_len     int32 [R]: tokens of this step (0: the request sits out).
+ *   block_table int32 [R, max_blocks] in/out: the entries of the blocks taken
+ *               in this call are written, no other.
+ *   free_blocks int32 [num_blocks], free_count int32 [1]: a stack of the free
+ *               block ids, of which the last is taken first.
+ *   parent      int32 [T] or NULL: the request's own number of the token's
+ *               parent, below the token's own, or -1 for a token that hangs
+ *               from the committed ones alone.  NULL: a chain, whose token j
+ *               follows token j - 1.
+ *   T           capacity of the packed arrays.
+ *   cu_tokens   int32 [R + 1] out.
+ *   kv_len      int32 [R] out: seq_len + new_len, or 0 for a request that takes
+ *               no part (see status).
+ *   slot        int64 [T] out: block id * block_size + place, -1 for none.
+ *   position    int32 [T] out: seq_len + the token's depth below its root;
+ *               -1 beyond the last token.
+ *   mask        uint32 [T, mask_words] out (only with parent): bit x % 32 of
+ *               word x / 32 says that the token sees its request's token x:
+ *               itself and its ancestors.
+ *   free_count_out int32 [1] out;  status int32 [R] out or NULL.
+ * Requests are served in order: from the first one whose blocks are not there,
+ * or whose tokens go beyond T, no request takes blocks (SV_ST_NO_BLOCKS).  A
+ * negative length, a request longer than its table row, or a tree above
+ * SV_MAX_TREE tokens or 32 * mask_words sets SV_ST_BAD_LENGTH; it takes none
+ * either, the others are served.  Requests that take no part have slots of -1.
+ * A parent that is not below its token counts as -1 (SV_ST_BAD_TREE); a block id
+ * outside [0, num_blocks) gives slots of -1 (SV_ST_BAD_BLOCK).
+ * The outputs must not overlap the inputs.  A call repeated on the same inputs
+ * writes the same values.
+ * ---------------------------------------------------------------------- */
+int sv_step_tables(const int32_t* seq_len, const int32_t* new_len, int32_t R, int32_t block_size,
+                   int32_t* block_table, int32_t max_blocks, const int32_t* free_blocks,
+                   const int32_t* free_count, int32_t num_blocks, const int32_t* parent, int32_t T,
+                   int32_t* cu_tokens, int32_t* kv_len, int64_t* slot, int32_t* position, uint32_t* mask,
+                   int32_t mask_words, int32_t* free_count_out, int32_t* status, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * sv_rope_cache -- rotary positions on q and k, and k and v written into their
+ * cache slots, in one pass.
+ *
+ *   q, k, v     heads of the T packed tokens (k and v: kv_heads of the cache).
+ *   position    int32 [T];  slot int64 [T]: -1 (or any slot outside the cache)
+ *               writes nothing to the cache.
+ *   freqs       uint64 [rot_dim / 2]: turns per position of each pair as a 64-bit
+ *               fraction, round(2^64 * inv_freq / (2 pi)) (sv_rope_freqs).  The
+ *               product with the position wraps at whole turns by itself, so
+ *               angles are exact to 2^-32 turns at every position.
+ *   rot_dim     rotated entries of a head, even, 0 <= rot_dim <= head_dim; the
+ *               rest of q and k passes unchanged.
+ *   interleaved 0: pair i is entries (i, i + rot_dim / 2); 1: (2 i, 2 i + 1).
+ *   mscale      factor on cosine and sine (1 unless the scaling asks for one).
+ *   q_out       T x q.heads heads with q's dtype; may be q itself.
+ *   cache       one layer (layers == 1); written at the slots.
+ * (x, y) -> mscale * (x cos - y sin, x sin + y cos) in fp32, rounded once.
+ * Slots that repeat within a call leave either token's values.
+ * ---------------------------------------------------------------------- */
+int sv_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, const int64_t* slot,
+                  const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float mscale, sv_heads q_out,
+                  sv_kv_cache cache, sv_stream_t stream);
+
+/* Frequencies for sv_rope_cache, computed on the host in fp64 into HOST
+ * uint64 [rot_dim / 2].  inv_freq_i = base^(-2 i / rot_dim), then by `scaling`:
+ *   SV_ROPE_PLAIN     as it is;
+ *   SV_ROPE_LINEAR    / factor (positions interpolated);
+ *   SV_ROPE_BASE      the base raised to base * factor^(rot_dim / (rot_dim - 2));
+ *   SV_ROPE_BY_DIM    per pair between inv_freq (kept, pairs that turn more than
+ *                     `high` times within `trained` positions) and inv_freq / factor
+ *                     (fewer than `low`), blended linearly in the pair's index;
+ *   SV_ROPE_BY_TURNS  the same, blended linearly in the number of turns. */
+enum { SV_ROPE_PLAIN = 0, SV_ROPE_LINEAR = 1, SV_ROPE_BASE = 2, SV_ROPE_BY_DIM = 3, SV_ROPE_BY_TURNS = 4 };
+int sv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained, double low,
+                  double high, uint64_t* freqs);
+
+/* ------------------------------------------------------------------------
+ * sv_tree_attention -- attention of the step's tokens over the paged cache.
+ *
+ *   q           heads of the T packed tokens; q.heads is a multiple of
+ *               cache.kv_heads, query head h reads key head h / (q.heads / kv_heads).
+ *   cache       one layer; K and V of every position below kv_len are in it,
+ *               those of the step's tokens included.
+ *   block_table int32 [R, max_blocks];  kv_len int32 [R] (0: no keys);
+ *               cu_tokens int32 [R + 1].
+ *   max_tokens  upper bound of a request's tokens in this step: only the first
+ *               max_tokens of a request attend.
+ *   mask        uint32 [T, mask_words] or NULL.  The request's n tokens are its
+ *               last n positions; a token sees every position before them, and of
+ *               those n the ones whose mask bit is set (bits at or above
+ *               32 * mask_words count as 0).  NULL: itself and those before it.
+ *   scale       factor on the scores q . k.
+ *   out         T x q.heads heads with q's dtype;  lse float [T, q.heads] or NULL:
+ *               ln of the sum of exp(score) over the visible positions.
+ *   status      int32 [R] out or NULL (SV_ST_TIMEOUT).
+ * out = sum_x softmax_x(scale q . k_x) v_x.  Where a token sees nothing, out is
+ * 0 and lse -inf.  Keys and values at positions that a token does not see have
+ * no influence on it, whatever they hold.  Scores and sums are fp32; the
+ * probabilities are rounded to the cache's type for the product with V.
+ * A block id outside [0, num_blocks) reads as keys and values of 0.
+ * kv_len is clamped to [0, max_blocks * block_size], cu_tokens to [0, T].
+ * Workspace: sv_tree_attention_workspace with the same R, T, max_tokens, heads,
+ * and max_kv = max_blocks * block_size.
+ * ---------------------------------------------------------------------- */
+size_t sv_tree_attention_workspace(int32_t R, int32_t T, int32_t max_tokens, int32_t heads, int32_t kv_heads,
+                                   int32_t head_dim, int64_t max_kv);
+int sv_tree_attention(sv_heads q, sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks,
+                      const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, int32_t max_tokens,
+                      const uint32_t* mask, int32_t mask_words, float scale, sv_heads out, float* lse,
+                      int32_t* status, void* workspace, size_t workspace_bytes, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * sv_cache_commit -- keep the accepted path of a verified tree.
+ *
+ *   cache       every layer (layers, layer_stride); moved in place.
+ *   block_table, seq_len, kv_len, cu_tokens  as sv_step_tables took and left them.
+ *   accept_len  int32 [R]: accepted drafts a, clamped to [0, k].
+ *   branch      int32 [R] or NULL (branch 0): the accepted draft i is the
+ *               request's token 1 + branch * k + i (the layout of sv_verify_greedy).
+ *   path        int32 [R, k] or NULL: instead, token path[r, i], increasing in i
+ *               and at least 1.
+ *   k           drafts per branch, or the width of path, 0 <= k <= SV_MAX_K.
+ *   free_blocks int32 [num_blocks], free_count int32 [1]: as sv_step_tables left
+ *               them; the blocks that hold no kept token are pushed.
+ *   seq_len_out int32 [R] out: seq_len + 1 + a (the root and the accepted
+ *               drafts); seq_len for a request without tokens in this step.
+ *   free_count_out int32 [1] out;  status int32 [R] out or NULL.
+ * K and V of accepted draft i move to position seq_len + 1 + i.  An accepted
+ * token that is not one of the request's, or a path that does not increase,
+ * ends the accepted path before it (SV_ST_BAD_TREE).  The outputs must not
+ * overlap the inputs.
+ * ---------------------------------------------------------------------- */
+int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len,
+                    const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, const int32_t* accept_len,
+                    const int32_t* branch, const int32_t* path, int32_t k, int32_t* free_blocks,
+                    const int32_t* free_count, int32_t* seq_len_out, int32_t* free_count_out, int32_t* status,
+                    sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * sv_selftest_wait_timeout -- a self-test of the library's bounded waits; the

@@ -8,6 +8,8 @@ fallback.  If the library has not been built, ``load()`` raises.
 
 Entry points (same names as the C ABI in include/specverify.h):
   verify_greedy, verify_sample, cfg_merge_sample, accept_scan
+  step_tables, rope_cache (with rope_freqs), tree_attention, cache_commit: the
+  cache side of a verify step
 """
 from __future__ import annotations
 
@@ -18,16 +20,20 @@ from . import _build
 
 LIB_PATH = _build.LIB
 
-SV_BF16, SV_F32 = 0, 1
+SV_BF16, SV_F32, SV_F16 = 0, 1, 2
 ST_TOKEN_RANGE, ST_BAD_LOGITS, ST_OFF_SUPPORT, ST_RESIDUAL_ZERO = 1, 2, 4, 8
 ST_BAD_TEMP, ST_BAD_D2T, ST_TIMEOUT, ST_POOL_FULL = 16, 32, 64, 128
+ST_NO_BLOCKS, ST_BAD_TREE, ST_BAD_LENGTH, ST_BAD_BLOCK = 256, 512, 1024, 2048
 MAX_K, MAX_S, MAX_NGRAM, MAX_POOL = 256, 16, 64, 1 << 24
+MAX_HEAD_DIM, MAX_GROUP, MAX_TREE = 128, 128, 2049
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_DIM, ROPE_BY_TURNS = 0, 1, 2, 3, 4
 
 # kernels launched by one call of each entry point (reported by the benchmark)
 # kernels one call launches: verify_sample with a prebuilt d2t plan (or the identity map)
 # launches 2, and 2 more when it builds the plan itself; d2t_plan launches 2
 LAUNCHES = {"verify_greedy": 2, "verify_greedy_top2": 2, "infer_modality": 2, "pool_append": 1, "pool_lookup": 1, "suffix_append": 1, "verify_sample": 2, "verify_sample_plan_in_call": 4, "d2t_plan": 2,
-            "cfg_merge_sample": 2, "accept_scan": 1}
+            "cfg_merge_sample": 2, "accept_scan": 1, "step_tables": 1, "rope_cache": 1, "tree_attention": 1,
+            "cache_commit": 1}
 
 
 class SpecVerifyError(RuntimeError):
@@ -38,6 +44,18 @@ class SpecVerifyError(RuntimeError):
 
 class SvRows(C.Structure):
     _fields_ = [("data", C.c_void_p), ("dtype", C.c_int32), ("width", C.c_int32), ("row_stride", C.c_int64)]
+
+
+class SvKvCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int32), ("num_blocks", C.c_int32),
+                ("block_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("layers", C.c_int32),
+                ("block_stride", C.c_int64), ("token_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("layer_stride", C.c_int64)]
+
+
+class SvHeads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("dtype", C.c_int32), ("tokens", C.c_int32), ("heads", C.c_int32),
+                ("head_dim", C.c_int32), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 _lib = None
@@ -87,6 +105,14 @@ def load(path: str | None = None):
     lib.sv_suffix_append.argtypes = [P, i32, i32, P, P, i32, P]
     lib.sv_accept_scan.argtypes = [P, P, P, i32, i32, P, P, P]
     lib.sv_accept_scan.restype = C.c_int
+    i64, f64 = C.c_int64, C.c_double
+    lib.sv_step_tables.argtypes = [P, P, i32, i32, P, i32, P, P, i32, P, i32, P, P, P, P, P, i32, P, P, P]
+    lib.sv_rope_cache.argtypes = [SvHeads, SvHeads, SvHeads, P, P, P, i32, i32, f32, SvHeads, SvKvCache, P]
+    lib.sv_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, P]
+    lib.sv_tree_attention_workspace.argtypes = [i32, i32, i32, i32, i32, i32, i64]
+    lib.sv_tree_attention_workspace.restype = sz
+    lib.sv_tree_attention.argtypes = [SvHeads, SvKvCache, P, i32, P, P, i32, i32, P, i32, f32, SvHeads, P, P, P, sz, P]
+    lib.sv_cache_commit.argtypes = [SvKvCache, P, i32, P, P, P, i32, P, P, P, i32, P, P, P, P, P, P]
     lib.sv_selftest_wait_timeout.argtypes = [P, P, C.c_int64, P]
     lib.sv_selftest_wait_timeout.restype = C.c_int
     _lib = lib
@@ -343,6 +369,188 @@ def accept_scan(accept, draft, fix, out: dict | None = None, stream=None) -> dic
         out = dict(accept_len=_empty(R, torch.int32, dev), tokens=_empty((R, k + 1), torch.int32, dev))
     _check(lib.sv_accept_scan(_ptr(accept), _ptr(draft), _ptr(fix), R, k, _ptr(out["accept_len"]),
                               _ptr(out["tokens"]), _stream(stream)))
+    return out
+
+
+def _half_type(t) -> int:
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return SV_BF16
+    if t.dtype == torch.float16:
+        return SV_F16
+    raise TypeError(f"heads and caches must be bfloat16 or float16, got {t.dtype}")
+
+
+def heads_of(t) -> SvHeads:
+    """Describe a CUDA tensor of heads [tokens, heads, head_dim] (tokens and heads may be strided)."""
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError("heads must be a 3-D CUDA tensor [tokens, heads, head_dim]")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if D > 1 and sd != 1:
+        raise ValueError("entries of a head must be contiguous")
+    return SvHeads(t.data_ptr(), _half_type(t), T, H, D, st, sh)
+
+
+def cache_of(k, v) -> SvKvCache:
+    """Describe a paged cache: K and V tensors [num_blocks, block_size, kv_heads, head_dim], or with the layers in
+    front, of one dtype and the same strides (any order of the axes but the last)."""
+    if not k.is_cuda or not v.is_cuda or k.dim() not in (4, 5) or k.shape != v.shape:
+        raise ValueError("caches must be 4-D or 5-D CUDA tensors of one shape")
+    if k.dtype != v.dtype:
+        raise TypeError("K and V caches must have one dtype")
+    if k.stride() != v.stride():
+        raise ValueError("K and V caches must have the same strides")
+    if k.shape[-1] > 1 and k.stride(-1) != 1:
+        raise ValueError("entries of a head must be contiguous")
+    layers, layer_stride = (1, 0) if k.dim() == 4 else (k.shape[0], k.stride(0))
+    nb, bs, H, D = k.shape[-4:]
+    sb, st, sh, _ = k.stride()[-4:]
+    return SvKvCache(k.data_ptr(), v.data_ptr(), _half_type(k), nb, bs, H, D, layers, sb, st, sh, layer_stride)
+
+
+def _ints(t, name, n=None):
+    """An int32 CUDA tensor that is passed as it lies."""
+    import torch
+
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    return C.c_void_p(t.data_ptr())
+
+
+def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_size: int, T: int, parent=None,
+                mask_words: int = 0, out: dict | None = None, stream=None) -> dict:
+    """Lay a step's tokens out in the paged cache.  seq_len, new_len int32 [R]; block_table int32
+    [R, max_blocks], whose new entries are written in place; free_blocks int32 [num_blocks] with free_count
+    int32 [1] of them free; T the capacity of the packed arrays; parent int32 [T] or None (a chain).  Returns
+    cu_tokens [R + 1], kv_len [R], slot int64 [T], position [T], free_count [1], status [R] and, with parents,
+    mask int32 [T, mask_words] (ancestor bits)."""
+    import torch
+
+    lib = load()
+    R, dev = seq_len.numel(), seq_len.device
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be [R, max_blocks]")
+    if out is None:
+        out = dict(cu_tokens=_empty(R + 1, torch.int32, dev), kv_len=_empty(R, torch.int32, dev),
+                   slot=_empty(T, torch.int64, dev), position=_empty(T, torch.int32, dev),
+                   free_count=_empty(1, torch.int32, dev), status=_empty(R, torch.int32, dev))
+        if parent is not None:
+            out["mask"] = _empty((T, mask_words), torch.int32, dev)
+    mask = out.get("mask") if parent is not None else None
+    if R == 0:  # nothing to lay out
+        out["cu_tokens"].zero_()
+        out["free_count"].copy_(free_count)
+        for name in ("slot", "position"):
+            out[name].fill_(-1)
+        if mask is not None:
+            mask.zero_()
+        return out
+    _check(lib.sv_step_tables(_ints(seq_len, "seq_len"), _ints(new_len, "new_len", R), R, block_size,
+                              _ints(block_table, "block_table"), block_table.shape[1],
+                              _ints(free_blocks, "free_blocks"), _ints(free_count, "free_count", 1),
+                              free_blocks.numel(), None if parent is None else _ints(parent, "parent", T), T,
+                              _ptr(out["cu_tokens"]), _ptr(out["kv_len"]), _ptr(out["slot"]),
+                              _ptr(out["position"]), _ptr(mask), mask_words if mask is not None else 0,
+                              _ptr(out["free_count"]), _ptr(out.get("status")), _stream(stream)))
+    return out
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+               trained: float = 0.0, low: float = 0.0, high: float = 0.0, device="cuda"):
+    """Frequencies for rope_cache: an int64 tensor [rot_dim / 2] of 64-bit turn fractions (see sv_rope_freqs for
+    the scalings)."""
+    import torch
+
+    host = torch.zeros(max(rot_dim, 0) // 2, dtype=torch.int64)
+    _check(load().sv_rope_freqs(rot_dim, base, scaling, factor, trained, low, high, _ptr(host)))
+    return host.to(device)
+
+
+def rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, interleaved: bool = False, mscale: float = 1.0,
+               q_out=None, stream=None):
+    """Rotate q [T, heads, D] and k [T, kv_heads, D] at position int32 [T] and write k and v into the paged cache
+    at slot int64 [T] (-1: not cached).  freqs: rope_freqs(rot_dim).  Returns the rotated q (q_out may be q)."""
+    import torch
+
+    lib = load()
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if slot.dtype != torch.int64 or not slot.is_contiguous() or slot.numel() != q.shape[0]:
+        raise ValueError("slot must be a contiguous int64 tensor with an entry for each token")
+    if freqs.dtype not in (torch.int64, torch.uint64) or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous int64 tensor from rope_freqs")
+    _check(lib.sv_rope_cache(heads_of(q), heads_of(k), heads_of(v), _ints(position, "position", q.shape[0]),
+                             _ptr(slot), _ptr(freqs), 2 * freqs.numel(), 1 if interleaved else 0, mscale,
+                             heads_of(q_out), cache_of(k_cache, v_cache), _stream(stream)))
+    return q_out
+
+
+def tree_attention_workspace(R: int, T: int, max_tokens: int, heads: int, kv_heads: int, head_dim: int,
+                             max_kv: int) -> int:
+    return int(load().sv_tree_attention_workspace(R, T, max_tokens, heads, kv_heads, head_dim, max_kv))
+
+
+def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_tokens: int, mask=None,
+                   scale: float | None = None, with_lse: bool = False, out: dict | None = None, workspace=None,
+                   stream=None) -> dict:
+    """Attention of the packed step tokens q [T, heads, D] over the paged cache.  block_table int32
+    [R, max_blocks]; kv_len int32 [R]; cu_tokens int32 [R + 1]; max_tokens bounds a request's tokens; mask int32
+    [T, words] (which of its request's step tokens a token sees) or None (a chain); scale defaults to
+    D ** -0.5.  Returns out [T, heads, D] and, with_lse, lse float32 [T, heads]."""
+    import torch
+
+    lib = load()
+    T, heads, D = q.shape
+    R, max_blocks = block_table.shape
+    if out is None:
+        out = dict(out=torch.empty(q.shape, dtype=q.dtype, device=q.device))
+        if with_lse:
+            out["lse"] = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    if mask is not None and (mask.dim() != 2 or mask.shape[0] != T):
+        raise ValueError("mask must be [T, words]")
+    cache = cache_of(k_cache, v_cache)
+    if workspace is None:
+        workspace = _workspace(lib.sv_tree_attention_workspace(R, T, max_tokens, heads, cache.kv_heads, D,
+                                                               max_blocks * cache.block_size), q.device, None)
+    _check(lib.sv_tree_attention(heads_of(q), cache, _ints(block_table, "block_table"), max_blocks,
+                                 _ints(kv_len, "kv_len", R), _ints(cu_tokens, "cu_tokens", R + 1), R, max_tokens,
+                                 None if mask is None else _ints(mask, "mask"),
+                                 0 if mask is None else mask.shape[1], D ** -0.5 if scale is None else scale,
+                                 heads_of(out["out"]), _ptr(out.get("lse")), _ptr(out.get("status")),
+                                 _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    return out
+
+
+def cache_commit(k_cache, v_cache, block_table, seq_len, kv_len, cu_tokens, accept_len, k: int, free_blocks,
+                 free_count, branch=None, path=None, out: dict | None = None, stream=None) -> dict:
+    """Keep the accepted path of a verified tree: the accepted drafts' keys and values move behind the root in every
+    layer of the caches ([layers, ] num_blocks, block_size, kv_heads, head_dim), and the blocks without a kept token
+    are pushed on free_blocks.  accept_len int32 [R] and branch int32 [R] as verify_greedy returns them, or path
+    int32 [R, k] of the accepted tokens' numbers.  Returns seq_len [R], free_count [1] and status [R]."""
+    import torch
+
+    lib = load()
+    R, dev = seq_len.numel(), seq_len.device
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be [R, max_blocks]")
+    if out is None:
+        out = dict(seq_len=_empty(R, torch.int32, dev), free_count=_empty(1, torch.int32, dev),
+                   status=_empty(R, torch.int32, dev))
+    if R == 0:
+        out["free_count"].copy_(free_count)
+        return out
+    _check(lib.sv_cache_commit(cache_of(k_cache, v_cache), _ints(block_table, "block_table"), block_table.shape[1],
+                               _ints(seq_len, "seq_len"), _ints(kv_len, "kv_len", R),
+                               _ints(cu_tokens, "cu_tokens", R + 1), R, _ints(accept_len, "accept_len", R),
+                               None if branch is None else _ints(branch, "branch", R),
+                               None if path is None else _ints(path, "path", R * k), k,
+                               _ints(free_blocks, "free_blocks", k_cache.shape[-4]),
+                               _ints(free_count, "free_count", 1), _ptr(out["seq_len"]), _ptr(out["free_count"]),
+                               _ptr(out.get("status")), _stream(stream)))
     return out
 
 

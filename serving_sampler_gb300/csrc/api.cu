@@ -1,6 +1,7 @@
 // The C ABI of specverify: argument checks, then the kernel launchers.
 // Declarations and the contract of every call are in include/specverify.h.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -46,6 +47,42 @@ static int check_workspace(const void* ws, size_t bytes, size_t need)
 }
 
 static int launched(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_LAUNCH; }
+
+static int check_cache(const sv_kv_cache& c, bool data)
+{
+    if (c.dtype != SV_BF16 && c.dtype != SV_F16) return SV_ERR_DTYPE;
+    if (c.num_blocks < 1 || c.block_size < 1 || c.kv_heads < 1 || c.layers < 1 || c.head_dim < 1)
+        return SV_ERR_SHAPE;
+    if (c.head_dim > SV_MAX_HEAD_DIM) return SV_ERR_LIMIT;
+    if (c.head_dim % 8 != 0 || c.block_size % 8 != 0) return SV_ERR_SHAPE;
+    // every axis steps by at least one head's entries where it has more than one step
+    const int64_t least = c.head_dim;
+    if ((c.num_blocks > 1 && c.block_stride < least) || c.token_stride < least ||
+        (c.kv_heads > 1 && c.head_stride < least) || (c.layers > 1 && c.layer_stride < least) ||
+        c.block_stride < 0 || c.head_stride < 0 || c.layer_stride < 0)
+        return SV_ERR_SHAPE;
+    if (data && (c.k == nullptr || c.v == nullptr)) return SV_ERR_INVALID_ARG;
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || c.token_stride % 8 != 0 ||
+        (c.num_blocks > 1 && c.block_stride % 8 != 0) || (c.kv_heads > 1 && c.head_stride % 8 != 0) ||
+        (c.layers > 1 && c.layer_stride % 8 != 0))
+        return SV_ERR_ALIGN;
+    return SV_OK;
+}
+
+// Heads of packed tokens that go with `dtype`, `head_dim` and `tokens`.
+static int check_heads(const sv_heads& h, int32_t dtype, int32_t head_dim, int32_t tokens)
+{
+    if (h.dtype != dtype) return SV_ERR_DTYPE;
+    if (h.heads < 1 || h.head_dim != head_dim || h.tokens != tokens) return SV_ERR_SHAPE;
+    if ((h.tokens > 1 && h.token_stride < head_dim) || (h.heads > 1 && h.head_stride < head_dim) ||
+        h.token_stride < 0 || h.head_stride < 0)
+        return SV_ERR_SHAPE;
+    if (tokens > 0 && h.data == nullptr) return SV_ERR_INVALID_ARG;
+    if (!aligned(h.data, 16) || (h.tokens > 1 && h.token_stride % 8 != 0) ||
+        (h.heads > 1 && h.head_stride % 8 != 0))
+        return SV_ERR_ALIGN;
+    return SV_OK;
+}
 
 static bool have_device()
 {
@@ -344,6 +381,168 @@ int sv_accept_scan(const uint8_t* accept, const int32_t* draft, const int32_t* f
         return SV_ERR_ALIGN;
     if (!have_device()) return SV_ERR_DEVICE;
     return launched(launch_accept_scan(accept, draft, fix, R, k, accept_len, tokens, stream));
+}
+
+int sv_step_tables(const int32_t* seq_len, const int32_t* new_len, int32_t R, int32_t block_size,
+                   int32_t* block_table, int32_t max_blocks, const int32_t* free_blocks,
+                   const int32_t* free_count, int32_t num_blocks, const int32_t* parent, int32_t T,
+                   int32_t* cu_tokens, int32_t* kv_len, int64_t* slot, int32_t* position, uint32_t* mask,
+                   int32_t mask_words, int32_t* free_count_out, int32_t* status, sv_stream_t stream)
+{
+    if (R < 0 || T < 0 || block_size < 1 || max_blocks < 0 || num_blocks < 0) return SV_ERR_INVALID_ARG;
+    if (mask_words < 0 || (parent != nullptr && mask_words < 1)) return SV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX) return SV_ERR_LIMIT;
+    if (R == 0) return SV_OK;
+    if (seq_len == nullptr || new_len == nullptr || free_count == nullptr || cu_tokens == nullptr ||
+        kv_len == nullptr || free_count_out == nullptr || (max_blocks > 0 && block_table == nullptr) ||
+        (num_blocks > 0 && free_blocks == nullptr))
+        return SV_ERR_INVALID_ARG;
+    if (T > 0 && (slot == nullptr || position == nullptr || (parent != nullptr && mask == nullptr)))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(seq_len, 4) || !aligned(new_len, 4) || !aligned(block_table, 4) || !aligned(free_blocks, 4) ||
+        !aligned(free_count, 4) || !aligned(parent, 4) || !aligned(cu_tokens, 4) || !aligned(kv_len, 4) ||
+        !aligned(slot, 8) || !aligned(position, 4) || !aligned(mask, 4) || !aligned(free_count_out, 4) ||
+        !aligned(status, 4))
+        return SV_ERR_ALIGN;
+    if (!have_device()) return SV_ERR_DEVICE;
+    const StepTablesArgs a{seq_len,     new_len,    R,      block_size, max_blocks, num_blocks, T,
+                           mask_words,  block_table, free_blocks, free_count, parent, cu_tokens, kv_len,
+                           slot,        position,   mask,   free_count_out, status};
+    return launched(launch_step_tables(a, stream));
+}
+
+int sv_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, const int64_t* slot,
+                  const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float mscale, sv_heads q_out,
+                  sv_kv_cache cache, sv_stream_t stream)
+{
+    if (interleaved != 0 && interleaved != 1) return SV_ERR_INVALID_ARG;
+    if (q.tokens < 0) return SV_ERR_INVALID_ARG;
+    if (int rc = check_cache(cache, q.tokens > 0)) return rc;
+    if (cache.layers != 1) return SV_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > cache.head_dim) return SV_ERR_SHAPE;
+    if (q.tokens == 0) return SV_OK;
+    if (int rc = check_heads(q, cache.dtype, cache.head_dim, q.tokens)) return rc;
+    if (int rc = check_heads(k, cache.dtype, cache.head_dim, q.tokens)) return rc;
+    if (int rc = check_heads(v, cache.dtype, cache.head_dim, q.tokens)) return rc;
+    if (int rc = check_heads(q_out, cache.dtype, cache.head_dim, q.tokens)) return rc;
+    if (k.heads != cache.kv_heads || v.heads != cache.kv_heads || q_out.heads != q.heads) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(q.heads) + 2 * static_cast<int64_t>(cache.kv_heads) > 65536) return SV_ERR_LIMIT;
+    if (position == nullptr || slot == nullptr || (rot_dim > 0 && freqs == nullptr)) return SV_ERR_INVALID_ARG;
+    if (!aligned(position, 4) || !aligned(slot, 8) || !aligned(freqs, 8)) return SV_ERR_ALIGN;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_rope_cache(RopeArgs{q, k, v, q_out, position, slot, freqs, rot_dim, interleaved,
+                                               mscale, cache},
+                                      stream));
+}
+
+int sv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained, double low,
+                  double high, uint64_t* freqs)
+{
+    if (rot_dim < 0 || rot_dim % 2 != 0 || !(base > 0.0) || !std::isfinite(base)) return SV_ERR_INVALID_ARG;
+    if (scaling < SV_ROPE_PLAIN || scaling > SV_ROPE_BY_TURNS) return SV_ERR_INVALID_ARG;
+    if (scaling != SV_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor))) return SV_ERR_INVALID_ARG;
+    if (scaling == SV_ROPE_BASE && rot_dim == 2) return SV_ERR_SHAPE;  // its exponent has no value there
+    const bool parts = scaling == SV_ROPE_BY_DIM || scaling == SV_ROPE_BY_TURNS;
+    if (parts && (!(trained > 0.0) || !(low > 0.0) || !(high > low) || !std::isfinite(trained) || !std::isfinite(high)))
+        return SV_ERR_INVALID_ARG;
+    if (scaling == SV_ROPE_BY_DIM && !(base > 1.0)) return SV_ERR_INVALID_ARG;
+    if (rot_dim == 0) return SV_OK;
+    if (freqs == nullptr) return SV_ERR_INVALID_ARG;
+    if (!aligned(freqs, 8)) return SV_ERR_ALIGN;
+    const double two_pi = 6.283185307179586476925286766559;
+    const int32_t half = rot_dim / 2;
+    const double b = scaling == SV_ROPE_BASE ? base * std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2)) : base;
+    // the pair index (not rounded) whose frequency turns `t` times within the trained positions
+    auto index_of = [&](double t) { return half * std::log(trained / (t * two_pi)) / std::log(base); };
+    for (int32_t i = 0; i < half; ++i) {
+        double f = std::pow(b, -static_cast<double>(i) / half);
+        if (scaling == SV_ROPE_LINEAR) f /= factor;
+        if (parts) {
+            double keep;  // 1: the frequency stays, 0: stretched by the factor
+            if (scaling == SV_ROPE_BY_TURNS) {
+                keep = (trained * f / two_pi - low) / (high - low);
+            } else {
+                const double first = std::max(0.0, std::floor(index_of(high)));
+                const double last = std::min(static_cast<double>(rot_dim - 1), std::ceil(index_of(low)));
+                keep = 1.0 - (i - first) / std::max(last - first, 1e-3);
+            }
+            keep = std::min(1.0, std::max(0.0, keep));
+            f = f / factor * (1.0 - keep) + f * keep;
+        }
+        // whole turns per position drop out; 2^64 itself would be a whole turn
+        double turns = f / two_pi;
+        turns -= std::floor(turns);
+        const double scaled = std::nearbyint(turns * 18446744073709551616.0);
+        freqs[i] = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+    }
+    return SV_OK;
+}
+
+size_t sv_tree_attention_workspace(int32_t R, int32_t T, int32_t max_tokens, int32_t heads, int32_t kv_heads,
+                                   int32_t head_dim, int64_t max_kv)
+{
+    if (R < 0 || T < 0 || max_tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 ||
+        head_dim > SV_MAX_HEAD_DIM || max_kv < 0 || max_kv > INT32_MAX || heads / kv_heads > SV_MAX_GROUP)
+        return 0;
+    return attn_workspace_bytes(R, T, max_tokens, heads, kv_heads, head_dim, max_kv);
+}
+
+int sv_tree_attention(sv_heads q, sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks,
+                      const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, int32_t max_tokens,
+                      const uint32_t* mask, int32_t mask_words, float scale, sv_heads out, float* lse,
+                      int32_t* status, void* workspace, size_t workspace_bytes, sv_stream_t stream)
+{
+    if (R < 0 || q.tokens < 0 || max_tokens < 0 || max_blocks < 0) return SV_ERR_INVALID_ARG;
+    if (mask_words < 0 || (mask != nullptr && mask_words < 1)) return SV_ERR_INVALID_ARG;
+    if (int rc = check_cache(cache, R > 0 && q.tokens > 0)) return rc;
+    if (cache.layers != 1) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(max_blocks) * cache.block_size > INT32_MAX) return SV_ERR_LIMIT;
+    if (R == 0 || q.tokens == 0) return SV_OK;
+    if (int rc = check_heads(q, cache.dtype, cache.head_dim, q.tokens)) return rc;
+    if (int rc = check_heads(out, cache.dtype, cache.head_dim, q.tokens)) return rc;
+    if (out.heads != q.heads || q.heads % cache.kv_heads != 0) return SV_ERR_SHAPE;
+    if (q.heads / cache.kv_heads > SV_MAX_GROUP) return SV_ERR_LIMIT;
+    if (kv_len == nullptr || cu_tokens == nullptr || (max_blocks > 0 && block_table == nullptr))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(kv_len, 4) || !aligned(cu_tokens, 4) || !aligned(mask, 4) ||
+        !aligned(lse, 4) || !aligned(status, 4))
+        return SV_ERR_ALIGN;
+    if (int rc = check_workspace(workspace, workspace_bytes,
+                                 attn_workspace_bytes(R, q.tokens, max_tokens, q.heads, cache.kv_heads, q.head_dim,
+                                                      static_cast<int64_t>(max_blocks) * cache.block_size)))
+        return rc;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_tree_attention(AttnArgs{q, out, cache, block_table, max_blocks, kv_len, cu_tokens, R,
+                                                   max_tokens, mask, mask_words, scale, lse, status, workspace},
+                                          stream));
+}
+
+int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len,
+                    const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, const int32_t* accept_len,
+                    const int32_t* branch, const int32_t* path, int32_t k, int32_t* free_blocks,
+                    const int32_t* free_count, int32_t* seq_len_out, int32_t* free_count_out, int32_t* status,
+                    sv_stream_t stream)
+{
+    if (R < 0 || k < 0 || max_blocks < 0) return SV_ERR_INVALID_ARG;
+    if (k > SV_MAX_K) return SV_ERR_LIMIT;
+    if (branch != nullptr && path != nullptr) return SV_ERR_INVALID_ARG;
+    if (cache.layers > 16384) return SV_ERR_LIMIT;  // two rows of the launch grid a layer
+    if (int rc = check_cache(cache, R > 0)) return rc;
+    if (static_cast<int64_t>(max_blocks) * cache.block_size > INT32_MAX) return SV_ERR_LIMIT;
+    if (R == 0) return SV_OK;
+    if (seq_len == nullptr || kv_len == nullptr || cu_tokens == nullptr || accept_len == nullptr ||
+        free_blocks == nullptr || free_count == nullptr || seq_len_out == nullptr || free_count_out == nullptr ||
+        (max_blocks > 0 && block_table == nullptr))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(kv_len, 4) || !aligned(cu_tokens, 4) ||
+        !aligned(accept_len, 4) || !aligned(branch, 4) || !aligned(path, 4) || !aligned(free_blocks, 4) ||
+        !aligned(free_count, 4) || !aligned(seq_len_out, 4) || !aligned(free_count_out, 4) || !aligned(status, 4))
+        return SV_ERR_ALIGN;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_cache_commit(CommitArgs{cache, block_table, max_blocks, seq_len, kv_len, cu_tokens, R,
+                                                   accept_len, branch, path, k, free_blocks, free_count,
+                                                   seq_len_out, free_count_out, status},
+                                        stream));
 }
 
 }  // extern "C"

@@ -104,6 +104,64 @@ cudaError_t launch_cfg_merge_sample(const Rows& cond, const Rows& uncond, const 
                                     int32_t* tokens, float* tv, int32_t* status, void* workspace,
                                     cudaStream_t stream);
 
+// ---- the cache side of a verify step ----------------------------------------
+
+struct StepTablesArgs {
+    const int32_t *seq_len, *new_len;
+    int32_t R, block_size, max_blocks, num_blocks, T, mask_words;
+    int32_t* block_table;
+    const int32_t *free_blocks, *free_count, *parent;
+    int32_t *cu_tokens, *kv_len;
+    int64_t* slot;
+    int32_t* position;
+    uint32_t* mask;
+    int32_t *free_count_out, *status;
+};
+cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream);
+
+struct CommitArgs {
+    sv_kv_cache cache;
+    const int32_t* block_table;
+    int32_t max_blocks;
+    const int32_t *seq_len, *kv_len, *cu_tokens;
+    int32_t R;
+    const int32_t *accept_len, *branch, *path;
+    int32_t k;
+    int32_t* free_blocks;
+    const int32_t* free_count;
+    int32_t *seq_len_out, *free_count_out, *status;
+};
+cudaError_t launch_cache_commit(const CommitArgs& a, cudaStream_t stream);
+
+struct RopeArgs {
+    sv_heads q, k, v, q_out;
+    const int32_t* position;
+    const int64_t* slot;
+    const uint64_t* freqs;
+    int32_t rot_dim, interleaved;
+    float mscale;
+    sv_kv_cache cache;
+};
+cudaError_t launch_rope_cache(const RopeArgs& a, cudaStream_t stream);
+
+struct AttnArgs {
+    sv_heads q, out;
+    sv_kv_cache cache;
+    const int32_t* block_table;
+    int32_t max_blocks;
+    const int32_t *kv_len, *cu_tokens;
+    int32_t R, max_tokens;
+    const uint32_t* mask;
+    int32_t mask_words;
+    float scale;
+    float* lse;
+    int32_t* status;
+    void* workspace;
+};
+size_t attn_workspace_bytes(int32_t R, int32_t T, int32_t max_tokens, int32_t heads, int32_t kv_heads,
+                            int32_t head_dim, int64_t max_kv);
+cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream);
+
 // number of SMs of the current device
 int device_sm_count();
 
