@@ -32,7 +32,7 @@ ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_DIM, ROPE_BY_TURNS = 0, 1, 2, 3, 4
 # kernels one call launches: verify_sample with a prebuilt d2t plan (or the identity map)
 # launches 2, and 2 more when it builds the plan itself; d2t_plan launches 2
 LAUNCHES = {"verify_greedy": 2, "verify_greedy_top2": 2, "infer_modality": 2, "pool_append": 1, "pool_lookup": 1, "suffix_append": 1, "verify_sample": 2, "verify_sample_plan_in_call": 4, "d2t_plan": 2,
-            "cfg_merge_sample": 2, "accept_scan": 1, "step_tables": 1, "rope_cache": 1, "tree_attention": 1,
+            "cfg_merge_sample": 2, "accept_scan": 1, "step_tables": 1, "rope_cache": 1, "tree_attention": 2,
             "cache_commit": 1}
 
 
