@@ -7,13 +7,12 @@
 // (a negative scale turns the sign of Q inside the product).
 //
 // One persistent CTA per SM, warp roles:
-//   warp 0      copies K and V tiles, page by page, with tensor maps into a ring of
+//   warps 0, 2  copy K and V tiles, block by block, with tensor maps into a ring of
 //               five stages (the block ids of the next tile are fetched before the
 //               wait for a stage);
 //   warp 1      issues the products; S in tensor memory, P over S in tensor memory as
 //               the left operand of P V, O in tensor memory;
-//   warp 2      copies Q;
-//   warp 3      cleans V where a tile holds positions that not every row sees: rows
+//   warp 3      copies Q, and cleans V where a tile holds positions that not every row sees: rows
 //               behind the last key become 0 (P is 0 there, but 0 * NaN is not), and so
 //               do NaN and infinite entries, which are noted and added in 32 bits at
 //               the end of the group to the rows that do see them;
@@ -185,6 +184,14 @@ struct Ring {
             phase ^= 1u;
         }
     }
+    __device__ __forceinline__ void prev2(int32_t n)
+    {
+        stage -= 2;
+        if (stage < 0) {
+            stage += n;
+            phase ^= 1u;
+        }
+    }
 };
 
 struct Shared {
@@ -201,10 +208,10 @@ struct Shared {
 // Bounded wait; gives up as well when another role of the CTA has given up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Shared& sh)
 {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_poll(bar, parity)) return true;
     const long long t0 = clock64();
     volatile int* stop = &sh.stop;
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_poll(bar, parity)) {
         if (*stop != 0) return false;
         if (clock64() - t0 > kWaitLimitCycles) {
             *stop = 1;
@@ -249,6 +256,11 @@ __device__ __forceinline__ Join join_at(float m, float mg)
 __device__ __forceinline__ float join_sum(float x, float y, const Join& j)
 {
     return __fmaf_rn(y, j.b, __fmul_rn(x, j.a));
+}
+// the same on two entries at once: the two roundings are those of join_sum
+__device__ __forceinline__ float2 join_sum2(float2 x, float2 y, const Join& j)
+{
+    return fma2(y, make_float2(j.b, j.b), mul2(x, make_float2(j.a, j.a)));
 }
 __device__ __forceinline__ float final_lse(float m, float l)
 {
@@ -321,21 +333,23 @@ __device__ void find_share(const AttnParams& p, Shared& sh)
     __syncthreads();
 }
 
-// ---- warp 0: K and V -------------------------------------------------------------
+// ---- warps 0 and 2: K and V --------------------------------------------------------
+// Tile t of the line fills stages 2 t (K) and 2 t + 1 (V) of the ring; warp 0 copies K
+// and warp 2 V (one warp for both could not issue the copies of 16-token blocks fast
+// enough).  One lane issues, block by block; lane i holds block and place of box i.
 template <int DP>
-__device__ void copy_kv(const AttnParams& p, Shared& sh, unsigned char* ring, const CUtensorMap* mk,
-                        const CUtensorMap* mv)
+__device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring, const CUtensorMap* map, int first)
 {
     constexpr int kChunks = DP / 64;
     constexpr uint32_t kStage = kTile * DP * 2;
     const int lane = threadIdx.x & 31;
     Walk w{sh.start, sh.end, -1, {}};
     Run u;
-    int32_t stage = 0;
-    uint32_t phase = 0;
-    bool wrapped = false, ok = true;
-    int32_t filled = 0;
+    Ring rt{first, 0};
+    int32_t fills = 0;  // of this warp; from the ring's second turn on a stage is waited for
+    bool ok = true;
     const int32_t subs = kTile / p.box_rows;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
     while (ok && next_run(p, w, u)) {
         const int32_t* table = p.block_table + static_cast<int64_t>(w.known) * p.max_blocks;
         const int32_t t1 = min(u.gb * u.gt, u.nt);
@@ -346,108 +360,68 @@ __device__ void copy_kv(const AttnParams& p, Shared& sh, unsigned char* ring, co
             return lane < subs && x < u.kv_end ? table[x / p.block_size] : 0;
         };
         int32_t id = block_of(t);
-        for (; ok && t < t1; ++t) {
-            const int32_t now = id;
-            if (t + 1 < t1) id = block_of(t + 1);
-            const int32_t x = t * kTile + lane * p.box_rows;
-            const int32_t place = x % p.block_size;
+        for (; t < t1; ++t) {
+            const int32_t block = id;
+            if (t + 1 < t1) id = block_of(t + 1);  // in flight while this tile is issued
+            const int32_t place = (t * kTile + lane * p.box_rows) % p.block_size;
             const int32_t live = min(subs, (u.kv_end - t * kTile + p.box_rows - 1) / p.box_rows);
-            for (int kv = 0; kv < 2; ++kv) {
-                if (wrapped) ok = warp_wait(&sh.kv_empty[stage], phase ^ 1u, sh);
-                if (!ok) break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&sh.kv_full[stage], static_cast<uint32_t>(live * p.box_rows * 128 * kChunks));
-                __syncwarp();
-                if (lane < live) {
-                    unsigned char* dst = ring + static_cast<size_t>(stage) * kStage + lane * p.box_rows * 128;
+            uint64_t* full = &sh.kv_full[rt.stage];
+            // the stage's fill before this one is the ring's last turn: `first + 2 * fills` stages in
+            if (first + 2 * fills >= p.stages && !warp_wait(&sh.kv_empty[rt.stage], rt.phase ^ 1u, sh)) {
+                ok = false;
+                break;
+            }
+            unsigned char* dst = ring + static_cast<size_t>(rt.stage) * kStage;
+            if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(live) * box_bytes * kChunks);
+            for (int sub = 0; sub < live; ++sub) {
+                const int32_t blk = __shfl_sync(0xFFFFFFFFu, block, sub), pl = __shfl_sync(0xFFFFFFFFu, place, sub);
+                if (elect_one()) {
 #pragma unroll
                     for (int ch = 0; ch < kChunks; ++ch)
-                        tma_load_4d(dst + ch * kTile * 128, kv == 0 ? mk : mv, &sh.kv_full[stage], ch * 64, place,
-                                    u.head, now);
-                }
-                __syncwarp();
-                filled = min(filled + 1, p.stages);
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                    wrapped = true;
+                        tma_load_4d(dst + sub * box_bytes + ch * kTile * 128, map, full, ch * 64, pl, u.head, blk);
                 }
             }
+            __syncwarp();
+            ++fills;
+            rt.next2(p.stages);
         }
     }
     // a CTA that gave up does not leave before its copies have landed
     if (!ok || sh.stop != 0) {
-        for (int32_t i = 0; i < filled; ++i) {
-            if (--stage < 0) {
-                stage = p.stages - 1;
-                phase ^= 1u;
-            }
-            mbar_wait_bounded(&sh.kv_full[stage], phase);
+        for (int32_t i = min(fills, p.stages); i > 0; --i) {
+            rt.prev2(p.stages);
+            mbar_wait_bounded(&sh.kv_full[rt.stage], rt.phase);
         }
     }
 }
 
-// ---- warp 2: Q ---------------------------------------------------------------------
-template <int DP>
-__device__ void copy_q(const AttnParams& p, Shared& sh, unsigned char* q_smem, const CUtensorMap* mq)
-{
-    constexpr int kChunks = DP / 64;
-    constexpr uint32_t kQ = kTile * DP * 2;
-    const int lane = threadIdx.x & 31;
-    Walk w{sh.start, sh.end, -1, {}};
-    Run u;
-    uint32_t used[2] = {0, 0};
-    int32_t runs = 0;
-    const uint32_t bytes = static_cast<uint32_t>(p.group * p.tile_tokens * 128 * kChunks);
-    bool ok = true;
-    while (ok && next_run(p, w, u)) {
-        if (min(u.gb * u.gt, u.nt) <= u.ga * u.gt) continue;
-        const int tiles = u.second ? 2 : 1;
-        for (int s = 0; s < tiles; ++s) {
-            const int b = p.pairs == 2 ? s : runs & 1;
-            if (used[b] > 0) ok = warp_wait(&sh.q_empty[b], (used[b] - 1) & 1u, sh);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&sh.q_full[b], bytes);
-#pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch)
-                    tma_load_3d(q_smem + b * kQ + ch * kTile * 128, mq, &sh.q_full[b], ch * 64, u.head * p.group,
-                                u.tok0 + (u.tile0 + s) * p.tile_tokens);
-            }
-            __syncwarp();
-            ++used[b];
-        }
-        ++runs;
-    }
-    if (!ok || sh.stop != 0)
-        for (int b = 0; b < 2; ++b)
-            if (used[b] > 0) mbar_wait_bounded(&sh.q_full[b], (used[b] - 1) & 1u);
-}
-
-// ---- warp 3: V that not every row sees -----------------------------------------------
-// It follows every stage, also those it has nothing to do with, and each stage waits for
+// ---- warp 3: Q, and V that not every row sees ---------------------------------------
+// Q of a run is copied when the run's first tile is waited for.  The warp follows every stage, also those it has nothing to do with, and each stage waits for
 // its arrival before it is filled again: the parity of a barrier tells two fills of a
 // stage apart only for a warp that is never a whole turn of the ring ahead or behind.
 template <int DP, bool F16>
-__device__ void clean_v(const AttnParams& p, Shared& sh, unsigned char* ring)
+__device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q_smem, unsigned char* ring,
+                               const CUtensorMap* mq)
 {
     constexpr int kChunks = DP / 64;
-    constexpr uint32_t kStage = kTile * DP * 2;
+    constexpr uint32_t kStage = kTile * DP * 2, kQ = kTile * DP * 2;
     constexpr uint32_t kExp = F16 ? 0x7C007C00u : 0x7F807F80u;
     const int lane = threadIdx.x & 31;
     Walk w{sh.start, sh.end, -1, {}};
     Run u;
     Ring rk{0, 0}, rv{1, 0};
-    uint32_t group = 0;
-    while (next_run(p, w, u)) {
+    uint32_t group = 0, used[2] = {0, 0};
+    int32_t runs = 0;
+    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens * 128 * kChunks);
+    auto follow = [&]() {
         const int32_t all = seen_by_all(p, u, u.tile0);
         for (int32_t g = u.ga; g < u.gb; ++g, ++group) {
             const int32_t t1 = min((g + 1) * u.gt, u.nt);
             for (int32_t t = g * u.gt; t < t1; ++t, rk.next2(p.stages), rv.next2(p.stages)) {
                 const int32_t x0 = t * kTile;
-                if (!warp_wait(&sh.kv_full[rk.stage], rk.phase, sh)) return;
+                if (!warp_wait(&sh.kv_full[rk.stage], rk.phase, sh)) return false;
                 if (lane == 0) mbar_arrive(&sh.kv_empty[rk.stage]);
-                if (!warp_wait(&sh.kv_full[rv.stage], rv.phase, sh)) return;
+                if (!warp_wait(&sh.kv_full[rv.stage], rv.phase, sh)) return false;
                 if (x0 + kTile > all) {
                     unsigned char* base = ring + static_cast<size_t>(rv.stage) * kStage;
                     const int32_t first = max(0, all - x0), end = min(kTile, u.kv_end - x0);
@@ -477,7 +451,33 @@ __device__ void clean_v(const AttnParams& p, Shared& sh, unsigned char* ring)
                 if (lane == 0) mbar_arrive(&sh.kv_empty[rv.stage]);
             }
         }
+        return true;
+    };
+    bool ok = true;
+    while (ok && next_run(p, w, u)) {
+        if (min(u.gb * u.gt, u.nt) > u.ga * u.gt) {
+            const int tiles = u.second ? 2 : 1;
+            for (int s = 0; ok && s < tiles; ++s) {
+                const int b = p.pairs == 2 ? s : runs & 1;
+                if (used[b] > 0) ok = warp_wait(&sh.q_empty[b], (used[b] - 1) & 1u, sh);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sh.q_full[b], q_bytes);
+#pragma unroll
+                    for (int ch = 0; ch < kChunks; ++ch)
+                        tma_load_3d(q_smem + b * kQ + ch * kTile * 128, mq, &sh.q_full[b], ch * 64, u.head * p.group,
+                                    u.tok0 + (u.tile0 + s) * p.tile_tokens);
+                }
+                __syncwarp();
+                ++used[b];
+            }
+            ++runs;
+        }
+        ok = ok && follow();
     }
+    if (!ok || sh.stop != 0)
+        for (int b = 0; b < 2; ++b)
+            if (used[b] > 0) mbar_wait_bounded(&sh.q_full[b], (used[b] - 1) & 1u);
 }
 
 // ---- warp 1: products -------------------------------------------------------------------
@@ -485,7 +485,6 @@ template <int DP>
 __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr, uint32_t ring_addr, uint32_t tmem)
 {
     constexpr uint32_t kStage = kTile * DP * 2, kQ = kTile * DP * 2, kChunk = kTile * 128;
-    const bool lead = (threadIdx.x & 31) == 0;
     Walk w{sh.start, sh.end, -1, {}};
     Run u;
     Ring rk{0, 0}, rv{1, 0};  // next key tile to multiply with Q, next value tile
@@ -496,7 +495,7 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
 
     // S[b] = Q[q] K[stage]
     auto qk = [&](int b, int q, int32_t stage) {
-        if (lead) {
+        if (elect_one()) {
             const uint64_t qa = smem_operand(q_addr + q * kQ, 16, 1024);
             const uint64_t kb = smem_operand(ring_addr + stage * kStage, 16, 1024);
 #pragma unroll
@@ -509,7 +508,7 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
     };
     // O[o] (+)= P[b] V[stage]
     auto pv = [&](int b, int o, int32_t stage, bool add) {
-        if (lead) {
+        if (elect_one()) {
             const uint64_t vb = smem_operand(ring_addr + stage * kStage, kChunk, 1024);
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
@@ -519,7 +518,7 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
         }
     };
     auto release = [&](uint64_t* bar) {
-        if (lead) product_commit(bar);
+        if (elect_one()) product_commit(bar);
     };
 
     bool ok = true;
@@ -632,7 +631,53 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const Run& u,
     return bits & below(u.kv_end - x);
 }
 
-template <int DP, bool F16>
+// 16 probabilities of a row: 2^(c z - m), hidden ones 0; packed over the scores
+template <bool F16, bool MASKED>
+__device__ __forceinline__ void exp_chunk(const uint32_t (&z)[16], uint32_t bits, float2 c2, float2 off2, float2& s0,
+                                          float2& s1, uint32_t addr)
+{
+    uint32_t pk[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float2 x = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, off2);
+        x.x = exp2_fast(x.x);
+        x.y = exp2_fast(x.y);
+        if (MASKED) {
+            x.x = (bits >> (2 * e)) & 1u ? x.x : 0.0f;
+            x.y = (bits >> (2 * e + 1)) & 1u ? x.y : 0.0f;
+        }
+        if (e & 1)
+            s1 = add2(s1, x);
+        else
+            s0 = add2(s0, x);
+        pk[e] = pack_pair<F16>(x.x, x.y);
+    }
+    tmem_st8(addr, pk);
+}
+
+// A row's probabilities of a whole tile, and their sum.  The loads of 16 scores run
+// while the 16 before them are worked on; P lies over scores that have been read.
+template <bool F16, bool MASKED>
+__device__ __forceinline__ float exp_tile(uint32_t s_addr, const uint32_t (&bits)[4], float c, float off)
+{
+    const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
+    float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+    uint32_t za[16], zb[16];
+    tmem_ld16(za, s_addr);
+#pragma unroll
+    for (int ch = 0; ch < 8; ch += 2) {
+        tmem_wait_ld(za);
+        tmem_ld16(zb, s_addr + (ch + 1) * 16);
+        exp_chunk<F16, MASKED>(za, bits[ch / 2], c2, off2, s0, s1, s_addr + ch * 8);
+        tmem_wait_ld(zb);
+        if (ch + 2 < 8) tmem_ld16(za, s_addr + (ch + 2) * 16);
+        exp_chunk<F16, MASKED>(zb, bits[ch / 2] >> 16, c2, off2, s0, s1, s_addr + (ch + 1) * 8);
+    }
+    s0 = add2(s0, s1);
+    return s0.x + s0.y;
+}
+
+template <int DP, bool F16, int PAIRS>
 __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int s)
 {
     const int row = threadIdx.x & (kTile - 1);
@@ -643,11 +688,11 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
     Walk w{sh.start, sh.end, -1, {}};
     Run u;
     uint32_t n = 0, group = 0;  // key tiles and groups so far
-    float acc[DP];
+    float2 acc[DP / 2];
     // The product of tile x is waited for on the barrier of its S buffer: the buffer's next tile
     // is not there before that product is complete, so the barrier is never a phase behind.
     auto wait_pv = [&](uint32_t x) {
-        return p.pairs == 2 ? warp_wait(&sh.pv_done[s], x & 1u, sh) : warp_wait(&sh.pv_done[x & 1u], (x >> 1) & 1u, sh);
+        return PAIRS == 2 ? warp_wait(&sh.pv_done[s], x & 1u, sh) : warp_wait(&sh.pv_done[x & 1u], (x >> 1) & 1u, sh);
     };
     const uint32_t o_addr = tmem + lane_base + 2 * kTile + s * kTile;
 
@@ -664,6 +709,8 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
         const int32_t all = seen_by_all(p, u, u.tile0 + s), cleaned = seen_by_all(p, u, u.tile0);
         const bool whole = u.ga == 0;  // from the first group on: joined here
         float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int e = 0; e < DP / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
         const int32_t slot_row = s * kTile + row;
         float* const slots = p.slots + static_cast<int64_t>(blockIdx.x) * p.slots_per_cta * p.slot_floats;
 
@@ -671,29 +718,35 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
             const int32_t ta = g * u.gt, tb = min(ta + u.gt, u.nt);
             float ref = -INFINITY, off = 0.0f, l = 0.0f;
             for (int32_t t = ta; t < tb; ++t, ++n) {
-                const int b = p.pairs == 2 ? s : static_cast<int>(n & 1u);
-                const uint32_t turn = p.pairs == 2 ? n & 1u : (n >> 1) & 1u;
+                const int b = PAIRS == 2 ? s : static_cast<int>(n & 1u);
+                const uint32_t turn = PAIRS == 2 ? n & 1u : (n >> 1) & 1u;
                 if (!warp_wait(&sh.s_full[b], turn, sh)) return;
                 tmem_fence_after();
                 if (warp_live) {
                     const uint32_t s_addr = tmem + lane_base + b * kTile;
                     const int32_t x0 = t * kTile;
                     const bool masked = x0 + kTile > all;
-                    uint32_t z[32];
-                    float top = -INFINITY;
+                    uint32_t bits[4] = {0, 0, 0, 0};
+                    float top;
+                    if (masked) {
+                        top = -INFINITY;
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        tmem_ld32(z, s_addr + ch * 32);
-                        tmem_wait_ld();
-                        if (masked) {
-                            const uint32_t bits = live ? seen_bits(p, u, mine, words, x0 + ch * 32) : 0u;
+                        for (int ch = 0; ch < 4; ++ch) {
+                            if (live) bits[ch] = seen_bits(p, u, mine, words, x0 + ch * 32);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                top = fmaxf(top, (bits >> e) & 1u ? __uint_as_float(z[e]) : -INFINITY);
-                        } else {
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t z[16];
+                                tmem_ld16(z, s_addr + ch * 32 + half * 16);
+                                tmem_wait_ld(z);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(z[e]));
+                                for (int e = 0; e < 16; ++e)
+                                    top = fmaxf(top, (bits[ch] >> (half * 16 + e)) & 1u ? __uint_as_float(z[e]) : -INFINITY);
+                            }
                         }
+                    } else {
+                        top = -INFINITY;
+#pragma unroll 1
+                        for (int col = 0; col < kTile; col += 32) top = fmaxf(top, tmem_max32(s_addr + col));
                     }
                     if (t == ta) {
                         ref = top;
@@ -708,10 +761,11 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                             l *= f;
                             if (!wait_pv(n - 1)) return;
                             tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int ch = 0; ch < DP / 32; ++ch) {
+                                uint32_t z[32];
                                 tmem_ld32(z, o_addr + ch * 32);
-                                tmem_wait_ld();
+                                tmem_wait_ld(z);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(__uint_as_float(z[e]) * f);
                                 tmem_st32(o_addr + ch * 32, z);
@@ -719,31 +773,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                         }
                     }
                     off = ref == -INFINITY ? 0.0f : ref * c;
-                    float2 sum = make_float2(0.0f, 0.0f);
-                    const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        tmem_ld32(z, s_addr + ch * 32);
-                        tmem_wait_ld();
-                        if (masked) {
-                            const uint32_t bits = live ? seen_bits(p, u, mine, words, x0 + ch * 32) : 0u;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                z[e] = (bits >> e) & 1u ? z[e] : __float_as_uint(-INFINITY);
-                        }
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 x = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2,
-                                            off2);
-                            x.x = exp2_fast(x.x);
-                            x.y = exp2_fast(x.y);
-                            sum = add2(sum, x);
-                            pk[e] = pack_pair<F16>(x.x, x.y);
-                        }
-                        tmem_st16(s_addr + ch * 16, pk);
-                    }
-                    l += sum.x + sum.y;
+                    l += masked ? exp_tile<F16, true>(s_addr, bits, c, off) : exp_tile<F16, false>(s_addr, bits, c, off);
                     tmem_wait_st();
                 }
                 tmem_fence_before();
@@ -758,23 +788,17 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                 tmem_fence_after();
             }
             if (!warp_live) continue;
-            const bool odd = any && *reinterpret_cast<volatile uint32_t*>(&sh.odd[group % kGroupRing]) == group + 1;
-            const Join j = join_at(M, mg);
-            float* slot = slots + static_cast<int64_t>(1 + g - u.ga) * p.slot_floats;
-#pragma unroll
-            for (int ch = 0; ch < DP / 32; ++ch) {
-                uint32_t z[32];
-                if (any) {
+            if (any && *reinterpret_cast<volatile uint32_t*>(&sh.odd[group % kGroupRing]) == group + 1) {
+                // non-finite values join the sums of the rows that see them
+                const int32_t x1 = min(tb * kTile, u.kv_end);
+                const int32_t* table = p.block_table + static_cast<int64_t>(w.known) * p.max_blocks;
+#pragma unroll 1
+                for (int ch = 0; ch < DP / 32; ++ch) {
+                    uint32_t z[32];
                     tmem_ld32(z, o_addr + ch * 32);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) z[e] = 0u;
-                }
-                if (odd && live) {  // non-finite values that this row sees
-                    const int32_t x1 = min(tb * kTile, u.kv_end);
-                    const int32_t* table = p.block_table + static_cast<int64_t>(w.known) * p.max_blocks;
-                    for (int32_t x = max(ta * kTile, cleaned); x < x1; ++x) {
+                    tmem_wait_ld(z);
+#pragma unroll 1
+                    for (int32_t x = max(ta * kTile, cleaned); live && x < x1; ++x) {
                         if (!(seen_bits(p, u, i, words, x) & 1u)) continue;
                         const int32_t blk = table[x / p.block_size];
                         if (blk < 0 || blk >= p.num_blocks) continue;
@@ -788,34 +812,42 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                             }
                         }
                     }
+                    __syncwarp();
+                    tmem_st32(o_addr + ch * 32, z);
                 }
-                if (!whole) {
-                    if (live) {
+                tmem_wait_st();
+            }
+            const Join j = join_at(M, mg);
+            float* slot = slots + static_cast<int64_t>(1 + g - u.ga) * p.slot_floats;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<uint4*>(slot)[(ch * 8 + e) * p.slot_rows + slot_row] =
-                                make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
-                    }
-                } else if (g == 0) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) acc[ch * 32 + e] = __uint_as_float(z[e]);
+            for (int ch = 0; ch < DP / 16; ++ch) {
+                uint32_t z[16];
+                if (any) {
+                    tmem_ld16(z, o_addr + ch * 16);
+                    tmem_wait_ld(z);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        acc[ch * 32 + e] = join_sum(acc[ch * 32 + e], __uint_as_float(z[e]), j);
+                    for (int e = 0; e < 16; ++e) z[e] = 0u;
+                }
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        acc[ch * 8 + e] =
+                            join_sum2(acc[ch * 8 + e],
+                                      make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
+                } else if (live) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<uint4*>(slot)[(ch * 4 + e) * p.slot_rows + slot_row] =
+                            make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
                 }
             }
-            if (!whole) {
-                if (live) {
-                    slot[DP * p.slot_rows + slot_row] = mg;
-                    slot[(DP + 1) * p.slot_rows + slot_row] = l;
-                }
-            } else if (g == 0) {
-                M = mg;
-                L = l;
-            } else {
+            if (whole) {
                 L = join_sum(L, l, j);
                 M = j.m;
+            } else if (live) {
+                slot[DP * p.slot_rows + slot_row] = mg;
+                slot[(DP + 1) * p.slot_rows + slot_row] = l;
             }
         }
         if (!whole || !live) continue;
@@ -829,8 +861,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                 if (e * 8 < D) {
                     uint32_t o[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[k] = pack_pair<F16>(acc[8 * e + 2 * k] * inv, acc[8 * e + 2 * k + 1] * inv);
+                    for (int k = 0; k < 4; ++k) o[k] = pack_pair<F16>(acc[4 * e + k].x * inv, acc[4 * e + k].y * inv);
                     *reinterpret_cast<uint4*>(dst + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
@@ -839,7 +870,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
 #pragma unroll
             for (int e = 0; e < DP / 4; ++e)
                 reinterpret_cast<float4*>(slots)[e * p.slot_rows + slot_row] =
-                    make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+                    make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
             slots[DP * p.slot_rows + slot_row] = M;
             slots[(DP + 1) * p.slot_rows + slot_row] = L;
         }
@@ -894,15 +925,15 @@ __global__ void __launch_bounds__(PAIRS == 2 ? 384 : 256, 1)
 
     if (warp < 4) {
         if (warp == 0)
-            copy_kv<DP>(p, sh, ring, &mk, &mv);
+            copy_tiles<DP>(p, sh, ring, &mk, 0);
         else if (warp == 1)
             issue_products<DP>(p, sh, smem_addr(base), smem_addr(ring), tmem);
         else if (warp == 2)
-            copy_q<DP>(p, sh, base, &mq);
+            copy_tiles<DP>(p, sh, ring, &mv, 1);
         else
-            clean_v<DP, F16>(p, sh, ring);
+            copy_q_clean_v<DP, F16>(p, sh, base, ring, &mq);
     } else {
-        softmax_rows<DP, F16>(p, sh, tmem, PAIRS == 2 ? (warp - 4) >> 2 : 0);
+        softmax_rows<DP, F16, PAIRS>(p, sh, tmem, PAIRS == 2 ? (warp - 4) >> 2 : 0);
     }
     tmem_fence_before();
     __syncthreads();
