@@ -8,31 +8,36 @@
 //
 // One persistent CTA per SM, warp roles:
 //   warps 0, 2  copy K and V tiles, block by block, with tensor maps into a ring of
-//               five stages (the block ids of the next tile are fetched before the
-//               wait for a stage);
+//               stages (the block ids of the next tile are fetched before the wait for
+//               a stage);
 //   warp 1      issues the products; S in tensor memory, P over S in tensor memory as
 //               the left operand of P V, O in tensor memory;
-//   warp 3      copies Q, and cleans V where a tile holds positions that not every row sees: rows
-//               behind the last key become 0 (P is 0 there, but 0 * NaN is not), and so
-//               do NaN and infinite entries, which are noted and added in 32 bits at
-//               the end of the group to the rows that do see them;
-//   warps 4-7   softmax and sums of the first row tile, one row per thread;
-//   warps 8-11  of the second row tile, when requests have more rows than one tile
-//               holds: both tiles use the same K and V from shared memory.
+//   warp 3      copies Q, and cleans V where a tile holds positions that not every row
+//               sees: rows behind the last key become 0 (P is 0 there, but 0 * NaN is
+//               not), and so do NaN and infinite entries, which are noted and added in
+//               32 bits at the end of the group to the rows that do see them;
+//   warps 4-7, 8-11   two streams of softmax, one row per thread; each stream has an S and
+//               an O of its own, so that while one's softmax runs the other's products do.
+//
+// Streams.  Where a request's rows fit one tile the streams split its keys: of a group's
+// tiles the even ones go to stream 0 and the odd ones to stream 1, and at the group's end
+// each warpgroup joins half of the columns of both.  Where a request has more rows the
+// streams are two row tiles that use the same K and V from shared memory.
 //
 // Order of sums.  A request's keys are cut into groups of whole tiles by a rule on
-// its own lengths (request_of).  Within a group O and the sum l belong to a
-// reference m, the row maximum of the group's first tile; a later tile's maximum
-// replaces it only when it is more than 2^8 above (O is then rescaled), which no
-// 32-bit sum notices.  Groups are joined from the first to the last, (O, l, m) with
-// (O', l', m') at max(m, m').  A CTA that has an item from its first group on joins
-// in registers; other groups go to the workspace and attn_join_kernel joins them in
-// the same order with the same instructions, so the bits do not depend on where the
-// work was cut.
+// its own lengths (request_of).  Within a group a stream's O and sum l belong to a
+// reference m, the row maximum of its first tile; a later tile's maximum replaces it
+// only when it is more than 2^8 above (O is then rescaled), which no 32-bit sum
+// notices.  (O, l, m) and (O', l', m') are joined at max(m, m'): the streams of a
+// group, then the groups from the first to the last.  A CTA that has an item from its
+// first group on joins in registers; other groups go to the workspace and
+// attn_join_kernel joins them in the same order with the same instructions, so the bits
+// do not depend on where the work was cut.
 //
-// Work.  An item is (request, key head, pair of row tiles), a unit one group of an
-// item.  All units lie on one line, in cost of tiles plus one per group, cut evenly
-// over the CTAs; every CTA finds its share itself from the lengths on the device.
+// Work.  An item is (request, key head, row tile or pair of them), a unit one group of
+// an item.  All units lie on one line, in cost of tiles plus one per group and two per
+// item, cut evenly over the CTAs; every CTA finds its share itself from the lengths on
+// the device.
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>
@@ -47,7 +52,9 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 128;       // rows of a row tile, keys of a key tile
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 12;
+constexpr int kAttnThreads = 384;
+constexpr size_t kMaxShared = 232448;  // bytes of shared memory a CTA can have
 constexpr int kGroupRing = 16;   // groups whose notes of non-finite values are kept
 constexpr float kGrow = 8.0f;    // log2 by which a tile's maximum may pass the reference
 
@@ -65,7 +72,8 @@ struct AttnParams {
     const uint32_t* mask;
     int32_t R, T, max_blocks, max_kv, max_tokens, mask_words;
     int32_t block_size, num_blocks, kv_heads, group, tile_tokens, head_dim;
-    int32_t pairs;     // row tiles an item holds: 1 or 2
+    int32_t box_tokens;  // tokens a copy of Q brings
+    int32_t q_chunk;     // bytes of 64 columns of Q
     int32_t box_rows;  // rows one copy brings: they divide a block and a tile
     int32_t stages, sms;
     float c;
@@ -85,14 +93,16 @@ struct AttnParams {
 
 struct Request {
     int32_t tok0, na, kv, ctx;  // first token, tokens that attend, keys, keys before the tokens
-    int32_t tiles, per_head;    // row tiles; items of a key head
+    int32_t tiles, per_head;    // row tiles, items of a key head
     int32_t gt, ng, cost;       // key tiles of a group, groups and cost of an item over all keys
 };
 
-// Groups: one request alone should give about two units to every SM, so the tiles of
-// an item are cut into at most 2 * SMs / (key heads * tile pairs) groups; a group
-// holds at least 2 tiles (8 where there are more rows than one tile holds: such
-// items are bound by the products, and a group's end costs a pass over O).
+// Groups.  Few and long ones cost least (a group's end is a pass over O and leaves the
+// products idle); many and short ones let a request alone fill the machine.  A group has
+// about the square root of the item's tiles, at least 2 (8 where two row tiles share
+// them: such items are bound by products and exponentials); where that is near, the
+// number that gives a request alone one or two units for every SM; and an even number,
+// so that a tile's stream is its parity.
 __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
 {
     Request q;
@@ -102,21 +112,23 @@ __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
     q.kv = min(max(p.kv_len[r], 0), p.max_kv);
     q.ctx = q.kv - (t1 - t0);
     q.tiles = (q.na + p.tile_tokens - 1) / p.tile_tokens;
-    const int32_t tile_pairs = (q.tiles + 1) / 2;
-    q.per_head = p.pairs == 2 ? tile_pairs : q.tiles;
+    q.per_head = (q.tiles + 1) / 2;
     const int32_t nt = (q.kv + kTile - 1) / kTile;
-    const int32_t most = max(1, min(p.sms, 2 * p.sms / max(1, p.kv_heads * tile_pairs)));
-    q.gt = max(q.tiles > 1 ? 8 : 2, (nt + most - 1) / most);
+    const int32_t wave = max(1, p.sms / max(1, p.kv_heads * q.per_head));
+    const int32_t root = static_cast<int32_t>(ceilf(sqrtf(static_cast<float>(nt))));
+    const int32_t one = (nt + wave - 1) / wave, two = (nt + 2 * wave - 1) / (2 * wave);
+    const int32_t even = 5 * two >= 4 * root ? two : 5 * one >= 4 * root ? one : root;
+    q.gt = (max(q.tiles > 1 ? 8 : 2, even) + 1) & ~1;
     q.ng = max(1, (nt + q.gt - 1) / q.gt);
-    q.cost = nt + q.ng;
+    q.cost = nt + q.ng + 2;
     return q;
 }
 
 // An item's groups that lie in a CTA's share.
 struct Run {
     int32_t tok0, na, ctx, kv_end;  // keys [0, kv_end) are looked at
-    int32_t head, tile0;            // key head, first row tile
-    bool second;                    // a second row tile
+    int32_t head, tile;             // key head, (first) row tile
+    bool split, second;             // the streams split the keys; a second row tile
     int32_t gt, ga, gb, ng;         // tiles of a group, groups [ga, gb) of ng
     int32_t nt;                     // key tiles of the item
 };
@@ -127,10 +139,10 @@ struct Walk {
     Request q;
 };
 
-__device__ __forceinline__ int32_t item_tiles(const AttnParams& p, const Request& q, int32_t tile0, int32_t* kv_end)
+__device__ __forceinline__ int32_t item_tiles(const AttnParams& p, const Request& q, int32_t tile, int32_t* kv_end)
 {
     int32_t e = q.kv;
-    if (p.mask == nullptr) e = min(e, q.ctx + min(q.na, (tile0 + p.pairs) * p.tile_tokens));
+    if (p.mask == nullptr) e = min(e, q.ctx + min(q.na, (tile + 2) * p.tile_tokens));
     *kv_end = max(e, 0);
     return (*kv_end + kTile - 1) / kTile;
 }
@@ -148,8 +160,8 @@ __device__ __forceinline__ bool next_run(const AttnParams& p, Walk& w, Run& out)
             continue;
         }
         out.head = w.at.item / q.per_head;
-        out.tile0 = (w.at.item - out.head * q.per_head) * p.pairs;
-        out.nt = item_tiles(p, q, out.tile0, &out.kv_end);
+        out.tile = 2 * (w.at.item - out.head * q.per_head);
+        out.nt = item_tiles(p, q, out.tile, &out.kv_end);
         out.ng = max(1, (out.nt + q.gt - 1) / q.gt);
         out.ga = w.at.g;
         out.gb = w.end.r == w.at.r && w.end.item == w.at.item ? min(out.ng, w.end.g) : out.ng;
@@ -160,7 +172,8 @@ __device__ __forceinline__ bool next_run(const AttnParams& p, Walk& w, Run& out)
         out.na = q.na;
         out.ctx = q.ctx;
         out.gt = q.gt;
-        out.second = p.pairs == 2 && out.tile0 + 1 < q.tiles;
+        out.split = q.tiles == 1;
+        out.second = out.tile + 1 < q.tiles;
         return true;
     }
     return false;
@@ -196,10 +209,14 @@ struct Ring {
 
 struct Shared {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t q_full[2], q_empty[2];              // by buffer
+    uint64_t s_full[2], p_full[2], pv_done[2];   // by stream, a phase per tile
+    uint64_t g_done, o_free;                     // a phase per group whose keys are split
+    uint64_t drain;
     uint64_t v_ok[kMaxStages];  // the stage's V has been cleaned
     int64_t scan[16];
     Start start, end;
+    float ref[2][kTile], sum[2][kTile];  // of a stream's group, by row
     uint32_t tmem;
     uint32_t odd[kGroupRing];  // 1 + number of the group whose V had non-finite entries
     int stop;
@@ -361,10 +378,10 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
         };
         int32_t id = block_of(t);
         for (; t < t1; ++t) {
-            const int32_t block = id;
+            const int32_t block = id, x0 = t * kTile;
             if (t + 1 < t1) id = block_of(t + 1);  // in flight while this tile is issued
-            const int32_t place = (t * kTile + lane * p.box_rows) % p.block_size;
-            const int32_t live = min(subs, (u.kv_end - t * kTile + p.box_rows - 1) / p.box_rows);
+            const int32_t place = (x0 + lane * p.box_rows) % p.block_size;
+            const int32_t live = min(subs, (u.kv_end - x0 + p.box_rows - 1) / p.box_rows);
             uint64_t* full = &sh.kv_full[rt.stage];
             // the stage's fill before this one is the ring's last turn: `first + 2 * fills` stages in
             if (first + 2 * fills >= p.stages && !warp_wait(&sh.kv_empty[rt.stage], rt.phase ^ 1u, sh)) {
@@ -382,13 +399,13 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
                 }
             }
             __syncwarp();
-            ++fills;
+            fills = min(fills + 1, 1 << 20);
             rt.next2(p.stages);
         }
     }
     // a CTA that gave up does not leave before its copies have landed
     if (!ok || sh.stop != 0) {
-        for (int32_t i = min(fills, p.stages); i > 0; --i) {
+        for (int32_t i = min(fills, (p.stages + 1) / 2); i > 0; --i) {
             rt.prev2(p.stages);
             mbar_wait_bounded(&sh.kv_full[rt.stage], rt.phase);
         }
@@ -396,210 +413,192 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
 }
 
 // ---- warp 3: Q, and V that not every row sees ---------------------------------------
-// Q of a run is copied when the run's first tile is waited for.  The warp follows every stage, also those it has nothing to do with, and each stage waits for
-// its arrival before it is filled again: the parity of a barrier tells two fills of a
-// stage apart only for a warp that is never a whole turn of the ring ahead or behind.
-template <int DP, bool F16>
+// The warp follows every stage, also those it has nothing to do with, and each stage
+// waits for its arrival before it is filled again: the parity of a barrier tells two
+// fills of a stage apart only for a warp that is never a whole turn of the ring ahead
+// or behind.
+template <int DP, bool F16, bool MULTI>
 __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q_smem, unsigned char* ring,
                                const CUtensorMap* mq)
 {
     constexpr int kChunks = DP / 64;
-    constexpr uint32_t kStage = kTile * DP * 2, kQ = kTile * DP * 2;
+    constexpr uint32_t kStage = kTile * DP * 2;
     constexpr uint32_t kExp = F16 ? 0x7C007C00u : 0x7F807F80u;
     const int lane = threadIdx.x & 31;
     Walk w{sh.start, sh.end, -1, {}};
     Run u;
     Ring rk{0, 0}, rv{1, 0};
-    uint32_t group = 0, used[2] = {0, 0};
-    int32_t runs = 0;
-    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens * 128 * kChunks);
-    auto follow = [&]() {
-        const int32_t all = seen_by_all(p, u, u.tile0);
-        for (int32_t g = u.ga; g < u.gb; ++g, ++group) {
-            const int32_t t1 = min((g + 1) * u.gt, u.nt);
-            for (int32_t t = g * u.gt; t < t1; ++t, rk.next2(p.stages), rv.next2(p.stages)) {
-                const int32_t x0 = t * kTile;
-                if (!warp_wait(&sh.kv_full[rk.stage], rk.phase, sh)) return false;
-                if (lane == 0) mbar_arrive(&sh.kv_empty[rk.stage]);
-                if (!warp_wait(&sh.kv_full[rv.stage], rv.phase, sh)) return false;
-                if (x0 + kTile > all) {
-                    unsigned char* base = ring + static_cast<size_t>(rv.stage) * kStage;
-                    const int32_t first = max(0, all - x0), end = min(kTile, u.kv_end - x0);
-                    bool odd = false;
-                    for (int32_t v = first * 8 + lane; v < kTile * 8; v += 32) {
+    uint32_t groups = 0, runs = 0, used[2] = {0, 0};
+    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.box_tokens * 128 * kChunks);
+    bool ok = true;
+    for (; ok && next_run(p, w, u); groups += u.gb - u.ga) {
+        const int32_t t1 = min(u.gb * u.gt, u.nt);
+        if (u.ga * u.gt >= t1) continue;
+        for (int i = 0; ok && i < (u.second ? 2 : 1); ++i) {
+            const int b = MULTI ? i : runs & 1;
+            if (used[b] > 0) ok = warp_wait(&sh.q_empty[b], (used[b] - 1) & 1u, sh);
+            if (!ok) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sh.q_full[b], q_bytes);
 #pragma unroll
-                        for (int ch = 0; ch < kChunks; ++ch) {
-                            uint4* at = reinterpret_cast<uint4*>(base + ch * kTile * 128) + v;
-                            if ((v >> 3) >= end) {
-                                *at = make_uint4(0, 0, 0, 0);
-                            } else {
-                                const uint4 x = *at;
-                                const uint32_t bx = __vcmpeq2(x.x & kExp, kExp), by = __vcmpeq2(x.y & kExp, kExp),
-                                               bz = __vcmpeq2(x.z & kExp, kExp), bw = __vcmpeq2(x.w & kExp, kExp);
-                                if ((bx | by | bz | bw) != 0) {
-                                    odd = true;
-                                    *at = make_uint4(x.x & ~bx, x.y & ~by, x.z & ~bz, x.w & ~bw);
-                                }
+                for (int ch = 0; ch < kChunks; ++ch)
+                    tma_load_3d(q_smem + (b * kChunks + ch) * p.q_chunk, mq, &sh.q_full[b], ch * 64, u.head * p.group,
+                                u.tok0 + (u.tile + i) * p.tile_tokens);
+            }
+            __syncwarp();
+            ++used[b];
+        }
+        ++runs;
+        const int32_t all = seen_by_all(p, u, u.tile);
+        for (int32_t t = u.ga * u.gt; ok && t < t1; ++t) {
+            const int32_t x0 = t * kTile;
+            ok = warp_wait(&sh.kv_full[rk.stage], rk.phase, sh);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&sh.kv_empty[rk.stage]);
+            ok = warp_wait(&sh.kv_full[rv.stage], rv.phase, sh);
+            if (!ok) break;
+            if (x0 + kTile > all) {
+                unsigned char* base = ring + static_cast<size_t>(rv.stage) * kStage;
+                const int32_t first = max(0, all - x0), end = min(kTile, u.kv_end - x0);
+                bool odd = false;
+                for (int32_t v = first * 8 + lane; v < kTile * 8; v += 32) {
+#pragma unroll
+                    for (int ch = 0; ch < kChunks; ++ch) {
+                        uint4* at = reinterpret_cast<uint4*>(base + ch * kTile * 128) + v;
+                        if ((v >> 3) >= end) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else {
+                            const uint4 x = *at;
+                            const uint32_t bx = __vcmpeq2(x.x & kExp, kExp), by = __vcmpeq2(x.y & kExp, kExp),
+                                           bz = __vcmpeq2(x.z & kExp, kExp), bw = __vcmpeq2(x.w & kExp, kExp);
+                            if ((bx | by | bz | bw) != 0) {
+                                odd = true;
+                                *at = make_uint4(x.x & ~bx, x.y & ~by, x.z & ~bz, x.w & ~bw);
                             }
                         }
                     }
-                    if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) sh.odd[group % kGroupRing] = group + 1;
-                    fence_async_proxy();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.v_ok[rv.stage]);
                 }
-                if (lane == 0) mbar_arrive(&sh.kv_empty[rv.stage]);
-            }
-        }
-        return true;
-    };
-    bool ok = true;
-    while (ok && next_run(p, w, u)) {
-        if (min(u.gb * u.gt, u.nt) > u.ga * u.gt) {
-            const int tiles = u.second ? 2 : 1;
-            for (int s = 0; ok && s < tiles; ++s) {
-                const int b = p.pairs == 2 ? s : runs & 1;
-                if (used[b] > 0) ok = warp_wait(&sh.q_empty[b], (used[b] - 1) & 1u, sh);
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sh.q_full[b], q_bytes);
-#pragma unroll
-                    for (int ch = 0; ch < kChunks; ++ch)
-                        tma_load_3d(q_smem + b * kQ + ch * kTile * 128, mq, &sh.q_full[b], ch * 64, u.head * p.group,
-                                    u.tok0 + (u.tile0 + s) * p.tile_tokens);
-                }
+                const uint32_t group = groups + (t / u.gt - u.ga);
+                if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) sh.odd[group % kGroupRing] = group + 1;
+                fence_async_proxy();
                 __syncwarp();
-                ++used[b];
+                if (lane == 0) mbar_arrive(&sh.v_ok[rv.stage]);
             }
-            ++runs;
+            if (lane == 0) mbar_arrive(&sh.kv_empty[rv.stage]);
+            rk.next2(p.stages);
+            rv.next2(p.stages);
         }
-        ok = ok && follow();
     }
-    if (!ok || sh.stop != 0)
+    if (!ok || sh.stop != 0)  // the copies of Q that were issued
         for (int b = 0; b < 2; ++b)
             if (used[b] > 0) mbar_wait_bounded(&sh.q_full[b], (used[b] - 1) & 1u);
 }
 
 // ---- warp 1: products -------------------------------------------------------------------
-template <int DP>
+template <int DP, bool MULTI>
 __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr, uint32_t ring_addr, uint32_t tmem)
 {
-    constexpr uint32_t kStage = kTile * DP * 2, kQ = kTile * DP * 2, kChunk = kTile * 128;
+    constexpr uint32_t kStage = kTile * DP * 2, kChunk = kTile * 128;
     Walk w{sh.start, sh.end, -1, {}};
     Run u;
-    Ring rk{0, 0}, rv{1, 0};  // next key tile to multiply with Q, next value tile
-    uint32_t tiles[2] = {0, 0};  // per row tile: PV products issued
-    uint32_t q_used[2] = {0, 0};
-    uint32_t cleaned = 0;  // a bit per stage: parity of its cleanings
-    int32_t runs = 0;
+    Ring rk{0, 0}, rv{1, 0};     // next key tile to multiply with Q, next value tile
+    uint32_t tiles[2] = {0, 0};  // by stream
+    uint32_t used[2] = {0, 0};   // runs by buffer of Q
+    uint32_t groups = 0;         // groups whose keys are split
+    uint32_t cleaned = 0;        // a bit per stage: parity of its cleanings
+    uint32_t runs = 0;
 
-    // S[b] = Q[q] K[stage]
-    auto qk = [&](int b, int q, int32_t stage) {
-        if (elect_one()) {
-            const uint64_t qa = smem_operand(q_addr + q * kQ, 16, 1024);
-            const uint64_t kb = smem_operand(ring_addr + stage * kStage, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                const uint32_t off = ((k / 4) * kChunk + (k % 4) * 32) >> 4;
-                product_ss(tmem + b * kTile, qa + off, kb + off, p.word_qk, k > 0);
-            }
-            product_commit(&sh.s_full[b]);
-        }
+    auto wait_k = [&]() {
+        if (!warp_wait(&sh.kv_full[rk.stage], rk.phase, sh)) return false;
+        tmem_fence_after();
+        return true;
     };
-    // O[o] (+)= P[b] V[stage]
-    auto pv = [&](int b, int o, int32_t stage, bool add) {
+    auto wait_v = [&](bool clean) {
+        if (!clean) return warp_wait(&sh.kv_full[rv.stage], rv.phase, sh);
+        if (!warp_wait(&sh.v_ok[rv.stage], (cleaned >> rv.stage) & 1u, sh)) return false;
+        cleaned ^= 1u << rv.stage;
+        return true;
+    };
+    // S of stream s = Q[b] K; `free_k`: the tile's last use, `free_q`: the run's
+    auto qk = [&](int s, int b, bool free_k, bool free_q) {
         if (elect_one()) {
-            const uint64_t vb = smem_operand(ring_addr + stage * kStage, kChunk, 1024);
+            const uint64_t qa = smem_operand(q_addr + b * (DP / 64) * p.q_chunk, 16, 1024);
+            const uint64_t kb = smem_operand(ring_addr + rk.stage * kStage, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                product_ss(tmem + s * kTile, qa + (((k / 4) * p.q_chunk + (k % 4) * 32) >> 4),
+                           kb + (((k / 4) * kChunk + (k % 4) * 32) >> 4), p.word_qk, k > 0);
+            product_commit(&sh.s_full[s]);
+            if (free_k) product_commit(&sh.kv_empty[rk.stage]);
+            if (free_q) product_commit(&sh.q_empty[b]);
+        }
+        if (free_k) rk.next2(p.stages);
+    };
+    // O of stream s (+)= P V
+    auto pv = [&](int s, bool first, bool free_v) {
+        if (!warp_wait(&sh.p_full[s], tiles[s] & 1u, sh)) return false;
+        tmem_fence_after();
+        if (elect_one()) {
+            const uint64_t vb = smem_operand(ring_addr + rv.stage * kStage, kChunk, 1024);
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-                product_ts(tmem + 2 * kTile + o * kTile, tmem + b * kTile + k * 8, vb + ((k * 2048) >> 4), p.word_pv,
-                           add || k > 0);
-            product_commit(&sh.pv_done[b]);
+                product_ts(tmem + (2 + s) * kTile, tmem + s * kTile + k * 8, vb + ((k * 2048) >> 4), p.word_pv,
+                           !first || k > 0);
+            product_commit(&sh.pv_done[s]);
+            if (free_v) product_commit(&sh.kv_empty[rv.stage]);
         }
-    };
-    auto release = [&](uint64_t* bar) {
-        if (elect_one()) product_commit(bar);
+        ++tiles[s];
+        if (free_v) rv.next2(p.stages);
+        return true;
     };
 
     bool ok = true;
     while (ok && next_run(p, w, u)) {
-        const int32_t t0 = u.ga * u.gt, t1 = min(u.gb * u.gt, u.nt);
-        if (t0 >= t1) continue;
-        const int32_t all = seen_by_all(p, u, u.tile0);
-        const int rows = u.second ? 2 : 1;
-        const int qb = p.pairs == 2 ? 0 : runs & 1;
-        for (int s = 0; s < rows; ++s) {
-            ok = ok && warp_wait(&sh.q_full[qb + s], q_used[qb + s] & 1u, sh);
-            ++q_used[qb + s];
-        }
-        if (!ok) break;
-        tmem_fence_after();
-        int32_t in_group = 0;  // tiles of the group so far
-        auto wait_v = [&](int32_t t) {
-            if (t * kTile + kTile <= all) return warp_wait(&sh.kv_full[rv.stage], rv.phase, sh);
-            const bool got = warp_wait(&sh.v_ok[rv.stage], (cleaned >> rv.stage) & 1u, sh);
-            cleaned ^= 1u << rv.stage;
-            return got;
-        };
-        if (p.pairs == 1) {
-            // one row tile: S alternates between two buffers, Q K^T of the next tile goes ahead of P V
-            auto next_qk = [&](int32_t t, uint32_t n) {
-                if (!warp_wait(&sh.kv_full[rk.stage], rk.phase, sh)) return false;
-                tmem_fence_after();
-                qk(n & 1u, qb, rk.stage);
-                release(&sh.kv_empty[rk.stage]);
-                if (t + 1 == t1) release(&sh.q_empty[qb]);
-                rk.next2(p.stages);
-                return true;
-            };
-            ok = next_qk(t0, tiles[0]);
-            for (int32_t t = t0; ok && t < t1; ++t) {
-                const uint32_t n = tiles[0];
-                if (t + 1 < t1) ok = next_qk(t + 1, n + 1);
-                ok = ok && wait_v(t) && warp_wait(&sh.p_full[n & 1u], (n >> 1) & 1u, sh);
+        const int32_t ta = u.ga * u.gt, tb = min(u.gb * u.gt, u.nt);
+        if (ta >= tb) continue;
+        const int32_t all = seen_by_all(p, u, u.tile);
+        if (!MULTI || u.split) {
+            const int b = MULTI ? 0 : runs & 1;
+            ok = warp_wait(&sh.q_full[b], used[b] & 1u, sh);
+            ++used[b];
+            ok = ok && wait_k();
+            if (!ok) break;
+            qk(0, b, true, ta + 1 == tb);
+            if (ta + 1 < tb) {
+                ok = wait_k();
                 if (!ok) break;
-                tmem_fence_after();
-                pv(n & 1u, 0, rv.stage, in_group > 0);
-                release(&sh.kv_empty[rv.stage]);
-                rv.next2(p.stages);
-                ++tiles[0];
+                qk(1, b, true, ta + 2 == tb);
+            }
+            int32_t in_group = 0;
+            for (int32_t t = ta; ok && t < tb; ++t) {
+                const int s = t & 1;
+                // the group's first products write O: what lay there has been read
+                if (in_group == 0 && groups++ > 0) ok = warp_wait(&sh.o_free, groups & 1u, sh);
+                ok = ok && wait_v((t + 1) * kTile > all) && pv(s, in_group < 2, true);
+                if (ok && t + 2 < tb) {
+                    ok = wait_k();
+                    if (ok) qk(s, b, true, t + 3 == tb);
+                }
                 if (++in_group == u.gt) in_group = 0;
             }
         } else {
-            // two row tiles take turns: while one's softmax runs, the other's products do
-            ok = warp_wait(&sh.kv_full[rk.stage], rk.phase, sh);
-            if (!ok) break;
-            tmem_fence_after();
+            const int rows = u.second ? 2 : 1;
             for (int s = 0; s < rows; ++s) {
-                qk(s, s, rk.stage);
-                if (t0 + 1 == t1) release(&sh.q_empty[s]);
+                ok = ok && warp_wait(&sh.q_full[s], used[s] & 1u, sh);
+                ++used[s];
             }
-            release(&sh.kv_empty[rk.stage]);
-            rk.next2(p.stages);
-            for (int32_t t = t0; ok && t < t1; ++t) {
-                for (int s = 0; s < rows; ++s) {
-                    ok = ok && warp_wait(&sh.p_full[s], tiles[s] & 1u, sh);
-                    if (s == 0) ok = ok && wait_v(t);
-                    if (!ok) break;
-                    tmem_fence_after();
-                    pv(s, s, rv.stage, in_group > 0);
-                    ++tiles[s];
-                    if (t + 1 < t1) {
-                        if (s == 0) {
-                            ok = warp_wait(&sh.kv_full[rk.stage], rk.phase, sh);
-                            if (!ok) break;
-                            tmem_fence_after();
-                        }
-                        qk(s, s, rk.stage);
-                        if (t + 2 == t1) release(&sh.q_empty[s]);
+            ok = ok && wait_k();
+            if (!ok) break;
+            for (int s = 0; s < rows; ++s) qk(s, s, s + 1 == rows, ta + 1 == tb);
+            int32_t in_group = 0;
+            for (int32_t t = ta; ok && t < tb; ++t) {
+                for (int s = 0; ok && s < rows; ++s) {
+                    if (s == 0) ok = wait_v((t + 1) * kTile > all);
+                    ok = ok && pv(s, in_group == 0, s + 1 == rows);
+                    if (ok && t + 1 < tb) {
+                        if (s == 0) ok = wait_k();
+                        if (ok) qk(s, s, s + 1 == rows, t + 2 == tb);
                     }
-                }
-                if (!ok) break;
-                release(&sh.kv_empty[rv.stage]);
-                rv.next2(p.stages);
-                if (t + 1 < t1) {
-                    release(&sh.kv_empty[rk.stage]);
-                    rk.next2(p.stages);
                 }
                 if (++in_group == u.gt) in_group = 0;
             }
@@ -607,7 +606,7 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
         ++runs;
     }
     if (!ok || sh.stop != 0) {  // the products that were issued end before tensor memory is given back
-        release(&sh.drain);
+        if (elect_one()) product_commit(&sh.drain);
         mbar_wait_bounded(&sh.drain, 0);
     }
 }
@@ -631,223 +630,279 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const Run& u,
     return bits & below(u.kv_end - x);
 }
 
-// 16 probabilities of a row: 2^(c z - m), hidden ones 0; packed over the scores
-template <bool F16, bool MASKED>
-__device__ __forceinline__ void exp_chunk(const uint32_t (&z)[16], uint32_t bits, float2 c2, float2 off2, float2& s0,
-                                          float2& s1, uint32_t addr)
-{
-    uint32_t pk[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float2 x = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, off2);
-        x.x = exp2_fast(x.x);
-        x.y = exp2_fast(x.y);
-        if (MASKED) {
-            x.x = (bits >> (2 * e)) & 1u ? x.x : 0.0f;
-            x.y = (bits >> (2 * e + 1)) & 1u ? x.y : 0.0f;
-        }
-        if (e & 1)
-            s1 = add2(s1, x);
-        else
-            s0 = add2(s0, x);
-        pk[e] = pack_pair<F16>(x.x, x.y);
-    }
-    tmem_st8(addr, pk);
-}
-
-// A row's probabilities of a whole tile, and their sum.  The loads of 16 scores run
-// while the 16 before them are worked on; P lies over scores that have been read.
+// A row's probabilities of a whole tile, P = 2^(c z - m) with hidden ones 0, and their
+// sum.  Sixteen at a time, in three stages that run beside each other: loads of the
+// sixteen after, exponentials of these, rounding, sum and store of those before, so
+// that the special-function unit (a warp's exponential takes it 8 cycles, 1024 for
+// a tile) never waits for a load or a store.  P lies over scores that have been read.
 template <bool F16, bool MASKED>
 __device__ __forceinline__ float exp_tile(uint32_t s_addr, const uint32_t (&bits)[4], float c, float off)
 {
     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
     float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
     uint32_t za[16], zb[16];
+    float2 xa[8], xb[8];
+    auto take = [&](const uint32_t(&z)[16], float2(&x)[8], int ch) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, off2);
+            x[e].x = exp2_fast(x[e].x);
+            x[e].y = exp2_fast(x[e].y);
+            if (MASKED) {
+                const uint32_t b = bits[ch / 2] >> (16 * (ch & 1) + 2 * e);
+                x[e].x = b & 1u ? x[e].x : 0.0f;
+                x[e].y = b & 2u ? x[e].y : 0.0f;
+            }
+        }
+    };
+    auto put = [&](const float2(&x)[8], int ch) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e & 1)
+                s1 = add2(s1, x[e]);
+            else
+                s0 = add2(s0, x[e]);
+            pk[e] = pack_pair<F16>(x[e].x, x[e].y);
+        }
+        tmem_st8(s_addr + ch * 8, pk);
+    };
     tmem_ld16(za, s_addr);
+    tmem_wait_ld(za);
+    tmem_ld16(zb, s_addr + 16);
 #pragma unroll
     for (int ch = 0; ch < 8; ch += 2) {
-        tmem_wait_ld(za);
-        tmem_ld16(zb, s_addr + (ch + 1) * 16);
-        exp_chunk<F16, MASKED>(za, bits[ch / 2], c2, off2, s0, s1, s_addr + ch * 8);
+        take(za, xa, ch);
+        if (ch > 0) put(xb, ch - 1);
         tmem_wait_ld(zb);
         if (ch + 2 < 8) tmem_ld16(za, s_addr + (ch + 2) * 16);
-        exp_chunk<F16, MASKED>(zb, bits[ch / 2] >> 16, c2, off2, s0, s1, s_addr + (ch + 1) * 8);
+        take(zb, xb, ch + 1);
+        put(xa, ch);
+        if (ch + 2 < 8) {
+            tmem_wait_ld(za);
+            tmem_ld16(zb, s_addr + (ch + 3) * 16);
+        }
     }
+    put(xb, 7);
     s0 = add2(s0, s1);
     return s0.x + s0.y;
 }
 
-template <int DP, bool F16, int PAIRS>
+// One stream's state of a row within a group.
+struct RowState {
+    float ref, off, l;  // reference (as it comes from the product, and scaled) and sum
+};
+
+// The softmax of one tile of a stream: scores out, probabilities in their place.
+// Returns false when a wait gave up.
+template <int DP, bool F16>
+__device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, const Run& u, int s, uint32_t s_addr,
+                                             uint32_t o_addr, int32_t t, bool first, uint32_t n, int32_t all, bool live,
+                                             int32_t mine, const uint32_t* words, RowState& st)
+{
+    const float c = p.c;
+    const int32_t x0 = t * kTile;
+    const bool masked = x0 + kTile > all;
+    uint32_t bits[4] = {0, 0, 0, 0};
+    float top = -INFINITY;
+    if (masked) {
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+            if (live) bits[ch] = seen_bits(p, u, mine, words, x0 + ch * 32);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t z[16];
+                tmem_ld16(z, s_addr + ch * 32 + half * 16);
+                tmem_wait_ld(z);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    top = fmaxf(top, (bits[ch] >> (half * 16 + e)) & 1u ? __uint_as_float(z[e]) : -INFINITY);
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int col = 0; col < kTile; col += 32) top = fmaxf(top, tmem_max32(s_addr + col));
+    }
+    if (first) {
+        st.ref = top;
+    } else {
+        const bool grow = live && top > st.ref && (st.ref == -INFINITY || (top - st.ref) * c > kGrow);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+            float f = 1.0f;
+            if (grow) {
+                f = st.ref == -INFINITY ? 0.0f : exp2_fast((st.ref - top) * c);
+                st.ref = top;
+            }
+            st.l *= f;
+            // this tile's scores follow the product of the tile before last, so the barrier is not a
+            // phase behind the one that is waited for
+            if (!warp_wait(&sh.pv_done[s], (n - 1) & 1u, sh)) return false;
+            tmem_fence_after();
+#pragma unroll 1
+            for (int ch = 0; ch < DP / 16; ++ch) {
+                uint32_t z[16];
+                tmem_ld16(z, o_addr + ch * 16);
+                tmem_wait_ld(z);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(__uint_as_float(z[e]) * f);
+                tmem_st16(o_addr + ch * 16, z);
+            }
+        }
+    }
+    st.off = st.ref == -INFINITY ? 0.0f : st.ref * c;
+    st.l += masked ? exp_tile<F16, true>(s_addr, bits, c, st.off) : exp_tile<F16, false>(s_addr, bits, c, st.off);
+    tmem_wait_st();
+    return true;
+}
+
+// Non-finite values that were taken out of V join the sums of the rows that see them:
+// positions [x0, x1) of the run, of which those whose tile belongs to the stream.
+template <int DP, bool F16>
+__device__ __noinline__ void add_odd(const AttnParams& p, const Run& u, int32_t r, uint32_t o_addr, int32_t x0, int32_t x1,
+                                     int32_t ta, int s, bool live, int32_t i, const uint32_t* words)
+{
+    const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.max_blocks;
+#pragma unroll 1
+    for (int ch = 0; ch < DP / 16; ++ch) {
+        uint32_t z[16];
+        tmem_ld16(z, o_addr + ch * 16);
+        tmem_wait_ld(z);
+#pragma unroll 1
+        for (int32_t x = x0; live && x < x1; ++x) {
+            if (u.split && ((x / kTile - ta) & 1) != s) continue;
+            if (!(seen_bits(p, u, i, words, x) & 1u)) continue;
+            const int32_t blk = table[x / p.block_size];
+            if (blk < 0 || blk >= p.num_blocks) continue;
+            const uint16_t* v = p.v + blk * p.block_stride + (x % p.block_size) * p.token_stride + u.head * p.head_stride +
+                                ch * 16;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                if (ch * 16 + e < p.head_dim) {
+                    const float y = widen<F16>(v[e]);
+                    if (!isfinite(y)) z[e] = __float_as_uint(__uint_as_float(z[e]) + y);
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st16(o_addr + ch * 16, z);
+    }
+    tmem_wait_st();
+}
+
+template <int DP, bool F16, bool MULTI>
 __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int s)
 {
+    constexpr int kHalf = DP / 2;               // columns of O that a warpgroup joins when the keys are split
+    constexpr int kCols = MULTI ? DP : kHalf;   // and at most
     const int row = threadIdx.x & (kTile - 1);
     const uint32_t lane_base = static_cast<uint32_t>(row & ~31) << 16;
-    const int D = p.head_dim;
-    const float c = p.c;
     const int token = row / p.group, head = row - token * p.group;
     Walk w{sh.start, sh.end, -1, {}};
     Run u;
-    uint32_t n = 0, group = 0;  // key tiles and groups so far
-    float2 acc[DP / 2];
-    // The product of tile x is waited for on the barrier of its S buffer: the buffer's next tile
-    // is not there before that product is complete, so the barrier is never a phase behind.
-    auto wait_pv = [&](uint32_t x) {
-        return PAIRS == 2 ? warp_wait(&sh.pv_done[s], x & 1u, sh) : warp_wait(&sh.pv_done[x & 1u], (x >> 1) & 1u, sh);
-    };
-    const uint32_t o_addr = tmem + lane_base + 2 * kTile + s * kTile;
+    uint32_t n = 0, base = 0, joined = 0;  // tiles of this stream, groups, groups whose keys are split
+    const uint32_t s_addr = tmem + lane_base + s * kTile, o_addr = tmem + lane_base + (2 + s) * kTile;
 
-    while (next_run(p, w, u)) {
-        if (s == 1 && !u.second) {
-            group += u.gb - u.ga;
-            continue;
-        }
-        const int32_t i = (u.tile0 + s) * p.tile_tokens + token;
+    for (; next_run(p, w, u); base += u.gb - u.ga) {
+        const bool split = !MULTI || u.split;
+        if (!split && s == 1 && !u.second) continue;
+        const int32_t tile = u.tile + (split ? 0 : s);
+        const int32_t i = tile * p.tile_tokens + token;
         const bool live = row < p.tile_tokens * p.group && i < u.na;
         const bool warp_live = __any_sync(0xFFFFFFFFu, live);
         const int32_t mine = live ? i : 0;
         const uint32_t* words = p.mask == nullptr ? nullptr : p.mask + static_cast<int64_t>(u.tok0 + mine) * p.mask_words;
-        const int32_t all = seen_by_all(p, u, u.tile0 + s), cleaned = seen_by_all(p, u, u.tile0);
+        const int32_t all = seen_by_all(p, u, tile), cleaned = seen_by_all(p, u, u.tile);
         const bool whole = u.ga == 0;  // from the first group on: joined here
-        float M = -INFINITY, L = 0.0f;
-#pragma unroll
-        for (int e = 0; e < DP / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
-        const int32_t slot_row = s * kTile + row;
+        const int slot_row = split ? row : s * kTile + row;
+        const int col0 = split ? s * kHalf : 0;
         float* const slots = p.slots + static_cast<int64_t>(blockIdx.x) * p.slots_per_cta * p.slot_floats;
+        float M = -INFINITY, L = 0.0f;
+        float2 acc[kCols / 2];
+#pragma unroll
+        for (int e = 0; e < kCols / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
 
-        for (int32_t g = u.ga; g < u.gb; ++g, ++group) {
+        for (int32_t g = u.ga; u.nt > 0 && g < u.gb; ++g) {
             const int32_t ta = g * u.gt, tb = min(ta + u.gt, u.nt);
-            float ref = -INFINITY, off = 0.0f, l = 0.0f;
-            for (int32_t t = ta; t < tb; ++t, ++n) {
-                const int b = PAIRS == 2 ? s : static_cast<int>(n & 1u);
-                const uint32_t turn = PAIRS == 2 ? n & 1u : (n >> 1) & 1u;
-                if (!warp_wait(&sh.s_full[b], turn, sh)) return;
+            const int32_t step = split ? 2 : 1, mine0 = ta + (split ? s : 0);
+            RowState st{-INFINITY, 0.0f, 0.0f};
+            for (int32_t t = mine0; t < tb; t += step, ++n) {
+                if (!warp_wait(&sh.s_full[s], n & 1u, sh)) return;
                 tmem_fence_after();
-                if (warp_live) {
-                    const uint32_t s_addr = tmem + lane_base + b * kTile;
-                    const int32_t x0 = t * kTile;
-                    const bool masked = x0 + kTile > all;
-                    uint32_t bits[4] = {0, 0, 0, 0};
-                    float top;
-                    if (masked) {
-                        top = -INFINITY;
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) {
-                            if (live) bits[ch] = seen_bits(p, u, mine, words, x0 + ch * 32);
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                uint32_t z[16];
-                                tmem_ld16(z, s_addr + ch * 32 + half * 16);
-                                tmem_wait_ld(z);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    top = fmaxf(top, (bits[ch] >> (half * 16 + e)) & 1u ? __uint_as_float(z[e]) : -INFINITY);
-                            }
-                        }
-                    } else {
-                        top = -INFINITY;
-#pragma unroll 1
-                        for (int col = 0; col < kTile; col += 32) top = fmaxf(top, tmem_max32(s_addr + col));
-                    }
-                    if (t == ta) {
-                        ref = top;
-                    } else {
-                        const bool grow = live && top > ref && (ref == -INFINITY || (top - ref) * c > kGrow);
-                        if (__any_sync(0xFFFFFFFFu, grow)) {
-                            float f = 1.0f;
-                            if (grow) {
-                                f = ref == -INFINITY ? 0.0f : exp2_fast((ref - top) * c);
-                                ref = top;
-                            }
-                            l *= f;
-                            if (!wait_pv(n - 1)) return;
-                            tmem_fence_after();
-#pragma unroll 1
-                            for (int ch = 0; ch < DP / 32; ++ch) {
-                                uint32_t z[32];
-                                tmem_ld32(z, o_addr + ch * 32);
-                                tmem_wait_ld(z);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(__uint_as_float(z[e]) * f);
-                                tmem_st32(o_addr + ch * 32, z);
-                            }
-                        }
-                    }
-                    off = ref == -INFINITY ? 0.0f : ref * c;
-                    l += masked ? exp_tile<F16, true>(s_addr, bits, c, off) : exp_tile<F16, false>(s_addr, bits, c, off);
-                    tmem_wait_st();
-                }
+                if (warp_live && !softmax_tile<DP, F16>(p, sh, u, s, s_addr, o_addr, t, t == mine0, n, all, live, mine,
+                                                        words, st))
+                    return;
                 tmem_fence_before();
-                mbar_arrive(&sh.p_full[b]);
+                mbar_arrive(&sh.p_full[s]);
             }
-
-            // the group's end: O, l and the reference
-            const float mg = ref == -INFINITY ? -INFINITY : off;
-            const bool any = tb > ta;
-            if (any) {
-                if (!wait_pv(n - 1)) return;
+            // the stream's part of the group is done
+            float mg = st.ref == -INFINITY ? -INFINITY : st.off, lg = st.l;
+            if (mine0 < tb) {
+                if (!warp_wait(&sh.pv_done[s], (n - 1) & 1u, sh)) return;
                 tmem_fence_after();
+                const uint32_t group = base + (g - u.ga);
+                if (warp_live && *reinterpret_cast<volatile uint32_t*>(&sh.odd[group % kGroupRing]) == group + 1)
+                    add_odd<DP, F16>(p, u, w.known, o_addr, max(ta * kTile, cleaned), min(tb * kTile, u.kv_end), ta, s,
+                                     live, mine, words);
             }
-            if (!warp_live) continue;
-            if (any && *reinterpret_cast<volatile uint32_t*>(&sh.odd[group % kGroupRing]) == group + 1) {
-                // non-finite values join the sums of the rows that see them
-                const int32_t x1 = min(tb * kTile, u.kv_end);
-                const int32_t* table = p.block_table + static_cast<int64_t>(w.known) * p.max_blocks;
-#pragma unroll 1
-                for (int ch = 0; ch < DP / 32; ++ch) {
-                    uint32_t z[32];
-                    tmem_ld32(z, o_addr + ch * 32);
-                    tmem_wait_ld(z);
-#pragma unroll 1
-                    for (int32_t x = max(ta * kTile, cleaned); live && x < x1; ++x) {
-                        if (!(seen_bits(p, u, i, words, x) & 1u)) continue;
-                        const int32_t blk = table[x / p.block_size];
-                        if (blk < 0 || blk >= p.num_blocks) continue;
-                        const uint16_t* v = p.v + blk * p.block_stride + (x % p.block_size) * p.token_stride +
-                                            u.head * p.head_stride + ch * 32;
+            Join in{0.0f, 1.0f, 0.0f};  // of the group's streams
+            if (split) {
+                sh.ref[s][row] = mg;
+                sh.sum[s][row] = lg;
+                tmem_fence_before();
+                mbar_arrive(&sh.g_done);
+                if (!warp_wait(&sh.g_done, joined & 1u, sh)) return;
+                ++joined;
+                tmem_fence_after();
+                in = join_at(sh.ref[0][row], sh.ref[1][row]);
+                lg = join_sum(sh.sum[0][row], sh.sum[1][row], in);
+                mg = in.m;
+            }
+            if (warp_live) {
+                const Join j = join_at(M, mg);
+                float* slot = slots + static_cast<int64_t>(1 + g - u.ga) * p.slot_floats;
+                const bool both = split && ta + 1 < tb;
+                const uint32_t at = split ? tmem + lane_base + 2 * kTile + col0 : o_addr;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (ch * 32 + e < D) {
-                                const float y = widen<F16>(v[e]);
-                                if (!isfinite(y)) z[e] = __float_as_uint(__uint_as_float(z[e]) + y);
-                            }
+                for (int ch = 0; ch < kCols / 16; ++ch) {
+                    if (MULTI && split && ch >= kHalf / 16) break;
+                    uint32_t z[16], y[16];
+                    tmem_ld16(z, at + ch * 16);
+                    if (both) tmem_ld16(y, at + kTile + ch * 16);
+                    tmem_wait_ld(z);
+                    if (both) {
+                        tmem_wait_ld(y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 x = join_sum2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
+                                                       make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
+                                                       in);
+                            z[2 * e] = __float_as_uint(x.x);
+                            z[2 * e + 1] = __float_as_uint(x.y);
                         }
                     }
-                    __syncwarp();
-                    tmem_st32(o_addr + ch * 32, z);
-                }
-                tmem_wait_st();
-            }
-            const Join j = join_at(M, mg);
-            float* slot = slots + static_cast<int64_t>(1 + g - u.ga) * p.slot_floats;
+                    if (whole) {
 #pragma unroll
-            for (int ch = 0; ch < DP / 16; ++ch) {
-                uint32_t z[16];
-                if (any) {
-                    tmem_ld16(z, o_addr + ch * 16);
-                    tmem_wait_ld(z);
-                } else {
+                        for (int e = 0; e < 8; ++e)
+                            acc[ch * 8 + e] = join_sum2(
+                                acc[ch * 8 + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
+                    } else if (live) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) z[e] = 0u;
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(slot)[(col0 / 4 + ch * 4 + e) * p.slot_rows + slot_row] =
+                                make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+                    }
                 }
                 if (whole) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[ch * 8 + e] =
-                            join_sum2(acc[ch * 8 + e],
-                                      make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
-                } else if (live) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        reinterpret_cast<uint4*>(slot)[(ch * 4 + e) * p.slot_rows + slot_row] =
-                            make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+                    L = join_sum(L, lg, j);
+                    M = j.m;
+                } else if (live && col0 == 0) {
+                    slot[DP * p.slot_rows + slot_row] = mg;
+                    slot[(DP + 1) * p.slot_rows + slot_row] = lg;
                 }
             }
-            if (whole) {
-                L = join_sum(L, l, j);
-                M = j.m;
-            } else if (live) {
-                slot[DP * p.slot_rows + slot_row] = mg;
-                slot[(DP + 1) * p.slot_rows + slot_row] = l;
+            if (split) {
+                tmem_fence_before();
+                mbar_arrive(&sh.o_free);
             }
         }
         if (!whole || !live) continue;
@@ -855,45 +910,56 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
             const int64_t t = u.tok0 + i;
             const int h = u.head * p.group + head;
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            uint16_t* dst = p.out + t * p.out_token_stride + h * p.out_head_stride;
+            uint16_t* dst = p.out + t * p.out_token_stride + h * p.out_head_stride + col0;
 #pragma unroll
-            for (int e = 0; e < DP / 8; ++e) {
-                if (e * 8 < D) {
+            for (int e = 0; e < kCols / 8; ++e) {
+                if (col0 + e * 8 < p.head_dim && !(MULTI && split && e >= kHalf / 8)) {
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[k] = pack_pair<F16>(acc[4 * e + k].x * inv, acc[4 * e + k].y * inv);
                     *reinterpret_cast<uint4*>(dst + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-            if (p.lse != nullptr) p.lse[t * p.kv_heads * p.group + h] = final_lse(M, L);
+            if (col0 == 0 && p.lse != nullptr) p.lse[t * p.kv_heads * p.group + h] = final_lse(M, L);
         } else {
 #pragma unroll
-            for (int e = 0; e < DP / 4; ++e)
-                reinterpret_cast<float4*>(slots)[e * p.slot_rows + slot_row] =
-                    make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
-            slots[DP * p.slot_rows + slot_row] = M;
-            slots[(DP + 1) * p.slot_rows + slot_row] = L;
+            for (int e = 0; e < kCols / 4; ++e)
+                if (!(MULTI && split && e >= kHalf / 4))
+                    reinterpret_cast<float4*>(slots)[(col0 / 4 + e) * p.slot_rows + slot_row] =
+                        make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
+            if (col0 == 0) {
+                slots[DP * p.slot_rows + slot_row] = M;
+                slots[(DP + 1) * p.slot_rows + slot_row] = L;
+            }
         }
     }
 }
 
-constexpr size_t attn_shared_bytes(int dp, int stages)
+// Shared memory: Q of two runs, the ring, the barriers.  A product reads 128 rows of Q
+// where fewer were copied; what lies behind them gives rows of S that nobody uses.
+__host__ __device__ inline size_t attn_shared_bytes(int dp, int stages, int q_chunk)
 {
-    return 1024 + static_cast<size_t>(2 + stages) * kTile * dp * 2 + sizeof(Shared);
+    return static_cast<size_t>(2 * (dp / 64)) * q_chunk + static_cast<size_t>(stages) * kTile * dp * 2 +
+           sizeof(Shared);
 }
 
-template <int DP, bool F16, int PAIRS>
-__global__ void __launch_bounds__(PAIRS == 2 ? 384 : 256, 1)
-    tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mq,
+// MULTI: some request may have more rows than one tile.  Its running sums take twice the
+// registers: the 384 threads launch with 168 each, the softmax warps take 208 and the
+// other four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).
+template <int DP, bool F16, bool MULTI>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    tree_attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mq,
                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
 {
-    extern __shared__ unsigned char raw[];
-    unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-    constexpr uint32_t kQ = kTile * DP * 2;
-    unsigned char* ring = base + 2 * kQ;
-    Shared& sh = *reinterpret_cast<Shared*>(ring + static_cast<size_t>(p.stages) * kQ);
+    extern __shared__ __align__(1024) unsigned char base[];  // the swizzle repeats every 1024 bytes
+    unsigned char* ring = base + 2 * (DP / 64) * p.q_chunk;
+    Shared& sh = *reinterpret_cast<Shared*>(ring + static_cast<size_t>(p.stages) * (kTile * DP * 2));
     const int tid = threadIdx.x, warp = tid >> 5;
     pdl_launch_dependents();
+    if ((smem_addr(base) & 1023u) != 0) {  // never seen: the array's alignment is declared
+        if (tid == 0) p.flags[blockIdx.x] = kFlagTimeout;
+        return;
+    }
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -908,6 +974,8 @@ __global__ void __launch_bounds__(PAIRS == 2 ? 384 : 256, 1)
             mbar_init(&sh.p_full[i], kTile);
             mbar_init(&sh.pv_done[i], 1);
         }
+        mbar_init(&sh.g_done, 2 * kTile);
+        mbar_init(&sh.o_free, 2 * kTile);
         mbar_init(&sh.drain, 1);
         fence_barrier_init();
         sh.stop = 0;
@@ -924,16 +992,18 @@ __global__ void __launch_bounds__(PAIRS == 2 ? 384 : 256, 1)
     }
 
     if (warp < 4) {
+        if (MULTI) registers_lower<88>();
         if (warp == 0)
             copy_tiles<DP>(p, sh, ring, &mk, 0);
         else if (warp == 1)
-            issue_products<DP>(p, sh, smem_addr(base), smem_addr(ring), tmem);
+            issue_products<DP, MULTI>(p, sh, smem_addr(base), smem_addr(ring), tmem);
         else if (warp == 2)
             copy_tiles<DP>(p, sh, ring, &mv, 1);
         else
-            copy_q_clean_v<DP, F16>(p, sh, base, ring, &mq);
+            copy_q_clean_v<DP, F16, MULTI>(p, sh, base, ring, &mq);
     } else {
-        softmax_rows<DP, F16, PAIRS>(p, sh, tmem, PAIRS == 2 ? (warp - 4) >> 2 : 0);
+        if (MULTI) registers_raise<208>();
+        softmax_rows<DP, F16, MULTI>(p, sh, tmem, (warp - 4) >> 2);
     }
     tmem_fence_before();
     __syncthreads();
@@ -948,7 +1018,7 @@ constexpr int kJoinThreads = 256;
 // blockIdx.x = c: the item that is cut where CTA c's share ends, if its first group lies in that
 // share; blockIdx.y: 256 of its (row, four columns).  Groups are joined as softmax_rows does.
 template <int DP, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams p, int32_t ctas)
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p, int32_t ctas)
 {
     pdl_wait_primary();
     if (p.status != nullptr && blockIdx.y == 0) {
@@ -962,7 +1032,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     const Start s = p.starts[c], e = p.starts[c + 1];
     if (e.g == 0 || (s.r == e.r && s.item == e.item && s.g > 0)) return;
     const Request q = request_of(p, e.r);
-    const int32_t head = e.item / q.per_head, tile0 = (e.item - head * q.per_head) * p.pairs;
+    const int32_t head = e.item / q.per_head, tile0 = 2 * (e.item - head * q.per_head);
     int32_t kv_end;
     const int32_t nt = item_tiles(p, q, tile0, &kv_end);
     const int32_t ng = max(1, (nt + q.gt - 1) / q.gt);
@@ -1054,7 +1124,8 @@ int attn_ctas()
 }
 
 struct AttnLayout {
-    int32_t pairs, tile_tokens, slot_rows, slots_per_cta;
+    int32_t tile_tokens, slot_rows, slots_per_cta;
+    bool multi;  // some request may have more rows than one tile
     int64_t slot_floats;
     size_t starts, flags, slots, total;
 };
@@ -1069,12 +1140,12 @@ AttnLayout attn_layout(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_
     const int32_t G = heads / kv_heads, dp = head_dim <= 64 ? 64 : 128;
     a.tile_tokens = kTile / G;
     const int64_t tiles = (static_cast<int64_t>(max_tokens) + a.tile_tokens - 1) / a.tile_tokens;
-    a.pairs = tiles > 1 ? 2 : 1;
-    a.slot_rows = a.pairs == 2 ? 2 * kTile : std::min<int32_t>(kTile, (std::max(max_tokens, 1) * G + 7) / 8 * 8);
+    a.multi = tiles > 1;
+    a.slot_rows = a.multi ? 2 * kTile : std::min<int32_t>(kTile, (std::max(max_tokens, 1) * G + 7) / 8 * 8);
     a.slot_floats = static_cast<int64_t>(a.slot_rows) * (dp + 2);
     const int64_t nt = (max_kv + kTile - 1) / kTile;
     const int64_t groups = std::max<int64_t>(1, std::min(std::max<int64_t>(1, std::min(sms, 2 * sms / kv_heads)), (nt + 1) / 2));
-    const int64_t share = R * std::max<int64_t>(1, (tiles + 1) / 2) * kv_heads * (nt + groups) / sms + 1;
+    const int64_t share = R * std::max<int64_t>(1, (tiles + 1) / 2) * kv_heads * (nt + groups + 2) / sms + 1;
     a.slots_per_cta = static_cast<int32_t>(1 + std::min(groups, share / 3 + 3));
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     a.starts = 0;
@@ -1084,16 +1155,16 @@ AttnLayout attn_layout(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_
     return a;
 }
 
-template <int DP, bool F16, int PAIRS>
+template <int DP, bool F16, bool MULTI>
 cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                         cudaStream_t stream)
 {
-    auto kern = tree_attention_kernel<DP, F16, PAIRS>;
-    const size_t bytes = attn_shared_bytes(DP, p.stages);
+    auto kern = tree_attention_kernel<DP, F16, MULTI>;
+    const size_t bytes = attn_shared_bytes(DP, p.stages, p.q_chunk);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas();
-    kern<<<ctas, PAIRS == 2 ? 384 : 256, bytes, stream>>>(p, mq, mk, mv);
+    kern<<<ctas, kAttnThreads, bytes, stream>>>(p, mq, mk, mv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas, (p.slot_rows * (DP / 4) + kJoinThreads - 1) / kJoinThreads);
@@ -1138,10 +1209,13 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.group = a.q.heads / a.cache.kv_heads;
     p.tile_tokens = lay.tile_tokens;
     p.head_dim = a.q.head_dim;
-    p.pairs = lay.pairs;
+    p.box_tokens = std::max(1, std::min(lay.tile_tokens, a.max_tokens));
+    p.q_chunk = (p.group * p.box_tokens * 128 + 1023) / 1024 * 1024;
     p.box_rows = std::min(kTile, a.cache.block_size & -a.cache.block_size);
     p.sms = attn_ctas();
-    p.stages = dp == 128 ? 5 : 10;
+    // the ring takes what Q leaves of an SM's 227 KB: 5 or 6 stages of 32 KB, up to 12 of 16 KB
+    const size_t fixed = attn_shared_bytes(dp, 0, p.q_chunk);
+    p.stages = static_cast<int32_t>(std::min<size_t>(kMaxStages, (kMaxShared - fixed) / (kTile * dp * 2)));
     // a scale of 0 weighs all alike; the smallest factor keeps hidden scores at -inf
     p.c = std::max(fabsf(a.scale) * 1.44269504088896341f, 1e-30f);
     p.word_qk = product_word(f16, kTile, kTile, false, a.scale < 0.0f);
@@ -1167,7 +1241,7 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     const uint64_t D = static_cast<uint64_t>(a.q.head_dim);
     const uint64_t qd[3] = {D, static_cast<uint64_t>(a.q.heads), static_cast<uint64_t>(a.q.tokens)};
     const int64_t qs[3] = {1, a.q.head_stride, a.q.token_stride};
-    const uint32_t qb[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(p.tile_tokens)};
+    const uint32_t qb[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(p.box_tokens)};
     const uint64_t kd[4] = {D, static_cast<uint64_t>(p.block_size), static_cast<uint64_t>(p.kv_heads),
                             static_cast<uint64_t>(p.num_blocks)};
     const int64_t ks[4] = {1, p.token_stride, p.head_stride, p.block_stride};
@@ -1175,16 +1249,16 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     if (!encode(&mq, a.cache.dtype, 3, a.q.data, qd, qs, qb) || !encode(&mk, a.cache.dtype, 4, a.cache.k, kd, ks, kb) ||
         !encode(&mv, a.cache.dtype, 4, a.cache.v, kd, ks, kb))
         return cudaErrorInvalidValue;
-    const int kind = (dp == 128 ? 4 : 0) | (f16 ? 2 : 0) | (p.pairs == 2 ? 1 : 0);
+    const int kind = (dp == 128 ? 4 : 0) | (f16 ? 2 : 0) | (lay.multi ? 1 : 0);
     switch (kind) {
-        case 0: return launch_attn<64, false, 1>(p, mq, mk, mv, stream);
-        case 1: return launch_attn<64, false, 2>(p, mq, mk, mv, stream);
-        case 2: return launch_attn<64, true, 1>(p, mq, mk, mv, stream);
-        case 3: return launch_attn<64, true, 2>(p, mq, mk, mv, stream);
-        case 4: return launch_attn<128, false, 1>(p, mq, mk, mv, stream);
-        case 5: return launch_attn<128, false, 2>(p, mq, mk, mv, stream);
-        case 6: return launch_attn<128, true, 1>(p, mq, mk, mv, stream);
-        default: return launch_attn<128, true, 2>(p, mq, mk, mv, stream);
+        case 0: return launch_attn<64, false, false>(p, mq, mk, mv, stream);
+        case 1: return launch_attn<64, false, true>(p, mq, mk, mv, stream);
+        case 2: return launch_attn<64, true, false>(p, mq, mk, mv, stream);
+        case 3: return launch_attn<64, true, true>(p, mq, mk, mv, stream);
+        case 4: return launch_attn<128, false, false>(p, mq, mk, mv, stream);
+        case 5: return launch_attn<128, false, true>(p, mq, mk, mv, stream);
+        case 6: return launch_attn<128, true, false>(p, mq, mk, mv, stream);
+        default: return launch_attn<128, true, true>(p, mq, mk, mv, stream);
     }
 }
 
