@@ -59,13 +59,16 @@ class SvHeads(C.Structure):
 
 
 _lib = None
+torch = None  # set by load()
 
 
 def load(path: str | None = None):
     """Load libspecverify.so (built in-tree by ``_build.build()``)."""
-    global _lib
+    global _lib, torch
     if _lib is not None:
         return _lib
+    import torch  # the calls below the loader use the module's name: an import statement in each costs more
+
     path = path or LIB_PATH
     if not os.path.exists(path):
         raise RuntimeError(
@@ -373,22 +376,21 @@ def accept_scan(accept, draft, fix, out: dict | None = None, stream=None) -> dic
 
 
 def _half_type(t) -> int:
-    import torch
-
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return SV_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return SV_F16
     raise TypeError(f"heads and caches must be bfloat16 or float16, got {t.dtype}")
 
 
 def heads_of(t) -> SvHeads:
     """Describe a CUDA tensor of heads [tokens, heads, head_dim] (tokens and heads may be strided)."""
+    load()
     if not t.is_cuda or t.dim() != 3:
         raise ValueError("heads must be a 3-D CUDA tensor [tokens, heads, head_dim]")
     T, H, D = t.shape
     st, sh, sd = t.stride()
-    if D > 1 and sd != 1:
+    if sd != 1 and D > 1:
         raise ValueError("entries of a head must be contiguous")
     return SvHeads(t.data_ptr(), _half_type(t), T, H, D, st, sh)
 
@@ -396,29 +398,47 @@ def heads_of(t) -> SvHeads:
 def cache_of(k, v) -> SvKvCache:
     """Describe a paged cache: K and V tensors [num_blocks, block_size, kv_heads, head_dim], or with the layers in
     front, of one dtype and the same strides (any order of the axes but the last)."""
-    if not k.is_cuda or not v.is_cuda or k.dim() not in (4, 5) or k.shape != v.shape:
+    load()
+    shape, strides = k.shape, k.stride()
+    n = len(shape)
+    if not k.is_cuda or not v.is_cuda or n not in (4, 5) or shape != v.shape:
         raise ValueError("caches must be 4-D or 5-D CUDA tensors of one shape")
-    if k.dtype != v.dtype:
+    if k.dtype is not v.dtype:
         raise TypeError("K and V caches must have one dtype")
-    if k.stride() != v.stride():
+    if strides != v.stride():
         raise ValueError("K and V caches must have the same strides")
-    if k.shape[-1] > 1 and k.stride(-1) != 1:
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError("entries of a head must be contiguous")
-    layers, layer_stride = (1, 0) if k.dim() == 4 else (k.shape[0], k.stride(0))
-    nb, bs, H, D = k.shape[-4:]
-    sb, st, sh, _ = k.stride()[-4:]
+    layers, layer_stride = (1, 0) if n == 4 else (shape[0], strides[0])
+    nb, bs, H, D = shape[-4:]
+    sb, st, sh, _ = strides[-4:]
     return SvKvCache(k.data_ptr(), v.data_ptr(), _half_type(k), nb, bs, H, D, layers, sb, st, sh, layer_stride)
 
 
-def _ints(t, name, n=None):
-    """An int32 CUDA tensor that is passed as it lies."""
-    import torch
-
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+def _ints(t, name, n=-1) -> int:
+    """The address of an int32 CUDA tensor that is passed as it lies."""
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
-    if n is not None and t.numel() != n:
+    if n >= 0 and t.numel() != n:
         raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    return C.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    """The given stream's handle, or the current one's (without building a stream object for it)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _new_ints(like, *sizes):
+    """Int32 tensors of these sizes in one allocation and one split: allocating each costs more than the launch that
+    fills them."""
+    return torch.unsafe_split_with_sizes(torch.empty(sum(sizes), dtype=torch.int32, device=like.device), sizes)
 
 
 def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_size: int, T: int, parent=None,
@@ -428,18 +448,19 @@ def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_si
     int32 [1] of them free; T the capacity of the packed arrays; parent int32 [T] or None (a chain).  Returns
     cu_tokens [R + 1], kv_len [R], slot int64 [T], position [T], free_count [1], status [R] and, with parents,
     mask int32 [T, mask_words] (ancestor bits)."""
-    import torch
-
     lib = load()
-    R, dev = seq_len.numel(), seq_len.device
+    R = seq_len.numel()
     if block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("block_table must be [R, max_blocks]")
+    a_seq, a_table = _ints(seq_len, "seq_len"), _ints(block_table, "block_table")
     if out is None:
-        out = dict(cu_tokens=_empty(R + 1, torch.int32, dev), kv_len=_empty(R, torch.int32, dev),
-                   slot=_empty(T, torch.int64, dev), position=_empty(T, torch.int32, dev),
-                   free_count=_empty(1, torch.int32, dev), status=_empty(R, torch.int32, dev))
+        # the 64-bit slots lie first, as pairs of 32-bit entries
+        slot, cu, kv, position, count, status, mask = _new_ints(
+            seq_len, 2 * T, R + 1, R, T, 1, R, T * mask_words if parent is not None else 0)
+        out = dict(cu_tokens=cu, kv_len=kv, slot=slot.view(torch.int64), position=position, free_count=count,
+                   status=status)
         if parent is not None:
-            out["mask"] = _empty((T, mask_words), torch.int32, dev)
+            out["mask"] = mask.view(T, mask_words)
     mask = out.get("mask") if parent is not None else None
     if R == 0:  # nothing to lay out
         out["cu_tokens"].zero_()
@@ -449,13 +470,14 @@ def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_si
         if mask is not None:
             mask.zero_()
         return out
-    _check(lib.sv_step_tables(_ints(seq_len, "seq_len"), _ints(new_len, "new_len", R), R, block_size,
-                              _ints(block_table, "block_table"), block_table.shape[1],
-                              _ints(free_blocks, "free_blocks"), _ints(free_count, "free_count", 1),
-                              free_blocks.numel(), None if parent is None else _ints(parent, "parent", T), T,
-                              _ptr(out["cu_tokens"]), _ptr(out["kv_len"]), _ptr(out["slot"]),
-                              _ptr(out["position"]), _ptr(mask), mask_words if mask is not None else 0,
-                              _ptr(out["free_count"]), _ptr(out.get("status")), _stream(stream)))
+    rc = lib.sv_step_tables(a_seq, _ints(new_len, "new_len", R), R, block_size, a_table, block_table.shape[1],
+                            _ints(free_blocks, "free_blocks"), _ints(free_count, "free_count", 1),
+                            free_blocks.numel(), None if parent is None else _ints(parent, "parent", T), T,
+                            out["cu_tokens"].data_ptr(), out["kv_len"].data_ptr(), out["slot"].data_ptr(),
+                            out["position"].data_ptr(), _at(mask), mask_words if mask is not None else 0,
+                            out["free_count"].data_ptr(), _at(out.get("status")), _raw_stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -463,10 +485,9 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, f
                trained: float = 0.0, low: float = 0.0, high: float = 0.0, device="cuda"):
     """Frequencies for rope_cache: an int64 tensor [rot_dim / 2] of 64-bit turn fractions (see sv_rope_freqs for
     the scalings)."""
-    import torch
-
+    lib = load()
     host = torch.zeros(max(rot_dim, 0) // 2, dtype=torch.int64)
-    _check(load().sv_rope_freqs(rot_dim, base, scaling, factor, trained, low, high, _ptr(host)))
+    _check(lib.sv_rope_freqs(rot_dim, base, scaling, factor, trained, low, high, _ptr(host)))
     return host.to(device)
 
 
@@ -474,18 +495,19 @@ def rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, interleaved: bo
                q_out=None, stream=None):
     """Rotate q [T, heads, D] and k [T, kv_heads, D] at position int32 [T] and write k and v into the paged cache
     at slot int64 [T] (-1: not cached).  freqs: rope_freqs(rot_dim).  Returns the rotated q (q_out may be q)."""
-    import torch
-
     lib = load()
+    T = q.shape[0]
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if slot.dtype != torch.int64 or not slot.is_contiguous() or slot.numel() != q.shape[0]:
+    if slot.dtype is not torch.int64 or not slot.is_contiguous() or slot.numel() != T:
         raise ValueError("slot must be a contiguous int64 tensor with an entry for each token")
     if freqs.dtype not in (torch.int64, torch.uint64) or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous int64 tensor from rope_freqs")
-    _check(lib.sv_rope_cache(heads_of(q), heads_of(k), heads_of(v), _ints(position, "position", q.shape[0]),
-                             _ptr(slot), _ptr(freqs), 2 * freqs.numel(), 1 if interleaved else 0, mscale,
-                             heads_of(q_out), cache_of(k_cache, v_cache), _stream(stream)))
+    rc = lib.sv_rope_cache(heads_of(q), heads_of(k), heads_of(v), _ints(position, "position", T), slot.data_ptr(),
+                           freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, mscale, heads_of(q_out),
+                           cache_of(k_cache, v_cache), _raw_stream(stream))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -501,8 +523,6 @@ def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_toke
     [R, max_blocks]; kv_len int32 [R]; cu_tokens int32 [R + 1]; max_tokens bounds a request's tokens; mask int32
     [T, words] (which of its request's step tokens a token sees) or None (a chain); scale defaults to
     D ** -0.5.  Returns out [T, heads, D] and, with_lse, lse float32 [T, heads]."""
-    import torch
-
     lib = load()
     T, heads, D = q.shape
     R, max_blocks = block_table.shape
@@ -516,12 +536,13 @@ def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_toke
     if workspace is None:
         workspace = _workspace(lib.sv_tree_attention_workspace(R, T, max_tokens, heads, cache.kv_heads, D,
                                                                max_blocks * cache.block_size), q.device, None)
-    _check(lib.sv_tree_attention(heads_of(q), cache, _ints(block_table, "block_table"), max_blocks,
-                                 _ints(kv_len, "kv_len", R), _ints(cu_tokens, "cu_tokens", R + 1), R, max_tokens,
-                                 None if mask is None else _ints(mask, "mask"),
-                                 0 if mask is None else mask.shape[1], D ** -0.5 if scale is None else scale,
-                                 heads_of(out["out"]), _ptr(out.get("lse")), _ptr(out.get("status")),
-                                 _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    rc = lib.sv_tree_attention(heads_of(q), cache, _ints(block_table, "block_table"), max_blocks,
+                               _ints(kv_len, "kv_len", R), _ints(cu_tokens, "cu_tokens", R + 1), R, max_tokens,
+                               None if mask is None else _ints(mask, "mask"), 0 if mask is None else mask.shape[1],
+                               D ** -0.5 if scale is None else scale, heads_of(out["out"]), _at(out.get("lse")),
+                               _at(out.get("status")), workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -531,26 +552,25 @@ def cache_commit(k_cache, v_cache, block_table, seq_len, kv_len, cu_tokens, acce
     layer of the caches ([layers, ] num_blocks, block_size, kv_heads, head_dim), and the blocks without a kept token
     are pushed on free_blocks.  accept_len int32 [R] and branch int32 [R] as verify_greedy returns them, or path
     int32 [R, k] of the accepted tokens' numbers.  Returns seq_len [R], free_count [1] and status [R]."""
-    import torch
-
     lib = load()
-    R, dev = seq_len.numel(), seq_len.device
+    R = seq_len.numel()
     if block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("block_table must be [R, max_blocks]")
+    a_seq = _ints(seq_len, "seq_len")
     if out is None:
-        out = dict(seq_len=_empty(R, torch.int32, dev), free_count=_empty(1, torch.int32, dev),
-                   status=_empty(R, torch.int32, dev))
+        out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, R, 1, R)))
     if R == 0:
         out["free_count"].copy_(free_count)
         return out
-    _check(lib.sv_cache_commit(cache_of(k_cache, v_cache), _ints(block_table, "block_table"), block_table.shape[1],
-                               _ints(seq_len, "seq_len"), _ints(kv_len, "kv_len", R),
-                               _ints(cu_tokens, "cu_tokens", R + 1), R, _ints(accept_len, "accept_len", R),
-                               None if branch is None else _ints(branch, "branch", R),
-                               None if path is None else _ints(path, "path", R * k), k,
-                               _ints(free_blocks, "free_blocks", k_cache.shape[-4]),
-                               _ints(free_count, "free_count", 1), _ptr(out["seq_len"]), _ptr(out["free_count"]),
-                               _ptr(out.get("status")), _stream(stream)))
+    rc = lib.sv_cache_commit(cache_of(k_cache, v_cache), _ints(block_table, "block_table"), block_table.shape[1], a_seq,
+                             _ints(kv_len, "kv_len", R), _ints(cu_tokens, "cu_tokens", R + 1), R,
+                             _ints(accept_len, "accept_len", R), None if branch is None else _ints(branch, "branch", R),
+                             None if path is None else _ints(path, "path", R * k), k,
+                             _ints(free_blocks, "free_blocks", k_cache.shape[-4]), _ints(free_count, "free_count", 1),
+                             out["seq_len"].data_ptr(), out["free_count"].data_ptr(), _at(out.get("status")),
+                             _raw_stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 

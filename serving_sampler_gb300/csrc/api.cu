@@ -1,6 +1,7 @@
 // The C ABI of specverify: argument checks, then the kernel launchers.
 // Declarations and the contract of every call are in include/specverify.h.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -10,11 +11,16 @@
 
 namespace sv {
 
+// A device's SM count does not change: asked for once per device.
 int device_sm_count()
 {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) != 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -406,7 +412,7 @@ int sv_step_tables(const int32_t* seq_len, const int32_t* new_len, int32_t R, in
         return SV_ERR_ALIGN;
     if (!have_device()) return SV_ERR_DEVICE;
     const StepTablesArgs a{seq_len,     new_len,    R,      block_size, max_blocks, num_blocks, T,
-                           mask_words,  block_table, free_blocks, free_count, parent, cu_tokens, kv_len,
+                           mask_words,  divisor_of(block_size), block_table, free_blocks, free_count, parent, cu_tokens, kv_len,
                            slot,        position,   mask,   free_count_out, status};
     return launched(launch_step_tables(a, stream));
 }
@@ -526,8 +532,9 @@ int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_b
     if (R < 0 || k < 0 || max_blocks < 0) return SV_ERR_INVALID_ARG;
     if (k > SV_MAX_K) return SV_ERR_LIMIT;
     if (branch != nullptr && path != nullptr) return SV_ERR_INVALID_ARG;
-    if (cache.layers > 16384) return SV_ERR_LIMIT;  // two rows of the launch grid a layer
     if (int rc = check_cache(cache, R > 0)) return rc;
+    // 128 16-byte columns of the heads to a row of the launch grid
+    if (2ll * cache.layers * cache.kv_heads * (cache.head_dim / 8) > 65535ll * 128) return SV_ERR_LIMIT;
     if (static_cast<int64_t>(max_blocks) * cache.block_size > INT32_MAX) return SV_ERR_LIMIT;
     if (R == 0) return SV_OK;
     if (seq_len == nullptr || kv_len == nullptr || cu_tokens == nullptr || accept_len == nullptr ||
@@ -540,8 +547,8 @@ int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_b
         return SV_ERR_ALIGN;
     if (!have_device()) return SV_ERR_DEVICE;
     return launched(launch_cache_commit(CommitArgs{cache, block_table, max_blocks, seq_len, kv_len, cu_tokens, R,
-                                                   accept_len, branch, path, k, free_blocks, free_count,
-                                                   seq_len_out, free_count_out, status},
+                                                   accept_len, branch, path, k, divisor_of(cache.block_size),
+                                                   free_blocks, free_count, seq_len_out, free_count_out, status},
                                         stream));
 }
 

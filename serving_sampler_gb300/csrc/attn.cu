@@ -39,6 +39,7 @@
 // item, cut evenly over the CTAs; every CTA finds its share itself from the lengths on
 // the device.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -71,6 +72,7 @@ struct AttnParams {
     const int32_t *block_table, *kv_len, *cu_tokens;
     const uint32_t* mask;
     int32_t R, T, max_blocks, max_kv, max_tokens, mask_words;
+    Divisor by_block;
     int32_t block_size, num_blocks, kv_heads, group, tile_tokens, head_dim;
     int32_t box_tokens;  // tokens a copy of Q brings
     int32_t q_chunk;     // bytes of 64 columns of Q
@@ -115,7 +117,7 @@ __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
     q.per_head = (q.tiles + 1) / 2;
     const int32_t nt = (q.kv + kTile - 1) / kTile;
     const int32_t wave = max(1, p.sms / max(1, p.kv_heads * q.per_head));
-    const int32_t root = static_cast<int32_t>(ceilf(sqrtf(static_cast<float>(nt))));
+    const int32_t root = 2 * static_cast<int32_t>(0.5f * sqrtf(static_cast<float>(nt)) + 0.5f);
     const int32_t one = (nt + wave - 1) / wave, two = (nt + 2 * wave - 1) / (2 * wave);
     const int32_t even = 5 * two >= 4 * root ? two : 5 * one >= 4 * root ? one : root;
     q.gt = (max(q.tiles > 1 ? 8 : 2, even) + 1) & ~1;
@@ -374,13 +376,13 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
         if (t >= t1) continue;
         auto block_of = [&](int32_t tile) -> int32_t {
             const int32_t x = tile * kTile + lane * p.box_rows;
-            return lane < subs && x < u.kv_end ? table[x / p.block_size] : 0;
+            return lane < subs && x < u.kv_end ? table[p.by_block.quotient(x)] : 0;
         };
         int32_t id = block_of(t);
         for (; t < t1; ++t) {
             const int32_t block = id, x0 = t * kTile;
             if (t + 1 < t1) id = block_of(t + 1);  // in flight while this tile is issued
-            const int32_t place = (x0 + lane * p.box_rows) % p.block_size;
+            const int32_t at = x0 + lane * p.box_rows, place = at - p.by_block.quotient(at) * p.block_size;
             const int32_t live = min(subs, (u.kv_end - x0 + p.box_rows - 1) / p.box_rows);
             uint64_t* full = &sh.kv_full[rt.stage];
             // the stage's fill before this one is the ring's last turn: `first + 2 * fills` stages in
@@ -1028,8 +1030,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         for (int32_t r = blockIdx.x * kJoinThreads + threadIdx.x; r < p.R; r += gridDim.x * kJoinThreads)
             p.status[r] = st;
     }
+    // all shares at once: the ones that an item goes through are read one after the other
+    extern __shared__ Start s_starts[];
+    for (int32_t i = threadIdx.x; i <= ctas; i += kJoinThreads) s_starts[i] = p.starts[i];
+    __syncthreads();
     const int32_t c = blockIdx.x;
-    const Start s = p.starts[c], e = p.starts[c + 1];
+    const Start s = s_starts[c], e = s_starts[c + 1];
     if (e.g == 0 || (s.r == e.r && s.item == e.item && s.g > 0)) return;
     const Request q = request_of(p, e.r);
     const int32_t head = e.item / q.per_head, tile0 = 2 * (e.item - head * q.per_head);
@@ -1050,23 +1056,42 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const float* x = p.slots + static_cast<int64_t>(c) * p.slots_per_cta * p.slot_floats;
     float4 acc = *reinterpret_cast<const float4*>(x + at_o);
     float M = x[at_m], L = x[at_l];
-    int32_t g = e.g;
-    for (int32_t o = c + 1; g < ng; ++o) {
-        const Start f = p.starts[o + 1];
-        const int32_t gb = f.r == e.r && f.item == e.item ? min(ng, f.g) : ng;
-        x = p.slots + (static_cast<int64_t>(o) * p.slots_per_cta + 1) * p.slot_floats;
-#pragma unroll 4
-        for (; g < gb; ++g, x += p.slot_floats) {
-            const float4 y = *reinterpret_cast<const float4*>(x + at_o);
-            const float mg = x[at_m], lg = x[at_l];
-            const Join j = join_at(M, mg);
-            acc.x = join_sum(acc.x, y.x, j);
-            acc.y = join_sum(acc.y, y.y, j);
-            acc.z = join_sum(acc.z, y.z, j);
-            acc.w = join_sum(acc.w, y.w, j);
-            L = join_sum(L, lg, j);
-            M = j.m;
+    // the other groups, eight loaded before the first of them is joined
+    int32_t g = e.g, o = c, gb = e.g;
+    while (g < ng) {
+        constexpr int kAhead = 8;
+        float4 y[kAhead];
+        float mg[kAhead], lg[kAhead];
+        int32_t n = 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            while (g + n < ng && g + n >= gb) {  // the CTA that has the next group
+                ++o;
+                const Start f = s_starts[o + 1];
+                gb = f.r == e.r && f.item == e.item ? min(ng, f.g) : ng;
+                x = p.slots + (static_cast<int64_t>(o) * p.slots_per_cta + 1) * p.slot_floats;
+            }
+            if (g + n < ng) {
+                y[k] = *reinterpret_cast<const float4*>(x + at_o);
+                mg[k] = x[at_m];
+                lg[k] = x[at_l];
+                x += p.slot_floats;
+                ++n;
+            }
         }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (k < n) {
+                const Join j = join_at(M, mg[k]);
+                acc.x = join_sum(acc.x, y[k].x, j);
+                acc.y = join_sum(acc.y, y[k].y, j);
+                acc.z = join_sum(acc.z, y[k].z, j);
+                acc.w = join_sum(acc.w, y[k].w, j);
+                L = join_sum(L, lg[k], j);
+                M = j.m;
+            }
+        }
+        g += n;
     }
     const int64_t t = q.tok0 + i;
     const int32_t h = head * p.group + (row - token * p.group);
@@ -1161,14 +1186,23 @@ cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& mq, const CUtens
 {
     auto kern = tree_attention_kernel<DP, F16, MULTI>;
     const size_t bytes = attn_shared_bytes(DP, p.stages, p.q_chunk);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    // the kernel's shared-memory limit is raised once per device, to the most that it can use
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const int ctas = attn_ctas();
+    if (dev >= 64 || ((raised.load(std::memory_order_relaxed) >> dev) & 1u) == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxShared));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) raised.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    const int ctas = p.sms;
     kern<<<ctas, kAttnThreads, bytes, stream>>>(p, mq, mk, mv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas, (p.slot_rows * (DP / 4) + kJoinThreads - 1) / kJoinThreads);
     cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(ctas + 1) * sizeof(Start);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1203,6 +1237,7 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.max_kv = max_kv;
     p.max_tokens = a.max_tokens;
     p.mask_words = a.mask_words;
+    p.by_block = divisor_of(a.cache.block_size);
     p.block_size = a.cache.block_size;
     p.num_blocks = a.cache.num_blocks;
     p.kv_heads = a.cache.kv_heads;

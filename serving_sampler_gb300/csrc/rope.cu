@@ -7,12 +7,12 @@
 // frequency is off by p * 2^-24 radians.  They become a float in [-1, 1) half
 // turns for sincospif.
 //
-// One CTA takes one token (and a share of its heads, when there are few tokens):
-// rot_dim / 2 threads take the token's sines while everybody's first loads are in
-// flight, then the CTA runs over (head, 16-byte vector).  A head is held by one
-// group of lanes of a warp (head_dim / 8 rounded up to a power of two), and the
-// other half of each pair comes from a lane of that group, so q may be rotated in
-// place: a group has loaded its head before it stores any of it.
+// rope_cache_kernel: a CTA takes a few tokens.  Its threads take the sines of all of
+// them while their first loads are in flight, then each takes items of two 16-byte
+// vectors: the two halves of eight pairs (or eight pairs that lie side by side, or two
+// vectors that pass), so that no entry has to come from another thread and q may be
+// rotated in place.  Items of all heads of the CTA's tokens lie on one line, which
+// keeps every lane busy for any head size.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,8 +23,9 @@
 namespace sv {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;  // heads a lane group has in flight
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 1;   // items a thread works on, with as many in flight
+constexpr int kRopeTokens = 4;  // most tokens of a CTA
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w)
@@ -42,150 +43,201 @@ __device__ __forceinline__ uint32_t pack2(float x, float y)
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <bool F16>
-__device__ __forceinline__ float entry(const uint16_t* p)
+
+// cosine and sine of pair `pair` at position p
+__device__ __forceinline__ float2 turn_of(const RopeArgs& a, int32_t p, int pair)
 {
-    const uint32_t w = *p;
-    return F16 ? unpack2<true>(w).x : __uint_as_float(w << 16);
+    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(p)) * a.freqs[pair];
+    const float turn = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
+    float s, c;
+    sincospif(turn, &s, &c);
+    return make_float2(c * a.mscale, s * a.mscale);
+}
+
+// The cache offset of a slot, -1 for one outside the cache.
+__device__ __forceinline__ int64_t slot_offset(const RopeArgs& a, int64_t slot)
+{
+    const int64_t block = slot >= 0 ? slot / a.cache.block_size : -1;
+    if (block < 0 || block >= a.cache.num_blocks) return -1;
+    return block * a.cache.block_stride + (slot - block * a.cache.block_size) * a.cache.token_stride;
 }
 
 struct RopeGeom {
-    int32_t vecs;       // 16-byte vectors of a head
-    int32_t group_log;  // log2 of the lanes that hold a head
-    int32_t half;       // rotated pairs
-    int32_t rows;       // q heads, then k heads, then v heads
-    bool by_lanes;      // half layout whose partner vectors are whole: half % 8 == 0
+    int32_t vecs;               // 16-byte vectors of a head
+    int32_t half;               // rotated pairs
+    int32_t rows;               // q heads, then k heads, then v heads
+    int32_t items, line;        // items of a head, of a token
+    uint32_t by_items;          // ceil(2^32 / items), for division by multiplication (0 for one item)
+    int32_t tokens;             // of a CTA
 };
 
-template <bool F16>
-__global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const RopeArgs a, const RopeGeom g)
+// Items of a head: their two vectors, and the first of the eight pairs they hold (-1: they pass).
+struct RopeItem {
+    int32_t token, row, a, b, pair;
+};
+template <bool SIDE>
+__device__ __forceinline__ RopeItem item_of(const RopeArgs& a, const RopeGeom& g, uint32_t x)
 {
-    __shared__ float2 s_cs[SV_MAX_HEAD_DIM / 2];
+    RopeItem m;
+    uint32_t in = x;
+    m.token = 0;
+#pragma unroll
+    for (int i = 1; i < kRopeTokens; ++i) {
+        if (in >= static_cast<uint32_t>(g.line)) {
+            in -= g.line;
+            ++m.token;
+        }
+    }
+    m.row = static_cast<int32_t>(g.by_items != 0 ? __umulhi(in, g.by_items) : in);
+    const int32_t j = static_cast<int32_t>(in - m.row * g.items);
+    const bool turns = m.row < a.q.heads + a.cache.kv_heads;
+    const int32_t cut = g.half / 8;  // rotated items when the halves lie apart
+    m.a = 2 * j;
+    m.b = 2 * j + 1;
+    m.pair = -1;
+    if (turns && SIDE) {
+        m.pair = 8 * j;
+    } else if (turns && j < cut) {
+        m.a = j;
+        m.b = j + cut;
+        m.pair = 8 * j;
+    }
+    return m;
+}
+
+// SIDE: the entries of a pair lie side by side; otherwise half a rotated part apart (a multiple of 8).
+template <bool F16, bool SIDE>
+__global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const __grid_constant__ RopeArgs a, const RopeGeom g)
+{
+    __shared__ __align__(16) float2 s_cs[kRopeTokens][SV_MAX_HEAD_DIM / 2 + 8];
+    __shared__ int64_t s_at[kRopeTokens];
     const int tid = threadIdx.x;
-    const int64_t t = blockIdx.x;
-    const int lane = tid & ((1 << g.group_log) - 1);
-    const int groups = kRopeThreads >> g.group_log;
-    const int stride = groups * gridDim.y;
-    const bool on = lane < g.vecs;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * g.tokens;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), a.q.tokens - t0));
     const int Hq = a.q.heads, Hk = a.cache.kv_heads;
+    const uint32_t total = static_cast<uint32_t>(tokens) * g.line, step = kRopeThreads * gridDim.y;
 
-    const int64_t slot = a.slot[t];
-    const int64_t block = slot >= 0 ? slot / a.cache.block_size : -1;
-    const bool cached = block >= 0 && block < a.cache.num_blocks;
-    const int64_t cache_at = cached ? block * a.cache.block_stride +
-                                          (slot - block * a.cache.block_size) * a.cache.token_stride
-                                    : 0;
-
-    auto source = [&](int row) -> const uint16_t* {
-        if (row < Hq)
-            return static_cast<const uint16_t*>(a.q.data) + t * a.q.token_stride + row * a.q.head_stride;
-        if (row < Hq + Hk)
-            return static_cast<const uint16_t*>(a.k.data) + t * a.k.token_stride + (row - Hq) * a.k.head_stride;
-        return static_cast<const uint16_t*>(a.v.data) + t * a.v.token_stride + (row - Hq - Hk) * a.v.head_stride;
-    };
-    auto target = [&](int row) -> uint16_t* {
-        if (row < Hq)
-            return static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) + t * a.q_out.token_stride +
-                   row * a.q_out.head_stride;
-        if (!cached) return nullptr;
-        if (row < Hq + Hk) return static_cast<uint16_t*>(a.cache.k) + cache_at + (row - Hq) * a.cache.head_stride;
-        return static_cast<uint16_t*>(a.cache.v) + cache_at + (row - Hq - Hk) * a.cache.head_stride;
-    };
-
-    uint4 val[kRopeBatch];
-    const int first = (tid >> g.group_log) + groups * blockIdx.y;
-    auto load = [&](int row0) {
+    auto load = [&](uint32_t x0, uint4 (&va)[kRopeBatch], uint4 (&vb)[kRopeBatch]) {
 #pragma unroll
         for (int u = 0; u < kRopeBatch; ++u) {
-            const int row = row0 + u * stride;
-            val[u] = make_uint4(0, 0, 0, 0);
-            if (on && row < g.rows) val[u] = *reinterpret_cast<const uint4*>(source(row) + lane * 8);
+            const uint32_t x = x0 + u * step;
+            if (x < total) {
+                const RopeItem m = item_of<SIDE>(a, g, x);
+                const sv_heads& h = m.row < Hq ? a.q : m.row < Hq + Hk ? a.k : a.v;
+                const int row = m.row < Hq ? m.row : m.row < Hq + Hk ? m.row - Hq : m.row - Hq - Hk;
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(h.data) +
+                                                                  (t0 + m.token) * h.token_stride + row * h.head_stride);
+                va[u] = src[m.a];
+                if (m.b < g.vecs) vb[u] = src[m.b];
+            }
         }
     };
-    load(first);
-    if (tid < g.half) {
-        const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(a.position[t])) * a.freqs[tid];
-        const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
-        float s, c;
-        sincospif(x, &s, &c);
-        s_cs[tid] = make_float2(c * a.mscale, s * a.mscale);
+    uint4 na[kRopeBatch], nb[kRopeBatch];
+    uint32_t x0 = blockIdx.y * kRopeThreads + tid;
+    load(x0, na, nb);
+    if (tid < tokens) s_at[tid] = slot_offset(a, a.slot[t0 + tid]);
+    for (int y = tid; y < tokens * g.half; y += kRopeThreads) {
+        const int i = y / g.half, pair = y - i * g.half;
+        s_cs[i][pair] = turn_of(a, a.position[t0 + i], pair);
     }
     __syncthreads();
 
-    const int shift = g.half / 8;  // vectors between the halves of a pair (by_lanes)
-    const uint32_t all = 0xFFFFFFFFu;
-    for (int row0 = first;; row0 += kRopeBatch * stride) {
-        // every lane of a warp makes the same number of rounds: the group's first row decides
-        if (__all_sync(all, row0 >= g.rows)) break;
-        if (row0 != first) load(row0);
+    for (; x0 < total; x0 += kRopeBatch * step) {
+        uint4 va[kRopeBatch], vb[kRopeBatch];
 #pragma unroll
         for (int u = 0; u < kRopeBatch; ++u) {
-            const int row = row0 + u * stride;
-            const bool live = row < g.rows;
-            uint32_t w[4] = {val[u].x, val[u].y, val[u].z, val[u].w};
-            uint32_t o[4];
-            if (g.by_lanes) {
-                const bool low = lane < shift, rotated = lane < 2 * shift;
-                const int other = (tid & 31 & ~((1 << g.group_log) - 1)) | (low ? lane + shift : rotated ? lane - shift : lane);
-                uint32_t m[4];
+            va[u] = na[u];
+            vb[u] = nb[u];
+        }
+        load(x0 + kRopeBatch * step, na, nb);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m[i] = __shfl_sync(all, w[i], other);
+        for (int u = 0; u < kRopeBatch; ++u) {
+            const uint32_t x = x0 + u * step;
+            if (x >= total) break;
+            const RopeItem m = item_of<SIDE>(a, g, x);
+            uint32_t wa[4] = {va[u].x, va[u].y, va[u].z, va[u].w}, wb[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+            if (m.pair >= 0) {
+                const float4* cs = reinterpret_cast<const float4*>(&s_cs[m.token][m.pair]);
+                if (SIDE) {
+                    // the last rotated item may hold fewer than eight pairs: the others pass
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (rotated && live && row < Hq + Hk) {
-                        const float2 x = unpack2<F16>(w[i]), y = unpack2<F16>(m[i]);
-                        const int p = (low ? lane : lane - shift) * 8 + 2 * i;
-                        const float2 e = s_cs[p], f = s_cs[p + 1];
-                        const float se = low ? -e.y : e.y, sf = low ? -f.y : f.y;
-                        o[i] = pack2<F16>(fmaf(y.x, se, x.x * e.x), fmaf(y.y, sf, x.y * f.x));
-                    } else {
-                        o[i] = w[i];
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t& w = e < 4 ? wa[e] : wb[e - 4];
+                        const float4 f2 = cs[e / 2];
+                        const float c = e & 1 ? f2.z : f2.x, s = e & 1 ? f2.w : f2.y;
+                        const float2 v = unpack2<F16>(w);
+                        if (m.pair + e < g.half) w = pack2<F16>(fmaf(-v.y, s, v.x * c), fmaf(v.x, s, v.y * c));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 f = cs[e];  // two pairs
+                        const float2 v = unpack2<F16>(wa[e]), w = unpack2<F16>(wb[e]);
+                        wa[e] = pack2<F16>(fmaf(-w.x, f.y, v.x * f.x), fmaf(-w.y, f.w, v.y * f.z));
+                        wb[e] = pack2<F16>(fmaf(v.x, f.y, w.x * f.x), fmaf(v.y, f.w, w.y * f.z));
                     }
                 }
-            } else if (a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = lane * 4 + i;
-                    if (p < g.half && live && row < Hq + Hk) {
-                        const float2 x = unpack2<F16>(w[i]), e = s_cs[p];
-                        o[i] = pack2<F16>(fmaf(-x.y, e.y, x.x * e.x), fmaf(x.x, e.y, x.y * e.x));
-                    } else {
-                        o[i] = w[i];
-                    }
-                }
+            }
+            uint4* dst;
+            if (m.row < Hq) {
+                dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) +
+                                               (t0 + m.token) * a.q_out.token_stride + m.row * a.q_out.head_stride);
             } else {
-                // pairs that straddle vectors: partners read one by one (from L1, the group has the line)
+                const int64_t at = s_at[m.token];
+                if (at < 0) continue;
+                const bool key = m.row < Hq + Hk;
+                dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(key ? a.cache.k : a.cache.v) + at +
+                                               (m.row - (key ? Hq : Hq + Hk)) * a.cache.head_stride);
+            }
+            dst[m.a] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+            if (m.b < g.vecs) dst[m.b] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+        }
+    }
+}
+
+// Halves that lie apart by no multiple of 8 entries: a warp takes a head, entry by entry; it has
+// read all of it before it writes any.
+template <bool F16>
+__global__ void __launch_bounds__(kRopeThreads) rope_entries_kernel(const __grid_constant__ RopeArgs a, const RopeGeom g)
+{
+    constexpr int kMost = SV_MAX_HEAD_DIM / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = blockIdx.x;
+    const int Hq = a.q.heads, Hk = a.cache.kv_heads, D = a.cache.head_dim;
+    const int64_t at = slot_offset(a, a.slot[t]);
+    auto widen = [](uint16_t w) { return unpack2<F16>(w).x; };
+    float2 cs[kMost];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (on && live && row < Hq + Hk) {
-                        const uint16_t* src = source(row);
-                        float y[2];
-                        const float2 x = unpack2<F16>(w[i]);
-                        const float v[2] = {x.x, x.y};
+    for (int e = 0; e < kMost; ++e) {
+        const int d = lane + 32 * e;
+        if (d < 2 * g.half) cs[e] = turn_of(a, a.position[t], d < g.half ? d : d - g.half);
+    }
+    for (int row = threadIdx.x / 32 + blockIdx.y * (kRopeThreads / 32); row < g.rows;
+         row += gridDim.y * (kRopeThreads / 32)) {
+        const sv_heads& h = row < Hq ? a.q : row < Hq + Hk ? a.k : a.v;
+        const int r = row < Hq ? row : row < Hq + Hk ? row - Hq : row - Hq - Hk;
+        const uint16_t* src = static_cast<const uint16_t*>(h.data) + t * h.token_stride + r * h.head_stride;
+        uint16_t out[kMost];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int d = lane * 8 + 2 * i + q;
-                            if (d < g.half) {
-                                const float2 e = s_cs[d];
-                                y[q] = fmaf(-entry<F16>(src + d + g.half), e.y, v[q] * e.x);
-                            } else if (d < 2 * g.half) {
-                                const float2 e = s_cs[d - g.half];
-                                y[q] = fmaf(entry<F16>(src + d - g.half), e.y, v[q] * e.x);
-                            } else {
-                                y[q] = v[q];
-                            }
-                        }
-                        o[i] = pack2<F16>(y[0], y[1]);
-                    } else {
-                        o[i] = w[i];
-                    }
+        for (int e = 0; e < kMost; ++e) {
+            const int d = lane + 32 * e;
+            if (d < D) {
+                out[e] = src[d];
+                if (row < Hq + Hk && d < 2 * g.half) {
+                    const bool low = d < g.half;
+                    const float y = widen(src[low ? d + g.half : d - g.half]);
+                    out[e] = static_cast<uint16_t>(pack2<F16>(fmaf(low ? -y : y, cs[e].y, widen(out[e]) * cs[e].x), 0.0f));
                 }
-                __syncwarp();  // partners are read before q is overwritten in place
             }
-            if (on && live) {
-                uint16_t* dst = target(row);
-                if (dst != nullptr) *reinterpret_cast<uint4*>(dst + lane * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+        }
+        __syncwarp();
+        uint16_t* dst = row < Hq ? static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) + t * a.q_out.token_stride +
+                                       r * a.q_out.head_stride
+                                 : static_cast<uint16_t*>(row < Hq + Hk ? a.cache.k : a.cache.v) + at + r * a.cache.head_stride;
+        if (row < Hq || at >= 0) {
+#pragma unroll
+            for (int e = 0; e < kMost; ++e)
+                if (lane + 32 * e < D) dst[lane + 32 * e] = out[e];
         }
     }
 }
@@ -196,19 +248,42 @@ cudaError_t launch_rope_cache(const RopeArgs& a, cudaStream_t stream)
 {
     RopeGeom g{};
     g.vecs = a.cache.head_dim / 8;
-    while ((1 << g.group_log) < g.vecs) ++g.group_log;
     g.half = a.rot_dim / 2;
     g.rows = a.q.heads + 2 * a.cache.kv_heads;
-    g.by_lanes = !a.interleaved && g.half % 8 == 0;
-    // few tokens: their heads are spread over the SMs
-    const int groups = kRopeThreads >> g.group_log;
-    const int most = (g.rows + groups - 1) / groups;
-    const int want = (device_sm_count() + a.q.tokens - 1) / a.q.tokens;
-    const dim3 grid(static_cast<unsigned>(a.q.tokens), static_cast<unsigned>(std::max(1, std::min(want, most))));
-    if (a.cache.dtype == SV_F16)
-        rope_cache_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a, g);
-    else
-        rope_cache_kernel<false><<<grid, kRopeThreads, 0, stream>>>(a, g);
+    g.items = (g.vecs + 1) / 2;
+    g.line = g.rows * g.items;
+    // exact: at most 8 items, and fewer than 2^20 of a token (65,536 rows)
+    g.by_items = g.items > 1 ? static_cast<uint32_t>((0x100000000ull + g.items - 1) / g.items) : 0u;
+    const int sms = device_sm_count();
+    const bool f16 = a.cache.dtype == SV_F16;
+    auto cdiv = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+    if (!a.interleaved && g.half % 8 != 0) {
+        const int64_t most = cdiv(g.rows, kRopeThreads / 32), want = cdiv(8 * sms, a.q.tokens);
+        const dim3 grid(static_cast<unsigned>(a.q.tokens), static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
+        if (f16)
+            rope_entries_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a, g);
+        else
+            rope_entries_kernel<false><<<grid, kRopeThreads, 0, stream>>>(a, g);
+        return cudaGetLastError();
+    }
+    // from about eight CTAs of four tokens per SM on a CTA takes four: the loads of a token then run
+    // beside the arithmetic of the one before; few tokens' heads are spread over the SMs
+    g.tokens = a.q.tokens >= kRopeTokens * 8 * sms ? kRopeTokens : 1;
+    const int64_t most = cdiv(static_cast<int64_t>(g.tokens) * g.line, kRopeThreads);
+    const int64_t want = cdiv(2 * sms, a.q.tokens);
+    const dim3 grid(static_cast<unsigned>(cdiv(a.q.tokens, g.tokens)),
+                    static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
+    if (a.interleaved) {
+        if (f16)
+            rope_cache_kernel<true, true><<<grid, kRopeThreads, 0, stream>>>(a, g);
+        else
+            rope_cache_kernel<false, true><<<grid, kRopeThreads, 0, stream>>>(a, g);
+    } else {
+        if (f16)
+            rope_cache_kernel<true, false><<<grid, kRopeThreads, 0, stream>>>(a, g);
+        else
+            rope_cache_kernel<false, false><<<grid, kRopeThreads, 0, stream>>>(a, g);
+    }
     return cudaGetLastError();
 }
 

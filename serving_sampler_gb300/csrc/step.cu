@@ -71,9 +71,10 @@ __device__ __forceinline__ void block_prefix2(int64_t& a, int64_t& b, int64_t* s
     }
 }
 
-__device__ __forceinline__ int32_t blocks_of(int64_t tokens, int32_t block_size)
+// blocks that hold `tokens` tokens, 0 <= tokens < 2^31
+__device__ __forceinline__ int32_t blocks_of(int32_t tokens, const Divisor& by_block)
 {
-    return static_cast<int32_t>((tokens + block_size - 1) / block_size);
+    return tokens > 0 ? by_block.quotient(tokens - 1) + 1 : 0;
 }
 
 // What one request asks for.
@@ -91,8 +92,8 @@ __device__ __forceinline__ Ask ask_of(const StepTablesArgs& a, int32_t r)
     const int64_t total = static_cast<int64_t>(L) + n;
     q.bad = L < 0 || n < 0 || total > static_cast<int64_t>(a.max_blocks) * a.block_size ||
             (a.parent != nullptr && (n > SV_MAX_TREE || n > 32 * static_cast<int64_t>(a.mask_words)));
-    q.held = q.bad ? 0 : blocks_of(L, a.block_size);
-    q.need = q.bad ? 0 : blocks_of(total, a.block_size) - q.held;
+    q.held = q.bad ? 0 : blocks_of(L, a.by_block);
+    q.need = q.bad ? 0 : blocks_of(static_cast<int32_t>(total), a.by_block) - q.held;
     return q;
 }
 
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepTab
         for (int32_t j = tid; j < t1 - t0; j += kStepThreads) {
             int64_t slot = -1;
             if (takes) {
-                const int32_t at = L + j, b = at / a.block_size;
+                const int32_t at = L + j, b = a.by_block.quotient(at);
                 const int32_t id = b < q.held ? table[b] : a.free_blocks[count - 1 - (pre + b - q.held)];
                 if (id >= 0 && id < a.num_blocks)
                     slot = static_cast<int64_t>(id) * a.block_size + (at - b * a.block_size);
@@ -267,20 +268,21 @@ __device__ __forceinline__ Keep keep_of(const CommitArgs& c, int32_t r)
         q.bad = most < q.a;
         q.a = most;
     }
-    q.held = q.takes ? blocks_of(c.kv_len[r], c.cache.block_size) : 0;
-    q.kept = q.takes ? blocks_of(static_cast<int64_t>(q.root) + 1 + q.a, c.cache.block_size) : 0;
+    q.held = q.takes ? blocks_of(c.kv_len[r], c.by_block) : 0;
+    q.kept = q.takes ? blocks_of(q.root + 1 + q.a, c.by_block) : 0;
     return q;
 }
 
 constexpr int kMoveBatch = 8;
 
-// Grid: x = requests, then the CTAs that give blocks back; y = layers x {K, V}.
-// A thread owns 16-byte columns of the heads and walks the path upward, eight
-// tokens' loads before their stores.  That order is safe in place: the i-th
+// Grid: x = requests, then the CTAs that give blocks back; y = 128 16-byte columns of
+// the heads of all layers, K and V.  A thread owns a column and walks the path upward,
+// eight tokens' loads before their stores.  That order is safe in place: the i-th
 // destination is token 1 + i, the path increases, so a token still to be read
-// (number >= 1 + its index) is never below the ones already written.
-// Bound by the latency of a path's ceil(a / 8) dependent rounds for few requests
-// and by memory for many.
+// (number >= 1 + its index) is never below the ones already written.  The places are
+// looked up once per CTA, all at a time, so that a round is one trip to memory.
+// Bound by the latency of a path's ceil(a / 8) rounds for few requests and by memory
+// for many.
 __global__ void __launch_bounds__(kStepThreads) cache_commit_kernel(const CommitArgs c, int32_t releasers)
 {
     __shared__ int64_t s_sum[2 * kStepWarps];
@@ -323,43 +325,38 @@ __global__ void __launch_bounds__(kStepThreads) cache_commit_kernel(const Commit
     }
 
     const int32_t r = blockIdx.x;
+    if (c.path == nullptr && (c.branch == nullptr || c.branch[r] == 0)) return;  // they lie where they belong
     const Keep q = keep_of(c, r);
     if (q.a == 0) return;
-    const int32_t layer = blockIdx.y >> 1;
-    uint16_t* base = static_cast<uint16_t*>((blockIdx.y & 1) ? c.cache.v : c.cache.k) +
-                     static_cast<int64_t>(layer) * c.cache.layer_stride;
+    __shared__ int64_t s_src[SV_MAX_K], s_dst[SV_MAX_K];
     const int32_t* table = c.block_table + static_cast<int64_t>(r) * c.max_blocks;
-    const int32_t vecs = c.cache.head_dim / 8, columns = c.cache.kv_heads * vecs;
-    const int32_t bs = c.cache.block_size;
     auto place = [&](int32_t token) -> int64_t {
-        const int32_t at = q.root + token, b = at / bs;
-        const int32_t id = table[b];
+        const int32_t at = q.root + token, b = c.by_block.quotient(at), id = table[b];
         if (id < 0 || id >= c.cache.num_blocks) return -1;
-        return static_cast<int64_t>(id) * c.cache.block_stride + static_cast<int64_t>(at - b * bs) * c.cache.token_stride;
+        return id * c.cache.block_stride + (at - b * c.cache.block_size) * c.cache.token_stride;
     };
-    for (int32_t col = tid; col < columns; col += kStepThreads) {
-        const int32_t h = col / vecs;
-        uint16_t* p = base + static_cast<int64_t>(h) * c.cache.head_stride + (col - h * vecs) * 8;
-        for (int32_t i0 = 0; i0 < q.a; i0 += kMoveBatch) {
-            uint4 val[kMoveBatch];
-            int64_t dst[kMoveBatch];
+    for (int32_t i = tid; i < q.a; i += kStepThreads) {
+        const int32_t x = path_at(c, r, i);
+        const int64_t src = place(x), dst = place(1 + i);
+        s_src[i] = src;
+        s_dst[i] = src < 0 || x == 1 + i ? -1 : dst;
+    }
+    __syncthreads();
+    const int32_t vecs = c.cache.head_dim / 8, columns = c.cache.kv_heads * vecs;
+    const int64_t column = static_cast<int64_t>(blockIdx.y) * kStepThreads + tid;
+    const int32_t plane = static_cast<int32_t>(column / columns), col = static_cast<int32_t>(column - static_cast<int64_t>(plane) * columns);
+    if (plane >= 2 * c.cache.layers) return;
+    const int32_t h = col / vecs;
+    uint16_t* p = static_cast<uint16_t*>((plane & 1) ? c.cache.v : c.cache.k) + (plane >> 1) * c.cache.layer_stride +
+                  h * c.cache.head_stride + (col - h * vecs) * 8;
+    for (int32_t i0 = 0; i0 < q.a; i0 += kMoveBatch) {
+        uint4 val[kMoveBatch];
 #pragma unroll
-            for (int u = 0; u < kMoveBatch; ++u) {
-                const int32_t i = i0 + u;
-                dst[u] = -1;
-                if (i < q.a) {
-                    const int32_t x = path_at(c, r, i);
-                    const int64_t src = x == 1 + i ? -1 : place(x);
-                    if (src >= 0) {
-                        val[u] = *reinterpret_cast<const uint4*>(p + src);
-                        dst[u] = place(1 + i);
-                    }
-                }
-            }
+        for (int u = 0; u < kMoveBatch; ++u)
+            if (i0 + u < q.a && s_dst[i0 + u] >= 0) val[u] = *reinterpret_cast<const uint4*>(p + s_src[i0 + u]);
 #pragma unroll
-            for (int u = 0; u < kMoveBatch; ++u)
-                if (dst[u] >= 0) *reinterpret_cast<uint4*>(p + dst[u]) = val[u];
-        }
+        for (int u = 0; u < kMoveBatch; ++u)
+            if (i0 + u < q.a && s_dst[i0 + u] >= 0) *reinterpret_cast<uint4*>(p + s_dst[i0 + u]) = val[u];
     }
 }
 
@@ -375,7 +372,10 @@ cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream)
 cudaError_t launch_cache_commit(const CommitArgs& a, cudaStream_t stream)
 {
     const int32_t releasers = std::min(32, (a.R + kStepThreads - 1) / kStepThreads);
-    const dim3 grid(static_cast<unsigned>(a.R) + releasers, 2u * a.cache.layers);
+    const int64_t columns = 2ll * a.cache.layers * a.cache.kv_heads * (a.cache.head_dim / 8);
+    const int64_t rows = (columns + kStepThreads - 1) / kStepThreads;
+    if (rows > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(a.R) + releasers, static_cast<unsigned>(rows));
     cache_commit_kernel<<<grid, kStepThreads, 0, stream>>>(a, releasers);
     return cudaGetLastError();
 }

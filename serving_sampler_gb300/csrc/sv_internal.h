@@ -105,10 +105,30 @@ cudaError_t launch_cfg_merge_sample(const Rows& cond, const Rows& uncond, const 
                                     cudaStream_t stream);
 
 // ---- the cache side of a verify step ----------------------------------------
+// Division of numbers below 2^31 by a divisor known on the host: one high product, an
+// addition and a shift (Granlund and Montgomery 1994, the form with an m of 33 bits).
+struct Divisor {
+    uint32_t d, m, shift;
+#ifdef __CUDACC__
+    __device__ __forceinline__ int32_t quotient(int32_t n) const
+    {
+        const uint32_t u = static_cast<uint32_t>(n);
+        return static_cast<int32_t>((__umulhi(u, m) + u) >> shift);
+    }
+#endif
+};
+inline Divisor divisor_of(int32_t d)
+{
+    Divisor x{static_cast<uint32_t>(d), 0, 0};
+    while ((1ull << x.shift) < x.d) ++x.shift;
+    x.m = static_cast<uint32_t>((((1ull << x.shift) - x.d) << 32) / x.d + 1);
+    return x;
+}
 
 struct StepTablesArgs {
     const int32_t *seq_len, *new_len;
     int32_t R, block_size, max_blocks, num_blocks, T, mask_words;
+    Divisor by_block;
     int32_t* block_table;
     const int32_t *free_blocks, *free_count, *parent;
     int32_t *cu_tokens, *kv_len;
@@ -127,6 +147,7 @@ struct CommitArgs {
     int32_t R;
     const int32_t *accept_len, *branch, *path;
     int32_t k;
+    Divisor by_block;
     int32_t* free_blocks;
     const int32_t* free_count;
     int32_t *seq_len_out, *free_count_out, *status;

@@ -118,7 +118,7 @@ def test_commit_checks(m):
     assert call(R=-1) == -1 and call(k=-1) == -1 and call(mb=-1) == -1
     assert call(k=257) == -4
     assert call(branch=BUF, path=BUF) == -1
-    assert call(cache=_cache(m, layers=20000)) == -4
+    assert call(cache=_cache(m, layers=600000)) == -4
     assert call(cache=_cache(m, layers=2, layer_stride=4)) == -3
     assert call(accept=None) == -1 and call(free=None) == -1 and call(seq_out=None) == -1
     assert call(branch=P(0x10002)) == -7
