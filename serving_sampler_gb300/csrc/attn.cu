@@ -12,7 +12,7 @@
 //               a stage);
 //   warp 1      issues the products; S in tensor memory, P over S in tensor memory as
 //               the left operand of P V, O in tensor memory;
-//   warp 3      copies Q, and cleans V where a tile holds positions that not every row
+//   warp 3      lists the CTA's runs of work for the others, copies Q, and cleans V where a tile holds positions that not every row
 //               sees: rows behind the last key become 0 (P is 0 there, but 0 * NaN is
 //               not), and so do NaN and infinite entries, which are noted and added in
 //               32 bits at the end of the group to the rows that do see them;
@@ -35,9 +35,9 @@
 // do not depend on where the work was cut.
 //
 // Work.  An item is (request, key head, row tile or pair of them), a unit one group of
-// an item.  All units lie on one line, in cost of tiles plus one per group and two per
-// item, cut evenly over the CTAs; every CTA finds its share itself from the lengths on
-// the device.
+// an item.  All units lie on one line, in cost of two per tile, two per group and eight
+// per item, cut evenly over the CTAs; every CTA finds its share itself from the lengths
+// on the device.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -54,8 +54,19 @@ namespace {
 
 constexpr int kTile = 128;       // rows of a row tile, keys of a key tile
 constexpr int kMaxStages = 12;
+// Tensor memory: S of the two streams, then O.  Heads of 64 leave room for a second O of each
+// stream, so that a group's products need not wait until the group before has been read.
+template <int DP>
+constexpr int kSums = DP == 64 ? 2 : 1;
+template <int DP>
+__device__ __forceinline__ uint32_t o_column(uint32_t group, int s)
+{
+    return 2 * kTile + (kSums<DP> == 2 ? (group & 1u) * 2 * DP : 0u) + s * DP;
+}
 constexpr int kAttnThreads = 384;
 constexpr size_t kMaxShared = 232448;  // bytes of shared memory a CTA can have
+constexpr int kRunRing = 4;       // runs that are listed at a time
+constexpr int kRunReaders = 11;   // warps that read them: two that copy, the products, eight of softmax
 constexpr int kGroupRing = 16;   // groups whose notes of non-finite values are kept
 constexpr float kGrow = 8.0f;    // log2 by which a tile's maximum may pass the reference
 
@@ -122,12 +133,13 @@ __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
     const int32_t even = 5 * two >= 4 * root ? two : 5 * one >= 4 * root ? one : root;
     q.gt = (max(q.tiles > 1 ? 8 : 2, even) + 1) & ~1;
     q.ng = max(1, (nt + q.gt - 1) / q.gt);
-    q.cost = nt + q.ng + 2;
+    q.cost = 2 * nt + 2 * q.ng + 8;
     return q;
 }
 
 // An item's groups that lie in a CTA's share.
 struct Run {
+    int32_t r;                      // request, -1 behind the last run
     int32_t tok0, na, ctx, kv_end;  // keys [0, kv_end) are looked at
     int32_t head, tile;             // key head, (first) row tile
     bool split, second;             // the streams split the keys; a second row tile
@@ -170,6 +182,7 @@ __device__ __forceinline__ bool next_run(const AttnParams& p, Walk& w, Run& out)
         w.at.item += 1;
         w.at.g = 0;
         if (out.ga >= out.gb) continue;
+        out.r = w.at.r;
         out.tok0 = q.tok0;
         out.na = q.na;
         out.ctx = q.ctx;
@@ -213,8 +226,10 @@ struct Shared {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
     uint64_t q_full[2], q_empty[2];              // by buffer
     uint64_t s_full[2], p_full[2], pv_done[2];   // by stream, a phase per tile
-    uint64_t g_done, o_free;                     // a phase per group whose keys are split
+    uint64_t g_done, o_free[2];                  // a phase per group whose keys are split (o_free: of every other)
+    uint64_t run_full[kRunRing], run_empty[kRunRing];
     uint64_t drain;
+    Run runs[kRunRing];
     uint64_t v_ok[kMaxStages];  // the stage's V has been cleaned
     int64_t scan[16];
     Start start, end;
@@ -243,6 +258,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Shared
 {
     return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, sh)) != 0;
 }
+
+// The list of runs, for a warp: one after the other, each given back when nothing of it is
+// looked at any more.
+struct Runs {
+    uint32_t k = 0;
+    __device__ __forceinline__ const Run* get(Shared& sh) const
+    {
+        return warp_wait(&sh.run_full[k % kRunRing], (k / kRunRing) & 1u, sh) ? &sh.runs[k % kRunRing] : nullptr;
+    }
+    __device__ __forceinline__ void give_back(Shared& sh, uint32_t which) const
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.run_empty[which % kRunRing]);
+    }
+};
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_pair(float x, float y)
@@ -294,7 +324,7 @@ __device__ __forceinline__ Start locate(const AttnParams& p, const Request& q, i
     const int64_t off = at - first;
     int32_t item = static_cast<int32_t>(off / q.cost);
     const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(item) * q.cost);
-    int32_t g = (in + q.gt) / (q.gt + 1);
+    int32_t g = (in + 2 * q.gt + 1) / (2 * q.gt + 2);
     if (g >= q.ng) {
         g = 0;
         ++item;
@@ -362,15 +392,19 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
     constexpr int kChunks = DP / 64;
     constexpr uint32_t kStage = kTile * DP * 2;
     const int lane = threadIdx.x & 31;
-    Walk w{sh.start, sh.end, -1, {}};
-    Run u;
+    Runs runs;
     Ring rt{first, 0};
     int32_t fills = 0;  // of this warp; from the ring's second turn on a stage is waited for
     bool ok = true;
     const int32_t subs = kTile / p.box_rows;
     const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
-    while (ok && next_run(p, w, u)) {
-        const int32_t* table = p.block_table + static_cast<int64_t>(w.known) * p.max_blocks;
+    for (; ok; ++runs.k) {
+        const Run* const next = runs.get(sh);
+        ok = next != nullptr;
+        if (!ok || next->r < 0) break;
+        const Run u = *next;
+        runs.give_back(sh, runs.k);
+        const int32_t* table = p.block_table + static_cast<int64_t>(u.r) * p.max_blocks;
         const int32_t t1 = min(u.gb * u.gt, u.nt);
         int32_t t = u.ga * u.gt;
         if (t >= t1) continue;
@@ -428,18 +462,30 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
     constexpr uint32_t kExp = F16 ? 0x7C007C00u : 0x7F807F80u;
     const int lane = threadIdx.x & 31;
     Walk w{sh.start, sh.end, -1, {}};
-    Run u;
     Ring rk{0, 0}, rv{1, 0};
-    uint32_t groups = 0, runs = 0, used[2] = {0, 0};
+    uint32_t groups = 0, listed = 0, q_runs = 0, used[2] = {0, 0};
+    bool more = true;  // runs to list
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.box_tokens * 128 * kChunks);
-    bool ok = true;
-    for (; ok && next_run(p, w, u); groups += u.gb - u.ga) {
-        const int32_t t1 = min(u.gb * u.gt, u.nt);
-        if (u.ga * u.gt >= t1) continue;
-        for (int i = 0; ok && i < (u.second ? 2 : 1); ++i) {
-            const int b = MULTI ? i : runs & 1;
-            if (used[b] > 0) ok = warp_wait(&sh.q_empty[b], (used[b] - 1) & 1u, sh);
-            if (!ok) break;
+    // Lists the next run, or the list's end.
+    auto list = [&]() {
+        if (!more) return true;
+        if (listed >= kRunRing && !warp_wait(&sh.run_empty[listed % kRunRing], (listed / kRunRing - 1) & 1u, sh)) return false;
+        Run u;
+        more = next_run(p, w, u);
+        if (!more) u.r = -1;
+        if (lane == 0) {
+            sh.runs[listed % kRunRing] = u;
+            mbar_arrive(&sh.run_full[listed % kRunRing]);
+        }
+        __syncwarp();
+        ++listed;
+        return true;
+    };
+    // Q of a run
+    auto copy_q = [&](const Run& u) {
+        for (int i = 0; i < (u.second ? 2 : 1); ++i) {
+            const int b = MULTI ? i : q_runs & 1;
+            if (used[b] > 0 && !warp_wait(&sh.q_empty[b], (used[b] - 1) & 1u, sh)) return false;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&sh.q_full[b], q_bytes);
 #pragma unroll
@@ -450,7 +496,28 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
             __syncwarp();
             ++used[b];
         }
-        ++runs;
+        ++q_runs;
+        return true;
+    };
+    // Two runs are listed ahead of the one that is followed: a slot of the list is free again when the
+    // softmax of the run after it has begun, which needs no more than the runs followed so far.  With two
+    // buffers Q is a run ahead too.  (Two row tiles take both; their Q is waited for by products that
+    // this warp's work on the run comes before, so it cannot be ahead.)
+    bool ok = list() && list();
+    if (ok && !MULTI && sh.runs[0].r >= 0 && sh.runs[0].nt > 0) ok = copy_q(sh.runs[0]);
+    for (uint32_t k = 0; ok; ++k) {
+        ok = list();
+        const Run u = sh.runs[k % kRunRing];
+        if (!ok || u.r < 0) break;
+        if (MULTI) {
+            if (u.nt > 0) ok = copy_q(u);
+        } else {
+            const Run& v = sh.runs[(k + 1) % kRunRing];
+            if (v.r >= 0 && v.nt > 0) ok = copy_q(v);
+        }
+        if (!ok) break;
+        const int32_t t1 = min(u.gb * u.gt, u.nt);
+        if (u.ga * u.gt >= t1) continue;
         const int32_t all = seen_by_all(p, u, u.tile);
         for (int32_t t = u.ga * u.gt; ok && t < t1; ++t) {
             const int32_t x0 = t * kTile;
@@ -490,6 +557,7 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
             rk.next2(p.stages);
             rv.next2(p.stages);
         }
+        groups += u.gb - u.ga;
     }
     if (!ok || sh.stop != 0)  // the copies of Q that were issued
         for (int b = 0; b < 2; ++b)
@@ -501,12 +569,13 @@ template <int DP, bool MULTI>
 __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr, uint32_t ring_addr, uint32_t tmem)
 {
     constexpr uint32_t kStage = kTile * DP * 2, kChunk = kTile * 128;
-    Walk w{sh.start, sh.end, -1, {}};
-    Run u;
+    Runs list;
     Ring rk{0, 0}, rv{1, 0};     // next key tile to multiply with Q, next value tile
     uint32_t tiles[2] = {0, 0};  // by stream
     uint32_t used[2] = {0, 0};   // runs by buffer of Q
-    uint32_t groups = 0;         // groups whose keys are split
+    uint32_t groups = 0;         // groups so far,
+    uint32_t splits = 0, freed = 0;  // those whose keys are split, and of them the ones seen to be read
+    bool after_split = false;    // the group before was one
     uint32_t cleaned = 0;        // a bit per stage: parity of its cleanings
     uint32_t runs = 0;
 
@@ -536,6 +605,20 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
         }
         if (free_k) rk.next2(p.stages);
     };
+    // A group's first products write O.  What lay there, of the group before (of the one before that
+    // where there are two O), has been read: a warpgroup reads its own stream before it lets the next
+    // products begin, and says so where it reads the other's.
+    auto begin_group = [&]() {
+        const uint32_t need = splits - (kSums<DP> == 2 && after_split ? 1u : 0u);
+        for (; freed < need; ++freed)
+            if (!warp_wait(&sh.o_free[freed & 1u], (freed >> 1) & 1u, sh)) return false;
+        return true;
+    };
+    auto end_group = [&](bool split) {
+        ++groups;
+        splits += split;
+        after_split = split;
+    };
     // O of stream s (+)= P V
     auto pv = [&](int s, bool first, bool free_v) {
         if (!warp_wait(&sh.p_full[s], tiles[s] & 1u, sh)) return false;
@@ -544,7 +627,7 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
             const uint64_t vb = smem_operand(ring_addr + rv.stage * kStage, kChunk, 1024);
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-                product_ts(tmem + (2 + s) * kTile, tmem + s * kTile + k * 8, vb + ((k * 2048) >> 4), p.word_pv,
+                product_ts(tmem + o_column<DP>(groups, s), tmem + s * kTile + k * 8, vb + ((k * 2048) >> 4), p.word_pv,
                            !first || k > 0);
             product_commit(&sh.pv_done[s]);
             if (free_v) product_commit(&sh.kv_empty[rv.stage]);
@@ -555,7 +638,12 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
     };
 
     bool ok = true;
-    while (ok && next_run(p, w, u)) {
+    for (; ok; ++list.k) {
+        const Run* const next = list.get(sh);
+        ok = next != nullptr;
+        if (!ok || next->r < 0) break;
+        const Run u = *next;
+        list.give_back(sh, list.k);
         const int32_t ta = u.ga * u.gt, tb = min(u.gb * u.gt, u.nt);
         if (ta >= tb) continue;
         const int32_t all = seen_by_all(p, u, u.tile);
@@ -574,14 +662,16 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
             int32_t in_group = 0;
             for (int32_t t = ta; ok && t < tb; ++t) {
                 const int s = t & 1;
-                // the group's first products write O: what lay there has been read
-                if (in_group == 0 && groups++ > 0) ok = warp_wait(&sh.o_free, groups & 1u, sh);
+                if (in_group == 0) ok = begin_group();
                 ok = ok && wait_v((t + 1) * kTile > all) && pv(s, in_group < 2, true);
                 if (ok && t + 2 < tb) {
                     ok = wait_k();
                     if (ok) qk(s, b, true, t + 3 == tb);
                 }
-                if (++in_group == u.gt) in_group = 0;
+                if (++in_group == u.gt || t + 1 == tb) {
+                    in_group = 0;
+                    end_group(true);
+                }
             }
         } else {
             const int rows = u.second ? 2 : 1;
@@ -594,6 +684,7 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
             for (int s = 0; s < rows; ++s) qk(s, s, s + 1 == rows, ta + 1 == tb);
             int32_t in_group = 0;
             for (int32_t t = ta; ok && t < tb; ++t) {
+                if (in_group == 0) ok = begin_group();
                 for (int s = 0; ok && s < rows; ++s) {
                     if (s == 0) ok = wait_v((t + 1) * kTile > all);
                     ok = ok && pv(s, in_group == 0, s + 1 == rows);
@@ -602,7 +693,10 @@ __device__ void issue_products(const AttnParams& p, Shared& sh, uint32_t q_addr,
                         if (ok) qk(s, s, s + 1 == rows, t + 2 == tb);
                     }
                 }
-                if (++in_group == u.gt) in_group = 0;
+                if (++in_group == u.gt || t + 1 == tb) {
+                    in_group = 0;
+                    end_group(false);
+                }
             }
         }
         ++runs;
@@ -632,29 +726,24 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const Run& u,
     return bits & below(u.kv_end - x);
 }
 
-// A row's probabilities of a whole tile, P = 2^(c z - m) with hidden ones 0, and their
+// A row's probabilities of a whole tile, P = 2^(c z - m), and their
 // sum.  Sixteen at a time, in three stages that run beside each other: loads of the
 // sixteen after, exponentials of these, rounding, sum and store of those before, so
 // that the special-function unit (a warp's exponential takes it 8 cycles, 1024 for
 // a tile) never waits for a load or a store.  P lies over scores that have been read.
-template <bool F16, bool MASKED>
-__device__ __forceinline__ float exp_tile(uint32_t s_addr, const uint32_t (&bits)[4], float c, float off)
+template <bool F16>
+__device__ __forceinline__ float exp_tile(uint32_t s_addr, float c, float off)
 {
     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
     float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
     uint32_t za[16], zb[16];
     float2 xa[8], xb[8];
-    auto take = [&](const uint32_t(&z)[16], float2(&x)[8], int ch) {
+    auto take = [&](const uint32_t(&z)[16], float2(&x)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, off2);
             x[e].x = exp2_fast(x[e].x);
             x[e].y = exp2_fast(x[e].y);
-            if (MASKED) {
-                const uint32_t b = bits[ch / 2] >> (16 * (ch & 1) + 2 * e);
-                x[e].x = b & 1u ? x[e].x : 0.0f;
-                x[e].y = b & 2u ? x[e].y : 0.0f;
-            }
         }
     };
     auto put = [&](const float2(&x)[8], int ch) {
@@ -674,11 +763,11 @@ __device__ __forceinline__ float exp_tile(uint32_t s_addr, const uint32_t (&bits
     tmem_ld16(zb, s_addr + 16);
 #pragma unroll
     for (int ch = 0; ch < 8; ch += 2) {
-        take(za, xa, ch);
+        take(za, xa);
         if (ch > 0) put(xb, ch - 1);
         tmem_wait_ld(zb);
         if (ch + 2 < 8) tmem_ld16(za, s_addr + (ch + 2) * 16);
-        take(zb, xb, ch + 1);
+        take(zb, xb);
         put(xa, ch);
         if (ch + 2 < 8) {
             tmem_wait_ld(za);
@@ -705,22 +794,22 @@ __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, co
     const float c = p.c;
     const int32_t x0 = t * kTile;
     const bool masked = x0 + kTile > all;
-    uint32_t bits[4] = {0, 0, 0, 0};
     float top = -INFINITY;
-    if (masked) {
+    if (masked) {  // hidden scores become -inf where they stand
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+            const uint32_t bits = live ? seen_bits(p, u, mine, words, x0 + (ch & ~1) * 16) >> (16 * (ch & 1)) : 0u;
+            uint32_t z[16];
+            tmem_ld16(z, s_addr + ch * 16);
+            tmem_wait_ld(z);
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-            if (live) bits[ch] = seen_bits(p, u, mine, words, x0 + ch * 32);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t z[16];
-                tmem_ld16(z, s_addr + ch * 32 + half * 16);
-                tmem_wait_ld(z);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    top = fmaxf(top, (bits[ch] >> (half * 16 + e)) & 1u ? __uint_as_float(z[e]) : -INFINITY);
+            for (int e = 0; e < 16; ++e) {
+                z[e] = (bits >> e) & 1u ? z[e] : 0xFF800000u;
+                top = fmaxf(top, __uint_as_float(z[e]));
             }
+            tmem_st16(s_addr + ch * 16, z);
         }
+        tmem_wait_st();
     } else {
 #pragma unroll 1
         for (int col = 0; col < kTile; col += 32) top = fmaxf(top, tmem_max32(s_addr + col));
@@ -752,25 +841,31 @@ __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, co
         }
     }
     st.off = st.ref == -INFINITY ? 0.0f : st.ref * c;
-    st.l += masked ? exp_tile<F16, true>(s_addr, bits, c, st.off) : exp_tile<F16, false>(s_addr, bits, c, st.off);
+    st.l += exp_tile<F16>(s_addr, c, st.off);
     tmem_wait_st();
     return true;
 }
 
-// Non-finite values that were taken out of V join the sums of the rows that see them:
-// positions [x0, x1) of the run, of which those whose tile belongs to the stream.
+// Non-finite values that were taken out of V join the sums of the rows that see them: those of
+// group g, of which the ones whose tile belongs to the stream.
 template <int DP, bool F16>
-__device__ __noinline__ void add_odd(const AttnParams& p, const Run& u, int32_t r, uint32_t o_addr, int32_t x0, int32_t x1,
-                                     int32_t ta, int s, bool live, int32_t i, const uint32_t* words)
+__device__ __noinline__ void add_odd(const AttnParams& p, const Run& u, int32_t g, uint32_t o_addr, int s)
 {
-    const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.max_blocks;
+    const int row = threadIdx.x & (kTile - 1), token = row / p.group;
+    const int32_t i = (u.tile + (u.split ? 0 : s)) * p.tile_tokens + token;
+    const int32_t ta = g * u.gt, x0 = max(ta * kTile, seen_by_all(p, u, u.tile));
+    const int32_t x1 = min(min(ta + u.gt, u.nt) * kTile, u.kv_end);
+    const int32_t* table = p.block_table + static_cast<int64_t>(u.r) * p.max_blocks;
+    // a row that is none sees what it may: its sums are not used
+    const uint32_t* words =
+        p.mask == nullptr ? nullptr : p.mask + static_cast<int64_t>(min(u.tok0 + i, p.T - 1)) * p.mask_words;
 #pragma unroll 1
     for (int ch = 0; ch < DP / 16; ++ch) {
         uint32_t z[16];
         tmem_ld16(z, o_addr + ch * 16);
         tmem_wait_ld(z);
 #pragma unroll 1
-        for (int32_t x = x0; live && x < x1; ++x) {
+        for (int32_t x = x0; x < x1; ++x) {
             if (u.split && ((x / kTile - ta) & 1) != s) continue;
             if (!(seen_bits(p, u, i, words, x) & 1u)) continue;
             const int32_t blk = table[x / p.block_size];
@@ -791,6 +886,18 @@ __device__ __noinline__ void add_odd(const AttnParams& p, const Run& u, int32_t 
     tmem_wait_st();
 }
 
+// What is left to do for a stream's last group when its products are complete: it is joined, and
+// what the run has is written.  That waits until the first scores of the next group have been
+// worked on, so that the products, the other stream and the stores run beside them.
+struct Left {
+    bool any, split, both, tiles, live, warp_live, whole, last, complete;
+    uint32_t run;  // number of its run
+    int32_t g;
+    int32_t slot;  // of a group that is joined elsewhere
+    int32_t t, h;  // the row's token and head
+    float mg, lg;
+};
+
 template <int DP, bool F16, bool MULTI>
 __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int s)
 {
@@ -799,140 +906,219 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
     const int row = threadIdx.x & (kTile - 1);
     const uint32_t lane_base = static_cast<uint32_t>(row & ~31) << 16;
     const int token = row / p.group, head = row - token * p.group;
-    Walk w{sh.start, sh.end, -1, {}};
-    Run u;
-    uint32_t n = 0, base = 0, joined = 0;  // tiles of this stream, groups, groups whose keys are split
-    const uint32_t s_addr = tmem + lane_base + s * kTile, o_addr = tmem + lane_base + (2 + s) * kTile;
+    Runs list;
+    uint32_t n = 0, groups = 0, joined = 0;  // tiles of this stream, groups, groups whose keys are split
+    const uint32_t s_addr = tmem + lane_base + s * kTile;
+    float* const slots = p.slots + static_cast<int64_t>(blockIdx.x) * p.slots_per_cta * p.slot_floats;
+    float M = -INFINITY, L = 0.0f;
+    float2 acc[kCols / 2];
+    Left left{};
 
-    for (; next_run(p, w, u); base += u.gb - u.ga) {
+    // `n` and `groups` are those behind the group that is left: it is settled before they move on.
+    // Its products are complete, non-finite values are in: both warpgroups may read it.
+    auto settle = [&]() {
+        if (left.tiles) {
+            if (!warp_wait(&sh.pv_done[s], (n - 1) & 1u, sh)) return false;
+            tmem_fence_after();
+            if (left.warp_live &&
+                *reinterpret_cast<volatile uint32_t*>(&sh.odd[(groups - 1) % kGroupRing]) == groups)
+                add_odd<DP, F16>(p, sh.runs[left.run % kRunRing], left.g, tmem + lane_base + o_column<DP>(groups - 1, s), s);
+        }
+        if (left.split) {
+            tmem_fence_before();
+            mbar_arrive(&sh.g_done);
+        }
+        return true;
+    };
+    // Joins it and, behind a run's last group, writes what the run has.
+    auto finish = [&]() {
+        left.any = false;
+        Join in{0.0f, 1.0f, 0.0f};  // of the group's streams
+        float mg = left.mg, lg = left.lg;
+        if (left.split) {
+            if (!warp_wait(&sh.g_done, joined & 1u, sh)) return false;
+            tmem_fence_after();
+            in = join_at(sh.ref[0][row], sh.ref[1][row]);
+            lg = join_sum(sh.sum[0][row], sh.sum[1][row], in);
+            mg = in.m;
+        }
+        if (left.warp_live) {
+            const Join j = join_at(M, mg);
+            const int col0 = left.split ? s * kHalf : 0, slot_row = left.split ? row : s * kTile + row;
+            const uint32_t at = tmem + lane_base + o_column<DP>(groups - 1, left.split ? 0 : s) + col0;
+            float* const slot = slots + left.slot * p.slot_floats;
+#pragma unroll
+            for (int ch = 0; ch < kCols / 16; ++ch) {
+                if (MULTI && left.split && ch >= kHalf / 16) break;
+                uint32_t z[16], y[16];
+                tmem_ld16(z, at + ch * 16);
+                if (left.both) tmem_ld16(y, at + DP + ch * 16);
+                tmem_wait_ld(z);
+                if (left.both) {
+                    tmem_wait_ld(y);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 x = join_sum2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
+                                                   make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), in);
+                        z[2 * e] = __float_as_uint(x.x);
+                        z[2 * e + 1] = __float_as_uint(x.y);
+                    }
+                }
+                if (left.whole) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        acc[ch * 8 + e] = join_sum2(
+                            acc[ch * 8 + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
+                } else if (left.live) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<uint4*>(slot)[(col0 / 4 + ch * 4 + e) * p.slot_rows + slot_row] =
+                            make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+                }
+            }
+            if (left.whole) {
+                L = join_sum(L, lg, j);
+                M = j.m;
+            } else if (left.live && col0 == 0) {
+                slot[DP * p.slot_rows + slot_row] = mg;
+                slot[(DP + 1) * p.slot_rows + slot_row] = lg;
+            }
+        }
+        if (left.split) {
+            tmem_fence_before();
+            mbar_arrive(&sh.o_free[joined & 1u]);
+            ++joined;
+        }
+        if (left.last && left.whole) {
+            const int col0 = left.split ? s * kHalf : 0, slot_row = left.split ? row : s * kTile + row;
+            if (left.live && left.complete) {
+                uint16_t* const out = p.out + left.t * p.out_token_stride + left.h * p.out_head_stride + col0;
+                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+                for (int e = 0; e < kCols / 8; ++e) {
+                    if (col0 + e * 8 < p.head_dim && !(MULTI && left.split && e >= kHalf / 8)) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[k] = pack_pair<F16>(acc[4 * e + k].x * inv, acc[4 * e + k].y * inv);
+                        *reinterpret_cast<uint4*>(out + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                if (col0 == 0 && p.lse != nullptr)
+                    p.lse[static_cast<int64_t>(left.t) * p.kv_heads * p.group + left.h] = final_lse(M, L);
+            } else if (left.live) {
+#pragma unroll
+                for (int e = 0; e < kCols / 4; ++e)
+                    if (!(MULTI && left.split && e >= kHalf / 4))
+                        reinterpret_cast<float4*>(slots)[(col0 / 4 + e) * p.slot_rows + slot_row] =
+                            make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
+                if (col0 == 0) {
+                    slots[DP * p.slot_rows + slot_row] = M;
+                    slots[(DP + 1) * p.slot_rows + slot_row] = L;
+                }
+            }
+        }
+        if (left.last) {  // the next run starts from nothing
+            list.give_back(sh, left.run);
+            M = -INFINITY;
+            L = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kCols / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
+        }
+        return true;
+    };
+#pragma unroll
+    for (int e = 0; e < kCols / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
+
+    // Every turn of the inner loop has at most one tile of this stream and what is left of the group
+    // before; turns without a tile (no second row tile, a group's only tile is the other stream's, no
+    // run is left) have only that.
+    for (bool more = true; more; ++list.k) {
+        const Run* const next = list.get(sh);
+        if (next == nullptr) return;
+        const Run& u = *next;
+        more = u.r >= 0;
         const bool split = !MULTI || u.split;
-        if (!split && s == 1 && !u.second) continue;
+        const bool idle = !more || (!split && s == 1 && !u.second);
         const int32_t tile = u.tile + (split ? 0 : s);
         const int32_t i = tile * p.tile_tokens + token;
-        const bool live = row < p.tile_tokens * p.group && i < u.na;
+        const bool live = !idle && row < p.tile_tokens * p.group && i < u.na;
         const bool warp_live = __any_sync(0xFFFFFFFFu, live);
         const int32_t mine = live ? i : 0;
         const uint32_t* words = p.mask == nullptr ? nullptr : p.mask + static_cast<int64_t>(u.tok0 + mine) * p.mask_words;
-        const int32_t all = seen_by_all(p, u, tile), cleaned = seen_by_all(p, u, u.tile);
-        const bool whole = u.ga == 0;  // from the first group on: joined here
-        const int slot_row = split ? row : s * kTile + row;
-        const int col0 = split ? s * kHalf : 0;
-        float* const slots = p.slots + static_cast<int64_t>(blockIdx.x) * p.slots_per_cta * p.slot_floats;
-        float M = -INFINITY, L = 0.0f;
-        float2 acc[kCols / 2];
-#pragma unroll
-        for (int e = 0; e < kCols / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
-
-        for (int32_t g = u.ga; u.nt > 0 && g < u.gb; ++g) {
-            const int32_t ta = g * u.gt, tb = min(ta + u.gt, u.nt);
-            const int32_t step = split ? 2 : 1, mine0 = ta + (split ? s : 0);
-            RowState st{-INFINITY, 0.0f, 0.0f};
-            for (int32_t t = mine0; t < tb; t += step, ++n) {
-                if (!warp_wait(&sh.s_full[s], n & 1u, sh)) return;
-                tmem_fence_after();
-                if (warp_live && !softmax_tile<DP, F16>(p, sh, u, s, s_addr, o_addr, t, t == mine0, n, all, live, mine,
-                                                        words, st))
-                    return;
-                tmem_fence_before();
-                mbar_arrive(&sh.p_full[s]);
+        const int32_t all = seen_by_all(p, u, tile);
+        if (!idle && u.nt == 0) {  // no key: nothing is joined, the row is 0
+            if (live) {
+                const int64_t t_out = u.tok0 + i;
+                const int h_out = u.head * p.group + head, col0 = split ? s * kHalf : 0;
+                uint16_t* const out = p.out + t_out * p.out_token_stride + h_out * p.out_head_stride + col0;
+                for (int e = 0; e < (split ? kHalf : DP) / 8; ++e)
+                    if (col0 + e * 8 < p.head_dim) *reinterpret_cast<uint4*>(out + e * 8) = make_uint4(0, 0, 0, 0);
+                if (col0 == 0 && p.lse != nullptr) p.lse[t_out * p.kv_heads * p.group + h_out] = -INFINITY;
             }
-            // the stream's part of the group is done
-            float mg = st.ref == -INFINITY ? -INFINITY : st.off, lg = st.l;
-            if (mine0 < tb) {
-                if (!warp_wait(&sh.pv_done[s], (n - 1) & 1u, sh)) return;
-                tmem_fence_after();
-                const uint32_t group = base + (g - u.ga);
-                if (warp_live && *reinterpret_cast<volatile uint32_t*>(&sh.odd[group % kGroupRing]) == group + 1)
-                    add_odd<DP, F16>(p, u, w.known, o_addr, max(ta * kTile, cleaned), min(tb * kTile, u.kv_end), ta, s,
-                                     live, mine, words);
-            }
-            Join in{0.0f, 1.0f, 0.0f};  // of the group's streams
-            if (split) {
-                sh.ref[s][row] = mg;
-                sh.sum[s][row] = lg;
-                tmem_fence_before();
-                mbar_arrive(&sh.g_done);
-                if (!warp_wait(&sh.g_done, joined & 1u, sh)) return;
-                ++joined;
-                tmem_fence_after();
-                in = join_at(sh.ref[0][row], sh.ref[1][row]);
-                lg = join_sum(sh.sum[0][row], sh.sum[1][row], in);
-                mg = in.m;
-            }
-            if (warp_live) {
-                const Join j = join_at(M, mg);
-                float* slot = slots + static_cast<int64_t>(1 + g - u.ga) * p.slot_floats;
-                const bool both = split && ta + 1 < tb;
-                const uint32_t at = split ? tmem + lane_base + 2 * kTile + col0 : o_addr;
-#pragma unroll
-                for (int ch = 0; ch < kCols / 16; ++ch) {
-                    if (MULTI && split && ch >= kHalf / 16) break;
-                    uint32_t z[16], y[16];
-                    tmem_ld16(z, at + ch * 16);
-                    if (both) tmem_ld16(y, at + kTile + ch * 16);
-                    tmem_wait_ld(z);
-                    if (both) {
-                        tmem_wait_ld(y);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 x = join_sum2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
-                                                       make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
-                                                       in);
-                            z[2 * e] = __float_as_uint(x.x);
-                            z[2 * e + 1] = __float_as_uint(x.y);
-                        }
-                    }
-                    if (whole) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            acc[ch * 8 + e] = join_sum2(
-                                acc[ch * 8 + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
-                    } else if (live) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4*>(slot)[(col0 / 4 + ch * 4 + e) * p.slot_rows + slot_row] =
-                                make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
-                    }
-                }
-                if (whole) {
-                    L = join_sum(L, lg, j);
-                    M = j.m;
-                } else if (live && col0 == 0) {
-                    slot[DP * p.slot_rows + slot_row] = mg;
-                    slot[(DP + 1) * p.slot_rows + slot_row] = lg;
-                }
-            }
-            if (split) {
-                tmem_fence_before();
-                mbar_arrive(&sh.o_free);
-            }
+            list.give_back(sh, list.k);
+            continue;
         }
-        if (!whole || !live) continue;
-        if (u.gb == u.ng) {
-            const int64_t t = u.tok0 + i;
-            const int h = u.head * p.group + head;
-            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            uint16_t* dst = p.out + t * p.out_token_stride + h * p.out_head_stride + col0;
-#pragma unroll
-            for (int e = 0; e < kCols / 8; ++e) {
-                if (col0 + e * 8 < p.head_dim && !(MULTI && split && e >= kHalf / 8)) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = pack_pair<F16>(acc[4 * e + k].x * inv, acc[4 * e + k].y * inv);
-                    *reinterpret_cast<uint4*>(dst + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+
+        const int32_t g1 = idle ? u.ga + 1 : u.gb;
+        for (int32_t g = u.ga; g < g1; ++g) {
+            const int32_t ta = g * u.gt, tb = idle ? ta : min(ta + u.gt, u.nt);
+            const int32_t mine0 = ta + (split ? s : 0);
+            const uint32_t column = o_column<DP>(groups, 0);
+            RowState st{-INFINITY, 0.0f, 0.0f};
+            for (int32_t t = mine0; t == mine0 || t < tb; t += split ? 2 : 1) {
+                const bool has = t < tb;
+                if (has) {
+                    if (!warp_wait(&sh.s_full[s], n & 1u, sh)) return;
+                    tmem_fence_after();
+                    if (warp_live && !softmax_tile<DP, F16>(p, sh, u, s, s_addr, tmem + lane_base + column + s * DP, t,
+                                                            t == mine0, n, all, live, mine, words, st))
+                        return;
                 }
+                const bool due = left.any;
+                // a barrier's phase is waited for before the next one can complete
+                if (due && !settle()) return;
+                // where there is one O, this stream's next products may begin when the group before has
+                // been read, unless the other warpgroup reads it too and both say so
+                const bool late = due && !left.split && kSums<DP> == 1;
+                if (has && !late) {
+                    tmem_fence_before();
+                    mbar_arrive(&sh.p_full[s]);
+                }
+                if (due && !finish()) return;
+                if (has && late) {
+                    tmem_fence_before();
+                    mbar_arrive(&sh.p_full[s]);
+                }
+                n += has;
             }
-            if (col0 == 0 && p.lse != nullptr) p.lse[t * p.kv_heads * p.group + h] = final_lse(M, L);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kCols / 4; ++e)
-                if (!(MULTI && split && e >= kHalf / 4))
-                    reinterpret_cast<float4*>(slots)[(col0 / 4 + e) * p.slot_rows + slot_row] =
-                        make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
-            if (col0 == 0) {
-                slots[DP * p.slot_rows + slot_row] = M;
-                slots[(DP + 1) * p.slot_rows + slot_row] = L;
+            if (idle) break;
+            left.any = true;
+            left.split = split;
+            left.both = split && ta + 1 < tb;
+            left.tiles = mine0 < tb;
+            left.live = live;
+            left.warp_live = warp_live;
+            left.whole = u.ga == 0;  // from the first group on: joined here
+            left.last = g + 1 == u.gb;
+            left.complete = u.gb == u.ng;
+            left.run = list.k;
+            left.g = g;
+            left.slot = 1 + g - u.ga;
+            left.t = u.tok0 + i;
+            left.h = u.head * p.group + head;
+            left.mg = st.ref == -INFINITY ? -INFINITY : st.off;
+            left.lg = st.l;
+            if (split) {
+                // the other warpgroup has read what stands there
+                if (joined > 0 && !warp_wait(&sh.o_free[(joined - 1) & 1u], ((joined - 1) >> 1) & 1u, sh)) return;
+                sh.ref[s][row] = left.mg;
+                sh.sum[s][row] = left.lg;
             }
+            ++groups;
+        }
+        if (idle && more) {
+            if (u.nt > 0) groups += u.gb - u.ga;
+            list.give_back(sh, list.k);
         }
     }
 }
@@ -945,9 +1131,10 @@ __host__ __device__ inline size_t attn_shared_bytes(int dp, int stages, int q_ch
            sizeof(Shared);
 }
 
-// MULTI: some request may have more rows than one tile.  Its running sums take twice the
-// registers: the 384 threads launch with 168 each, the softmax warps take 208 and the
-// other four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).
+// MULTI: some request may have more rows than one tile.
+// The 384 threads launch with 168 registers each; the softmax warps take 208 and the other
+// four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).  What does not fit goes to local
+// memory, which has 25 KB of L1 left beside the ring and costs a trip to L2 for most.
 template <int DP, bool F16, bool MULTI>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     tree_attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mq,
@@ -977,7 +1164,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(&sh.pv_done[i], 1);
         }
         mbar_init(&sh.g_done, 2 * kTile);
-        mbar_init(&sh.o_free, 2 * kTile);
+        mbar_init(&sh.o_free[0], 2 * kTile);
+        mbar_init(&sh.o_free[1], 2 * kTile);
+        for (int i = 0; i < kRunRing; ++i) {
+            mbar_init(&sh.run_full[i], 1);
+            mbar_init(&sh.run_empty[i], kRunReaders);
+        }
         mbar_init(&sh.drain, 1);
         fence_barrier_init();
         sh.stop = 0;
@@ -994,7 +1186,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 
     if (warp < 4) {
-        if (MULTI) registers_lower<88>();
+        registers_lower<88>();
         if (warp == 0)
             copy_tiles<DP>(p, sh, ring, &mk, 0);
         else if (warp == 1)
@@ -1004,7 +1196,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         else
             copy_q_clean_v<DP, F16, MULTI>(p, sh, base, ring, &mq);
     } else {
-        if (MULTI) registers_raise<208>();
+        registers_raise<208>();
         softmax_rows<DP, F16, MULTI>(p, sh, tmem, (warp - 4) >> 2);
     }
     tmem_fence_before();
@@ -1157,7 +1349,7 @@ struct AttnLayout {
 
 // Slots of a CTA: one for the first groups of the item its share ends in, and one for each group of
 // the item it begins in.  Those are at most an item's groups, and no more than fit a share (a group
-// costs at least 3 on the line, but for an item's last).
+// costs at least 6 on the line, but for an item's last).
 AttnLayout attn_layout(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t max_kv)
 {
     AttnLayout a{};
@@ -1170,8 +1362,8 @@ AttnLayout attn_layout(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_
     a.slot_floats = static_cast<int64_t>(a.slot_rows) * (dp + 2);
     const int64_t nt = (max_kv + kTile - 1) / kTile;
     const int64_t groups = std::max<int64_t>(1, std::min(std::max<int64_t>(1, std::min(sms, 2 * sms / kv_heads)), (nt + 1) / 2));
-    const int64_t share = R * std::max<int64_t>(1, (tiles + 1) / 2) * kv_heads * (nt + groups + 2) / sms + 1;
-    a.slots_per_cta = static_cast<int32_t>(1 + std::min(groups, share / 3 + 3));
+    const int64_t share = R * std::max<int64_t>(1, (tiles + 1) / 2) * kv_heads * (2 * nt + 2 * groups + 8) / sms + 1;
+    a.slots_per_cta = static_cast<int32_t>(1 + std::min(groups, share / 6 + 3));
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     a.starts = 0;
     a.flags = up(a.starts + static_cast<size_t>(sms + 1) * sizeof(Start));
