@@ -112,10 +112,10 @@ struct Request {
 
 // Groups.  Few and long ones cost least (a group's end is a pass over O and leaves the
 // products idle); many and short ones let a request alone fill the machine.  A group has
-// about the square root of the item's tiles, at least 2 (8 where two row tiles share
-// them: such items are bound by products and exponentials); where that is near, the
-// number that gives a request alone one or two units for every SM; and an even number,
-// so that a tile's stream is its parity.
+// about one and a half times the square root of the item's tiles, at least 2 (16 where
+// two row tiles share them: such items are bound by exponentials and instructions); where
+// that is near, the number that gives a request alone one or two units for every SM; and
+// an even number, so that a tile's stream is its parity.
 __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
 {
     Request q;
@@ -128,10 +128,10 @@ __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
     q.per_head = (q.tiles + 1) / 2;
     const int32_t nt = (q.kv + kTile - 1) / kTile;
     const int32_t wave = max(1, p.sms / max(1, p.kv_heads * q.per_head));
-    const int32_t root = 2 * static_cast<int32_t>(0.5f * sqrtf(static_cast<float>(nt)) + 0.5f);
+    const int32_t root = 2 * static_cast<int32_t>(0.75f * sqrtf(static_cast<float>(nt)));
     const int32_t one = (nt + wave - 1) / wave, two = (nt + 2 * wave - 1) / (2 * wave);
     const int32_t even = 5 * two >= 4 * root ? two : 5 * one >= 4 * root ? one : root;
-    q.gt = (max(q.tiles > 1 ? 8 : 2, even) + 1) & ~1;
+    q.gt = (max(q.tiles > 1 ? 16 : 2, even) + 1) & ~1;
     q.ng = max(1, (nt + q.gt - 1) / q.gt);
     q.cost = 2 * nt + 2 * q.ng + 8;
     return q;
@@ -317,14 +317,15 @@ __device__ __forceinline__ float final_lse(float m, float l)
 }
 
 // ---- shares -------------------------------------------------------------------
-// Locate the unit that starts at or behind `at` on the line, inside request r whose
-// costs begin at `first`.
+// Locate the unit whose start is nearest to `at` on the line, inside request r whose
+// costs begin at `first`.  (The next one behind would give two groups to CTAs whose shares
+// are a little more than one: 138 us for 9 tokens over 131,071 keys.)
 __device__ __forceinline__ Start locate(const AttnParams& p, const Request& q, int32_t r, int64_t first, int64_t at)
 {
     const int64_t off = at - first;
     int32_t item = static_cast<int32_t>(off / q.cost);
     const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(item) * q.cost);
-    int32_t g = (in + 2 * q.gt + 1) / (2 * q.gt + 2);
+    int32_t g = (in + q.gt + 1) / (2 * q.gt + 2);
     if (g >= q.ng) {
         g = 0;
         ++item;
@@ -726,55 +727,34 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const Run& u,
     return bits & below(u.kv_end - x);
 }
 
-// A row's probabilities of a whole tile, P = 2^(c z - m), and their
-// sum.  Sixteen at a time, in three stages that run beside each other: loads of the
-// sixteen after, exponentials of these, rounding, sum and store of those before, so
-// that the special-function unit (a warp's exponential takes it 8 cycles, 1024 for
-// a tile) never waits for a load or a store.  P lies over scores that have been read.
-template <bool F16>
+// A row's probabilities of a whole tile, P = 2^(c z - m), and their sum, W at a time in a
+// loop that is not unrolled.  For 64 x 9 tokens over 4,250 keys it takes 200 us, two steps at
+// a time 206, and 222 unrolled with the next scores loaded ahead: the more code, the slower, as
+// the warps' roles share one instruction cache.  P lies over scores that have been read.
+// Every W gives the same bits.
+template <bool F16, int W>
 __device__ __forceinline__ float exp_tile(uint32_t s_addr, float c, float off)
 {
     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
     float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-    uint32_t za[16], zb[16];
-    float2 xa[8], xb[8];
-    auto take = [&](const uint32_t(&z)[16], float2(&x)[8]) {
+#pragma unroll 1
+    for (int step = 0; step < kTile / W; ++step) {
+        uint32_t z[W], pk[W / 2];
+        tmem_ld(z, s_addr + step * W);
+        tmem_wait_ld(z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, off2);
-            x[e].x = exp2_fast(x[e].x);
-            x[e].y = exp2_fast(x[e].y);
-        }
-    };
-    auto put = [&](const float2(&x)[8], int ch) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < W / 2; ++e) {
+            float2 x = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, off2);
+            x.x = exp2_fast(x.x);
+            x.y = exp2_fast(x.y);
             if (e & 1)
-                s1 = add2(s1, x[e]);
+                s1 = add2(s1, x);
             else
-                s0 = add2(s0, x[e]);
-            pk[e] = pack_pair<F16>(x[e].x, x[e].y);
+                s0 = add2(s0, x);
+            pk[e] = pack_pair<F16>(x.x, x.y);
         }
-        tmem_st8(s_addr + ch * 8, pk);
-    };
-    tmem_ld16(za, s_addr);
-    tmem_wait_ld(za);
-    tmem_ld16(zb, s_addr + 16);
-#pragma unroll
-    for (int ch = 0; ch < 8; ch += 2) {
-        take(za, xa);
-        if (ch > 0) put(xb, ch - 1);
-        tmem_wait_ld(zb);
-        if (ch + 2 < 8) tmem_ld16(za, s_addr + (ch + 2) * 16);
-        take(zb, xb);
-        put(xa, ch);
-        if (ch + 2 < 8) {
-            tmem_wait_ld(za);
-            tmem_ld16(zb, s_addr + (ch + 3) * 16);
-        }
+        tmem_st(s_addr + step * (W / 2), pk);
     }
-    put(xb, 7);
     s0 = add2(s0, s1);
     return s0.x + s0.y;
 }
@@ -786,7 +766,7 @@ struct RowState {
 
 // The softmax of one tile of a stream: scores out, probabilities in their place.
 // Returns false when a wait gave up.
-template <int DP, bool F16>
+template <int DP, bool F16, int W>
 __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, const Run& u, int s, uint32_t s_addr,
                                              uint32_t o_addr, int32_t t, bool first, uint32_t n, int32_t all, bool live,
                                              int32_t mine, const uint32_t* words, RowState& st)
@@ -800,14 +780,14 @@ __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, co
         for (int ch = 0; ch < 8; ++ch) {
             const uint32_t bits = live ? seen_bits(p, u, mine, words, x0 + (ch & ~1) * 16) >> (16 * (ch & 1)) : 0u;
             uint32_t z[16];
-            tmem_ld16(z, s_addr + ch * 16);
+            tmem_ld(z, s_addr + ch * 16);
             tmem_wait_ld(z);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 z[e] = (bits >> e) & 1u ? z[e] : 0xFF800000u;
                 top = fmaxf(top, __uint_as_float(z[e]));
             }
-            tmem_st16(s_addr + ch * 16, z);
+            tmem_st(s_addr + ch * 16, z);
         }
         tmem_wait_st();
     } else {
@@ -832,16 +812,16 @@ __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, co
 #pragma unroll 1
             for (int ch = 0; ch < DP / 16; ++ch) {
                 uint32_t z[16];
-                tmem_ld16(z, o_addr + ch * 16);
+                tmem_ld(z, o_addr + ch * 16);
                 tmem_wait_ld(z);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(__uint_as_float(z[e]) * f);
-                tmem_st16(o_addr + ch * 16, z);
+                tmem_st(o_addr + ch * 16, z);
             }
         }
     }
     st.off = st.ref == -INFINITY ? 0.0f : st.ref * c;
-    st.l += exp_tile<F16>(s_addr, c, st.off);
+    st.l += exp_tile<F16, W>(s_addr, c, st.off);
     tmem_wait_st();
     return true;
 }
@@ -862,7 +842,7 @@ __device__ __noinline__ void add_odd(const AttnParams& p, const Run& u, int32_t 
 #pragma unroll 1
     for (int ch = 0; ch < DP / 16; ++ch) {
         uint32_t z[16];
-        tmem_ld16(z, o_addr + ch * 16);
+        tmem_ld(z, o_addr + ch * 16);
         tmem_wait_ld(z);
 #pragma unroll 1
         for (int32_t x = x0; x < x1; ++x) {
@@ -881,7 +861,7 @@ __device__ __noinline__ void add_odd(const AttnParams& p, const Run& u, int32_t 
             }
         }
         __syncwarp();
-        tmem_st16(o_addr + ch * 16, z);
+        tmem_st(o_addr + ch * 16, z);
     }
     tmem_wait_st();
 }
@@ -903,6 +883,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
 {
     constexpr int kHalf = DP / 2;               // columns of O that a warpgroup joins when the keys are split
     constexpr int kCols = MULTI ? DP : kHalf;   // and at most
+    constexpr int kWide = kCols > 64 ? 8 : 16;  // columns at a time, as registers allow
     const int row = threadIdx.x & (kTile - 1);
     const uint32_t lane_base = static_cast<uint32_t>(row & ~31) << 16;
     const int token = row / p.group, head = row - token * p.group;
@@ -948,16 +929,16 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
             const uint32_t at = tmem + lane_base + o_column<DP>(groups - 1, left.split ? 0 : s) + col0;
             float* const slot = slots + left.slot * p.slot_floats;
 #pragma unroll
-            for (int ch = 0; ch < kCols / 16; ++ch) {
-                if (MULTI && left.split && ch >= kHalf / 16) break;
-                uint32_t z[16], y[16];
-                tmem_ld16(z, at + ch * 16);
-                if (left.both) tmem_ld16(y, at + DP + ch * 16);
+            for (int ch = 0; ch < kCols / kWide; ++ch) {
+                if (MULTI && left.split && ch >= kHalf / kWide) break;
+                uint32_t z[kWide], y[kWide];
+                tmem_ld(z, at + ch * kWide);
+                if (left.both) tmem_ld(y, at + DP + ch * kWide);
                 tmem_wait_ld(z);
                 if (left.both) {
                     tmem_wait_ld(y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < kWide / 2; ++e) {
                         const float2 x = join_sum2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
                                                    make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), in);
                         z[2 * e] = __float_as_uint(x.x);
@@ -966,13 +947,13 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                 }
                 if (left.whole) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[ch * 8 + e] = join_sum2(
-                            acc[ch * 8 + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
+                    for (int e = 0; e < kWide / 2; ++e)
+                        acc[ch * (kWide / 2) + e] = join_sum2(
+                            acc[ch * (kWide / 2) + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
                 } else if (left.live) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        reinterpret_cast<uint4*>(slot)[(col0 / 4 + ch * 4 + e) * p.slot_rows + slot_row] =
+                    for (int e = 0; e < kWide / 4; ++e)
+                        reinterpret_cast<uint4*>(slot)[(col0 / 4 + ch * (kWide / 4) + e) * p.slot_rows + slot_row] =
                             make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
                 }
             }
@@ -1070,7 +1051,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                 if (has) {
                     if (!warp_wait(&sh.s_full[s], n & 1u, sh)) return;
                     tmem_fence_after();
-                    if (warp_live && !softmax_tile<DP, F16>(p, sh, u, s, s_addr, tmem + lane_base + column + s * DP, t,
+                    if (warp_live && !softmax_tile<DP, F16, kWide>(p, sh, u, s, s_addr, tmem + lane_base + column + s * DP, t,
                                                             t == mine0, n, all, live, mine, words, st))
                         return;
                 }

@@ -446,6 +446,60 @@ def test_attention_does_not_depend_on_the_batch(sv):
         assert torch.equal(x["out"], got["out"][rows]) and torch.equal(x["lse"], got["lse"][rows]), rs
 
 
+@pytest.mark.parametrize("D,Hq,Hk", [(128, 8, 2), (64, 28, 4), (72, 6, 6)])
+def test_attention_does_not_depend_on_the_other_requests_rows(sv, D, Hq, Hk):
+    """Next to a request of several row tiles, or with room for one, a request has the bits that it has alone."""
+    rng = np.random.default_rng(D)
+    new = [9, 300, 1, 5, 0, 129]
+    ctx = [4000, 1500, 700, 128, 10, 0]
+    par = [[int(rng.integers(-1, j)) if j else -1 for j in range(n)] for n in new]
+    c = Case(ctx, new, Hq, Hk, D, torch.bfloat16, 16, parents=par, seed=D)
+    got = c.run(sv)
+    c.check(got)
+    words = c.mask.shape[1]
+    for r in (0, 2, 3, 5, 1):
+        t0, t1 = int(c.cu[r]), int(c.cu[r + 1])
+        for most in (new[r], 300):
+            x = sv.tree_attention(c.q[t0:t1], c.kc, c.vc, c.table[r:r + 1], _i32([c.kv[r]]), _i32([0, new[r]]), most,
+                                  mask=_i32(c.mask[t0:t1]).view(-1, words), scale=c.scale, with_lse=True)
+            torch.cuda.synchronize()
+            assert torch.equal(x["out"], got["out"][t0:t1]) and torch.equal(x["lse"], got["lse"][t0:t1]), (r, most)
+
+
+@pytest.mark.parametrize("R", [385, 1500])
+def test_attention_many_short_requests(sv, R):
+    rng = np.random.default_rng(R)
+    new = rng.integers(0, 4, R)
+    ctx = rng.integers(0, 40, R)
+    c = Case(ctx.tolist(), new.tolist(), 4, 2, 64, torch.bfloat16, 16, seed=R)
+    c.check(c.run(sv))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
+def test_attention_scales(sv, scale):
+    c = Case([300, 5, 1000], [9, 3, 70], 8, 2, 64, torch.float16, 16, seed=31)
+    c.scale = scale
+    c.check(c.run(sv))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_scores_that_are_not_finite(sv, bad):
+    """A visible key whose score is NaN or +inf makes the whole row and its lse NaN; the rows before it stay."""
+    for ctx, n, at in ((0, 1, 0), (0, 9, 4), (300, 9, 304), (2000, 9, 2004)):
+        clean = Case([ctx, 40], [n, n], 4, 2, 64, seed=33)
+        clean.q = clean.q.abs() + 0.5  # with a key of +inf the score is +inf
+        want = clean.run(sv)
+        c = Case([ctx, 40], [n, n], 4, 2, 64, seed=33)
+        c.q = clean.q
+        c.kc[int(c.table[0, at // c.bs]), at % c.bs, 1, 5] = bad
+        got = c.run(sv)
+        j = max(0, at - ctx)  # from this token on
+        assert torch.isnan(got["out"][j:n, 2:].float()).all() and torch.isnan(got["lse"][j:n, 2:]).all(), (ctx, n)
+        for name in ("out", "lse"):
+            assert torch.equal(got[name][:j], want[name][:j]) and torch.equal(got[name][n:], want[name][n:])
+            assert torch.equal(got[name][:n, :2], want[name][:n, :2])
+
+
 def test_attention_bounds_of_tokens_and_masks(sv):
     """Tokens beyond max_tokens are left alone; bits beyond the mask's words count as 0."""
     par = branch_parents(1, 49)
