@@ -881,9 +881,8 @@ struct Left {
 template <int DP, bool F16, bool MULTI>
 __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int s)
 {
-    constexpr int kHalf = DP / 2;               // columns of O that a warpgroup joins when the keys are split
-    constexpr int kCols = MULTI ? DP : kHalf;   // and at most
-    constexpr int kWide = kCols > 64 ? 8 : 16;  // columns at a time, as registers allow
+    constexpr int kHalf = DP / 2;            // columns of O that a warpgroup joins when the keys are split
+    constexpr int kStep = MULTI ? 32 : 16;   // columns at a time
     const int row = threadIdx.x & (kTile - 1);
     const uint32_t lane_base = static_cast<uint32_t>(row & ~31) << 16;
     const int token = row / p.group, head = row - token * p.group;
@@ -892,7 +891,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
     const uint32_t s_addr = tmem + lane_base + s * kTile;
     float* const slots = p.slots + static_cast<int64_t>(blockIdx.x) * p.slots_per_cta * p.slot_floats;
     float M = -INFINITY, L = 0.0f;
-    float2 acc[kCols / 2];
+    float2 acc[MULTI ? 1 : kHalf / 2];  // the run's sums, unless they stand in slot 0
     Left left{};
 
     // `n` and `groups` are those behind the group that is left: it is settled before they move on.
@@ -923,46 +922,89 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
             lg = join_sum(sh.sum[0][row], sh.sum[1][row], in);
             mg = in.m;
         }
-        if (left.warp_live) {
-            const Join j = join_at(M, mg);
-            const int col0 = left.split ? s * kHalf : 0, slot_row = left.split ? row : s * kTile + row;
-            const uint32_t at = tmem + lane_base + o_column<DP>(groups - 1, left.split ? 0 : s) + col0;
-            float* const slot = slots + left.slot * p.slot_floats;
+        const int col0 = left.split ? s * kHalf : 0;
+        const int slot_row = MULTI || !left.split ? s * kTile + row : row;
+        const uint32_t at = tmem + lane_base + o_column<DP>(groups - 1, left.split ? 0 : s) + col0;
+        const bool write = left.last && left.whole && left.complete && left.live;
+        uint16_t* const out = p.out + left.t * p.out_token_stride + left.h * p.out_head_stride + col0;
+        Join j{M, 1.0f, 0.0f};
+        if (left.whole) {
+            j = join_at(M, mg);
+            L = join_sum(L, lg, j);
+            M = j.m;
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        // the group's kStep columns from `ch` on
+        auto load = [&](float2 (&x)[kStep / 2], int ch) {
+            uint32_t z[kStep], y[kStep];
+            tmem_ld(z, at + ch);
+            if (left.both) tmem_ld(y, at + DP + ch);
+            tmem_wait_ld(z);
 #pragma unroll
-            for (int ch = 0; ch < kCols / kWide; ++ch) {
-                if (MULTI && left.split && ch >= kHalf / kWide) break;
-                uint32_t z[kWide], y[kWide];
-                tmem_ld(z, at + ch * kWide);
-                if (left.both) tmem_ld(y, at + DP + ch * kWide);
-                tmem_wait_ld(z);
-                if (left.both) {
-                    tmem_wait_ld(y);
+            for (int e = 0; e < kStep / 2; ++e) x[e] = make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1]));
+            if (left.both) {
+                tmem_wait_ld(y);
 #pragma unroll
-                    for (int e = 0; e < kWide / 2; ++e) {
-                        const float2 x = join_sum2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
-                                                   make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), in);
-                        z[2 * e] = __float_as_uint(x.x);
-                        z[2 * e + 1] = __float_as_uint(x.y);
-                    }
-                }
+                for (int e = 0; e < kStep / 2; ++e)
+                    x[e] = join_sum2(x[e], make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), in);
+            }
+        };
+        auto store = [&](float4* to, const float2* x) {
+#pragma unroll
+            for (int e = 0; e < kStep / 4; ++e) to[e * p.slot_rows] = make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y);
+        };
+        auto put = [&](int ch, const float2* x) {
+#pragma unroll
+            for (int e = 0; e < kStep / 8; ++e) {
+                if (col0 + ch + e * 8 >= p.head_dim) break;
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = pack_pair<F16>(x[4 * e + k].x * inv, x[4 * e + k].y * inv);
+                *reinterpret_cast<uint4*>(out + ch + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        };
+        if (MULTI && left.warp_live) {
+            // A row's sums would fill 128 registers: they stand in slot 0, for this thread alone, and
+            // the next columns are fetched while these are joined.
+            float4* const sums = reinterpret_cast<float4*>(slots + (left.whole ? 0 : left.slot * p.slot_floats)) + slot_row;
+            const bool join = left.whole && left.g > 0 && left.live;
+            const int cols = left.split ? kHalf : DP;
+            float4 ahead[kStep / 4];
+            auto fetch = [&](int ch) {
+#pragma unroll
+                for (int e = 0; e < kStep / 4; ++e) ahead[e] = sums[(ch / 4 + e) * p.slot_rows];
+            };
+            if (join) fetch(0);
+#pragma unroll 1
+            for (int ch = 0; ch < cols; ch += kStep) {
+                float2 x[kStep / 2];
+                load(x, ch);
                 if (left.whole) {
 #pragma unroll
-                    for (int e = 0; e < kWide / 2; ++e)
-                        acc[ch * (kWide / 2) + e] = join_sum2(
-                            acc[ch * (kWide / 2) + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), j);
-                } else if (left.live) {
-#pragma unroll
-                    for (int e = 0; e < kWide / 4; ++e)
-                        reinterpret_cast<uint4*>(slot)[(col0 / 4 + ch * (kWide / 4) + e) * p.slot_rows + slot_row] =
-                            make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+                    for (int e = 0; e < kStep / 4; ++e) {
+                        const float4 a = join ? ahead[e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        x[2 * e] = join_sum2(make_float2(a.x, a.y), x[2 * e], j);
+                        x[2 * e + 1] = join_sum2(make_float2(a.z, a.w), x[2 * e + 1], j);
+                    }
+                    if (join && ch + kStep < cols) fetch(ch + kStep);
                 }
+                if (write)
+                    put(ch, x);
+                else if (left.live)
+                    store(sums + ch / 4 * p.slot_rows, x);
             }
-            if (left.whole) {
-                L = join_sum(L, lg, j);
-                M = j.m;
-            } else if (left.live && col0 == 0) {
-                slot[DP * p.slot_rows + slot_row] = mg;
-                slot[(DP + 1) * p.slot_rows + slot_row] = lg;
+        }
+        if (!MULTI && left.warp_live) {
+#pragma unroll
+            for (int ch = 0; ch < kHalf; ch += kStep) {
+                float2 x[kStep / 2];
+                load(x, ch);
+                if (left.whole) {
+#pragma unroll
+                    for (int e = 0; e < kStep / 2; ++e) acc[ch / 2 + e] = join_sum2(acc[ch / 2 + e], x[e], j);
+                } else if (left.live) {
+                    store(reinterpret_cast<float4*>(slots + left.slot * p.slot_floats) + (col0 + ch) / 4 * p.slot_rows + slot_row, x);
+                }
             }
         }
         if (left.split) {
@@ -970,45 +1012,37 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
             mbar_arrive(&sh.o_free[joined & 1u]);
             ++joined;
         }
-        if (left.last && left.whole) {
-            const int col0 = left.split ? s * kHalf : 0, slot_row = left.split ? row : s * kTile + row;
-            if (left.live && left.complete) {
-                uint16_t* const out = p.out + left.t * p.out_token_stride + left.h * p.out_head_stride + col0;
-                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        if (left.live && !write && (!left.whole || left.last)) {  // joined elsewhere
+            float* const slot = slots + (left.whole ? 0 : left.slot * p.slot_floats);
+            if (!MULTI && left.whole) {
 #pragma unroll
-                for (int e = 0; e < kCols / 8; ++e) {
-                    if (col0 + e * 8 < p.head_dim && !(MULTI && left.split && e >= kHalf / 8)) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) o[k] = pack_pair<F16>(acc[4 * e + k].x * inv, acc[4 * e + k].y * inv);
-                        *reinterpret_cast<uint4*>(out + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                }
-                if (col0 == 0 && p.lse != nullptr)
-                    p.lse[static_cast<int64_t>(left.t) * p.kv_heads * p.group + left.h] = final_lse(M, L);
-            } else if (left.live) {
-#pragma unroll
-                for (int e = 0; e < kCols / 4; ++e)
-                    if (!(MULTI && left.split && e >= kHalf / 4))
-                        reinterpret_cast<float4*>(slots)[(col0 / 4 + e) * p.slot_rows + slot_row] =
-                            make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
-                if (col0 == 0) {
-                    slots[DP * p.slot_rows + slot_row] = M;
-                    slots[(DP + 1) * p.slot_rows + slot_row] = L;
-                }
+                for (int ch = 0; ch < kHalf; ch += kStep)
+                    store(reinterpret_cast<float4*>(slot) + (col0 + ch) / 4 * p.slot_rows + slot_row, acc + ch / 2);
             }
+            if (col0 == 0) {
+                slot[DP * p.slot_rows + slot_row] = left.whole ? M : mg;
+                slot[(DP + 1) * p.slot_rows + slot_row] = left.whole ? L : lg;
+            }
+        }
+        if (write) {
+            if (!MULTI) {
+#pragma unroll
+                for (int ch = 0; ch < kHalf; ch += kStep) put(ch, acc + ch / 2);
+            }
+            if (col0 == 0 && p.lse != nullptr)
+                p.lse[static_cast<int64_t>(left.t) * p.kv_heads * p.group + left.h] = final_lse(M, L);
         }
         if (left.last) {  // the next run starts from nothing
             list.give_back(sh, left.run);
             M = -INFINITY;
             L = 0.0f;
 #pragma unroll
-            for (int e = 0; e < kCols / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
+            for (int e = 0; e < (MULTI ? 0 : kHalf / 2); ++e) acc[e] = make_float2(0.0f, 0.0f);
         }
         return true;
     };
 #pragma unroll
-    for (int e = 0; e < kCols / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
+    for (int e = 0; e < (MULTI ? 0 : kHalf / 2); ++e) acc[e] = make_float2(0.0f, 0.0f);
 
     // Every turn of the inner loop has at most one tile of this stream and what is left of the group
     // before; turns without a tile (no second row tile, a group's only tile is the other stream's, no
@@ -1051,7 +1085,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                 if (has) {
                     if (!warp_wait(&sh.s_full[s], n & 1u, sh)) return;
                     tmem_fence_after();
-                    if (warp_live && !softmax_tile<DP, F16, kWide>(p, sh, u, s, s_addr, tmem + lane_base + column + s * DP, t,
+                    if (warp_live && !softmax_tile<DP, F16, kStep>(p, sh, u, s, s_addr, tmem + lane_base + column + s * DP, t,
                                                             t == mine0, n, all, live, mine, words, st))
                         return;
                 }
@@ -1224,7 +1258,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int32_t token = row / p.group, i = tile * p.tile_tokens + token;
     if (row >= p.tile_tokens * p.group || i >= q.na) return;
 
-    const int64_t at_o = (static_cast<int64_t>(c4) * p.slot_rows + slot_row) * 4;
+    // where the streams split the keys next to two row tiles' room, the second half of the columns
+    // stands in the second tile's rows
+    const bool beside = p.slot_rows > kTile && q.tiles == 1 && c4 >= DP / 8;
+    const int64_t at_o = (static_cast<int64_t>(beside ? c4 - DP / 8 : c4) * p.slot_rows + slot_row + (beside ? kTile : 0)) * 4;
     const int64_t at_m = static_cast<int64_t>(DP) * p.slot_rows + slot_row, at_l = at_m + p.slot_rows;
     const float* x = p.slots + static_cast<int64_t>(c) * p.slots_per_cta * p.slot_floats;
     float4 acc = *reinterpret_cast<const float4*>(x + at_o);
