@@ -1222,12 +1222,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ---- groups that were cut across CTAs -----------------------------------------------------------
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kAhead = 4, kJoinBlocks = 8;
 
 // blockIdx.x = c: the item that is cut where CTA c's share ends, if its first group lies in that
-// share; blockIdx.y: 256 of its (row, four columns).  Groups are joined as softmax_rows does.
+// share; blockIdx.y: a part of its (row, eight columns).  Groups are joined as softmax_rows does.
+// Its time is that of a few dependent loads: eight blocks at most for an item, three on an SM,
+// each thread with eight columns (four columns and a block for every 256 of them: 30 us behind
+// the attention of 64 x 65 tokens instead of 13).
 template <int DP, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p, int32_t ctas)
+__global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid_constant__ AttnParams p, int32_t ctas)
 {
     pdl_wait_primary();
     if (p.status != nullptr && blockIdx.y == 0) {
@@ -1251,66 +1254,72 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int32_t ng = max(1, (nt + q.gt - 1) / q.gt);
     if (e.g >= ng) return;  // its groups all lie in CTA c's share
 
-    const int32_t index = blockIdx.y * kJoinThreads + threadIdx.x;
-    const int32_t slot_row = index % p.slot_rows, c4 = index / p.slot_rows;
-    if (c4 * 4 >= p.head_dim) return;
-    const int32_t tile = tile0 + slot_row / kTile, row = slot_row % kTile;
-    const int32_t token = row / p.group, i = tile * p.tile_tokens + token;
-    if (row >= p.tile_tokens * p.group || i >= q.na) return;
+    const int64_t at_m0 = static_cast<int64_t>(DP) * p.slot_rows;
+    for (int32_t index = blockIdx.y * kJoinThreads + threadIdx.x; index < p.slot_rows * (DP / 8); index += gridDim.y * kJoinThreads) {
+        const int32_t slot_row = index % p.slot_rows, c8 = index / p.slot_rows;
+        const int32_t tile = tile0 + slot_row / kTile, row = slot_row % kTile;
+        const int32_t token = row / p.group, i = tile * p.tile_tokens + token;
+        if (c8 * 8 >= p.head_dim || row >= p.tile_tokens * p.group || i >= q.na) continue;
 
-    // where the streams split the keys next to two row tiles' room, the second half of the columns
-    // stands in the second tile's rows
-    const bool beside = p.slot_rows > kTile && q.tiles == 1 && c4 >= DP / 8;
-    const int64_t at_o = (static_cast<int64_t>(beside ? c4 - DP / 8 : c4) * p.slot_rows + slot_row + (beside ? kTile : 0)) * 4;
-    const int64_t at_m = static_cast<int64_t>(DP) * p.slot_rows + slot_row, at_l = at_m + p.slot_rows;
-    const float* x = p.slots + static_cast<int64_t>(c) * p.slots_per_cta * p.slot_floats;
-    float4 acc = *reinterpret_cast<const float4*>(x + at_o);
-    float M = x[at_m], L = x[at_l];
-    // the other groups, eight loaded before the first of them is joined
-    int32_t g = e.g, o = c, gb = e.g;
-    while (g < ng) {
-        constexpr int kAhead = 8;
-        float4 y[kAhead];
-        float mg[kAhead], lg[kAhead];
-        int32_t n = 0;
+        // where the streams split the keys next to two row tiles' room, the second half of the
+        // columns stands in the second tile's rows
+        const bool beside = p.slot_rows > kTile && q.tiles == 1 && c8 >= DP / 16;
+        const int64_t at_o = (static_cast<int64_t>(beside ? c8 - DP / 16 : c8) * 2 * p.slot_rows + slot_row + (beside ? kTile : 0)) * 4;
+        const int64_t at_p = at_o + p.slot_rows * 4, at_m = at_m0 + slot_row, at_l = at_m + p.slot_rows;
+        const float* x = p.slots + static_cast<int64_t>(c) * p.slots_per_cta * p.slot_floats;
+        float4 sum[2] = {*reinterpret_cast<const float4*>(x + at_o), *reinterpret_cast<const float4*>(x + at_p)};
+        float M = x[at_m], L = x[at_l];
+        // the other groups, kAhead loaded before the first of them is joined
+        int32_t g = e.g, o = c, gb = e.g;
+        while (g < ng) {
+            float4 y[kAhead][2];
+            float mg[kAhead], lg[kAhead];
+            int32_t n = 0;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            while (g + n < ng && g + n >= gb) {  // the CTA that has the next group
-                ++o;
-                const Start f = s_starts[o + 1];
-                gb = f.r == e.r && f.item == e.item ? min(ng, f.g) : ng;
-                x = p.slots + (static_cast<int64_t>(o) * p.slots_per_cta + 1) * p.slot_floats;
+            for (int k = 0; k < kAhead; ++k) {
+                while (g + n < ng && g + n >= gb) {  // the CTA that has the next group
+                    ++o;
+                    const Start f = s_starts[o + 1];
+                    gb = f.r == e.r && f.item == e.item ? min(ng, f.g) : ng;
+                    x = p.slots + (static_cast<int64_t>(o) * p.slots_per_cta + 1) * p.slot_floats;
+                }
+                if (g + n < ng) {
+                    y[k][0] = *reinterpret_cast<const float4*>(x + at_o);
+                    y[k][1] = *reinterpret_cast<const float4*>(x + at_p);
+                    mg[k] = x[at_m];
+                    lg[k] = x[at_l];
+                    x += p.slot_floats;
+                    ++n;
+                }
             }
-            if (g + n < ng) {
-                y[k] = *reinterpret_cast<const float4*>(x + at_o);
-                mg[k] = x[at_m];
-                lg[k] = x[at_l];
-                x += p.slot_floats;
-                ++n;
-            }
-        }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (k < n) {
-                const Join j = join_at(M, mg[k]);
-                acc.x = join_sum(acc.x, y[k].x, j);
-                acc.y = join_sum(acc.y, y[k].y, j);
-                acc.z = join_sum(acc.z, y[k].z, j);
-                acc.w = join_sum(acc.w, y[k].w, j);
-                L = join_sum(L, lg[k], j);
-                M = j.m;
+            for (int k = 0; k < kAhead; ++k) {
+                if (k < n) {
+                    const Join j = join_at(M, mg[k]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        sum[h].x = join_sum(sum[h].x, y[k][h].x, j);
+                        sum[h].y = join_sum(sum[h].y, y[k][h].y, j);
+                        sum[h].z = join_sum(sum[h].z, y[k][h].z, j);
+                        sum[h].w = join_sum(sum[h].w, y[k][h].w, j);
+                    }
+                    L = join_sum(L, lg[k], j);
+                    M = j.m;
+                }
             }
+            g += n;
         }
-        g += n;
+        const int64_t t = q.tok0 + i;
+        const int32_t h = head * p.group + (row - token * p.group);
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        uint4 v;
+        v.x = pack_pair<F16>(sum[0].x * inv, sum[0].y * inv);
+        v.y = pack_pair<F16>(sum[0].z * inv, sum[0].w * inv);
+        v.z = pack_pair<F16>(sum[1].x * inv, sum[1].y * inv);
+        v.w = pack_pair<F16>(sum[1].z * inv, sum[1].w * inv);
+        *reinterpret_cast<uint4*>(p.out + t * p.out_token_stride + h * p.out_head_stride + c8 * 8) = v;
+        if (c8 == 0 && p.lse != nullptr) p.lse[t * p.kv_heads * p.group + h] = final_lse(M, L);
     }
-    const int64_t t = q.tok0 + i;
-    const int32_t h = head * p.group + (row - token * p.group);
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint2 v;
-    v.x = pack_pair<F16>(acc.x * inv, acc.y * inv);
-    v.y = pack_pair<F16>(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + t * p.out_token_stride + h * p.out_head_stride + c4 * 4) = v;
-    if (c4 == 0 && p.lse != nullptr) p.lse[t * p.kv_heads * p.group + h] = final_lse(M, L);
 }
 
 // ---- host ------------------------------------------------------------------------------------------
@@ -1410,7 +1419,7 @@ cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& mq, const CUtens
     kern<<<ctas, kAttnThreads, bytes, stream>>>(p, mq, mk, mv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, (p.slot_rows * (DP / 4) + kJoinThreads - 1) / kJoinThreads);
+    cfg.gridDim = dim3(ctas, std::min(kJoinBlocks, (p.slot_rows * (DP / 8) + kJoinThreads - 1) / kJoinThreads));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(ctas + 1) * sizeof(Start);
     cfg.stream = stream;
