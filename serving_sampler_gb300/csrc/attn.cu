@@ -12,10 +12,11 @@
 //               a stage);
 //   warp 1      issues the products; S in tensor memory, P over S in tensor memory as
 //               the left operand of P V, O in tensor memory;
-//   warp 3      lists the CTA's runs of work for the others, copies Q, and cleans V where a tile holds positions that not every row
-//               sees: rows behind the last key become 0 (P is 0 there, but 0 * NaN is
-//               not), and so do NaN and infinite entries, which are noted and added in
-//               32 bits at the end of the group to the rows that do see them;
+//   warp 3      lists the CTA's runs of work for the others, copies Q, and cleans V where a
+//               tile holds positions that not every row sees: rows behind the last key
+//               become 0 (P is 0 there, but 0 * NaN is not), and so do NaN and infinite
+//               entries, which are noted and added in 32 bits at the end of the group to
+//               the rows that do see them;
 //   warps 4-7, 8-11   two streams of softmax, one row per thread; each stream has an S and
 //               an O of its own, so that while one's softmax runs the other's products do.
 //
@@ -30,14 +31,27 @@
 // only when it is more than 2^8 above (O is then rescaled), which no 32-bit sum
 // notices.  (O, l, m) and (O', l', m') are joined at max(m, m'): the streams of a
 // group, then the groups from the first to the last.  A CTA that has an item from its
-// first group on joins in registers; other groups go to the workspace and
+// first group on joins as it goes; other groups go to the workspace and
 // attn_join_kernel joins them in the same order with the same instructions, so the bits
-// do not depend on where the work was cut.
+// do not depend on where the work was cut.  The sums so far stand in registers, half a
+// row in a thread; with several row tiles a thread has a whole row, whose 128 registers
+// left the softmax too few (292 us for 64 x 65 tokens, with spills), so they stand in
+// the workspace, which L2 holds, where the thread alone reads and writes them (221 us).
 //
 // Work.  An item is (request, key head, row tile or pair of them), a unit one group of
 // an item.  All units lie on one line, in cost of two per tile, two per group and eight
 // per item, cut evenly over the CTAs; every CTA finds its share itself from the lengths
 // on the device.
+//
+// What bounds it (bf16, heads of 128, GB300):
+//   64 x 9 tokens, 4 heads to a key head, 4,250 keys on average: bytes.  199 us for the
+//   1.2 GB of K and V, 6.0 TB/s, 0.89 of a copy's rate;
+//   64 x 65 tokens, 7 heads to a key head, 2,500 keys: the chain of a row tile, product,
+//   softmax, product, of which two alternate, as tensor memory has room for two S and two
+//   O.  190 us, 0.40 of the rate of a plain matrix product; the exponentials alone would
+//   take 74 us;
+//   9 tokens over 131,071 keys: bytes, 88 us, 6.1 TB/s, and 10 us for the join;
+//   one token, 1,000 keys: latency, two launches and a chain of loads, 12 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -99,7 +113,9 @@ struct AttnParams {
     int32_t* status;
     Start* starts;    // [CTAs + 1]
     uint32_t* flags;  // [CTAs]
-    float* slots;     // [CTAs][slots_per_cta]: O as [DP / 4][rows][4], then m [rows], l [rows]
+    // [CTAs][slots_per_cta]: O as [DP / 4][rows][4], then m [rows], l [rows].  Slot 0: what the CTA's
+    // last item has, and, with several row tiles, the sums of the run at hand
+    float* slots;
     int64_t slot_floats;
     int32_t slots_per_cta, slot_rows;
 };
@@ -112,8 +128,9 @@ struct Request {
 
 // Groups.  Few and long ones cost least (a group's end is a pass over O and leaves the
 // products idle); many and short ones let a request alone fill the machine.  A group has
-// about one and a half times the square root of the item's tiles, at least 2 (16 where
-// two row tiles share them: such items are bound by exponentials and instructions); where
+// about one and a half times the square root of the item's tiles, at least 2 (8 where two
+// row tiles share them: with 16, 64 x 65 tokens over 2,500 keys take 201 us instead of 218,
+// but 4 x 65 take 49 instead of 37 and a request alone 46 instead of 33); where
 // that is near, the number that gives a request alone one or two units for every SM; and
 // an even number, so that a tile's stream is its parity.
 __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
@@ -131,7 +148,7 @@ __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
     const int32_t root = 2 * static_cast<int32_t>(0.75f * sqrtf(static_cast<float>(nt)));
     const int32_t one = (nt + wave - 1) / wave, two = (nt + 2 * wave - 1) / (2 * wave);
     const int32_t even = 5 * two >= 4 * root ? two : 5 * one >= 4 * root ? one : root;
-    q.gt = (max(q.tiles > 1 ? 16 : 2, even) + 1) & ~1;
+    q.gt = (max(q.tiles > 1 ? 8 : 2, even) + 1) & ~1;
     q.ng = max(1, (nt + q.gt - 1) / q.gt);
     q.cost = 2 * nt + 2 * q.ng + 8;
     return q;
@@ -911,7 +928,8 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
         return true;
     };
     // Joins it and, behind a run's last group, writes what the run has.
-    auto finish = [&]() {
+    // With `open` the products that wait for O to have been read may then begin.
+    auto finish = [&](bool open) {
         left.any = false;
         Join in{0.0f, 1.0f, 0.0f};  // of the group's streams
         float mg = left.mg, lg = left.lg;
@@ -979,6 +997,10 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
             for (int ch = 0; ch < cols; ch += kStep) {
                 float2 x[kStep / 2];
                 load(x, ch);
+                if (open && ch + kStep >= cols) {
+                    tmem_fence_before();
+                    mbar_arrive(&sh.p_full[s]);
+                }
                 if (left.whole) {
 #pragma unroll
                     for (int e = 0; e < kStep / 4; ++e) {
@@ -993,6 +1015,10 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                 else if (left.live)
                     store(sums + ch / 4 * p.slot_rows, x);
             }
+        }
+        if (MULTI && open && !left.warp_live) {
+            tmem_fence_before();
+            mbar_arrive(&sh.p_full[s]);
         }
         if (!MULTI && left.warp_live) {
 #pragma unroll
@@ -1099,11 +1125,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                     tmem_fence_before();
                     mbar_arrive(&sh.p_full[s]);
                 }
-                if (due && !finish()) return;
-                if (has && late) {
-                    tmem_fence_before();
-                    mbar_arrive(&sh.p_full[s]);
-                }
+                if (due && !finish(MULTI && has && late)) return;
                 n += has;
             }
             if (idle) break;
