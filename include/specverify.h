@@ -535,7 +535,8 @@ int sv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, 
  *   status      int32 [R] out or NULL (SV_ST_TIMEOUT).
  * out = sum_x softmax_x(scale q . k_x) v_x.  Where a token sees nothing, out is
  * 0 and lse -inf.  Keys and values at positions that a token does not see have
- * no influence on it, whatever they hold.  Scores and sums are fp32; the
+ * no influence on it, whatever they hold; a score of NaN or +inf at one that it
+ * sees makes its row and lse NaN.  Scores and sums are fp32; the
  * probabilities are rounded to the cache's type for the product with V.
  * A block id outside [0, num_blocks) reads as keys and values of 0.
  * kv_len is clamped to [0, max_blocks * block_size], cu_tokens to [0, T].
@@ -568,7 +569,7 @@ int sv_tree_attention(sv_heads q, sv_kv_cache cache, const int32_t* block_table,
  * K and V of accepted draft i move to position seq_len + 1 + i.  An accepted
  * token that is not one of the request's, or a path that does not increase,
  * ends the accepted path before it (SV_ST_BAD_TREE).  The outputs must not
- * overlap the inputs.
+ * overlap the inputs.  layers * kv_heads * head_dim / 4 is at most 65535 * 128.
  * ---------------------------------------------------------------------- */
 int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len,
                     const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, const int32_t* accept_len,
