@@ -403,7 +403,7 @@ __device__ void find_share(const AttnParams& p, Shared& sh)
 // ---- warps 0 and 2: K and V --------------------------------------------------------
 // Tile t of the line fills stages 2 t (K) and 2 t + 1 (V) of the ring; warp 0 copies K
 // and warp 2 V (one warp for both could not issue the copies of 16-token blocks fast
-// enough).  One lane issues, block by block; lane i holds block and place of box i.
+// enough).  Lane i copies box i.
 template <int DP>
 __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring, const CUtensorMap* map, int first)
 {
@@ -444,13 +444,11 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
             }
             unsigned char* dst = ring + static_cast<size_t>(rt.stage) * kStage;
             if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(live) * box_bytes * kChunks);
-            for (int sub = 0; sub < live; ++sub) {
-                const int32_t blk = __shfl_sync(0xFFFFFFFFu, block, sub), pl = __shfl_sync(0xFFFFFFFFu, place, sub);
-                if (elect_one()) {
+            __syncwarp();
+            if (lane < live) {
 #pragma unroll
-                    for (int ch = 0; ch < kChunks; ++ch)
-                        tma_load_4d(dst + sub * box_bytes + ch * kTile * 128, map, full, ch * 64, pl, u.head, blk);
-                }
+                for (int ch = 0; ch < kChunks; ++ch)
+                    tma_load_4d(dst + lane * box_bytes + ch * kTile * 128, map, full, ch * 64, place, u.head, block);
             }
             __syncwarp();
             fills = min(fills + 1, 1 << 20);
@@ -744,23 +742,25 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, const Run& u,
     return bits & below(u.kv_end - x);
 }
 
-// A row's probabilities of a whole tile, P = 2^(c z - m), and their sum, W at a time in a
-// loop that is not unrolled.  For 64 x 9 tokens over 4,250 keys it takes 200 us, two steps at
-// a time 206, and 222 unrolled with the next scores loaded ahead: the more code, the slower, as
-// the warps' roles share one instruction cache.  P lies over scores that have been read.
-// Every W gives the same bits.
-template <bool F16, int W>
+// A row's probabilities of a whole tile, P = 2^(c z - m), and their sum, in a loop that is
+// not unrolled.  For 64 x 9 tokens over 4,250 keys the loop took 200 us, two steps at a time
+// 206, and 222 unrolled with the next scores loaded ahead: the more code, the slower, as the
+// warps' roles share one instruction cache.  32 columns a step instead of 16 gave 52 -> 50 us
+// for 17 x 33 tokens, loading the next ones ahead in the loop nothing more.  P lies over
+// scores that have been read.
+template <bool F16>
 __device__ __forceinline__ float exp_tile(uint32_t s_addr, float c, float off)
 {
     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
+    constexpr int kWide = 32;
     float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
 #pragma unroll 1
-    for (int step = 0; step < kTile / W; ++step) {
-        uint32_t z[W], pk[W / 2];
-        tmem_ld(z, s_addr + step * W);
+    for (int step = 0; step < kTile / kWide; ++step) {
+        uint32_t z[kWide], pk[kWide / 2];
+        tmem_ld(z, s_addr + step * kWide);
         tmem_wait_ld(z);
 #pragma unroll
-        for (int e = 0; e < W / 2; ++e) {
+        for (int e = 0; e < kWide / 2; ++e) {
             float2 x = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), c2, off2);
             x.x = exp2_fast(x.x);
             x.y = exp2_fast(x.y);
@@ -770,7 +770,7 @@ __device__ __forceinline__ float exp_tile(uint32_t s_addr, float c, float off)
                 s0 = add2(s0, x);
             pk[e] = pack_pair<F16>(x.x, x.y);
         }
-        tmem_st(s_addr + step * (W / 2), pk);
+        tmem_st(s_addr + step * (kWide / 2), pk);
     }
     s0 = add2(s0, s1);
     return s0.x + s0.y;
@@ -783,7 +783,7 @@ struct RowState {
 
 // The softmax of one tile of a stream: scores out, probabilities in their place.
 // Returns false when a wait gave up.
-template <int DP, bool F16, int W>
+template <int DP, bool F16>
 __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, const Run& u, int s, uint32_t s_addr,
                                              uint32_t o_addr, int32_t t, bool first, uint32_t n, int32_t all, bool live,
                                              int32_t mine, const uint32_t* words, RowState& st)
@@ -809,7 +809,7 @@ __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, co
         tmem_wait_st();
     } else {
 #pragma unroll 1
-        for (int col = 0; col < kTile; col += 32) top = fmaxf(top, tmem_max32(s_addr + col));
+        for (int col = 0; col < kTile; col += 64) top = fmaxf(top, tmem_max64(s_addr + col));
     }
     if (first) {
         st.ref = top;
@@ -838,7 +838,7 @@ __device__ __forceinline__ bool softmax_tile(const AttnParams& p, Shared& sh, co
         }
     }
     st.off = st.ref == -INFINITY ? 0.0f : st.ref * c;
-    st.l += exp_tile<F16, W>(s_addr, c, st.off);
+    st.l += exp_tile<F16>(s_addr, c, st.off);
     tmem_wait_st();
     return true;
 }
@@ -1111,7 +1111,7 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                 if (has) {
                     if (!warp_wait(&sh.s_full[s], n & 1u, sh)) return;
                     tmem_fence_after();
-                    if (warp_live && !softmax_tile<DP, F16, kStep>(p, sh, u, s, s_addr, tmem + lane_base + column + s * DP, t,
+                    if (warp_live && !softmax_tile<DP, F16>(p, sh, u, s, s_addr, tmem + lane_base + column + s * DP, t,
                                                             t == mine0, n, all, live, mine, words, st))
                         return;
                 }

@@ -126,21 +126,21 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32])
                  :
                  : "memory");
 }
-// the maximum of 32 columns of the thread's lane as fp32 (NaN is passed over)
-__device__ __forceinline__ float tmem_max32(uint32_t addr)
+// the maximum of 64 columns of the thread's lane as fp32 (NaN is passed over)
+__device__ __forceinline__ float tmem_max64(uint32_t addr)
 {
-    uint32_t m;  // the loaded columns are not needed here
+    uint32_t m, n;  // the loaded columns are not needed here
     asm volatile(
         "{\n"
-        ".reg .b32 r<32>;\n"
-        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
-        "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15, r16, r17, r18, r19, r20, r21, r22, r23, r24, r25, r26, r27, r28, r29, r30, r31}, %0, [%1];\n"
+        ".reg .b32 r<32>, q<32>;\n"
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15, r16, r17, r18, r19, r20, r21, r22, r23, r24, r25, r26, r27, r28, r29, r30, r31}, %0, [%2];\n"
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {q0, q1, q2, q3, q4, q5, q6, q7, q8, q9, q10, q11, q12, q13, q14, q15, q16, q17, q18, q19, q20, q21, q22, q23, q24, q25, q26, q27, q28, q29, q30, q31}, %1, [%3];\n"
         "}"
-        : "=r"(m)
-        : "r"(addr)
+        : "=r"(m), "=r"(n)
+        : "r"(addr), "r"(addr + 32)
         : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(m)::"memory");
-    return __uint_as_float(m);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(m), "+r"(n)::"memory");
+    return fmaxf(__uint_as_float(m), __uint_as_float(n));
 }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16])
 {
