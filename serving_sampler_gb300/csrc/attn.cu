@@ -97,7 +97,8 @@ struct AttnParams {
     const int32_t *block_table, *kv_len, *cu_tokens;
     const uint32_t* mask;
     int32_t R, T, max_blocks, max_kv, max_tokens, mask_words;
-    Divisor by_block;
+    Divisor by_block, by_tile, by_sms;  // block_size, tile_tokens, sms
+    int32_t wave;                       // items of a key head for every SM to have one, of one row tile or two
     int32_t block_size, num_blocks, kv_heads, group, tile_tokens, head_dim;
     int32_t box_tokens;  // tokens a copy of Q brings
     int32_t q_chunk;     // bytes of 64 columns of Q
@@ -126,6 +127,15 @@ struct Request {
     int32_t gt, ng, cost;       // key tiles of a group, groups and cost of an item over all keys
 };
 
+// A request's lengths as they come, loaded before they are looked at.
+struct Lengths {
+    int32_t t0, t1, kv;
+};
+__device__ __forceinline__ Lengths lengths_of(const AttnParams& p, int32_t r)
+{
+    return Lengths{p.cu_tokens[r], p.cu_tokens[r + 1], p.kv_len[r]};
+}
+
 // Groups.  Few and long ones cost least (a group's end is a pass over O and leaves the
 // products idle); many and short ones let a request alone fill the machine.  A group has
 // about one and a half times the square root of the item's tiles, at least 2 (8 where two
@@ -133,18 +143,18 @@ struct Request {
 // but 4 x 65 take 49 instead of 37 and a request alone 46 instead of 33); where
 // that is near, the number that gives a request alone one or two units for every SM; and
 // an even number, so that a tile's stream is its parity.
-__device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
+__device__ __forceinline__ Request request_from(const AttnParams& p, const Lengths& x)
 {
     Request q;
-    const int32_t t0 = min(max(p.cu_tokens[r], 0), p.T), t1 = min(max(p.cu_tokens[r + 1], t0), p.T);
+    const int32_t t0 = min(max(x.t0, 0), p.T), t1 = min(max(x.t1, t0), p.T);
     q.tok0 = t0;
     q.na = min(t1 - t0, p.max_tokens);
-    q.kv = min(max(p.kv_len[r], 0), p.max_kv);
+    q.kv = min(max(x.kv, 0), p.max_kv);
     q.ctx = q.kv - (t1 - t0);
-    q.tiles = (q.na + p.tile_tokens - 1) / p.tile_tokens;
+    q.tiles = p.by_tile.quotient(q.na + p.tile_tokens - 1);
     q.per_head = (q.tiles + 1) / 2;
     const int32_t nt = (q.kv + kTile - 1) / kTile;
-    const int32_t wave = max(1, p.sms / max(1, p.kv_heads * q.per_head));
+    const int32_t wave = q.per_head <= 1 ? p.wave : max(1, p.sms / (p.kv_heads * q.per_head));
     const int32_t root = 2 * static_cast<int32_t>(0.75f * sqrtf(static_cast<float>(nt)));
     const int32_t one = (nt + wave - 1) / wave, two = (nt + 2 * wave - 1) / (2 * wave);
     const int32_t even = 5 * two >= 4 * root ? two : 5 * one >= 4 * root ? one : root;
@@ -152,6 +162,10 @@ __device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
     q.ng = max(1, (nt + q.gt - 1) / q.gt);
     q.cost = 2 * nt + 2 * q.ng + 8;
     return q;
+}
+__device__ __forceinline__ Request request_of(const AttnParams& p, int32_t r)
+{
+    return request_from(p, lengths_of(p, r));
 }
 
 // An item's groups that lie in a CTA's share.
@@ -248,8 +262,10 @@ struct Shared {
     uint64_t drain;
     Run runs[kRunRing];
     uint64_t v_ok[kMaxStages];  // the stage's V has been cleaned
-    int64_t scan[16];
+    int64_t scan[16], more[16];
     Start start, end;
+    Request first;  // request first_r, which the share begins in or behind
+    int32_t first_r;
     float ref[2][kTile], sum[2][kTile];  // of a stream's group, by row
     uint32_t tmem;
     uint32_t odd[kGroupRing];  // 1 + number of the group whose V had non-finite entries
@@ -340,9 +356,10 @@ __device__ __forceinline__ float final_lse(float m, float l)
 __device__ __forceinline__ Start locate(const AttnParams& p, const Request& q, int32_t r, int64_t first, int64_t at)
 {
     const int64_t off = at - first;
-    int32_t item = static_cast<int32_t>(off / q.cost);
+    int32_t item = off <= 0x7FFFFFFF ? static_cast<int32_t>(static_cast<uint32_t>(off) / static_cast<uint32_t>(q.cost))
+                                     : static_cast<int32_t>(off / q.cost);
     const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(item) * q.cost);
-    int32_t g = (in + q.gt + 1) / (2 * q.gt + 2);
+    int32_t g = static_cast<int32_t>(static_cast<uint32_t>(in + q.gt + 1) / static_cast<uint32_t>(2 * q.gt + 2));
     if (g >= q.ng) {
         g = 0;
         ++item;
@@ -356,46 +373,77 @@ __device__ __forceinline__ int64_t request_cost(const AttnParams& p, const Reque
     return static_cast<int64_t>(q.per_head) * p.kv_heads * q.cost;
 }
 
-// Every thread of the CTA; sets sh.start and sh.end.
-__device__ void find_share(const AttnParams& p, Shared& sh)
+// Every thread of the CTA; sets sh.start, sh.first and sh.end.  `x`: the lengths of request
+// threadIdx.x.  On the way of every call, so kept short: one pass where there is a thread for every
+// request, and no 64-bit division (1.7 us less for every call).
+__device__ void find_share(const AttnParams& p, Shared& sh, const Lengths& x)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
-    int64_t mine = 0;
-    for (int32_t r = tid; r < p.R; r += nt) mine += request_cost(p, request_of(p, r));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
-    if (lane == 0) sh.scan[warp] = mine;
-    if (tid == 0) sh.start = sh.end = Start{p.R, 0, 0, 0};
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < warps; ++w) total += sh.scan[w];
-    const int64_t grid = gridDim.x, c = blockIdx.x;
-    const int64_t lo = total * c / grid, hi = total * (c + 1) / grid;
-    int64_t base = 0;
-    for (int32_t r0 = 0; r0 < p.R; r0 += nt) {
-        __syncthreads();
-        const int32_t r = r0 + tid;
-        Request q{};
-        int64_t cost = 0;
-        if (r < p.R) {
-            q = request_of(p, r);
-            cost = request_cost(p, q);
-        }
-        int64_t sum = cost;
+    auto scan = [&](int64_t sum) {
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
             if (lane >= d) sum += u;
         }
+        return sum;
+    };
+    Request q{};
+    int64_t cost = 0, rest = 0;
+    if (tid < p.R) {
+        q = request_from(p, x);
+        cost = request_cost(p, q);
+    }
+    for (int32_t r = tid + nt; r < p.R; r += nt) rest += request_cost(p, request_of(p, r));
+    int64_t sum = scan(cost);
+    if (p.R > nt) rest = scan(rest);
+    if (lane == 31) {
+        sh.scan[warp] = sum;
+        sh.more[warp] = rest;
+    }
+    if (tid == 0) {
+        sh.start = sh.end = Start{p.R, 0, 0, 0};
+        sh.first_r = -1;
+    }
+    __syncthreads();
+    int64_t first = sum - cost, total = 0, base = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) first += sh.scan[w];
+        base += sh.scan[w];
+        total += sh.scan[w] + sh.more[w];
+    }
+    // total * c / grid
+    const int32_t c = static_cast<int32_t>(blockIdx.x), grid = static_cast<int32_t>(gridDim.x);
+    auto part = [&](int32_t k) {
+        const int64_t each = total <= 0x7FFFFFFF ? p.by_sms.quotient(static_cast<int32_t>(total)) : total / grid;
+        return each * k + p.by_sms.quotient(static_cast<int32_t>(total - each * grid) * k);
+    };
+    const int64_t lo = part(c), hi = part(c + 1);
+    auto look = [&](int32_t r) {
+        if (lo >= first && lo < first + cost) {
+            sh.start = locate(p, q, r, first, lo);
+            sh.first = q;
+            sh.first_r = r;
+        }
+        if (hi >= first && hi < first + cost) sh.end = locate(p, q, r, first, hi);
+    };
+    look(tid);
+    for (int32_t r0 = nt; r0 < p.R; r0 += nt) {
+        __syncthreads();
+        const int32_t r = r0 + tid;
+        cost = 0;
+        if (r < p.R) {
+            q = request_of(p, r);
+            cost = request_cost(p, q);
+        }
+        sum = scan(cost);
         if (lane == 31) sh.scan[warp] = sum;
         __syncthreads();
-        int64_t first = base + sum - cost;
+        first = base + sum - cost;
         for (int w = 0; w < warps; ++w) {
             if (w < warp) first += sh.scan[w];
             base += sh.scan[w];
         }
-        if (lo >= first && lo < first + cost) sh.start = locate(p, q, r, first, lo);
-        if (hi >= first && hi < first + cost) sh.end = locate(p, q, r, first, hi);
+        look(r);
     }
     __syncthreads();
 }
@@ -477,7 +525,7 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
     constexpr uint32_t kStage = kTile * DP * 2;
     constexpr uint32_t kExp = F16 ? 0x7C007C00u : 0x7F807F80u;
     const int lane = threadIdx.x & 31;
-    Walk w{sh.start, sh.end, -1, {}};
+    Walk w{sh.start, sh.end, sh.first_r, sh.first};
     Ring rk{0, 0}, rv{1, 0};
     uint32_t groups = 0, listed = 0, q_runs = 0, used[2] = {0, 0};
     bool more = true;  // runs to list
@@ -519,8 +567,9 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
     // softmax of the run after it has begun, which needs no more than the runs followed so far.  With two
     // buffers Q is a run ahead too.  (Two row tiles take both; their Q is waited for by products that
     // this warp's work on the run comes before, so it cannot be ahead.)
-    bool ok = list() && list();
+    bool ok = list();
     if (ok && !MULTI && sh.runs[0].r >= 0 && sh.runs[0].nt > 0) ok = copy_q(sh.runs[0]);
+    ok = ok && list();
     for (uint32_t k = 0; ok; ++k) {
         ok = list();
         const Run u = sh.runs[k % kRunRing];
@@ -1182,6 +1231,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Shared& sh = *reinterpret_cast<Shared*>(ring + static_cast<size_t>(p.stages) * (kTile * DP * 2));
     const int tid = threadIdx.x, warp = tid >> 5;
     pdl_launch_dependents();
+    Lengths mine{};
+    if (tid < p.R) mine = lengths_of(p, tid);  // on their way while the barriers are made
     if ((smem_addr(base) & 1023u) != 0) {  // never seen: the array's alignment is declared
         if (tid == 0) p.flags[blockIdx.x] = kFlagTimeout;
         return;
@@ -1214,7 +1265,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (tid < kGroupRing) sh.odd[tid] = 0;
     if (warp == 2) tmem_alloc(&sh.tmem, 512);
     tmem_fence_before();
-    find_share(p, sh);  // ends with a barrier
+    find_share(p, sh, mine);  // ends with a barrier
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
     if (tid == 0) {
@@ -1479,6 +1530,7 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.max_tokens = a.max_tokens;
     p.mask_words = a.mask_words;
     p.by_block = divisor_of(a.cache.block_size);
+    p.by_tile = divisor_of(lay.tile_tokens);
     p.block_size = a.cache.block_size;
     p.num_blocks = a.cache.num_blocks;
     p.kv_heads = a.cache.kv_heads;
@@ -1489,6 +1541,8 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.q_chunk = (p.group * p.box_tokens * 128 + 1023) / 1024 * 1024;
     p.box_rows = std::min(kTile, a.cache.block_size & -a.cache.block_size);
     p.sms = attn_ctas();
+    p.by_sms = divisor_of(p.sms);
+    p.wave = std::max(1, p.sms / p.kv_heads);
     // the ring takes what Q leaves of an SM's 227 KB: 5 or 6 stages of 32 KB, up to 12 of 16 KB
     const size_t fixed = attn_shared_bytes(dp, 0, p.q_chunk);
     p.stages = static_cast<int32_t>(std::min<size_t>(kMaxStages, (kMaxShared - fixed) / (kTile * dp * 2)));
