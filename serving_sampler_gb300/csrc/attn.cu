@@ -379,71 +379,68 @@ __device__ __forceinline__ int64_t request_cost(const AttnParams& p, const Reque
 __device__ void find_share(const AttnParams& p, Shared& sh, const Lengths& x)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
-    auto scan = [&](int64_t sum) {
-#pragma unroll
+    // Request r0 + tid and where its costs begin; `base` becomes where the next requests' do.
+    Request q{};
+    int64_t cost = 0, first = 0, base = 0, total = 0;
+    auto take = [&](int32_t r0) {
+        const int32_t r = r0 + tid;
+        cost = 0;
+        if (r < p.R) {
+            q = request_from(p, r0 == 0 ? x : lengths_of(p, r));
+            cost = request_cost(p, q);
+        }
+        int64_t sum = cost;
+#pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
             if (lane >= d) sum += u;
         }
-        return sum;
-    };
-    Request q{};
-    int64_t cost = 0, rest = 0;
-    if (tid < p.R) {
-        q = request_from(p, x);
-        cost = request_cost(p, q);
-    }
-    for (int32_t r = tid + nt; r < p.R; r += nt) rest += request_cost(p, request_of(p, r));
-    int64_t sum = scan(cost);
-    if (p.R > nt) rest = scan(rest);
-    if (lane == 31) {
-        sh.scan[warp] = sum;
-        sh.more[warp] = rest;
-    }
-    if (tid == 0) {
-        sh.start = sh.end = Start{p.R, 0, 0, 0};
-        sh.first_r = -1;
-    }
-    __syncthreads();
-    int64_t first = sum - cost, total = 0, base = 0;
-    for (int w = 0; w < warps; ++w) {
-        if (w < warp) first += sh.scan[w];
-        base += sh.scan[w];
-        total += sh.scan[w] + sh.more[w];
-    }
-    // total * c / grid
-    const int32_t c = static_cast<int32_t>(blockIdx.x), grid = static_cast<int32_t>(gridDim.x);
-    auto part = [&](int32_t k) {
-        const int64_t each = total <= 0x7FFFFFFF ? p.by_sms.quotient(static_cast<int32_t>(total)) : total / grid;
-        return each * k + p.by_sms.quotient(static_cast<int32_t>(total - each * grid) * k);
-    };
-    const int64_t lo = part(c), hi = part(c + 1);
-    auto look = [&](int32_t r) {
-        if (lo >= first && lo < first + cost) {
-            sh.start = locate(p, q, r, first, lo);
-            sh.first = q;
-            sh.first_r = r;
-        }
-        if (hi >= first && hi < first + cost) sh.end = locate(p, q, r, first, hi);
-    };
-    look(tid);
-    for (int32_t r0 = nt; r0 < p.R; r0 += nt) {
         __syncthreads();
-        const int32_t r = r0 + tid;
-        cost = 0;
-        if (r < p.R) {
-            q = request_of(p, r);
-            cost = request_cost(p, q);
-        }
-        sum = scan(cost);
         if (lane == 31) sh.scan[warp] = sum;
         __syncthreads();
         first = base + sum - cost;
+#pragma unroll 1
         for (int w = 0; w < warps; ++w) {
             if (w < warp) first += sh.scan[w];
             base += sh.scan[w];
         }
-        look(r);
+    };
+    if (tid == 0) {
+        sh.start = sh.end = Start{p.R, 0, 0, 0};
+        sh.first_r = -1;
+    }
+    // Twice over the requests, of which the first time is for the total; where there is a thread for each
+    // of them, once.
+    const int32_t rounds = (p.R + nt - 1) / nt;
+    int64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int32_t k = rounds > 1 ? 0 : 1; k < 2 * rounds; ++k) {
+        if (k == rounds) base = 0;
+        take((k < rounds ? k : k - rounds) * nt);
+        if (k == (rounds > 1 ? rounds - 1 : 1)) {
+            total = base;
+            // total * c / grid
+            const int32_t c = static_cast<int32_t>(blockIdx.x), grid = static_cast<int32_t>(gridDim.x);
+            const int64_t each = total <= 0x7FFFFFFF ? p.by_sms.quotient(static_cast<int32_t>(total)) : total / grid;
+            const int32_t rest = static_cast<int32_t>(total - each * grid);
+            lo = each * c + p.by_sms.quotient(rest * c);
+            hi = each * (c + 1) + p.by_sms.quotient(rest * (c + 1));
+        }
+        if (k < rounds) continue;
+        const int32_t r = (k - rounds) * nt + tid;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+            const int64_t at = side == 0 ? lo : hi;
+            if (at < first || at >= first + cost) continue;
+            const Start found = locate(p, q, r, first, at);
+            if (side == 0) {
+                sh.start = found;
+                sh.first = q;
+                sh.first_r = r;
+            } else {
+                sh.end = found;
+            }
+        }
     }
     __syncthreads();
 }
@@ -532,7 +529,6 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.box_tokens * 128 * kChunks);
     // Lists the next run, or the list's end.
     auto list = [&]() {
-        if (!more) return true;
         if (listed >= kRunRing && !warp_wait(&sh.run_empty[listed % kRunRing], (listed / kRunRing - 1) & 1u, sh)) return false;
         Run u;
         more = next_run(p, w, u);
@@ -567,19 +563,21 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
     // softmax of the run after it has begun, which needs no more than the runs followed so far.  With two
     // buffers Q is a run ahead too.  (Two row tiles take both; their Q is waited for by products that
     // this warp's work on the run comes before, so it cannot be ahead.)
-    bool ok = list();
-    if (ok && !MULTI && sh.runs[0].r >= 0 && sh.runs[0].nt > 0) ok = copy_q(sh.runs[0]);
-    ok = ok && list();
+    bool ok = true;
+    uint32_t copied = 0;  // runs whose Q is (not MULTI)
     for (uint32_t k = 0; ok; ++k) {
-        ok = list();
+#pragma unroll 1
+        while (ok && more && listed < k + 3) {
+            ok = list();
+            const Run& v = sh.runs[copied % kRunRing];
+            if (ok && !MULTI && copied < k + 2 && copied < listed && v.r >= 0) {
+                if (v.nt > 0) ok = copy_q(v);
+                ++copied;
+            }
+        }
         const Run u = sh.runs[k % kRunRing];
         if (!ok || u.r < 0) break;
-        if (MULTI) {
-            if (u.nt > 0) ok = copy_q(u);
-        } else {
-            const Run& v = sh.runs[(k + 1) % kRunRing];
-            if (v.r >= 0 && v.nt > 0) ok = copy_q(v);
-        }
+        if (MULTI && u.nt > 0) ok = copy_q(u);
         if (!ok) break;
         const int32_t t1 = min(u.gb * u.gt, u.nt);
         if (u.ga * u.gt >= t1) continue;
