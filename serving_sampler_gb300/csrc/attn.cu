@@ -43,15 +43,17 @@
 // per item, cut evenly over the CTAs; every CTA finds its share itself from the lengths
 // on the device.
 //
-// What bounds it (bf16, heads of 128, GB300):
-//   64 x 9 tokens, 4 heads to a key head, 4,250 keys on average: bytes.  199 us for the
-//   1.2 GB of K and V, 6.0 TB/s, 0.89 of a copy's rate;
+// What bounds it (heads of 128 in bf16 unless said otherwise, time of the kernel, GB300):
+//   64 x 9 tokens, 4 heads to a key head, 4,250 keys on average: bytes.  200 us for the
+//   1.2 GB of K and V, 6.0 TB/s, 0.88 of a copy's rate.
 //   64 x 65 tokens, 7 heads to a key head, 2,500 keys: the chain of a row tile, product,
 //   softmax, product, of which two alternate, as tensor memory has room for two S and two
-//   O.  190 us, 0.40 of the rate of a plain matrix product; the exponentials alone would
-//   take 74 us;
-//   9 tokens over 131,071 keys: bytes, 88 us, 6.1 TB/s, and 10 us for the join;
-//   one token, 1,000 keys: latency, two launches and a chain of loads, 12 us.
+//   O, and the joining of groups (a fifth of the time).  194 us, 0.39 of the rate of a
+//   plain matrix product; the exponentials alone would take 74 us.
+//   17 x 33 tokens, one head to a key head, 64 entries in fp16, 1,700 keys: the same chain,
+//   as a tile's rows are 33; and 5 us before the first product.  41 us.
+//   9 tokens over 131,071 keys: bytes, 86 us, 6.2 TB/s, and 12 us for the join.
+//   One token, 777 keys: latency, two launches and a chain of loads, 10 us and 5.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -1217,8 +1219,8 @@ __host__ __device__ inline size_t attn_shared_bytes(int dp, int stages, int q_ch
 
 // MULTI: some request may have more rows than one tile.
 // The 384 threads launch with 168 registers each; the softmax warps take 208 and the other
-// four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).  What does not fit goes to local
-// memory, which has 25 KB of L1 left beside the ring and costs a trip to L2 for most.
+// four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).  Nothing may spill: local memory has
+// 25 KB of L1 left beside the ring and costs a trip to L2 for most.
 template <int DP, bool F16, bool MULTI>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     tree_attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mq,
