@@ -1461,7 +1461,10 @@ AttnLayout attn_layout(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_
     a.slot_rows = a.multi ? 2 * kTile : std::min<int32_t>(kTile, (std::max(max_tokens, 1) * G + 7) / 8 * 8);
     a.slot_floats = static_cast<int64_t>(a.slot_rows) * (dp + 2);
     const int64_t nt = (max_kv + kTile - 1) / kTile;
-    const int64_t groups = std::max<int64_t>(1, std::min(std::max<int64_t>(1, std::min(sms, 2 * sms / kv_heads)), (nt + 1) / 2));
+    // Groups of an item, at most (request_of): they are at least 4/5 of the square-root rule's size, and no
+    // more than two for every SM that a key head can have.
+    const int64_t groups = std::min(2 * std::max<int64_t>(1, sms / kv_heads),
+                                    static_cast<int64_t>(1.25 * std::sqrt(static_cast<double>(nt))) + 2);
     const int64_t share = R * std::max<int64_t>(1, (tiles + 1) / 2) * kv_heads * (2 * nt + 2 * groups + 8) / sms + 1;
     a.slots_per_cta = static_cast<int32_t>(1 + std::min(groups, share / 6 + 3));
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };

@@ -186,3 +186,21 @@ def test_rope_frequency_checks(m):
     assert f(2, 1e4, 2, 4.0, 0, 0, 0, BUF) == -3
     assert f(8, 1e4, 0, 1, 0, 0, 0, None) == -1 and f(8, 1e4, 0, 1, 0, 0, 0, P(0x10004)) == -7
     assert f(0, 1e4, 0, 1, 0, 0, 0, None) == 0
+
+
+@pytest.mark.parametrize("kv_heads", [1, 2, 8, 60, 200])
+@pytest.mark.parametrize("tokens", [1, 300])
+def test_attention_workspace_holds_every_group(m, kv_heads, tokens):
+    """Room for all but the first group of an item in every CTA, when many requests make the shares long."""
+    sms, D = 152, 128  # what the library takes where there is no device
+    rows = 256 if tokens > 128 else 8
+    per_head = -(-(-(-tokens // 128)) // 2)
+    for keys in (1000, 131072, 1 << 20, 20_000_000, 1 << 30):
+        nt = -(-keys // 128)
+        wave = max(1, sms // (kv_heads * per_head))
+        root, one, two = 2 * int(0.75 * nt ** 0.5), -(-nt // wave), -(-nt // (2 * wave))
+        even = two if 5 * two >= 4 * root else one if 5 * one >= 4 * root else root
+        size = (max(8 if tokens > 128 else 2, even) + 1) // 2 * 2
+        groups = -(-nt // size)
+        got = m.tree_attention_workspace(100_000, 100_000 * tokens, tokens, kv_heads, kv_heads, D, keys)
+        assert got >= sms * groups * rows * (D + 2) * 4, keys
