@@ -503,7 +503,12 @@ int sv_tree_attention(sv_heads q, sv_kv_cache cache, const int32_t* block_table,
     if (int rc = check_cache(cache, R > 0 && q.tokens > 0)) return rc;
     if (cache.layers != 1) return SV_ERR_SHAPE;
     if (static_cast<int64_t>(max_blocks) * cache.block_size > INT32_MAX) return SV_ERR_LIMIT;
-    if (R == 0 || q.tokens == 0) return SV_OK;
+    if (R == 0 || (q.tokens == 0 && status == nullptr)) return SV_OK;
+    if (q.tokens == 0) {  // nothing to attend for, and nothing went wrong
+        if (!aligned(status, 4)) return SV_ERR_ALIGN;
+        if (!have_device()) return SV_ERR_DEVICE;
+        return launched(cudaMemsetAsync(status, 0, static_cast<size_t>(R) * 4, stream));
+    }
     if (int rc = check_heads(q, cache.dtype, cache.head_dim, q.tokens)) return rc;
     if (int rc = check_heads(out, cache.dtype, cache.head_dim, q.tokens)) return rc;
     if (out.heads != q.heads || q.heads % cache.kv_heads != 0) return SV_ERR_SHAPE;

@@ -548,6 +548,23 @@ def test_attention_offsets_past_32_bits(sv):
     assert torch.equal(kc[nb - 1, bs - 1], x[0]) and torch.equal(vc[nb - 1, bs - 1], x[0])
 
 
+def test_attention_without_tokens_or_blocks(sv):
+    """No packed token at all, no token that attends, and a table without a column."""
+    c = Case([30, 7], [2, 1], 4, 2, 64, seed=16)
+    status = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    none = torch.empty((0, 4, 64), dtype=c.dtype, device="cuda")
+    sv.tree_attention(none, c.kc, c.vc, c.table, _i32(c.kv), _i32([0, 0, 0]), 0, out=dict(out=none, status=status))
+    torch.cuda.synchronize()
+    assert (status == 0).all()
+    out = dict(out=torch.full_like(c.q, 5.0), status=status.fill_(-1))
+    sv.tree_attention(c.q, c.kc, c.vc, c.table, _i32(c.kv), _i32(c.cu), 0, out=out)
+    torch.cuda.synchronize()
+    assert (out["out"] == 5).all() and (status == 0).all()
+    got = sv.tree_attention(c.q, c.kc, c.vc, c.table[:, :0].contiguous(), _i32(c.kv), _i32(c.cu), 2, with_lse=True)
+    torch.cuda.synchronize()
+    assert (got["out"] == 0).all() and torch.isneginf(got["lse"]).all()
+
+
 def test_attention_on_another_stream(sv):
     c = Case([900, 33], [9, 9], 8, 2, 128, seed=13)
     want = c.run(sv)
