@@ -95,6 +95,12 @@ __device__ __forceinline__ bool before(const Start& a, const Start& b)
     return a.r != b.r ? a.r < b.r : a.item != b.item ? a.item < b.item : a.g < b.g;
 }
 
+struct alignas(16) Request {
+    int32_t tok0, na, kv, ctx;  // first token, tokens that attend, keys, keys before the tokens
+    int32_t tiles, per_head;    // row tiles, items of a key head
+    int32_t gt, ng, cost;       // key tiles of a group, groups and cost of an item over all keys
+};
+
 struct AttnParams {
     const int32_t *block_table, *kv_len, *cu_tokens;
     const uint32_t* mask;
@@ -115,18 +121,13 @@ struct AttnParams {
     float* lse;
     int32_t* status;
     Start* starts;    // [CTAs + 1]
+    Request* firsts;  // [CTAs]: the request that a share begins in (looked at where it begins inside an item)
     uint32_t* flags;  // [CTAs]
     // [CTAs][slots_per_cta]: O as [DP / 4][rows][4], then m [rows], l [rows].  Slot 0: what the CTA's
     // last item has, and, with several row tiles, the sums of the run at hand
     float* slots;
     int64_t slot_floats;
     int32_t slots_per_cta, slot_rows;
-};
-
-struct Request {
-    int32_t tok0, na, kv, ctx;  // first token, tokens that attend, keys, keys before the tokens
-    int32_t tiles, per_head;    // row tiles, items of a key head
-    int32_t gt, ng, cost;       // key tiles of a group, groups and cost of an item over all keys
 };
 
 // A request's lengths as they come, loaded before they are looked at.
@@ -1270,6 +1271,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t tmem = sh.tmem;
     if (tid == 0) {
         p.starts[blockIdx.x] = sh.start;
+        p.firsts[blockIdx.x] = sh.first;
         if (blockIdx.x + 1 == gridDim.x) p.starts[gridDim.x] = Start{p.R, 0, 0, 0};
     }
 
@@ -1315,12 +1317,12 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
     }
     // all shares at once: the ones that an item goes through are read one after the other
     extern __shared__ Start s_starts[];
+    const int32_t c = blockIdx.x;
+    const Request q = p.firsts[min(c + 1, ctas - 1)];
     for (int32_t i = threadIdx.x; i <= ctas; i += kJoinThreads) s_starts[i] = p.starts[i];
     __syncthreads();
-    const int32_t c = blockIdx.x;
     const Start s = s_starts[c], e = s_starts[c + 1];
     if (e.g == 0 || (s.r == e.r && s.item == e.item && s.g > 0)) return;
-    const Request q = request_of(p, e.r);
     const int32_t head = e.item / q.per_head, tile0 = 2 * (e.item - head * q.per_head);
     int32_t kv_end;
     const int32_t nt = item_tiles(p, q, tile0, &kv_end);
@@ -1444,7 +1446,7 @@ struct AttnLayout {
     int32_t tile_tokens, slot_rows, slots_per_cta;
     bool multi;  // some request may have more rows than one tile
     int64_t slot_floats;
-    size_t starts, flags, slots, total;
+    size_t starts, firsts, flags, slots, total;
 };
 
 // Slots of a CTA: one for the first groups of the item its share ends in, and one for each group of
@@ -1469,7 +1471,8 @@ AttnLayout attn_layout(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_
     a.slots_per_cta = static_cast<int32_t>(1 + std::min(groups, share / 6 + 3));
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     a.starts = 0;
-    a.flags = up(a.starts + static_cast<size_t>(sms + 1) * sizeof(Start));
+    a.firsts = up(a.starts + static_cast<size_t>(sms + 1) * sizeof(Start));
+    a.flags = up(a.firsts + static_cast<size_t>(sms) * sizeof(Request));
     a.slots = up(a.flags + static_cast<size_t>(sms) * 4);
     a.total = up(a.slots + static_cast<size_t>(sms) * a.slots_per_cta * a.slot_floats * 4);
     return a;
@@ -1564,6 +1567,7 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.status = a.status;
     char* ws = static_cast<char*>(a.workspace);
     p.starts = reinterpret_cast<Start*>(ws + lay.starts);
+    p.firsts = reinterpret_cast<Request*>(ws + lay.firsts);
     p.flags = reinterpret_cast<uint32_t*>(ws + lay.flags);
     p.slots = reinterpret_cast<float*>(ws + lay.slots);
     p.slot_floats = lay.slot_floats;
