@@ -1121,15 +1121,15 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
     for (int e = 0; e < (MULTI ? 0 : kHalf / 2); ++e) acc[e] = make_float2(0.0f, 0.0f);
 
     // Every turn of the inner loop has at most one tile of this stream and what is left of the group
-    // before; turns without a tile (no second row tile, a group's only tile is the other stream's, no
-    // run is left) have only that.
+    // before; turns without a tile (no second row tile, a group's only tile is the other stream's, an
+    // item without keys, no run is left) have only that.
     for (bool more = true; more; ++list.k) {
         const Run* const next = list.get(sh);
         if (next == nullptr) return;
         const Run& u = *next;
         more = u.r >= 0;
         const bool split = !MULTI || u.split;
-        const bool idle = !more || (!split && s == 1 && !u.second);
+        bool idle = !more || (!split && s == 1 && !u.second);
         const int32_t tile = u.tile + (split ? 0 : s);
         const int32_t i = tile * p.tile_tokens + token;
         const bool live = !idle && row < p.tile_tokens * p.group && i < u.na;
@@ -1146,8 +1146,10 @@ __device__ void softmax_rows(const AttnParams& p, Shared& sh, uint32_t tmem, int
                     if (col0 + e * 8 < p.head_dim) *reinterpret_cast<uint4*>(out + e * 8) = make_uint4(0, 0, 0, 0);
                 if (col0 == 0 && p.lse != nullptr) p.lse[t_out * p.kv_heads * p.group + h_out] = -INFINITY;
             }
-            list.give_back(sh, list.k);
-            continue;
+            // A turn without a tile, as what is left may not wait for scores here: the run that it
+            // belongs to keeps its place in the list, and with a few runs like this one behind it the
+            // next one that has scores would find no place.
+            idle = true;
         }
 
         const int32_t g1 = idle ? u.ga + 1 : u.gb;
