@@ -535,7 +535,7 @@ __device__ void copy_q_clean_v(const AttnParams& p, Shared& sh, unsigned char* q
         if (listed >= kRunRing && !warp_wait(&sh.run_empty[listed % kRunRing], (listed / kRunRing - 1) & 1u, sh)) return false;
         Run u;
         more = next_run(p, w, u);
-        if (!more) u.r = -1;
+        if (!more) u = Run{-1};  // the softmax reads the rest of it too: one turn, no tile
         if (lane == 0) {
             sh.runs[listed % kRunRing] = u;
             mbar_arrive(&sh.run_full[listed % kRunRing]);
