@@ -82,7 +82,7 @@ enum {
     SV_ST_NO_BLOCKS = 256,    /* sv_step_tables: no room for the request's tokens; it takes no part */
     SV_ST_BAD_TREE = 512,     /* a parent, branch or path that is no tree of the request's tokens */
     SV_ST_BAD_LENGTH = 1024,  /* a length that is negative or above what the tables can hold */
-    SV_ST_BAD_BLOCK = 2048    /* a block id outside the pool; the tokens in it have no slot */
+    SV_ST_BAD_BLOCK = 2048    /* a block id outside the pool; the tokens in it are not in the cache */
 };
 
 /* limits */
@@ -568,8 +568,9 @@ int sv_tree_attention(sv_heads q, sv_kv_cache cache, const int32_t* block_table,
  *   free_count_out int32 [1] out;  status int32 [R] out or NULL.
  * K and V of accepted draft i move to position seq_len + 1 + i.  An accepted
  * token that is not one of the request's, or a path that does not increase,
- * ends the accepted path before it (SV_ST_BAD_TREE).  The outputs must not
- * overlap the inputs.  layers * kv_heads * head_dim / 4 is at most 65535 * 128.
+ * ends the accepted path before it (SV_ST_BAD_TREE).  A block of the step's
+ * tokens whose id is outside [0, num_blocks) is neither moved from or to nor
+ * given back (SV_ST_BAD_BLOCK).  The outputs must not overlap the inputs.  layers * kv_heads * head_dim / 4 is at most 65535 * 128.
  * ---------------------------------------------------------------------- */
 int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len,
                     const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, const int32_t* accept_len,

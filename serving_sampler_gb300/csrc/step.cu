@@ -275,6 +275,27 @@ __device__ __forceinline__ Keep keep_of(const CommitArgs& c, int32_t r)
     return q;
 }
 
+// What a request gives back: the blocks behind the ones it keeps, of which only ids of the pool go on the
+// free list, as any request may get them from there.  `bad`: a block of the step's tokens is outside the pool.
+struct Surplus {
+    int32_t blocks;
+    bool bad;
+};
+
+__device__ __forceinline__ bool in_pool(const CommitArgs& c, int32_t id) { return id >= 0 && id < c.cache.num_blocks; }
+
+__device__ __forceinline__ Surplus surplus_of(const CommitArgs& c, int32_t r, const Keep& q)
+{
+    Surplus s{0, false};
+    const int32_t* table = c.block_table + static_cast<int64_t>(r) * c.max_blocks;
+    for (int32_t b = q.takes ? c.by_block.quotient(q.root) : q.held; b < q.held; ++b) {
+        const bool in = in_pool(c, table[b]);
+        s.bad = s.bad || !in;
+        s.blocks += in && b >= q.kept;
+    }
+    return s;
+}
+
 constexpr int kMoveBatch = 8;
 
 // Grid: x = requests, then the CTAs that give blocks back; y = 128 16-byte columns of
@@ -297,26 +318,31 @@ __global__ void __launch_bounds__(kStepThreads) cache_commit_kernel(const Commit
         const int32_t r1 = static_cast<int32_t>(static_cast<int64_t>(c.R) * (i + 1) / releasers);
         const int64_t count = min(max(c.free_count[0], 0), c.cache.num_blocks);
         int64_t before = 0, none = 0;
-        for (int32_t r = tid; r < r0; r += kStepThreads) {
-            const Keep q = keep_of(c, r);
-            before += q.held - q.kept;
-        }
+        for (int32_t r = tid; r < r0; r += kStepThreads) before += surplus_of(c, r, keep_of(c, r)).blocks;
         block_sum2(before, none, s_sum);
         int64_t top = count + before;
         for (int32_t base = r0; base < r1; base += kStepThreads) {
             const int32_t r = base + tid;
             Keep q{};
-            if (r < r1) q = keep_of(c, r);
-            int64_t mine = q.held - q.kept, all = mine, zero = 0;
+            Surplus give{};
+            if (r < r1) {
+                q = keep_of(c, r);
+                give = surplus_of(c, r, q);
+            }
+            int64_t mine = give.blocks, all = mine, zero = 0;
             block_prefix2(mine, zero, s_sum);
             __syncthreads();
             int64_t at = top + mine;
             if (r < r1) {
                 const int32_t* table = c.block_table + static_cast<int64_t>(r) * c.max_blocks;
-                for (int32_t b = q.kept; b < q.held; ++b, ++at)
-                    if (at < c.cache.num_blocks) c.free_blocks[at] = table[b];
+                for (int32_t b = q.kept; b < q.held; ++b) {
+                    const int32_t id = table[b];
+                    if (!in_pool(c, id)) continue;
+                    if (at < c.cache.num_blocks) c.free_blocks[at] = id;
+                    ++at;
+                }
                 c.seq_len_out[r] = q.takes ? q.root + 1 + q.a : q.root;
-                if (c.status != nullptr) c.status[r] = q.bad ? SV_ST_BAD_TREE : 0;
+                if (c.status != nullptr) c.status[r] = (q.bad ? SV_ST_BAD_TREE : 0) | (give.bad ? SV_ST_BAD_BLOCK : 0);
             }
             zero = 0;
             block_sum2(all, zero, s_sum);
@@ -335,7 +361,7 @@ __global__ void __launch_bounds__(kStepThreads) cache_commit_kernel(const Commit
     const int32_t* table = c.block_table + static_cast<int64_t>(r) * c.max_blocks;
     auto place = [&](int32_t token) -> int64_t {
         const int32_t at = q.root + token, b = c.by_block.quotient(at), id = table[b];
-        if (id < 0 || id >= c.cache.num_blocks) return -1;
+        if (!in_pool(c, id)) return -1;
         return id * c.cache.block_stride + (at - b * c.cache.block_size) * c.cache.token_stride;
     };
     for (int32_t i = tid; i < q.a; i += kStepThreads) {

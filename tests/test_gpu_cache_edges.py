@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_cache import Case, _i32, branch_parents
+from tests.test_gpu_cache import Case, _commit_case, _i32, _np, _same, branch_parents
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,76 @@ def test_attention_where_only_few_requests_have_keys(sv, n, D):
         none = torch.tensor([x == 0 for x in kv]).repeat_interleave(n).cuda()
         assert (got["out"][none] == 0).all() and torch.isneginf(got["lse"][none]).all()
         c.check(got, keep)
+
+
+# --- commit: blocks outside the pool ------------------------------------------------------------------------------
+def _commit_plain(c, k, path):
+    """What is kept, one token and one block at a time: a block outside the pool holds nothing and is not given back."""
+    kc, vc, free = _np(c["kc"]).copy(), _np(c["vc"]).copy(), c["free"].copy()
+    nb, bs, top = kc.shape[1], kc.shape[2], c["count"]
+    seq, status = np.array(c["seq"], np.int32), np.zeros(len(c["seq"]), np.int32)
+    for r in range(len(seq)):
+        L, kv, table = int(c["seq"][r]), int(c["kv"][r]), c["table"][r]
+        n = int(c["cu"][r + 1] - c["cu"][r])
+        if n <= 0 or L + n != kv:
+            continue
+        a = min(max(int(c["accept"][r]), 0), k)
+        if any(not 0 <= table[(L + j) // bs] < nb for j in range(n)):
+            status[r] = 2048
+        for cache in (kc, vc):
+            for i in range(a):
+                src, dst = L + int(path[r, i]), L + 1 + i
+                if 0 <= table[src // bs] < nb and 0 <= table[dst // bs] < nb:
+                    cache[:, table[dst // bs], dst % bs] = cache[:, table[src // bs], src % bs]
+        seq[r] = L + 1 + a
+        for b in range(-(-int(seq[r]) // bs), -(-kv // bs)):
+            if 0 <= table[b] < nb:
+                free[top] = table[b]
+                top += 1
+    return dict(k=kc, v=vc, seq_len=seq, free=free, free_count=np.array([top], np.int32), status=status)
+
+
+@pytest.mark.parametrize("R,bs", [(12, 8), (300, 8), (40, 16)])
+@pytest.mark.parametrize("by_path", [False, True])
+def test_commit_gives_no_block_back_that_is_outside_the_pool(sv, R, bs, by_path):
+    """Two branches of 20 drafts; entries of many tables replaced among the committed, kept and surplus blocks."""
+    k, n = 20, 41
+    c = _commit_case(R, 2, k, 2, 2, 16, bs, seed=R)
+    rng = np.random.default_rng(R + 1)
+    nb = c["kc"].shape[1]
+    for r in range(0, R, 2):
+        held = -(-int(c["kv"][r]) // bs)
+        for b in rng.choice(held, min(held, 3), replace=False) if held else []:
+            c["table"][r, b] = rng.choice([-1, -(1 << 31), nb, nb + 7, (1 << 31) - 1])
+    if by_path:
+        path = np.stack([np.sort(rng.choice(np.arange(1, n), k, replace=False)) for _ in range(R)]).astype(np.int32)
+    else:
+        path = 1 + c["branch"][:, None] * k + np.arange(k)
+    want = _commit_plain(c, k, path)
+    assert (want["status"] == 2048).any() and (want["status"] == 0).any()
+    free = _i32(c["free"])
+    got = sv.cache_commit(c["kc"], c["vc"], _i32(c["table"]), _i32(c["seq"]), _i32(c["kv"]), _i32(c["cu"]),
+                          _i32(c["accept"]), k, free, _i32([c["count"]]),
+                          branch=None if by_path else _i32(c["branch"]), path=_i32(path) if by_path else None)
+    torch.cuda.synchronize()
+    for name in ("seq_len", "free_count", "status"):
+        _same(got[name], want[name], name)
+    _same(free, want["free"], "free")
+    np.testing.assert_array_equal(_np(c["kc"]), want["k"])
+    np.testing.assert_array_equal(_np(c["vc"]), want["v"])
+
+
+def test_a_block_outside_the_pool_reaches_no_other_request(sv):
+    """A request with a bad entry is committed; the next step's tokens of another request have slots all the same."""
+    bs, nb, k = 8, 6, 15
+    table = _i32([[0, -1, -1, -1], [1, -1, -1, -1]])
+    seq, free, count = _i32([8, 8]), _i32([2, 3, 4, 5, -1, -1]), _i32([4])
+    kc, vc = (torch.zeros(nb, bs, 1, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    step = sv.step_tables(seq, _i32([1 + k, 0]), table, free, count, bs, 1 + k)
+    assert table[0].tolist() == [0, 5, 4, -1] and step["free_count"].item() == 2
+    table[0, 2] = nb + 3
+    kept = sv.cache_commit(kc, vc, table, seq, step["kv_len"], step["cu_tokens"], _i32([0, 0]), k, free,
+                           step["free_count"])
+    assert kept["status"].tolist() == [2048, 0] and kept["free_count"].item() == 2
+    step = sv.step_tables(kept["seq_len"], _i32([0, 9]), table, free, kept["free_count"], bs, 9)
+    assert step["status"].tolist() == [0, 0] and (step["slot"] >= 0).all()
