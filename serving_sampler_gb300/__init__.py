@@ -484,7 +484,7 @@ def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_si
 def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
                trained: float = 0.0, low: float = 0.0, high: float = 0.0, device="cuda"):
     """Frequencies for rope_cache: an int64 tensor [rot_dim / 2] of 64-bit turn fractions (see sv_rope_freqs for
-    the scalings)."""
+    the scalings).  rope_cache takes them on the GPU."""
     lib = load()
     host = torch.zeros(max(rot_dim, 0) // 2, dtype=torch.int64)
     _check(lib.sv_rope_freqs(rot_dim, base, scaling, factor, trained, low, high, _ptr(host)))
@@ -499,10 +499,10 @@ def rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, interleaved: bo
     T = q.shape[0]
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if slot.dtype is not torch.int64 or not slot.is_contiguous() or slot.numel() != T:
-        raise ValueError("slot must be a contiguous int64 tensor with an entry for each token")
-    if freqs.dtype not in (torch.int64, torch.uint64) or not freqs.is_contiguous():
-        raise ValueError("freqs must be a contiguous int64 tensor from rope_freqs")
+    if slot.dtype is not torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != T:
+        raise ValueError("slot must be a contiguous int64 CUDA tensor with an entry for each token")
+    if freqs.dtype not in (torch.int64, torch.uint64) or not freqs.is_cuda or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous int64 CUDA tensor from rope_freqs")
     rc = lib.sv_rope_cache(heads_of(q), heads_of(k), heads_of(v), _ints(position, "position", T), slot.data_ptr(),
                            freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, mscale, heads_of(q_out),
                            cache_of(k_cache, v_cache), _raw_stream(stream))
