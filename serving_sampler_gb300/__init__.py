@@ -424,6 +424,14 @@ def _ints(t, name, n=-1) -> int:
     return t.data_ptr()
 
 
+def _check_out(out, **want):
+    """Tensors that a caller gave for outputs must have room for what the kernels write: name=(dtype, entries)."""
+    for name, (dtype, n) in want.items():
+        t = out.get(name)
+        if t is not None and (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n):
+            raise ValueError(f"out[{name!r}] must be a contiguous {dtype} CUDA tensor with room for {n} entries")
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -461,6 +469,14 @@ def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_si
                    status=status)
         if parent is not None:
             out["mask"] = mask.view(T, mask_words)
+    else:
+        i32 = torch.int32
+        _check_out(out, cu_tokens=(i32, R + 1), kv_len=(i32, R), slot=(torch.int64, T), position=(i32, T),
+                   free_count=(i32, 1), status=(i32, R))
+        if parent is not None:
+            _check_out(out, mask=(i32, T * mask_words))
+            if out["mask"].dim() == 2 and out["mask"].shape[1] != mask_words:
+                raise ValueError(f"out['mask'] must have rows of {mask_words} words")
     mask = out.get("mask") if parent is not None else None
     if R == 0:  # nothing to lay out
         out["cu_tokens"].zero_()
@@ -530,12 +546,16 @@ def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_toke
         out = dict(out=torch.empty(q.shape, dtype=q.dtype, device=q.device))
         if with_lse:
             out["lse"] = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    else:
+        _check_out(out, lse=(torch.float32, T * heads), status=(torch.int32, R))
     if mask is not None and (mask.dim() != 2 or mask.shape[0] != T):
         raise ValueError("mask must be [T, words]")
     cache = cache_of(k_cache, v_cache)
     if workspace is None:
         workspace = _workspace(lib.sv_tree_attention_workspace(R, T, max_tokens, heads, cache.kv_heads, D,
                                                                max_blocks * cache.block_size), q.device, None)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     rc = lib.sv_tree_attention(heads_of(q), cache, _ints(block_table, "block_table"), max_blocks,
                                _ints(kv_len, "kv_len", R), _ints(cu_tokens, "cu_tokens", R + 1), R, max_tokens,
                                None if mask is None else _ints(mask, "mask"), 0 if mask is None else mask.shape[1],
@@ -559,6 +579,8 @@ def cache_commit(k_cache, v_cache, block_table, seq_len, kv_len, cu_tokens, acce
     a_seq = _ints(seq_len, "seq_len")
     if out is None:
         out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, R, 1, R)))
+    else:
+        _check_out(out, seq_len=(torch.int32, R), free_count=(torch.int32, 1), status=(torch.int32, R))
     if R == 0:
         out["free_count"].copy_(free_count)
         return out

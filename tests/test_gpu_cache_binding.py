@@ -15,3 +15,54 @@ def test_rope_refuses_slots_and_frequencies_on_the_host(sv):
         sv.rope_cache(c.q, x, x, position, slot.cuda(), sv.rope_freqs(64, device="cpu"), c.kc, c.vc)
     with pytest.raises(ValueError, match="slot"):
         sv.rope_cache(c.q, x, x, position, slot, sv.rope_freqs(64), c.kc, c.vc)
+
+
+def _wrong(t):
+    """Tensors that cannot stand for an output like t."""
+    flat = t.reshape(-1)
+    yield flat[:-1].clone()                                        # an entry short
+    yield torch.empty(t.shape, dtype=t.dtype)                      # on the host
+    yield torch.empty(t.shape, dtype=torch.float64, device="cuda")  # another type
+    if flat.numel() > 1:
+        yield torch.empty(2 * flat.numel(), dtype=t.dtype, device="cuda")[::2]  # strided
+
+
+def test_outputs_without_room_are_refused(sv):
+    R, T, words, k = 2, 9, 2, 3
+    c = Case([20, 7], [5, 4], 4, 2, 64)
+    seq, new, free, count = _i32([20, 7]), _i32([5, 4]), _i32(range(40)), _i32([40])
+    parent = _i32([-1, 0, 1, 2, 3, -1, 0, 1, 2])
+    table = torch.zeros((R, 8), dtype=torch.int32, device="cuda")
+    caches = [torch.zeros((40, 16, 2, 64), dtype=c.dtype, device="cuda") for _ in range(2)]
+
+    def tables(out=None):
+        return sv.step_tables(seq, new, table, free, count, 16, T, parent=parent, mask_words=words, out=out)
+
+    def attend(out=None):
+        return sv.tree_attention(c.q, c.kc, c.vc, c.table, _i32(c.kv), _i32(c.cu), 5, with_lse=True, out=out)
+
+    def commit(out=None):
+        return sv.cache_commit(*caches, table, seq, _i32([25, 11]), _i32([0, 5, 9]), _i32([1, 2]), k, free, count,
+                               out=out)
+
+    for call in (tables, attend, commit):
+        out = call()
+        out.setdefault("status", torch.empty(R, dtype=torch.int32, device="cuda"))
+        for name, t in out.items():
+            if name == "out":
+                continue  # heads may be strided: the library checks them
+            for bad in _wrong(t):
+                with pytest.raises(ValueError, match=name):
+                    call(dict(out, **{name: bad}))
+        roomy = {name: t if name == "out" else torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+                 for name, t in out.items()}
+        assert call(roomy) is roomy
+        call({name: t for name, t in out.items() if name != "status"})  # asked for or not
+    with pytest.raises(ValueError, match="mask"):  # room enough, in rows of another width
+        tables(dict(tables(), mask=torch.empty((T, words + 1), dtype=torch.int32, device="cuda")))
+    with pytest.raises(sv.SpecVerifyError):
+        attend(dict(out=torch.empty_like(c.q)[:-1]))
+    with pytest.raises(ValueError, match="workspace"):
+        sv.tree_attention(c.q, c.kc, c.vc, c.table, _i32(c.kv), _i32(c.cu), 5,
+                          workspace=torch.empty(1 << 26, dtype=torch.uint8))
+    torch.cuda.synchronize()
