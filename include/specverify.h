@@ -532,7 +532,8 @@ int sv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, 
  *   scale       factor on the scores q . k.
  *   out         T x q.heads heads with q's dtype;  lse float [T, q.heads] or NULL:
  *               ln of the sum of exp(score) over the visible positions.
- *   status      int32 [R] out or NULL (SV_ST_TIMEOUT).
+ *   status      int32 [R] out or NULL: 0, or SV_ST_TIMEOUT for every request when
+ *               a wait gave up.  out and lse of every token that attends are then NaN.
  * out = sum_x softmax_x(scale q . k_x) v_x.  Where a token sees nothing, out is
  * 0 and lse -inf.  Keys and values at positions that a token does not see have
  * no influence on it, whatever they hold; a score of NaN or +inf at one that it
@@ -594,6 +595,16 @@ int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_b
  * Launches one warp on `stream`; nothing is in flight when it exits.
  * ---------------------------------------------------------------------- */
 int sv_selftest_wait_timeout(const void* src16, int32_t* status, int64_t limit_cycles, sv_stream_t stream);
+
+/* sv_selftest_tree_attention_stop -- sv_tree_attention with the thread block `cta`
+ * (0 <= cta; the launch has one per SM) giving up at its first wait, as after a wait
+ * that ran out: the call reports SV_ST_TIMEOUT and leaves NaN, and the next call is
+ * not affected.  The other arguments are those of sv_tree_attention. */
+int sv_selftest_tree_attention_stop(sv_heads q, sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks,
+                                    const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, int32_t max_tokens,
+                                    const uint32_t* mask, int32_t mask_words, float scale, sv_heads out, float* lse,
+                                    int32_t* status, void* workspace, size_t workspace_bytes, int32_t cta,
+                                    sv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -115,6 +115,7 @@ def load(path: str | None = None):
     lib.sv_tree_attention_workspace.argtypes = [i32, i32, i32, i32, i32, i32, i64]
     lib.sv_tree_attention_workspace.restype = sz
     lib.sv_tree_attention.argtypes = [SvHeads, SvKvCache, P, i32, P, P, i32, i32, P, i32, f32, SvHeads, P, P, P, sz, P]
+    lib.sv_selftest_tree_attention_stop.argtypes = lib.sv_tree_attention.argtypes[:-1] + [i32, P]
     lib.sv_cache_commit.argtypes = [SvKvCache, P, i32, P, P, P, i32, P, P, P, i32, P, P, P, P, P, P]
     lib.sv_selftest_wait_timeout.argtypes = [P, P, C.c_int64, P]
     lib.sv_selftest_wait_timeout.restype = C.c_int
@@ -534,11 +535,13 @@ def tree_attention_workspace(R: int, T: int, max_tokens: int, heads: int, kv_hea
 
 def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_tokens: int, mask=None,
                    scale: float | None = None, with_lse: bool = False, out: dict | None = None, workspace=None,
-                   stream=None) -> dict:
+                   stream=None, with_status: bool = False) -> dict:
     """Attention of the packed step tokens q [T, heads, D] over the paged cache.  block_table int32
     [R, max_blocks]; kv_len int32 [R]; cu_tokens int32 [R + 1]; max_tokens bounds a request's tokens; mask int32
     [T, words] (which of its request's step tokens a token sees) or None (a chain); scale defaults to
-    D ** -0.5.  Returns out [T, heads, D] and, with_lse, lse float32 [T, heads]."""
+    D ** -0.5.  Returns out [T, heads, D] and, with_lse, lse float32 [T, heads]; with_status, status int32 [R],
+    which is ST_TIMEOUT for every request when a wait on the device gave up.  out and lse are then NaN.  Rows of
+    tokens that do not attend (behind cu_tokens[R], or a request's behind max_tokens) are not written."""
     lib = load()
     T, heads, D = q.shape
     R, max_blocks = block_table.shape
@@ -546,6 +549,8 @@ def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_toke
         out = dict(out=torch.empty(q.shape, dtype=q.dtype, device=q.device))
         if with_lse:
             out["lse"] = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+        if with_status:
+            out["status"] = torch.empty(R, dtype=torch.int32, device=q.device)
     else:
         _check_out(out, lse=(torch.float32, T * heads), status=(torch.int32, R))
     if mask is not None and (mask.dim() != 2 or mask.shape[0] != T):

@@ -96,6 +96,37 @@ static bool have_device()
     return cudaGetDevice(&dev) == cudaSuccess;
 }
 
+static int tree_attention(const AttnArgs& a, size_t workspace_bytes, sv_stream_t stream)
+{
+    if (a.R < 0 || a.q.tokens < 0 || a.max_tokens < 0 || a.max_blocks < 0) return SV_ERR_INVALID_ARG;
+    if (a.mask_words < 0 || (a.mask != nullptr && a.mask_words < 1)) return SV_ERR_INVALID_ARG;
+    if (int rc = check_cache(a.cache, a.R > 0 && a.q.tokens > 0)) return rc;
+    if (a.cache.layers != 1) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(a.max_blocks) * a.cache.block_size > INT32_MAX) return SV_ERR_LIMIT;
+    if (a.R == 0 || (a.q.tokens == 0 && a.status == nullptr)) return SV_OK;
+    if (a.q.tokens == 0) {  // nothing to attend for, and nothing went wrong
+        if (!aligned(a.status, 4)) return SV_ERR_ALIGN;
+        if (!have_device()) return SV_ERR_DEVICE;
+        return launched(cudaMemsetAsync(a.status, 0, static_cast<size_t>(a.R) * 4, stream));
+    }
+    if (int rc = check_heads(a.q, a.cache.dtype, a.cache.head_dim, a.q.tokens)) return rc;
+    if (int rc = check_heads(a.out, a.cache.dtype, a.cache.head_dim, a.q.tokens)) return rc;
+    if (a.out.heads != a.q.heads || a.q.heads % a.cache.kv_heads != 0) return SV_ERR_SHAPE;
+    if (a.q.heads / a.cache.kv_heads > SV_MAX_GROUP) return SV_ERR_LIMIT;
+    if (a.kv_len == nullptr || a.cu_tokens == nullptr || (a.max_blocks > 0 && a.block_table == nullptr))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(a.block_table, 4) || !aligned(a.kv_len, 4) || !aligned(a.cu_tokens, 4) || !aligned(a.mask, 4) ||
+        !aligned(a.lse, 4) || !aligned(a.status, 4))
+        return SV_ERR_ALIGN;
+    if (int rc = check_workspace(a.workspace, workspace_bytes,
+                                 attn_workspace_bytes(a.R, a.q.tokens, a.max_tokens, a.q.heads, a.cache.kv_heads,
+                                                      a.q.head_dim,
+                                                      static_cast<int64_t>(a.max_blocks) * a.cache.block_size)))
+        return rc;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_tree_attention(a, stream));
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -498,34 +529,21 @@ int sv_tree_attention(sv_heads q, sv_kv_cache cache, const int32_t* block_table,
                       const uint32_t* mask, int32_t mask_words, float scale, sv_heads out, float* lse,
                       int32_t* status, void* workspace, size_t workspace_bytes, sv_stream_t stream)
 {
-    if (R < 0 || q.tokens < 0 || max_tokens < 0 || max_blocks < 0) return SV_ERR_INVALID_ARG;
-    if (mask_words < 0 || (mask != nullptr && mask_words < 1)) return SV_ERR_INVALID_ARG;
-    if (int rc = check_cache(cache, R > 0 && q.tokens > 0)) return rc;
-    if (cache.layers != 1) return SV_ERR_SHAPE;
-    if (static_cast<int64_t>(max_blocks) * cache.block_size > INT32_MAX) return SV_ERR_LIMIT;
-    if (R == 0 || (q.tokens == 0 && status == nullptr)) return SV_OK;
-    if (q.tokens == 0) {  // nothing to attend for, and nothing went wrong
-        if (!aligned(status, 4)) return SV_ERR_ALIGN;
-        if (!have_device()) return SV_ERR_DEVICE;
-        return launched(cudaMemsetAsync(status, 0, static_cast<size_t>(R) * 4, stream));
-    }
-    if (int rc = check_heads(q, cache.dtype, cache.head_dim, q.tokens)) return rc;
-    if (int rc = check_heads(out, cache.dtype, cache.head_dim, q.tokens)) return rc;
-    if (out.heads != q.heads || q.heads % cache.kv_heads != 0) return SV_ERR_SHAPE;
-    if (q.heads / cache.kv_heads > SV_MAX_GROUP) return SV_ERR_LIMIT;
-    if (kv_len == nullptr || cu_tokens == nullptr || (max_blocks > 0 && block_table == nullptr))
-        return SV_ERR_INVALID_ARG;
-    if (!aligned(block_table, 4) || !aligned(kv_len, 4) || !aligned(cu_tokens, 4) || !aligned(mask, 4) ||
-        !aligned(lse, 4) || !aligned(status, 4))
-        return SV_ERR_ALIGN;
-    if (int rc = check_workspace(workspace, workspace_bytes,
-                                 attn_workspace_bytes(R, q.tokens, max_tokens, q.heads, cache.kv_heads, q.head_dim,
-                                                      static_cast<int64_t>(max_blocks) * cache.block_size)))
-        return rc;
-    if (!have_device()) return SV_ERR_DEVICE;
-    return launched(launch_tree_attention(AttnArgs{q, out, cache, block_table, max_blocks, kv_len, cu_tokens, R,
-                                                   max_tokens, mask, mask_words, scale, lse, status, workspace},
-                                          stream));
+    return tree_attention(AttnArgs{q, out, cache, block_table, max_blocks, kv_len, cu_tokens, R, max_tokens, mask,
+                                   mask_words, scale, lse, status, workspace, -1},
+                          workspace_bytes, stream);
+}
+
+int sv_selftest_tree_attention_stop(sv_heads q, sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks,
+                                    const int32_t* kv_len, const int32_t* cu_tokens, int32_t R, int32_t max_tokens,
+                                    const uint32_t* mask, int32_t mask_words, float scale, sv_heads out, float* lse,
+                                    int32_t* status, void* workspace, size_t workspace_bytes, int32_t cta,
+                                    sv_stream_t stream)
+{
+    if (cta < 0) return SV_ERR_INVALID_ARG;
+    return tree_attention(AttnArgs{q, out, cache, block_table, max_blocks, kv_len, cu_tokens, R, max_tokens, mask,
+                                   mask_words, scale, lse, status, workspace, cta},
+                          workspace_bytes, stream);
 }
 
 int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len,

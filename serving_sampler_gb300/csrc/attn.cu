@@ -128,6 +128,7 @@ struct AttnParams {
     float* slots;
     int64_t slot_floats;
     int32_t slots_per_cta, slot_rows;
+    int32_t stop_cta;  // a CTA that gives up at its first wait (self-test; -1: none)
 };
 
 // A request's lengths as they come, loaded before they are looked at.
@@ -1263,7 +1264,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         mbar_init(&sh.drain, 1);
         fence_barrier_init();
-        sh.stop = 0;
+        sh.stop = static_cast<int32_t>(blockIdx.x) == p.stop_cta ? 1 : 0;
     }
     if (tid < kGroupRing) sh.odd[tid] = 0;
     if (warp == 2) tmem_alloc(&sh.tmem, 512);
@@ -1301,6 +1302,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---- groups that were cut across CTAs -----------------------------------------------------------
 constexpr int kJoinThreads = 256, kAhead = 4, kJoinBlocks = 8;
 
+// A CTA gave up a wait: NaN in every row, so that no caller takes what stands there for results.
+__device__ __noinline__ void spoil_rows(const AttnParams& p)
+{
+    const int32_t heads = p.kv_heads * p.group, vecs = p.head_dim / 8;
+    const uint32_t nan = 0x7FFF7FFFu;  // in bf16 as in fp16
+    for (int32_t r = blockIdx.y * gridDim.x + blockIdx.x; r < p.R; r += gridDim.x * gridDim.y) {
+        const Request q = request_of(p, r);
+        const int64_t n = static_cast<int64_t>(q.na) * heads * vecs;
+        for (int64_t x = threadIdx.x; x < n; x += kJoinThreads) {
+            const int64_t row = x / vecs, t = q.tok0 + row / heads;
+            const int32_t v = static_cast<int32_t>(x - row * vecs), h = static_cast<int32_t>(row % heads);
+            *reinterpret_cast<uint4*>(p.out + t * p.out_token_stride + h * p.out_head_stride + v * 8) =
+                make_uint4(nan, nan, nan, nan);
+            if (v == 0 && p.lse != nullptr) p.lse[t * heads + h] = NAN;
+        }
+    }
+}
+
 // blockIdx.x = c: the item that is cut where CTA c's share ends, if its first group lies in that
 // share; blockIdx.y: a part of its (row, eight columns).  Groups are joined as softmax_rows does.
 // Its time is that of a few dependent loads: eight blocks at most for an item, three on an SM,
@@ -1310,19 +1329,22 @@ template <int DP, bool F16>
 __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid_constant__ AttnParams p, int32_t ctas)
 {
     pdl_wait_primary();
-    if (p.status != nullptr && blockIdx.y == 0) {
-        uint32_t f = 0;
-        for (int32_t i = threadIdx.x; i < ctas; i += kJoinThreads) f |= p.flags[i];
-        const int32_t st = __syncthreads_or(static_cast<int>(f)) != 0 ? SV_ST_TIMEOUT : 0;
-        for (int32_t r = blockIdx.x * kJoinThreads + threadIdx.x; r < p.R; r += gridDim.x * kJoinThreads)
-            p.status[r] = st;
-    }
     // all shares at once: the ones that an item goes through are read one after the other
     extern __shared__ Start s_starts[];
     const int32_t c = blockIdx.x;
     const Request q = p.firsts[min(c + 1, ctas - 1)];
+    uint32_t f = 0;
+    for (int32_t i = threadIdx.x; i < ctas; i += kJoinThreads) f |= p.flags[i];
     for (int32_t i = threadIdx.x; i <= ctas; i += kJoinThreads) s_starts[i] = p.starts[i];
-    __syncthreads();
+    const bool gave_up = __syncthreads_or(static_cast<int>(f)) != 0;
+    if (p.status != nullptr && blockIdx.y == 0) {
+        for (int32_t r = blockIdx.x * kJoinThreads + threadIdx.x; r < p.R; r += gridDim.x * kJoinThreads)
+            p.status[r] = gave_up ? SV_ST_TIMEOUT : 0;
+    }
+    if (gave_up) {
+        spoil_rows(p);
+        return;
+    }
     const Start s = s_starts[c], e = s_starts[c + 1];
     if (e.g == 0 || (s.r == e.r && s.item == e.item && s.g > 0)) return;
     const int32_t head = e.item / q.per_head, tile0 = 2 * (e.item - head * q.per_head);
@@ -1575,6 +1597,7 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.slot_floats = lay.slot_floats;
     p.slots_per_cta = lay.slots_per_cta;
     p.slot_rows = lay.slot_rows;
+    p.stop_cta = a.stop_cta;
 
     CUtensorMap mq, mk, mv;
     const uint64_t D = static_cast<uint64_t>(a.q.head_dim);

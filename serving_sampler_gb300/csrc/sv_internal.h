@@ -178,6 +178,7 @@ struct AttnArgs {
     float* lse;
     int32_t* status;
     void* workspace;
+    int32_t stop_cta;  // self-test: the CTA that gives up at its first wait, -1 for none
 };
 size_t attn_workspace_bytes(int32_t R, int32_t T, int32_t max_tokens, int32_t heads, int32_t kv_heads,
                             int32_t head_dim, int64_t max_kv);

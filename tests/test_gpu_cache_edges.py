@@ -59,6 +59,33 @@ def test_attention_where_only_few_requests_have_keys(sv, n, D):
         c.check(got, keep)
 
 
+# --- attention: a wait that gave up -------------------------------------------------------------------------------
+@pytest.mark.parametrize("new,D,dtype", [([9, 9, 1, 4], 128, torch.bfloat16), ([70, 1, 300, 9], 128, torch.float16),
+                                         ([33, 33, 2, 1], 64, torch.bfloat16), ([300, 65, 9, 140], 64, torch.bfloat16)])
+def test_attention_that_gave_up_says_so(sv, new, D, dtype):
+    """One CTA gives up at its first wait: every request is reported, no row looks like a result, the next call is
+    right."""
+    c = Case([3000, 40, 900, 0], new, 16, 4, D, dtype, 16, seed=D + sum(new))
+    want = c.run(sv, with_status=True)
+    assert (want["status"] == 0).all()
+    kv, cu = _i32(c.kv), _i32(c.cu)
+    nbytes = sv.tree_attention_workspace(c.R, c.T, c.max_tokens, 16, 4, D, c.table.shape[1] * 16)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    for cta in (0, 75, torch.cuda.get_device_properties(0).multi_processor_count - 1):
+        out, lse = torch.zeros_like(c.q), torch.zeros(c.T, 16, device="cuda")
+        status = torch.zeros(c.R, dtype=torch.int32, device="cuda")
+        rc = sv.load().sv_selftest_tree_attention_stop(
+            sv.heads_of(c.q), sv.cache_of(c.kc, c.vc), c.table.data_ptr(), c.table.shape[1], kv.data_ptr(),
+            cu.data_ptr(), c.R, c.max_tokens, None, 0, c.scale, sv.heads_of(out), lse.data_ptr(), status.data_ptr(),
+            ws.data_ptr(), nbytes, cta, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert rc == 0 and (status == sv.ST_TIMEOUT).all()
+        assert torch.isnan(out.float()).all() and torch.isnan(lse).all()
+        again = c.run(sv, workspace=ws, with_status=True)
+        assert (again["status"] == 0).all()
+        assert torch.equal(again["out"], want["out"]) and torch.equal(again["lse"], want["lse"])
+
+
 # --- commit: blocks outside the pool ------------------------------------------------------------------------------
 def _commit_plain(c, k, path):
     """What is kept, one token and one block at a time: a block outside the pool holds nothing and is not given back."""
