@@ -247,14 +247,6 @@ struct Ring {
             phase ^= 1u;
         }
     }
-    __device__ __forceinline__ void prev2(int32_t n)
-    {
-        stage -= 2;
-        if (stage < 0) {
-            stage += n;
-            phase ^= 1u;
-        }
-    }
 };
 
 struct Shared {
@@ -264,6 +256,7 @@ struct Shared {
     uint64_t g_done, o_free[2];                  // a phase per group whose keys are split (o_free: of every other)
     uint64_t run_full[kRunRing], run_empty[kRunRing];
     uint64_t drain;
+    uint32_t filled[2];  // by the copiers of K and V, when they end
     Run runs[kRunRing];
     uint64_t v_ok[kMaxStages];  // the stage's V has been cleaned
     int64_t scan[16], more[16];
@@ -461,7 +454,7 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
     const int lane = threadIdx.x & 31;
     Runs runs;
     Ring rt{first, 0};
-    int32_t fills = 0;  // of this warp; from the ring's second turn on a stage is waited for
+    uint32_t fills = 0;  // of this warp; from the ring's second turn on a stage is waited for
     bool ok = true;
     const int32_t subs = kTile / p.box_rows;
     const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
@@ -487,7 +480,7 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
             const int32_t live = min(subs, (u.kv_end - x0 + p.box_rows - 1) / p.box_rows);
             uint64_t* full = &sh.kv_full[rt.stage];
             // the stage's fill before this one is the ring's last turn: `first + 2 * fills` stages in
-            if (first + 2 * fills >= p.stages && !warp_wait(&sh.kv_empty[rt.stage], rt.phase ^ 1u, sh)) {
+            if (first + 2 * fills >= static_cast<uint32_t>(p.stages) && !warp_wait(&sh.kv_empty[rt.stage], rt.phase ^ 1u, sh)) {
                 ok = false;
                 break;
             }
@@ -500,15 +493,24 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
                     tma_load_4d(dst + lane * box_bytes + ch * kTile * 128, map, full, ch * 64, place, u.head, block);
             }
             __syncwarp();
-            fills = min(fills + 1, 1 << 20);
+            ++fills;
             rt.next2(p.stages);
         }
     }
-    // a CTA that gave up does not leave before its copies have landed
-    if (!ok || sh.stop != 0) {
-        for (int32_t i = min(fills, (p.stages + 1) / 2); i > 0; --i) {
-            rt.prev2(p.stages);
-            mbar_wait_bounded(&sh.kv_full[rt.stage], rt.phase);
+    if (lane == 0) sh.filled[first] = fills;
+}
+
+// A CTA that gave up does not leave before its copies have landed.  Line 2 i + c of the ring is fill i of
+// copier c.  Each stage's last fill is waited for; of an earlier one the barrier's parity would say nothing.
+__device__ void drain_tiles(const AttnParams& p, Shared& sh)
+{
+    const uint32_t stages = static_cast<uint32_t>(p.stages);
+    for (uint32_t c = 0; c < 2; ++c) {
+        const uint32_t fills = sh.filled[c], end = c + 2 * fills;              // behind the copier's lines,
+        const uint32_t other = stages % 2 ? 1 - c + 2 * sh.filled[1 - c] : end;  // and those of the next fill of a stage
+        for (uint32_t i = fills - min(fills, (stages + 1) / 2); i < fills; ++i) {
+            const uint32_t line = c + 2 * i;
+            if (line + stages >= other) mbar_wait_bounded(&sh.kv_full[line % stages], (line / stages) & 1u);
         }
     }
 }
@@ -1297,6 +1299,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_fence_after();
     if (warp == 2) tmem_dealloc(tmem, 512);
     if (tid == 0) p.flags[blockIdx.x] = sh.stop != 0 ? kFlagTimeout : 0u;
+    if (warp == 0 && sh.stop != 0) drain_tiles(p, sh);
 }
 
 // ---- groups that were cut across CTAs -----------------------------------------------------------
