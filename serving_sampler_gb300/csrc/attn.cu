@@ -259,7 +259,7 @@ struct Shared {
     uint32_t filled[2];  // by the copiers of K and V, when they end
     Run runs[kRunRing];
     uint64_t v_ok[kMaxStages];  // the stage's V has been cleaned
-    int64_t scan[16], more[16];
+    int64_t scan[16];
     Start start, end;
     Request first;  // request first_r, which the share begins in or behind
     int32_t first_r;
@@ -1576,7 +1576,9 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.sms = attn_ctas();
     p.by_sms = divisor_of(p.sms);
     p.wave = std::max(1, p.sms / p.kv_heads);
-    // the ring takes what Q leaves of an SM's 227 KB: 5 or 6 stages of 32 KB, up to 12 of 16 KB
+    // the ring takes what Q leaves of an SM's 227 KB: 5 or 6 stages of 32 KB, 12 of 16 KB.  Where Q fills
+    // its tile, 5 and 12 just leave the 3,072 bytes of `Shared`'s place; with one stage fewer 64 x 65 tokens
+    // took 209.6 us a call instead of 210.5, and 17 x 33 the same 49.3: the ring does not bound them.
     const size_t fixed = attn_shared_bytes(dp, 0, p.q_chunk);
     p.stages = static_cast<int32_t>(std::min<size_t>(kMaxStages, (kMaxShared - fixed) / (kTile * dp * 2)));
     // a scale of 0 weighs all alike; the smallest factor keeps hidden scores at -inf
