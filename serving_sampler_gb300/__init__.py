@@ -10,6 +10,10 @@ Entry points (same names as the C ABI in include/specverify.h):
   verify_greedy, verify_sample, cfg_merge_sample, accept_scan
   step_tables, rope_cache (with rope_freqs), tree_attention, cache_commit: the
   cache side of a verify step
+
+Every call runs on the current stream, or on ``stream=``.  What it allocates by
+itself belongs to that stream; its inputs must be ready on it and stay alive
+until it has read them, as with any work on a stream that is not their own.
 """
 from __future__ import annotations
 
@@ -159,20 +163,27 @@ def rows_of(t, width: int | None = None) -> SvRows:
     return SvRows(t.data_ptr(), code, int(width if width is not None else t.shape[1]), int(stride))
 
 
-def _empty(shape, dtype, device):
-    import torch
+def _empty(shape, dtype, device, stream=None):
+    """An output.  It is made on the stream that writes it: the current one's memory may still be read by work ahead of
+    the call.  The caller's stream is noted, as that is where it will be read."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
-    return torch.empty(shape, dtype=dtype, device=device)
 
-
-def _workspace(nbytes, device, workspace):
-    import torch
-
+def _workspace(nbytes, device, workspace, stream=None):
+    """The given workspace, or one made on the stream that uses it, which gets its memory back."""
     if workspace is not None:
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError(f"workspace needs {nbytes} bytes")
         return workspace
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def _nbytes(t):
@@ -444,10 +455,10 @@ def _raw_stream(stream) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _new_ints(like, *sizes):
+def _new_ints(like, stream, *sizes):
     """Int32 tensors of these sizes in one allocation and one split: allocating each costs more than the launch that
     fills them."""
-    return torch.unsafe_split_with_sizes(torch.empty(sum(sizes), dtype=torch.int32, device=like.device), sizes)
+    return torch.unsafe_split_with_sizes(_empty(sum(sizes), torch.int32, like.device, stream), sizes)
 
 
 def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_size: int, T: int, parent=None,
@@ -465,7 +476,7 @@ def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_si
     if out is None:
         # the 64-bit slots lie first, as pairs of 32-bit entries
         slot, cu, kv, position, count, status, mask = _new_ints(
-            seq_len, 2 * T, R + 1, R, T, 1, R, T * mask_words if parent is not None else 0)
+            seq_len, stream, 2 * T, R + 1, R, T, 1, R, T * mask_words if parent is not None else 0)
         out = dict(cu_tokens=cu, kv_len=kv, slot=slot.view(torch.int64), position=position, free_count=count,
                    status=status)
         if parent is not None:
@@ -480,12 +491,13 @@ def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_si
                 raise ValueError(f"out['mask'] must have rows of {mask_words} words")
     mask = out.get("mask") if parent is not None else None
     if R == 0:  # nothing to lay out
-        out["cu_tokens"].zero_()
-        out["free_count"].copy_(free_count)
-        for name in ("slot", "position"):
-            out[name].fill_(-1)
-        if mask is not None:
-            mask.zero_()
+        with torch.cuda.stream(stream):
+            out["cu_tokens"].zero_()
+            out["free_count"].copy_(free_count)
+            for name in ("slot", "position"):
+                out[name].fill_(-1)
+            if mask is not None:
+                mask.zero_()
         return out
     rc = lib.sv_step_tables(a_seq, _ints(new_len, "new_len", R), R, block_size, a_table, block_table.shape[1],
                             _ints(free_blocks, "free_blocks"), _ints(free_count, "free_count", 1),
@@ -515,7 +527,7 @@ def rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, interleaved: bo
     lib = load()
     T = q.shape[0]
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
     if slot.dtype is not torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != T:
         raise ValueError("slot must be a contiguous int64 CUDA tensor with an entry for each token")
     if freqs.dtype not in (torch.int64, torch.uint64) or not freqs.is_cuda or not freqs.is_contiguous():
@@ -546,11 +558,11 @@ def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_toke
     T, heads, D = q.shape
     R, max_blocks = block_table.shape
     if out is None:
-        out = dict(out=torch.empty(q.shape, dtype=q.dtype, device=q.device))
+        out = dict(out=_empty(q.shape, q.dtype, q.device, stream))
         if with_lse:
-            out["lse"] = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+            out["lse"] = _empty((T, heads), torch.float32, q.device, stream)
         if with_status:
-            out["status"] = torch.empty(R, dtype=torch.int32, device=q.device)
+            out["status"] = _empty(R, torch.int32, q.device, stream)
     else:
         _check_out(out, lse=(torch.float32, T * heads), status=(torch.int32, R))
     if mask is not None and (mask.dim() != 2 or mask.shape[0] != T):
@@ -558,7 +570,7 @@ def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_toke
     cache = cache_of(k_cache, v_cache)
     if workspace is None:
         workspace = _workspace(lib.sv_tree_attention_workspace(R, T, max_tokens, heads, cache.kv_heads, D,
-                                                               max_blocks * cache.block_size), q.device, None)
+                                                               max_blocks * cache.block_size), q.device, None, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     rc = lib.sv_tree_attention(heads_of(q), cache, _ints(block_table, "block_table"), max_blocks,
@@ -583,11 +595,12 @@ def cache_commit(k_cache, v_cache, block_table, seq_len, kv_len, cu_tokens, acce
         raise ValueError("block_table must be [R, max_blocks]")
     a_seq = _ints(seq_len, "seq_len")
     if out is None:
-        out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, R, 1, R)))
+        out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, stream, R, 1, R)))
     else:
         _check_out(out, seq_len=(torch.int32, R), free_count=(torch.int32, 1), status=(torch.int32, R))
     if R == 0:
-        out["free_count"].copy_(free_count)
+        with torch.cuda.stream(stream):
+            out["free_count"].copy_(free_count)
         return out
     rc = lib.sv_cache_commit(cache_of(k_cache, v_cache), _ints(block_table, "block_table"), block_table.shape[1], a_seq,
                              _ints(kv_len, "kv_len", R), _ints(cu_tokens, "cu_tokens", R + 1), R,
