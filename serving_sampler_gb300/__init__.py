@@ -204,9 +204,9 @@ def verify_greedy(target, R: int, k: int, branches: int, draft, out: dict | None
     lib = load()
     dev = target.device
     if out is None:
-        out = dict(accept_len=_empty(R, torch.int32, dev), tokens=_empty((R, k + 1), torch.int32, dev),
-                   branch=_empty(R, torch.int32, dev), status=_empty(R, torch.int32, dev))
-    ws = _workspace(lib.sv_verify_greedy_workspace(R, k, branches, target.shape[1]), dev, workspace)
+        out = dict(accept_len=_empty(R, torch.int32, dev, stream), tokens=_empty((R, k + 1), torch.int32, dev, stream),
+                   branch=_empty(R, torch.int32, dev, stream), status=_empty(R, torch.int32, dev, stream))
+    ws = _workspace(lib.sv_verify_greedy_workspace(R, k, branches, target.shape[1]), dev, workspace, stream)
     _check(lib.sv_verify_greedy(rows_of(target), R, k, branches, _ptr(draft), _ptr(out["accept_len"]),
                                 _ptr(out["tokens"]), _ptr(out.get("branch")), _ptr(out.get("status")), _ptr(ws),
                                 _nbytes(ws), _stream(stream)))
@@ -227,10 +227,10 @@ def verify_greedy_top2(target, R: int, k: int, branches: int, draft, out: dict |
     dev = target.device
     rows = target.shape[0] if R == 0 else R * (1 + branches * k)
     if out is None:
-        out = dict(accept_len=_empty(R, torch.int32, dev), tokens=_empty((R, k + 1), torch.int32, dev),
-                   branch=_empty(R, torch.int32, dev), status=_empty(R, torch.int32, dev),
-                   top2=_empty((rows, 2), torch.int32, dev))
-    ws = _workspace(lib.sv_verify_greedy_top2_workspace(R, k, branches, target.shape[1]), dev, workspace)
+        out = dict(accept_len=_empty(R, torch.int32, dev, stream), tokens=_empty((R, k + 1), torch.int32, dev, stream),
+                   branch=_empty(R, torch.int32, dev, stream), status=_empty(R, torch.int32, dev, stream),
+                   top2=_empty((rows, 2), torch.int32, dev, stream))
+    ws = _workspace(lib.sv_verify_greedy_top2_workspace(R, k, branches, target.shape[1]), dev, workspace, stream)
     _check(lib.sv_verify_greedy_top2(rows_of(target), R, k, branches, _ptr(draft), _ptr(out["accept_len"]),
                                      _ptr(out["tokens"]), _ptr(out.get("branch")), _ptr(out.get("status")),
                                      _ptr(out["top2"]), _ptr(ws), _nbytes(ws), _stream(stream)))
@@ -249,8 +249,8 @@ def infer_modality(logits, part_start, out: dict | None = None, workspace=None, 
     N = logits.shape[0]
     ps = np.ascontiguousarray(np.asarray(part_start, dtype=np.int32))
     if out is None:
-        out = {key: _empty(N, torch.int32, dev) for key in ("amax", "part", "mask_lo", "mask_hi", "status")}
-    ws = _workspace(lib.sv_infer_modality_workspace(N, logits.shape[1]), dev, workspace)
+        out = {key: _empty(N, torch.int32, dev, stream) for key in ("amax", "part", "mask_lo", "mask_hi", "status")}
+    ws = _workspace(lib.sv_infer_modality_workspace(N, logits.shape[1]), dev, workspace, stream)
     _check(lib.sv_infer_modality(rows_of(logits), N, ps.ctypes.data, ps.size - 1, _ptr(out.get("amax")),
                                  _ptr(out["part"]), _ptr(out.get("mask_lo")), _ptr(out.get("mask_hi")),
                                  _ptr(out.get("status")), _ptr(ws), _nbytes(ws), _stream(stream)))
@@ -269,7 +269,7 @@ def d2t_plan(d2t, V: int, stream=None):
     lib = load()
     Vd = d2t.numel()
     nbytes = int(lib.sv_d2t_plan_bytes(V, Vd))
-    plan = torch.empty(nbytes, dtype=torch.uint8, device=d2t.device)
+    plan = _empty(nbytes, torch.uint8, d2t.device, stream)
     _check(lib.sv_d2t_plan_build(_ptr(d2t), Vd, V, _ptr(plan), nbytes, _stream(stream)))
     return plan
 
@@ -291,12 +291,12 @@ def verify_sample(target, draft_logits, d2t, R: int, k: int, draft, seeds, tempe
     else:
         Vd = V if d2t is None else d2t.numel()
     if out is None:
-        out = dict(accept_len=_empty(R, torch.int32, dev), tokens=_empty((R, k + 1), torch.int32, dev),
-                   status=_empty(R, torch.int32, dev))
+        out = dict(accept_len=_empty(R, torch.int32, dev, stream), tokens=_empty((R, k + 1), torch.int32, dev, stream),
+                   status=_empty(R, torch.int32, dev, stream))
         if stats:
             for name in ("tv", "p_draft", "q_draft"):
-                out[name] = _empty((R, k), torch.float32, dev)
-    ws = _workspace(lib.sv_verify_sample_workspace(R, k, V, Vd), dev, workspace)
+                out[name] = _empty((R, k), torch.float32, dev, stream)
+    ws = _workspace(lib.sv_verify_sample_workspace(R, k, V, Vd), dev, workspace, stream)
     _check(lib.sv_verify_sample(rows_of(target), rows_of(draft_logits, Vd), _ptr(d2t), _ptr(plan), R, k, _ptr(draft),
                                 _ptr(seeds), _ptr(temperature), _ptr(out["accept_len"]), _ptr(out["tokens"]),
                                 _ptr(out.get("tv")), _ptr(out.get("p_draft")), _ptr(out.get("q_draft")),
@@ -320,13 +320,14 @@ def cfg_merge_sample(cond, uncond, cb_id_base, cb_data_offset, S: int, W: int, w
     lib = load()
     dev = cond.device
     if out is None:
-        out = dict(accept_len=_empty(R, torch.int32, dev), tokens=_empty((R, k + 1, S), torch.int32, dev),
-                   status=_empty(R, torch.int32, dev))
+        out = dict(accept_len=_empty(R, torch.int32, dev, stream),
+                   tokens=_empty((R, k + 1, S), torch.int32, dev, stream),
+                   status=_empty(R, torch.int32, dev, stream))
         if stats:
-            out["tv"] = _empty((R, k, S), torch.float32, dev)
+            out["tv"] = _empty((R, k, S), torch.float32, dev, stream)
     base = (C.c_int32 * S)(*[int(b) for b in cb_id_base])
     off = None if cb_data_offset is None else (C.c_int32 * S)(*[int(o) for o in cb_data_offset])
-    ws = _workspace(lib.sv_cfg_merge_sample_workspace(R, k, S, W), dev, workspace)
+    ws = _workspace(lib.sv_cfg_merge_sample_workspace(R, k, S, W), dev, workspace, stream)
     _check(lib.sv_cfg_merge_sample(rows_of(cond, W), rows_of(uncond, W), C.cast(base, C.c_void_p),
                                    None if off is None else C.cast(off, C.c_void_p), S, float(w),
                                    rows_of(draft_logits, W), R, k, _ptr(draft), _ptr(seeds), _ptr(temperature),
@@ -357,7 +358,7 @@ def pool_lookup(pool, pool_len, suffix, gamma: int, out: dict | None = None, str
     N = suffix.shape[1]
     dev = pool.device
     if out is None:
-        out = dict(match_len=_empty(R, torch.int32, dev), cont=_empty((R, gamma), torch.int32, dev))
+        out = dict(match_len=_empty(R, torch.int32, dev, stream), cont=_empty((R, gamma), torch.int32, dev, stream))
     _check(lib.sv_pool_lookup(_ptr(pool), _ptr(pool_len), Lp, _ptr(suffix), N, R, gamma, _ptr(out["match_len"]),
                               _ptr(out["cont"]), _stream(stream)))
     return out
@@ -381,7 +382,7 @@ def accept_scan(accept, draft, fix, out: dict | None = None, stream=None) -> dic
     R, k = accept.shape
     dev = accept.device
     if out is None:
-        out = dict(accept_len=_empty(R, torch.int32, dev), tokens=_empty((R, k + 1), torch.int32, dev))
+        out = dict(accept_len=_empty(R, torch.int32, dev, stream), tokens=_empty((R, k + 1), torch.int32, dev, stream))
     _check(lib.sv_accept_scan(_ptr(accept), _ptr(draft), _ptr(fix), R, k, _ptr(out["accept_len"]),
                               _ptr(out["tokens"]), _stream(stream)))
     return out

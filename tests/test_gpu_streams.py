@@ -29,12 +29,12 @@ def _check_workspace(call, nbytes):
     assert all(torch.equal(got[name], want[name]) for name in want)
 
 
-def _check_outputs(call):
+def _check_outputs(call, between=0):
     """An output is not laid over what the caller's stream has still to read, nor over by the call's stream before the
-    caller's has read it."""
+    caller's has read it.  between: bytes of one that is not among those returned."""
     want = call(None)
     torch.cuda.synchronize()
-    sizes = {t.untyped_storage().nbytes() for t in want.values()}
+    sizes = {t.untyped_storage().nbytes() for t in want.values()} | ({between} if between else set())
     s = torch.cuda.Stream()
     for n in sizes:
         old = _blocks_of(n)
@@ -116,3 +116,85 @@ def test_calls_without_requests_keep_to_the_stream(sv):
         got = call(s)
         torch.cuda.synchronize()
         assert got["free_count"].item() == 7
+
+
+# --- verification ------------------------------------------------------------------------------------------------
+R, K, V = 16, 4, 5000
+
+
+def _logits(rows, width, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(rows, width, generator=g, device="cuda") * 3
+
+
+def _ids(*shape, top=V, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(top, shape, generator=g, device="cuda", dtype=torch.int32)
+
+
+def _greedy(sv):
+    x, draft = _logits(R * (1 + 2 * K), V, 1), _ids(R, 2, K)
+    return lambda s: sv.verify_greedy(x, R, K, 2, draft, stream=s), sv.verify_greedy_workspace(R, K, 2, V)
+
+
+def _greedy_top2(sv):
+    x, draft = _logits(R * (1 + 2 * K), V, 2), _ids(R, 2, K)
+    return lambda s: sv.verify_greedy_top2(x, R, K, 2, draft, stream=s), sv.verify_greedy_top2_workspace(R, K, 2, V)
+
+
+def _sample(sv):
+    x, d, draft = _logits(R * (K + 1), V, 3), _logits(R * K, V, 4), _ids(R, K)
+    seeds, temp = torch.arange(R, device="cuda"), torch.full((R,), 0.8, device="cuda")
+    return (lambda s: sv.verify_sample(x, d, None, R, K, draft, seeds, temp, stream=s),
+            sv.verify_sample_workspace(R, K, V, V))
+
+
+def _cfg(sv):
+    S, W = 3, 1024
+    x, y, d = _logits(R * (K + 1) * S, W, 5), _logits(R * (K + 1) * S, W, 6), _logits(R * K * S, W, 7)
+    draft = _ids(R, K, S, top=W) + torch.arange(S, dtype=torch.int32, device="cuda") * W
+    seeds, temp = torch.arange(R, device="cuda"), torch.full((R,), 0.8, device="cuda")
+
+    def call(s):
+        return sv.cfg_merge_sample(x, y, [0, W, 2 * W], None, S, W, 3.0, d, R, K, draft, seeds, temp, stream=s)
+
+    return call, sv.cfg_merge_sample_workspace(R, K, S, W)
+
+
+def _modality(sv):
+    x = _logits(R, V, 8)
+    return lambda s: sv.infer_modality(x, [0, 1000, 4000, V], stream=s), sv.load().sv_infer_modality_workspace(R, V)
+
+
+def _scan(sv):
+    accept, draft, fix = _ids(R, K, top=2).to(torch.uint8), _ids(R, K), _ids(R, K + 1)
+    return lambda s: sv.accept_scan(accept, draft, fix, stream=s), 0
+
+
+def _lookup(sv):
+    pool, suffix = _ids(R, 200, top=20), _ids(R, 4, top=20)
+    used = torch.full((R,), 200, dtype=torch.int32, device="cuda")
+    return lambda s: sv.pool_lookup(pool, used, suffix, 8, stream=s), 0
+
+
+@pytest.mark.parametrize("make", [_greedy, _greedy_top2, _sample, _cfg, _modality])
+def test_verification_workspaces_belong_to_the_stream(sv, make):
+    _check_workspace(*make(sv))
+
+
+@pytest.mark.parametrize("make", [_greedy, _greedy_top2, _sample, _cfg, _modality, _scan, _lookup])
+def test_verification_outputs_belong_to_the_stream(sv, make):
+    _check_outputs(make(sv)[0])
+
+
+def test_plans_belong_to_the_stream(sv):
+    """A plan has bytes that nothing writes or reads, so it is compared by what comes of it."""
+    Vd = 1000
+    d2t = torch.randperm(V, device="cuda")[:Vd].sort().values.to(torch.int32)
+    x, d, draft = _logits(R * (K + 1), V, 3), _logits(R * K, Vd, 4), d2t[_ids(R, K, top=Vd).long()]
+    seeds, temp = torch.arange(R, device="cuda"), torch.full((R,), 0.8, device="cuda")
+
+    def call(s):
+        return sv.verify_sample(x, d, d2t, R, K, draft, seeds, temp, plan=sv.d2t_plan(d2t, V, stream=s), stream=s)
+
+    _check_outputs(call, sv.d2t_plan(d2t, V).numel())
