@@ -449,11 +449,13 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream) -> int:
-    """The given stream's handle, or the current one's (without building a stream object for it)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _raw_stream(stream, t) -> int:
+    """The given stream's handle, or the current one's (without building a stream object for it).  The library launches
+    on the current device, which has to be the one of the tensors."""
+    device = torch._C._cuda_getDevice()
+    if t.get_device() != device:
+        raise ValueError(f"a tensor is on {t.device}, but cuda:{device} is the current device")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _new_ints(like, stream, *sizes):
@@ -505,7 +507,7 @@ def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_si
                             free_blocks.numel(), None if parent is None else _ints(parent, "parent", T), T,
                             out["cu_tokens"].data_ptr(), out["kv_len"].data_ptr(), out["slot"].data_ptr(),
                             out["position"].data_ptr(), _at(mask), mask_words if mask is not None else 0,
-                            out["free_count"].data_ptr(), _at(out.get("status")), _raw_stream(stream))
+                            out["free_count"].data_ptr(), _at(out.get("status")), _raw_stream(stream, seq_len))
     if rc:
         _check(rc)
     return out
@@ -535,7 +537,7 @@ def rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, interleaved: bo
         raise ValueError("freqs must be a contiguous int64 CUDA tensor from rope_freqs")
     rc = lib.sv_rope_cache(heads_of(q), heads_of(k), heads_of(v), _ints(position, "position", T), slot.data_ptr(),
                            freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, mscale, heads_of(q_out),
-                           cache_of(k_cache, v_cache), _raw_stream(stream))
+                           cache_of(k_cache, v_cache), _raw_stream(stream, q))
     if rc:
         _check(rc)
     return q_out
@@ -578,7 +580,7 @@ def tree_attention(q, k_cache, v_cache, block_table, kv_len, cu_tokens, max_toke
                                _ints(kv_len, "kv_len", R), _ints(cu_tokens, "cu_tokens", R + 1), R, max_tokens,
                                None if mask is None else _ints(mask, "mask"), 0 if mask is None else mask.shape[1],
                                D ** -0.5 if scale is None else scale, heads_of(out["out"]), _at(out.get("lse")),
-                               _at(out.get("status")), workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream))
+                               _at(out.get("status")), workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, q))
     if rc:
         _check(rc)
     return out
@@ -609,7 +611,7 @@ def cache_commit(k_cache, v_cache, block_table, seq_len, kv_len, cu_tokens, acce
                              None if path is None else _ints(path, "path", R * k), k,
                              _ints(free_blocks, "free_blocks", k_cache.shape[-4]), _ints(free_count, "free_count", 1),
                              out["seq_len"].data_ptr(), out["free_count"].data_ptr(), _at(out.get("status")),
-                             _raw_stream(stream))
+                             _raw_stream(stream, seq_len))
     if rc:
         _check(rc)
     return out

@@ -66,3 +66,24 @@ def test_outputs_without_room_are_refused(sv):
         sv.tree_attention(c.q, c.kc, c.vc, c.table, _i32(c.kv), _i32(c.cu), 5,
                           workspace=torch.empty(1 << 26, dtype=torch.uint8))
     torch.cuda.synchronize()
+
+
+def test_tensors_of_another_device_are_refused(sv, monkeypatch):
+    """Where the current device is another than the tensors', nothing is launched."""
+    c = Case([20], [3], 4, 2, 64)
+    seq, new, free, count = _i32([20]), _i32([3]), _i32(range(8)), _i32([8])
+    table = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    kv, cu, slot, freqs = _i32(c.kv), _i32(c.cu), torch.zeros(3, dtype=torch.int64, device="cuda"), sv.rope_freqs(64)
+    x, nb = c.q[:, :2].contiguous(), c.kc.shape[0]
+    calls = [lambda: sv.step_tables(seq, new, table, free, count, 16, 3),
+             lambda: sv.rope_cache(c.q, x, x, cu.new_zeros(3), slot, freqs, c.kc, c.vc),
+             lambda: sv.tree_attention(c.q, c.kc, c.vc, c.table, kv, cu, 3),
+             lambda: sv.cache_commit(c.kc, c.vc, c.table, seq, kv, cu, new, 2, free.new_zeros(nb), count)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    with monkeypatch.context() as m:
+        m.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+        for call in calls:
+            with pytest.raises(ValueError, match="current device"):
+                call()
