@@ -119,8 +119,7 @@ static int tree_attention(const AttnArgs& a, size_t workspace_bytes, sv_stream_t
         !aligned(a.lse, 4) || !aligned(a.status, 4))
         return SV_ERR_ALIGN;
     if (int rc = check_workspace(a.workspace, workspace_bytes,
-                                 attn_workspace_bytes(a.R, a.q.tokens, a.max_tokens, a.q.heads, a.cache.kv_heads,
-                                                      a.q.head_dim,
+                                 attn_workspace_bytes(a.R, a.max_tokens, a.q.heads, a.cache.kv_heads, a.q.head_dim,
                                                       static_cast<int64_t>(a.max_blocks) * a.cache.block_size)))
         return rc;
     if (!have_device()) return SV_ERR_DEVICE;
@@ -521,7 +520,7 @@ size_t sv_tree_attention_workspace(int32_t R, int32_t T, int32_t max_tokens, int
     if (R < 0 || T < 0 || max_tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 ||
         head_dim > SV_MAX_HEAD_DIM || max_kv < 0 || max_kv > INT32_MAX || heads / kv_heads > SV_MAX_GROUP)
         return 0;
-    return attn_workspace_bytes(R, T, max_tokens, heads, kv_heads, head_dim, max_kv);
+    return attn_workspace_bytes(R, max_tokens, heads, kv_heads, head_dim, max_kv);
 }
 
 int sv_tree_attention(sv_heads q, sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks,

@@ -1539,7 +1539,7 @@ cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& mq, const CUtens
 
 }  // namespace
 
-size_t attn_workspace_bytes(int32_t R, int32_t, int32_t max_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+size_t attn_workspace_bytes(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
                             int64_t max_kv)
 {
     return attn_layout(R, max_tokens, heads, kv_heads, head_dim, max_kv).total;

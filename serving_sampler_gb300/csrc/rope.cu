@@ -29,7 +29,6 @@ namespace sv {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeBatch = 1;   // items a thread works on, with as many in flight
 constexpr int kRopeTokens = 4;  // most tokens of a CTA
 
 template <bool F16>
@@ -122,24 +121,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const __grid_c
     const int Hq = a.q.heads, Hk = a.cache.kv_heads;
     const uint32_t total = static_cast<uint32_t>(tokens) * g.line, step = kRopeThreads * gridDim.y;
 
-    auto load = [&](uint32_t x0, uint4 (&va)[kRopeBatch], uint4 (&vb)[kRopeBatch]) {
-#pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-            const uint32_t x = x0 + u * step;
-            if (x < total) {
-                const RopeItem m = item_of<SIDE>(a, g, x);
-                const sv_heads& h = m.row < Hq ? a.q : m.row < Hq + Hk ? a.k : a.v;
-                const int row = m.row < Hq ? m.row : m.row < Hq + Hk ? m.row - Hq : m.row - Hq - Hk;
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(h.data) +
-                                                                  (t0 + m.token) * h.token_stride + row * h.head_stride);
-                va[u] = src[m.a];
-                if (m.b < g.vecs) vb[u] = src[m.b];
-            }
+    auto load = [&](uint32_t x, uint4& va, uint4& vb) {
+        if (x < total) {
+            const RopeItem m = item_of<SIDE>(a, g, x);
+            const sv_heads& h = m.row < Hq ? a.q : m.row < Hq + Hk ? a.k : a.v;
+            const int row = m.row < Hq ? m.row : m.row < Hq + Hk ? m.row - Hq : m.row - Hq - Hk;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(h.data) +
+                                                              (t0 + m.token) * h.token_stride + row * h.head_stride);
+            va = src[m.a];
+            if (m.b < g.vecs) vb = src[m.b];
         }
     };
-    uint4 na[kRopeBatch], nb[kRopeBatch];
-    uint32_t x0 = blockIdx.y * kRopeThreads + tid;
-    load(x0, na, nb);
+    uint4 na, nb;  // the next item, in flight
+    uint32_t x = blockIdx.y * kRopeThreads + tid;
+    load(x, na, nb);
     if (tid < tokens) s_at[tid] = slot_offset(a, a.slot[t0 + tid]);
     for (int y = tid; y < tokens * g.half; y += kRopeThreads) {
         const int i = y / g.half, pair = y - i * g.half;
@@ -147,56 +142,46 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const __grid_c
     }
     __syncthreads();
 
-    for (; x0 < total; x0 += kRopeBatch * step) {
-        uint4 va[kRopeBatch], vb[kRopeBatch];
+    for (; x < total; x += step) {
+        const uint4 va = na, vb = nb;
+        load(x + step, na, nb);
+        const RopeItem m = item_of<SIDE>(a, g, x);
+        uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+        if (m.pair >= 0) {
+            const float4* cs = reinterpret_cast<const float4*>(&s_cs[m.token][m.pair]);
+            if (SIDE) {
+                // the last rotated item may hold fewer than eight pairs: the others pass
 #pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-            va[u] = na[u];
-            vb[u] = nb[u];
-        }
-        load(x0 + kRopeBatch * step, na, nb);
+                for (int e = 0; e < 8; ++e) {
+                    uint32_t& w = e < 4 ? wa[e] : wb[e - 4];
+                    const float4 f2 = cs[e / 2];
+                    const float c = e & 1 ? f2.z : f2.x, s = e & 1 ? f2.w : f2.y;
+                    const float2 v = unpack2<F16>(w);
+                    if (m.pair + e < g.half) w = pack2<F16>(fmaf(-v.y, s, v.x * c), fmaf(v.x, s, v.y * c));
+                }
+            } else {
 #pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-            const uint32_t x = x0 + u * step;
-            if (x >= total) break;
-            const RopeItem m = item_of<SIDE>(a, g, x);
-            uint32_t wa[4] = {va[u].x, va[u].y, va[u].z, va[u].w}, wb[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
-            if (m.pair >= 0) {
-                const float4* cs = reinterpret_cast<const float4*>(&s_cs[m.token][m.pair]);
-                if (SIDE) {
-                    // the last rotated item may hold fewer than eight pairs: the others pass
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t& w = e < 4 ? wa[e] : wb[e - 4];
-                        const float4 f2 = cs[e / 2];
-                        const float c = e & 1 ? f2.z : f2.x, s = e & 1 ? f2.w : f2.y;
-                        const float2 v = unpack2<F16>(w);
-                        if (m.pair + e < g.half) w = pack2<F16>(fmaf(-v.y, s, v.x * c), fmaf(v.x, s, v.y * c));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 f = cs[e];  // two pairs
-                        const float2 v = unpack2<F16>(wa[e]), w = unpack2<F16>(wb[e]);
-                        wa[e] = pack2<F16>(fmaf(-w.x, f.y, v.x * f.x), fmaf(-w.y, f.w, v.y * f.z));
-                        wb[e] = pack2<F16>(fmaf(v.x, f.y, w.x * f.x), fmaf(v.y, f.w, w.y * f.z));
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float4 f = cs[e];  // two pairs
+                    const float2 v = unpack2<F16>(wa[e]), w = unpack2<F16>(wb[e]);
+                    wa[e] = pack2<F16>(fmaf(-w.x, f.y, v.x * f.x), fmaf(-w.y, f.w, v.y * f.z));
+                    wb[e] = pack2<F16>(fmaf(v.x, f.y, w.x * f.x), fmaf(v.y, f.w, w.y * f.z));
                 }
             }
-            uint4* dst;
-            if (m.row < Hq) {
-                dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) +
-                                               (t0 + m.token) * a.q_out.token_stride + m.row * a.q_out.head_stride);
-            } else {
-                const int64_t at = s_at[m.token];
-                if (at < 0) continue;
-                const bool key = m.row < Hq + Hk;
-                dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(key ? a.cache.k : a.cache.v) + at +
-                                               (m.row - (key ? Hq : Hq + Hk)) * a.cache.head_stride);
-            }
-            dst[m.a] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-            if (m.b < g.vecs) dst[m.b] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
         }
+        uint4* dst;
+        if (m.row < Hq) {
+            dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) +
+                                           (t0 + m.token) * a.q_out.token_stride + m.row * a.q_out.head_stride);
+        } else {
+            const int64_t at = s_at[m.token];
+            if (at < 0) continue;
+            const bool key = m.row < Hq + Hk;
+            dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(key ? a.cache.k : a.cache.v) + at +
+                                           (m.row - (key ? Hq : Hq + Hk)) * a.cache.head_stride);
+        }
+        dst[m.a] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+        if (m.b < g.vecs) dst[m.b] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
     }
 }
 

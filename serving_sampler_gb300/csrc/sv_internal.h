@@ -180,8 +180,8 @@ struct AttnArgs {
     void* workspace;
     int32_t stop_cta;  // self-test: the CTA that gives up at its first wait, -1 for none
 };
-size_t attn_workspace_bytes(int32_t R, int32_t T, int32_t max_tokens, int32_t heads, int32_t kv_heads,
-                            int32_t head_dim, int64_t max_kv);
+size_t attn_workspace_bytes(int32_t R, int32_t max_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                            int64_t max_kv);
 cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream);
 
 // number of SMs of the current device

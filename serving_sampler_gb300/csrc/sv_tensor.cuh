@@ -84,7 +84,7 @@ __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fenc
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 8 and 16 columns of the thread's lane
+// 16 and 32 columns of the thread's lane
 __device__ __forceinline__ void tmem_ld(uint32_t (&r)[16], uint32_t addr)
 {
     asm volatile(
