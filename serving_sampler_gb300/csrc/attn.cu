@@ -247,6 +247,14 @@ struct Ring {
             phase ^= 1u;
         }
     }
+    __device__ __forceinline__ void prev2(int32_t n)
+    {
+        stage -= 2;
+        if (stage < 0) {
+            stage += n;
+            phase ^= 1u;
+        }
+    }
 };
 
 struct Shared {
@@ -256,7 +264,6 @@ struct Shared {
     uint64_t g_done, o_free[2];                  // a phase per group whose keys are split (o_free: of every other)
     uint64_t run_full[kRunRing], run_empty[kRunRing];
     uint64_t drain;
-    uint32_t filled[2];  // by the copiers of K and V, when they end
     Run runs[kRunRing];
     uint64_t v_ok[kMaxStages];  // the stage's V has been cleaned
     int64_t scan[16];
@@ -443,9 +450,9 @@ __device__ void find_share(const AttnParams& p, Shared& sh, const Lengths& x)
 }
 
 // ---- warps 0 and 2: K and V --------------------------------------------------------
-// Tile t of the line fills stages 2 t (K) and 2 t + 1 (V) of the ring; warp 0 copies K
-// and warp 2 V (one warp for both could not issue the copies of 16-token blocks fast
-// enough).  Lane i copies box i.
+// Tile t of the line fills stages 2 t (K) and 2 t + 1 (V) of the ring, whose number of stages
+// is even: K and V have stages of their own.  Warp 0 copies K and warp 2 V (one warp for both
+// could not issue the copies of 16-token blocks fast enough).  Lane i copies box i.
 template <int DP>
 __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring, const CUtensorMap* map, int first)
 {
@@ -454,7 +461,7 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
     const int lane = threadIdx.x & 31;
     Runs runs;
     Ring rt{first, 0};
-    uint32_t fills = 0;  // of this warp; from the ring's second turn on a stage is waited for
+    int32_t fills = 0;  // of this warp; from the ring's second turn on a stage is waited for
     bool ok = true;
     const int32_t subs = kTile / p.box_rows;
     const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
@@ -480,7 +487,7 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
             const int32_t live = min(subs, (u.kv_end - x0 + p.box_rows - 1) / p.box_rows);
             uint64_t* full = &sh.kv_full[rt.stage];
             // the stage's fill before this one is the ring's last turn: `first + 2 * fills` stages in
-            if (first + 2 * fills >= static_cast<uint32_t>(p.stages) && !warp_wait(&sh.kv_empty[rt.stage], rt.phase ^ 1u, sh)) {
+            if (first + 2 * fills >= p.stages && !warp_wait(&sh.kv_empty[rt.stage], rt.phase ^ 1u, sh)) {
                 ok = false;
                 break;
             }
@@ -493,24 +500,15 @@ __device__ void copy_tiles(const AttnParams& p, Shared& sh, unsigned char* ring,
                     tma_load_4d(dst + lane * box_bytes + ch * kTile * 128, map, full, ch * 64, place, u.head, block);
             }
             __syncwarp();
-            ++fills;
+            fills = min(fills + 1, 1 << 20);
             rt.next2(p.stages);
         }
     }
-    if (lane == 0) sh.filled[first] = fills;
-}
-
-// A CTA that gave up does not leave before its copies have landed.  Line 2 i + c of the ring is fill i of
-// copier c.  Each stage's last fill is waited for; of an earlier one the barrier's parity would say nothing.
-__device__ void drain_tiles(const AttnParams& p, Shared& sh)
-{
-    const uint32_t stages = static_cast<uint32_t>(p.stages);
-    for (uint32_t c = 0; c < 2; ++c) {
-        const uint32_t fills = sh.filled[c], end = c + 2 * fills;              // behind the copier's lines,
-        const uint32_t other = stages % 2 ? 1 - c + 2 * sh.filled[1 - c] : end;  // and those of the next fill of a stage
-        for (uint32_t i = fills - min(fills, (stages + 1) / 2); i < fills; ++i) {
-            const uint32_t line = c + 2 * i;
-            if (line + stages >= other) mbar_wait_bounded(&sh.kv_full[line % stages], (line / stages) & 1u);
+    // a CTA that gave up does not leave before its copies have landed: the last fill of each of the copier's stages
+    if (!ok || sh.stop != 0) {
+        for (int32_t i = min(fills, p.stages / 2); i > 0; --i) {
+            rt.prev2(p.stages);
+            mbar_wait_bounded(&sh.kv_full[rt.stage], rt.phase);
         }
     }
 }
@@ -1299,7 +1297,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_fence_after();
     if (warp == 2) tmem_dealloc(tmem, 512);
     if (tid == 0) p.flags[blockIdx.x] = sh.stop != 0 ? kFlagTimeout : 0u;
-    if (warp == 0 && sh.stop != 0) drain_tiles(p, sh);
 }
 
 // ---- groups that were cut across CTAs -----------------------------------------------------------
@@ -1576,11 +1573,11 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream)
     p.sms = attn_ctas();
     p.by_sms = divisor_of(p.sms);
     p.wave = std::max(1, p.sms / p.kv_heads);
-    // the ring takes what Q leaves of an SM's 227 KB: 5 or 6 stages of 32 KB, 12 of 16 KB.  Where Q fills
-    // its tile, 5 and 12 just leave the 3,072 bytes of `Shared`'s place; with one stage fewer 64 x 65 tokens
-    // took 209.6 us a call instead of 210.5, and 17 x 33 the same 49.3: the ring does not bound them.
+    // The ring takes what Q leaves of an SM's 227 KB, in pairs of a stage for K and one for V: 4 or 6 of 32 KB,
+    // 12 of 16 KB.  A fifth stage of 32 KB, of which K and V take turns, costs more than it gives: 210.4 us a
+    // call for 64 x 65 tokens instead of 205.8, 233.3 for 64 x 32 with 4 heads to a key head instead of 226.0.
     const size_t fixed = attn_shared_bytes(dp, 0, p.q_chunk);
-    p.stages = static_cast<int32_t>(std::min<size_t>(kMaxStages, (kMaxShared - fixed) / (kTile * dp * 2)));
+    p.stages = static_cast<int32_t>(std::min<size_t>(kMaxStages, (kMaxShared - fixed) / (kTile * dp * 2))) & ~1;
     // a scale of 0 weighs all alike; the smallest factor keeps hidden scores at -inf
     p.c = std::max(fabsf(a.scale) * 1.44269504088896341f, 1e-30f);
     p.word_qk = product_word(f16, kTile, kTile, false, a.scale < 0.0f);
