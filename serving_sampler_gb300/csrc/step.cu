@@ -249,9 +249,10 @@ __device__ __forceinline__ Keep keep_of(const CommitArgs& c, int32_t r)
     Keep q;
     q.root = c.seq_len[r];
     q.n = c.cu_tokens[r + 1] - c.cu_tokens[r];
+    const int32_t kv = c.kv_len[r], accepted = c.accept_len[r];  // loaded with the lengths before
     const int64_t room = static_cast<int64_t>(c.max_blocks) * c.cache.block_size;
-    q.takes = q.root >= 0 && q.n > 0 && static_cast<int64_t>(q.root) + q.n == c.kv_len[r] && c.kv_len[r] <= room;
-    q.a = q.takes ? min(max(c.accept_len[r], 0), c.k) : 0;
+    q.takes = q.root >= 0 && q.n > 0 && static_cast<int64_t>(q.root) + q.n == kv && kv <= room;
+    q.a = q.takes ? min(max(accepted, 0), c.k) : 0;
     q.bad = false;
     if (c.path != nullptr) {
         int32_t last = 0;
@@ -270,7 +271,7 @@ __device__ __forceinline__ Keep keep_of(const CommitArgs& c, int32_t r)
         q.bad = most < q.a;
         q.a = most;
     }
-    q.held = q.takes ? blocks_of(c.kv_len[r], c.by_block) : 0;
+    q.held = q.takes ? blocks_of(kv, c.by_block) : 0;
     q.kept = q.takes ? blocks_of(q.root + 1 + q.a, c.by_block) : 0;
     return q;
 }
