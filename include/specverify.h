@@ -504,12 +504,14 @@ int sv_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, c
 /* Frequencies for sv_rope_cache, computed on the host in fp64 into HOST
  * uint64 [rot_dim / 2].  inv_freq_i = base^(-2 i / rot_dim), then by `scaling`:
  *   SV_ROPE_PLAIN     as it is;
- *   SV_ROPE_LINEAR    / factor (positions interpolated);
+ *   SV_ROPE_LINEAR    / factor (positions interpolated; Chen et al. 2023, arXiv:2306.15595);
  *   SV_ROPE_BASE      the base raised to base * factor^(rot_dim / (rot_dim - 2));
  *   SV_ROPE_BY_DIM    per pair between inv_freq (kept, pairs that turn more than
  *                     `high` times within `trained` positions) and inv_freq / factor
  *                     (fewer than `low`), blended linearly in the pair's index;
- *   SV_ROPE_BY_TURNS  the same, blended linearly in the number of turns. */
+ *   SV_ROPE_BY_TURNS  the same, blended linearly in the number of turns.
+ * The scalings by parts are those of Peng et al. 2023 (arXiv:2309.00071), whose ramp
+ * is the one in turns. */
 enum { SV_ROPE_PLAIN = 0, SV_ROPE_LINEAR = 1, SV_ROPE_BASE = 2, SV_ROPE_BY_DIM = 3, SV_ROPE_BY_TURNS = 4 };
 int sv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained, double low,
                   double high, uint64_t* freqs);

@@ -101,8 +101,9 @@ __device__ __forceinline__ Ask ask_of(const StepTablesArgs& a, int32_t r)
 // falling order of their number (a parent lies below its child), so the words of
 // its mask come out one after the other, from the highest to the lowest, without
 // any storage beyond the word in hand.
-// Bound by latency: sums over the lengths, a block's ids, then a chain of parents as deep
-// as the tree.  11.8 us for 1,024 requests of 65 tokens (1.9 MB), 3 for one of 9.
+// Bound by latency: the sums over the lengths before a CTA's range with their block reductions, a
+// block's ids, then the words of the masks.  11.9 us for 1,024 requests of 65 tokens (1.9 MB), 3 for
+// one of 9; the parts have not been timed apart.
 __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepTablesArgs a)
 {
     __shared__ int64_t s_sum[2 * kStepWarps];
@@ -307,7 +308,8 @@ constexpr int kMoveBatch = 8;
 // looked up once per CTA, all at a time, so that a round is one trip to memory.
 // Bound by the latency of a path's ceil(a / 8) rounds for few requests and by memory
 // for many: 9.9 us for 64 requests over 16 layers, 34 MB, 3.4 TB/s (20 us with the places
-// looked up token by token), 3.3 us for 4 requests over 4 layers.
+// looked up token by token), 8.0 where they lie in L2; 3.3 us for 4 requests over 4 layers.  By path
+// every thread checks the whole path: 16.6 us from a cold L2, where a branch takes 11.5.
 __global__ void __launch_bounds__(kStepThreads) cache_commit_kernel(const CommitArgs c, int32_t releasers)
 {
     __shared__ int64_t s_sum[2 * kStepWarps];
