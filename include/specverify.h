@@ -82,7 +82,10 @@ enum {
     SV_ST_NO_BLOCKS = 256,    /* sv_step_tables: no room for the request's tokens; it takes no part */
     SV_ST_BAD_TREE = 512,     /* a parent, branch or path that is no tree of the request's tokens */
     SV_ST_BAD_LENGTH = 1024,  /* a length that is negative or above what the tables can hold */
-    SV_ST_BAD_BLOCK = 2048    /* a block id outside the pool; the tokens in it are not in the cache */
+    SV_ST_BAD_BLOCK = 2048,   /* a block id outside the pool; the tokens in it are not in the cache */
+    SV_ST_BAD_PENALTY = 4096, /* sv_adjust_logits: a penalty that is no number it can be; left out */
+    SV_ST_BAD_MASK = 8192,    /* sv_adjust_logits: a mask index above the last mask; the row has none */
+    SV_ST_BAD_SOURCE = 16384  /* sv_cache_fork: no such source, or the row holds tokens; not forked */
 };
 
 /* limits */
@@ -96,6 +99,8 @@ enum {
 #define SV_MAX_HEAD_DIM 128   /* entries of a head (a multiple of 8) */
 #define SV_MAX_GROUP 128      /* query heads that share a key head */
 #define SV_MAX_TREE 2049      /* tokens of a drafted tree: the root and SV_MAX_BRANCHES * SV_MAX_K drafts */
+#define SV_MAX_HISTORY 524287 /* tokens of a request that sv_adjust_logits counts */
+#define SV_MAX_BLOCKS (1 << 22) /* blocks of a pool (sv_cache_free, sv_cache_compact) */
 
 /* A matrix of logit rows: row i, entry x is at data + (i * row_stride + x)
  * elements.  `data` must be aligned to the element size.  Rows whose start
@@ -379,6 +384,54 @@ int sv_suffix_append(int32_t* suffix, int32_t N, int32_t R, const int32_t* token
                      int32_t k, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * sv_adjust_logits -- penalties for repeated tokens, biases and grammar masks on
+ * the rows of a verify step, ahead of sv_verify_greedy or sv_verify_sample.
+ * Source: "Decode Before You Hear ..." method steps 2 and 4: every row of a step is
+ * verified as if decoding had reached it, so its penalties count the drafts on the
+ * way to it.
+ *
+ *   logits      rows of raw logits, width V, in the layout of sv_verify_greedy:
+ *               1 + branches * k rows a request, row 0 and the row behind draft i of
+ *               branch b at 1 + b * k + i.  branches 1 is that of sv_verify_sample;
+ *               k 0 is a plain decode step.
+ *   draft       int32 [R, branches, k]; NULL only where branches * k is 0.
+ *   rules       below.
+ *   out         rows of the adjusted logits, logits' dtype and width; may be logits
+ *               itself (same data and row_stride: only what changes is written), and
+ *               must not overlap it otherwise.
+ *   status      int32 [R] out or NULL.
+ * For token x in a row, z its logit in fp32:
+ *   seen   x is among the request's history or the drafts before the row;
+ *   count  times x occurs in the history behind the prompt and in those drafts;
+ *   z = seen ? (z > 0 ? z / repetition : z * repetition) : z   (Keskar et al. 2019)
+ *   z = count > 0 ? z - (presence + frequency * count) : z
+ *   z = z + bias(x)
+ *   out = x is allowed ? z rounded once : -inf, whatever z is.
+ * A row that allows nothing is all -inf.  Entries that no rule meets keep their
+ * bits, NaN among them.
+ * Drafts, history tokens and bias ids outside [0, V) are passed over and set
+ * SV_ST_TOKEN_RANGE; a length outside its range is clamped (SV_ST_BAD_LENGTH).
+ * ---------------------------------------------------------------------- */
+typedef struct sv_logit_rules {
+    const int32_t* history;     /* [R, history_width]: the prompt, then the output, root token included; or NULL */
+    const int32_t* history_len; /* [R]: tokens of history, in [0, history_width] */
+    const int32_t* prompt_len;  /* [R]: of them the prompt's, in [0, history_len]; NULL: none */
+    int32_t history_width;      /* <= SV_MAX_HISTORY */
+    const float* repetition;    /* [R], > 0 and finite (1: none); NULL: none.  Else SV_ST_BAD_PENALTY and none */
+    const float* presence;      /* [R], finite; NULL: none */
+    const float* frequency;     /* [R], finite; NULL: none */
+    const int32_t* bias_start;  /* [R + 1]: request r's biases are entries bias_start[r] .. bias_start[r + 1) - 1 */
+    const int32_t* bias_id;     /* [bias_entries]; of an id given twice the last entry counts */
+    const float* bias_value;    /* [bias_entries]; -inf bans a token */
+    int32_t bias_entries;       /* 0: no biases (bias_start may be NULL) */
+    const uint32_t* mask;       /* [masks, mask_words]: bit x % 32 of word x / 32 allows token x; NULL: no masks */
+    int32_t masks, mask_words;  /* mask_words * 32 >= V */
+    const int32_t* mask_row;    /* one for each row of logits: its mask, negative for none; NULL: row i has mask i */
+} sv_logit_rules;
+int sv_adjust_logits(sv_rows logits, int32_t R, int32_t k, int32_t branches, const int32_t* draft,
+                     sv_logit_rules rules, sv_rows out, int32_t* status, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * sv_accept_scan -- accept length and commit from caller-given accept flags.
  * Source: "Decode Before You Hear ..." step 4 (the accepted prefix stops at
  * the first failure); "speculative decoding for Omni models" section 3
@@ -501,6 +554,23 @@ int sv_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, c
                   const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float mscale, sv_heads q_out,
                   sv_kv_cache cache, sv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * sv_norm_rope_cache -- sv_rope_cache with an RMS norm of every head of q and k
+ * ahead of the rotation, in the same pass.
+ *
+ *   q_weight, k_weight  [head_dim] of weight_dtype (that of the heads, or SV_F32), or
+ *               NULL for weights of 1.
+ *   eps         >= 0 and finite.
+ * Every head x of q and k becomes y = x * (mean(x^2) + eps)^(-1/2) * weight over its
+ * head_dim entries (Zhang and Sennrich 2019), then is rotated as by sv_rope_cache; v is
+ * not normed.  All in fp32, rounded once.  The other arguments, their limits and what
+ * is written where are those of sv_rope_cache.
+ * ---------------------------------------------------------------------- */
+int sv_norm_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, const int64_t* slot,
+                       const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float mscale,
+                       const void* q_weight, const void* k_weight, int32_t weight_dtype, float eps, sv_heads q_out,
+                       sv_kv_cache cache, sv_stream_t stream);
+
 /* Frequencies for sv_rope_cache, computed on the host in fp64 into HOST
  * uint64 [rot_dim / 2].  inv_freq_i = base^(-2 i / rot_dim), then by `scaling`:
  *   SV_ROPE_PLAIN     as it is;
@@ -580,6 +650,81 @@ int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_b
                     const int32_t* branch, const int32_t* path, int32_t k, int32_t* free_blocks,
                     const int32_t* free_count, int32_t* seq_len_out, int32_t* free_count_out, int32_t* status,
                     sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages: sessions branched into several, sessions that leave, a pool packed to its
+ * front.  A request holds the blocks of its first ceil(seq_len / block_size) table
+ * entries.  Requests may hold a block together as long as all of its places are
+ * committed tokens': sv_step_tables, sv_rope_cache and sv_cache_commit write behind
+ * seq_len alone, so they never write such a block or give it back.  The tables are
+ * the only record of who holds what.
+ *
+ * In all three calls a seq_len outside [0, max_blocks * block_size] sets
+ * SV_ST_BAD_LENGTH, and a held block id outside [0, num_blocks) SV_ST_BAD_BLOCK; that
+ * entry is passed over.  The outputs must not overlap the inputs.  A call repeated on
+ * the same inputs writes the same values.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * sv_cache_fork -- requests that go on from another one's tokens.
+ *
+ *   cache       every layer (layers, layer_stride).
+ *   block_table int32 [R, max_blocks] in/out: the rows of new forks are written.
+ *   seq_len     int32 [R].
+ *   source      int32 [R]: the row that row r becomes a copy of, negative for none.  Row
+ *               r must hold no tokens (seq_len 0), the source may be given many times.
+ *   free_blocks int32 [num_blocks], free_count int32 [1]: as sv_step_tables takes them.
+ *   seq_len_out int32 [R] out: the source's length for a fork, seq_len for the others.
+ *   free_count_out int32 [1] out;  status int32 [R] out or NULL.
+ * A fork holds its source's full blocks together with it.  Where the last block is not
+ * full, its tokens' keys and values of every layer are copied into a block from the
+ * free stack.  Forks are served in order of r: once no block is left, those that need
+ * one are not made (SV_ST_NO_BLOCKS).  A source outside [0, R), or a row that holds
+ * tokens, is no fork (SV_ST_BAD_SOURCE); nor is a source of a bad length.
+ * layers * kv_heads * head_dim / 4 is at most 65535 * 128.
+ * ---------------------------------------------------------------------- */
+int sv_cache_fork(sv_kv_cache cache, int32_t* block_table, int32_t max_blocks, const int32_t* seq_len, int32_t R,
+                  const int32_t* source, const int32_t* free_blocks, const int32_t* free_count, int32_t* seq_len_out,
+                  int32_t* free_count_out, int32_t* status, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * sv_cache_free -- requests that leave.
+ *
+ *   block_table int32 [R, max_blocks];  seq_len int32 [R].
+ *   leave       int32 [R]: nonzero for a request that leaves.
+ *   free_blocks int32 [num_blocks] in/out, free_count int32 [1]: the blocks of leaving
+ *               requests that no other request holds and that are not on the stack
+ *               already are pushed, by rising id.
+ *   seq_len_out int32 [R] out: 0 for a request that leaves, seq_len for the others.
+ *   free_count_out int32 [1] out;  status int32 [R] out or NULL.
+ * A leaving request of a bad length gives nothing back and keeps its length; one that
+ * stays with a length above its table holds every entry of it.
+ * num_blocks <= SV_MAX_BLOCKS.
+ * ---------------------------------------------------------------------- */
+int sv_cache_free(const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len, const int32_t* leave,
+                  int32_t R, int32_t block_size, int32_t* free_blocks, const int32_t* free_count, int32_t num_blocks,
+                  int32_t* seq_len_out, int32_t* free_count_out, int32_t* status, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * sv_cache_compact -- the held blocks at the front of the pool.
+ *
+ *   cache       every layer; moved in place.
+ *   block_table int32 [R, max_blocks];  seq_len int32 [R].
+ *   block_table_out int32 [R, max_blocks] out: the tables after the move, -1 behind a
+ *               request's held entries.  Not block_table itself.
+ *   free_blocks int32 [num_blocks] out: the free stack, num_blocks - 1 at the bottom, -1
+ *               behind its free_count entries.  The lowest free id is taken first.
+ *   free_count  int32 [1] out: num_blocks - U, U the number of blocks held.
+ *   status      int32 [R] out or NULL.
+ * The i-th held block with an id of U or more (in rising order) moves to the i-th id below
+ * U that nobody holds; the others stay.  Blocks held by no request lose their
+ * contents.  A length above the table holds every entry of it, a negative one none.
+ * num_blocks <= SV_MAX_BLOCKS.  Workspace: sv_cache_compact_workspace(num_blocks).
+ * ---------------------------------------------------------------------- */
+size_t sv_cache_compact_workspace(int32_t num_blocks);
+int sv_cache_compact(sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len,
+                     int32_t R, int32_t* block_table_out, int32_t* free_blocks, int32_t* free_count, int32_t* status,
+                     void* workspace, size_t workspace_bytes, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * sv_selftest_wait_timeout -- a self-test of the library's bounded waits; the

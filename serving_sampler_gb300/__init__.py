@@ -8,8 +8,10 @@ fallback.  If the library has not been built, ``load()`` raises.
 
 Entry points (same names as the C ABI in include/specverify.h):
   verify_greedy, verify_sample, cfg_merge_sample, accept_scan
-  step_tables, rope_cache (with rope_freqs), tree_attention, cache_commit: the
-  cache side of a verify step
+  adjust_logits: penalties, biases and grammar masks on the rows before them
+  step_tables, rope_cache or norm_rope_cache (with rope_freqs), tree_attention,
+  cache_commit: the cache side of a verify step
+  cache_fork, cache_free, cache_compact: the pages that sessions begin and end with
 
 Every call runs on the current stream, or on ``stream=``.  What it allocates by
 itself belongs to that stream; its inputs must be ready on it and stay alive
@@ -28,8 +30,10 @@ SV_BF16, SV_F32, SV_F16 = 0, 1, 2
 ST_TOKEN_RANGE, ST_BAD_LOGITS, ST_OFF_SUPPORT, ST_RESIDUAL_ZERO = 1, 2, 4, 8
 ST_BAD_TEMP, ST_BAD_D2T, ST_TIMEOUT, ST_POOL_FULL = 16, 32, 64, 128
 ST_NO_BLOCKS, ST_BAD_TREE, ST_BAD_LENGTH, ST_BAD_BLOCK = 256, 512, 1024, 2048
+ST_BAD_PENALTY, ST_BAD_MASK, ST_BAD_SOURCE = 4096, 8192, 16384
 MAX_K, MAX_S, MAX_NGRAM, MAX_POOL = 256, 16, 64, 1 << 24
 MAX_HEAD_DIM, MAX_GROUP, MAX_TREE = 128, 128, 2049
+MAX_HISTORY, MAX_BLOCKS = 524287, 1 << 22
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_DIM, ROPE_BY_TURNS = 0, 1, 2, 3, 4
 
 # kernels launched by one call of each entry point (reported by the benchmark)
@@ -37,7 +41,8 @@ ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_DIM, ROPE_BY_TURNS = 0, 1, 2, 3, 4
 # launches 2, and 2 more when it builds the plan itself; d2t_plan launches 2
 LAUNCHES = {"verify_greedy": 2, "verify_greedy_top2": 2, "infer_modality": 2, "pool_append": 1, "pool_lookup": 1, "suffix_append": 1, "verify_sample": 2, "verify_sample_plan_in_call": 4, "d2t_plan": 2,
             "cfg_merge_sample": 2, "accept_scan": 1, "step_tables": 1, "rope_cache": 1, "tree_attention": 2,
-            "cache_commit": 1}
+            "cache_commit": 1, "adjust_logits": 1, "norm_rope_cache": 1, "cache_fork": 1, "cache_free": 1,
+            "cache_compact": 2}
 
 
 class SpecVerifyError(RuntimeError):
@@ -60,6 +65,14 @@ class SvKvCache(C.Structure):
 class SvHeads(C.Structure):
     _fields_ = [("data", C.c_void_p), ("dtype", C.c_int32), ("tokens", C.c_int32), ("heads", C.c_int32),
                 ("head_dim", C.c_int32), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class SvLogitRules(C.Structure):
+    _fields_ = [("history", C.c_void_p), ("history_len", C.c_void_p), ("prompt_len", C.c_void_p),
+                ("history_width", C.c_int32), ("repetition", C.c_void_p), ("presence", C.c_void_p),
+                ("frequency", C.c_void_p), ("bias_start", C.c_void_p), ("bias_id", C.c_void_p),
+                ("bias_value", C.c_void_p), ("bias_entries", C.c_int32), ("mask", C.c_void_p), ("masks", C.c_int32),
+                ("mask_words", C.c_int32), ("mask_row", C.c_void_p)]
 
 
 _lib = None
@@ -121,6 +134,14 @@ def load(path: str | None = None):
     lib.sv_tree_attention.argtypes = [SvHeads, SvKvCache, P, i32, P, P, i32, i32, P, i32, f32, SvHeads, P, P, P, sz, P]
     lib.sv_selftest_tree_attention_stop.argtypes = lib.sv_tree_attention.argtypes[:-1] + [i32, P]
     lib.sv_cache_commit.argtypes = [SvKvCache, P, i32, P, P, P, i32, P, P, P, i32, P, P, P, P, P, P]
+    lib.sv_norm_rope_cache.argtypes = [SvHeads, SvHeads, SvHeads, P, P, P, i32, i32, f32, P, P, i32, f32, SvHeads,
+                                       SvKvCache, P]
+    lib.sv_adjust_logits.argtypes = [SvRows, i32, i32, i32, P, SvLogitRules, SvRows, P, P]
+    lib.sv_cache_fork.argtypes = [SvKvCache, P, i32, P, i32, P, P, P, P, P, P, P]
+    lib.sv_cache_free.argtypes = [P, i32, P, P, i32, i32, P, P, i32, P, P, P, P]
+    lib.sv_cache_compact_workspace.argtypes = [i32]
+    lib.sv_cache_compact_workspace.restype = sz
+    lib.sv_cache_compact.argtypes = [SvKvCache, P, i32, P, i32, P, P, P, P, P, sz, P]
     lib.sv_selftest_wait_timeout.argtypes = [P, P, C.c_int64, P]
     lib.sv_selftest_wait_timeout.restype = C.c_int
     _lib = lib
@@ -543,6 +564,41 @@ def rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, interleaved: bo
     return q_out
 
 
+def _weight(w, name, D: int):
+    """The address of a norm's weights, which are passed as they lie."""
+    if w is None:
+        return None
+    if not w.is_cuda or not w.is_contiguous() or w.numel() != D:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {D} weights")
+    return w.data_ptr()
+
+
+def norm_rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    interleaved: bool = False, mscale: float = 1.0, q_out=None, stream=None):
+    """rope_cache with an RMS norm over the D entries of every head of q and k ahead of the rotation, in the same pass.
+    q_weight, k_weight [D]: weights in the heads' dtype or float32 (one dtype for both), or None for ones.  The other
+    arguments are those of rope_cache.  Returns the normed and rotated q (q_out may be q)."""
+    lib = load()
+    T, _, D = q.shape
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    if slot.dtype is not torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != T:
+        raise ValueError("slot must be a contiguous int64 CUDA tensor with an entry for each token")
+    if freqs.dtype not in (torch.int64, torch.uint64) or not freqs.is_cuda or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous int64 CUDA tensor from rope_freqs")
+    w = q_weight if q_weight is not None else k_weight
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have one dtype")
+    w_type = SV_F32 if w is None or w.dtype is torch.float32 else _half_type(w)
+    rc = lib.sv_norm_rope_cache(heads_of(q), heads_of(k), heads_of(v), _ints(position, "position", T), slot.data_ptr(),
+                                freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, mscale,
+                                _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D), w_type, eps,
+                                heads_of(q_out), cache_of(k_cache, v_cache), _raw_stream(stream, q))
+    if rc:
+        _check(rc)
+    return q_out
+
+
 def tree_attention_workspace(R: int, T: int, max_tokens: int, heads: int, kv_heads: int, head_dim: int,
                              max_kv: int) -> int:
     return int(load().sv_tree_attention_workspace(R, T, max_tokens, heads, kv_heads, head_dim, max_kv))
@@ -612,6 +668,158 @@ def cache_commit(k_cache, v_cache, block_table, seq_len, kv_len, cu_tokens, acce
                              _ints(free_blocks, "free_blocks", k_cache.shape[-4]), _ints(free_count, "free_count", 1),
                              out["seq_len"].data_ptr(), out["free_count"].data_ptr(), _at(out.get("status")),
                              _raw_stream(stream, seq_len))
+    if rc:
+        _check(rc)
+    return out
+
+
+def cache_fork(k_cache, v_cache, block_table, seq_len, source, free_blocks, free_count, out: dict | None = None,
+               stream=None) -> dict:
+    """Requests that go on from another one's tokens: row r of block_table int32 [R, max_blocks], which holds no tokens
+    (seq_len[r] 0), becomes a copy of row source[r] (int32 [R], negative for none).  Full blocks are held together; the
+    tokens of a last block that is not full are copied, in every layer of the caches ([layers, ] num_blocks,
+    block_size, kv_heads, head_dim), into a block from free_blocks int32 [num_blocks], of which free_count int32 [1]
+    are free.  The forks' rows are written in place.  Returns seq_len [R], free_count [1] and status [R]."""
+    lib = load()
+    R = seq_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be [R, max_blocks]")
+    a_seq = _ints(seq_len, "seq_len")
+    if out is None:
+        out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, stream, R, 1, R)))
+    else:
+        _check_out(out, seq_len=(torch.int32, R), free_count=(torch.int32, 1), status=(torch.int32, R))
+    if R == 0:
+        with torch.cuda.stream(stream):
+            out["free_count"].copy_(free_count)
+        return out
+    rc = lib.sv_cache_fork(cache_of(k_cache, v_cache), _ints(block_table, "block_table"), block_table.shape[1], a_seq, R,
+                           _ints(source, "source", R), _ints(free_blocks, "free_blocks", k_cache.shape[-4]),
+                           _ints(free_count, "free_count", 1), out["seq_len"].data_ptr(), out["free_count"].data_ptr(),
+                           _at(out.get("status")), _raw_stream(stream, seq_len))
+    if rc:
+        _check(rc)
+    return out
+
+
+def cache_free(block_table, seq_len, leave, free_blocks, free_count, block_size: int, out: dict | None = None,
+               stream=None) -> dict:
+    """Requests that leave (leave int32 [R], nonzero): the blocks that they hold and no other request does are pushed on
+    free_blocks int32 [num_blocks] by rising id.  Returns seq_len [R] (0 for those that left), free_count [1] and
+    status [R]."""
+    lib = load()
+    R = seq_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be [R, max_blocks]")
+    a_seq = _ints(seq_len, "seq_len")
+    if out is None:
+        out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, stream, R, 1, R)))
+    else:
+        _check_out(out, seq_len=(torch.int32, R), free_count=(torch.int32, 1), status=(torch.int32, R))
+    if R == 0:
+        with torch.cuda.stream(stream):
+            out["free_count"].copy_(free_count)
+        return out
+    rc = lib.sv_cache_free(_ints(block_table, "block_table"), block_table.shape[1], a_seq, _ints(leave, "leave", R), R,
+                           block_size, _ints(free_blocks, "free_blocks"), _ints(free_count, "free_count", 1),
+                           free_blocks.numel(), out["seq_len"].data_ptr(), out["free_count"].data_ptr(),
+                           _at(out.get("status")), _raw_stream(stream, seq_len))
+    if rc:
+        _check(rc)
+    return out
+
+
+def cache_compact_workspace(num_blocks: int) -> int:
+    return int(load().sv_cache_compact_workspace(num_blocks))
+
+
+def cache_compact(k_cache, v_cache, block_table, seq_len, out: dict | None = None, workspace=None, stream=None) -> dict:
+    """The blocks that the requests hold at the front of the pool: those above move into the gaps, in every layer of the
+    caches ([layers, ] num_blocks, block_size, kv_heads, head_dim).  Returns the new block_table [R, max_blocks] (-1
+    behind a request's blocks), free_blocks [num_blocks] (the lowest id on top, -1 behind them), free_count [1] and
+    status [R].  Blocks that no request holds lose their contents."""
+    lib = load()
+    R = seq_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be [R, max_blocks]")
+    cache = cache_of(k_cache, v_cache)
+    n, most = cache.num_blocks, block_table.shape[1]
+    if out is None:
+        table, free, count, status = _new_ints(seq_len, stream, R * most, n, 1, R)
+        out = dict(block_table=table.view(R, most), free_blocks=free, free_count=count, status=status)
+    else:
+        i32 = torch.int32
+        _check_out(out, block_table=(i32, R * most), free_blocks=(i32, n), free_count=(i32, 1), status=(i32, R))
+    if workspace is None:
+        workspace = _workspace(lib.sv_cache_compact_workspace(n), seq_len.device, None, stream)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    rc = lib.sv_cache_compact(cache, _ints(block_table, "block_table"), most, _ints(seq_len, "seq_len"), R,
+                              out["block_table"].data_ptr(), out["free_blocks"].data_ptr(),
+                              out["free_count"].data_ptr(), _at(out.get("status")), workspace.data_ptr(),
+                              _nbytes(workspace), _raw_stream(stream, seq_len))
+    if rc:
+        _check(rc)
+    return out
+
+
+def _floats(t, name, n):
+    """The address of a float32 CUDA tensor that is passed as it lies."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} entries")
+    return t.data_ptr()
+
+
+def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=None, history_len=None, prompt_len=None,
+                  repetition=None, presence=None, frequency=None, bias=None, mask=None, mask_row=None,
+                  out: dict | None = None, stream=None) -> dict:
+    """Penalties for repeated tokens, biases and grammar masks on a verify step's rows of logits
+    [R * (1 + branches * k), V] (the layout of verify_greedy; branches 1 is that of verify_sample, k 0 a plain step).
+
+    draft int32 [R, branches, k]; history int32 [R, width], of which history_len int32 [R] are the request's tokens so
+    far and prompt_len int32 [R] (or None) of those its prompt; repetition, presence, frequency float32 [R] or None;
+    bias (start int32 [R + 1], ids int32 [n], values float32 [n]) or None: request r's are start[r] .. start[r + 1] - 1;
+    mask int32 [masks, words] of allowed ids as bits with mask_row int32 [rows] (negative: none), or a mask for each row
+    without mask_row.  A row's drafts count as said before it.  Returns logits (out=dict(logits=logits) works in
+    place) and status [R]."""
+    lib = load()
+    rows = R * (1 + branches * k)
+    if logits.dim() != 2 or logits.shape[0] < rows:
+        raise ValueError(f"logits must be [{rows}, V]")
+    V = logits.shape[1]
+    if out is None:
+        out = dict(logits=_empty((rows, V), logits.dtype, logits.device, stream),
+                   status=_empty(R, torch.int32, logits.device, stream))
+    else:
+        _check_out(out, status=(torch.int32, R))
+        if out["logits"].dim() != 2 or out["logits"].shape[0] < rows:
+            raise ValueError(f"out['logits'] must be [{rows}, V]")
+    if V > 1 and (logits.stride(1) != 1 or out["logits"].stride(1) != 1):
+        raise ValueError("entries of a logit row must be contiguous")
+    if draft is None and branches * k > 0:
+        raise ValueError("draft must be [R, branches, k]")
+    if history is not None and (history.dim() != 2 or history.shape[0] != R or history_len is None):
+        raise ValueError("history must be [R, width], with history_len")
+    if mask is not None and mask.dim() != 2:
+        raise ValueError("mask must be [masks, words]")
+    start, ids, values = bias if bias is not None else (None, None, None)
+    n = 0 if bias is None else ids.numel()
+    rules = SvLogitRules(
+        None if history is None else _ints(history, "history"),
+        None if history is None else _ints(history_len, "history_len", R),
+        None if history is None or prompt_len is None else _ints(prompt_len, "prompt_len", R),
+        0 if history is None else history.shape[1], _floats(repetition, "repetition", R),
+        _floats(presence, "presence", R), _floats(frequency, "frequency", R),
+        None if bias is None else _ints(start, "the biases' start", R + 1),
+        None if bias is None else _ints(ids, "the biases' ids"), _floats(values, "the biases' values", n), n,
+        None if mask is None else _ints(mask, "mask"), 0 if mask is None else mask.shape[0],
+        0 if mask is None else mask.shape[1],
+        None if mask is None or mask_row is None else _ints(mask_row, "mask_row", rows))
+    rc = lib.sv_adjust_logits(rows_of(logits), R, k, branches,
+                              None if branches * k == 0 else _ints(draft, "draft", R * branches * k), rules,
+                              rows_of(out["logits"]), _at(out.get("status")), _raw_stream(stream, logits))
     if rc:
         _check(rc)
     return out

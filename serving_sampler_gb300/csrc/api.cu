@@ -96,6 +96,24 @@ static bool have_device()
     return cudaGetDevice(&dev) == cudaSuccess;
 }
 
+// Without tokens nothing but the sizes is looked at.
+static int check_rope(const RopeArgs& a)
+{
+    if (a.interleaved != 0 && a.interleaved != 1) return SV_ERR_INVALID_ARG;
+    if (a.q.tokens < 0) return SV_ERR_INVALID_ARG;
+    if (int rc = check_cache(a.cache, a.q.tokens > 0)) return rc;
+    if (a.cache.layers != 1) return SV_ERR_SHAPE;
+    if (a.rot_dim < 0 || a.rot_dim % 2 != 0 || a.rot_dim > a.cache.head_dim) return SV_ERR_SHAPE;
+    if (a.q.tokens == 0) return SV_OK;
+    for (const sv_heads* h : {&a.q, &a.k, &a.v, &a.q_out})
+        if (int rc = check_heads(*h, a.cache.dtype, a.cache.head_dim, a.q.tokens)) return rc;
+    if (a.k.heads != a.cache.kv_heads || a.v.heads != a.cache.kv_heads || a.q_out.heads != a.q.heads) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(a.q.heads) + 2 * static_cast<int64_t>(a.cache.kv_heads) > 65536) return SV_ERR_LIMIT;
+    if (a.position == nullptr || a.slot == nullptr || (a.rot_dim > 0 && a.freqs == nullptr)) return SV_ERR_INVALID_ARG;
+    if (!aligned(a.position, 4) || !aligned(a.slot, 8) || !aligned(a.freqs, 8)) return SV_ERR_ALIGN;
+    return SV_OK;
+}
+
 static int tree_attention(const AttnArgs& a, size_t workspace_bytes, sv_stream_t stream)
 {
     if (a.R < 0 || a.q.tokens < 0 || a.max_tokens < 0 || a.max_blocks < 0) return SV_ERR_INVALID_ARG;
@@ -451,24 +469,29 @@ int sv_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, c
                   const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float mscale, sv_heads q_out,
                   sv_kv_cache cache, sv_stream_t stream)
 {
-    if (interleaved != 0 && interleaved != 1) return SV_ERR_INVALID_ARG;
-    if (q.tokens < 0) return SV_ERR_INVALID_ARG;
-    if (int rc = check_cache(cache, q.tokens > 0)) return rc;
-    if (cache.layers != 1) return SV_ERR_SHAPE;
-    if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > cache.head_dim) return SV_ERR_SHAPE;
+    const RopeArgs a{q, k, v, q_out, position, slot, freqs, rot_dim, interleaved, mscale, cache};
+    if (int rc = check_rope(a)) return rc;
     if (q.tokens == 0) return SV_OK;
-    if (int rc = check_heads(q, cache.dtype, cache.head_dim, q.tokens)) return rc;
-    if (int rc = check_heads(k, cache.dtype, cache.head_dim, q.tokens)) return rc;
-    if (int rc = check_heads(v, cache.dtype, cache.head_dim, q.tokens)) return rc;
-    if (int rc = check_heads(q_out, cache.dtype, cache.head_dim, q.tokens)) return rc;
-    if (k.heads != cache.kv_heads || v.heads != cache.kv_heads || q_out.heads != q.heads) return SV_ERR_SHAPE;
-    if (static_cast<int64_t>(q.heads) + 2 * static_cast<int64_t>(cache.kv_heads) > 65536) return SV_ERR_LIMIT;
-    if (position == nullptr || slot == nullptr || (rot_dim > 0 && freqs == nullptr)) return SV_ERR_INVALID_ARG;
-    if (!aligned(position, 4) || !aligned(slot, 8) || !aligned(freqs, 8)) return SV_ERR_ALIGN;
     if (!have_device()) return SV_ERR_DEVICE;
-    return launched(launch_rope_cache(RopeArgs{q, k, v, q_out, position, slot, freqs, rot_dim, interleaved,
-                                               mscale, cache},
-                                      stream));
+    return launched(launch_rope_cache(a, stream));
+}
+
+int sv_norm_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, const int64_t* slot,
+                       const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float mscale,
+                       const void* q_weight, const void* k_weight, int32_t weight_dtype, float eps, sv_heads q_out,
+                       sv_kv_cache cache, sv_stream_t stream)
+{
+    const RopeArgs a{q, k, v, q_out, position, slot, freqs, rot_dim, interleaved, mscale, cache};
+    if (int rc = check_rope(a)) return rc;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return SV_ERR_INVALID_ARG;
+    if (q_weight != nullptr || k_weight != nullptr) {
+        if (weight_dtype != cache.dtype && weight_dtype != SV_F32) return SV_ERR_DTYPE;
+        const size_t size = weight_dtype == SV_F32 ? 4 : 2;
+        if (!aligned(q_weight, size) || !aligned(k_weight, size)) return SV_ERR_ALIGN;
+    }
+    if (q.tokens == 0) return SV_OK;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_norm_rope_cache(NormRopeArgs{a, q_weight, k_weight, weight_dtype, eps}, stream));
 }
 
 int sv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained, double low,
@@ -572,6 +595,112 @@ int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_b
                                                    accept_len, branch, path, k, divisor_of(cache.block_size),
                                                    free_blocks, free_count, seq_len_out, free_count_out, status},
                                         stream));
+}
+
+int sv_cache_fork(sv_kv_cache cache, int32_t* block_table, int32_t max_blocks, const int32_t* seq_len, int32_t R,
+                  const int32_t* source, const int32_t* free_blocks, const int32_t* free_count, int32_t* seq_len_out,
+                  int32_t* free_count_out, int32_t* status, sv_stream_t stream)
+{
+    if (R < 0 || max_blocks < 0) return SV_ERR_INVALID_ARG;
+    if (int rc = check_cache(cache, R > 0)) return rc;
+    // 128 16-byte columns of the heads to a row of the launch grid
+    if (2ll * cache.layers * cache.kv_heads * (cache.head_dim / 8) > 65535ll * 128) return SV_ERR_LIMIT;
+    if (static_cast<int64_t>(max_blocks) * cache.block_size > INT32_MAX) return SV_ERR_LIMIT;
+    if (R == 0) return SV_OK;
+    if (seq_len == nullptr || source == nullptr || free_blocks == nullptr || free_count == nullptr ||
+        seq_len_out == nullptr || free_count_out == nullptr || (max_blocks > 0 && block_table == nullptr))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(source, 4) || !aligned(free_blocks, 4) ||
+        !aligned(free_count, 4) || !aligned(seq_len_out, 4) || !aligned(free_count_out, 4) || !aligned(status, 4))
+        return SV_ERR_ALIGN;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_cache_fork(ForkArgs{cache, block_table, max_blocks, seq_len, R, source, free_blocks, free_count,
+                                               divisor_of(cache.block_size), seq_len_out, free_count_out, status},
+                                      stream));
+}
+
+int sv_cache_free(const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len, const int32_t* leave,
+                  int32_t R, int32_t block_size, int32_t* free_blocks, const int32_t* free_count, int32_t num_blocks,
+                  int32_t* seq_len_out, int32_t* free_count_out, int32_t* status, sv_stream_t stream)
+{
+    if (R < 0 || block_size < 1 || max_blocks < 0 || num_blocks < 0) return SV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX || num_blocks > SV_MAX_BLOCKS) return SV_ERR_LIMIT;
+    if (R == 0) return SV_OK;
+    if (seq_len == nullptr || leave == nullptr || free_count == nullptr || seq_len_out == nullptr ||
+        free_count_out == nullptr || (max_blocks > 0 && block_table == nullptr) || (num_blocks > 0 && free_blocks == nullptr))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(leave, 4) || !aligned(free_blocks, 4) ||
+        !aligned(free_count, 4) || !aligned(seq_len_out, 4) || !aligned(free_count_out, 4) || !aligned(status, 4))
+        return SV_ERR_ALIGN;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_cache_free(FreeArgs{block_table, max_blocks, seq_len, leave, R, block_size, num_blocks,
+                                               divisor_of(block_size), free_blocks, free_count, seq_len_out,
+                                               free_count_out, status},
+                                      stream));
+}
+
+size_t sv_cache_compact_workspace(int32_t num_blocks)
+{
+    return num_blocks < 1 || num_blocks > SV_MAX_BLOCKS ? 0 : compact_workspace_bytes(num_blocks);
+}
+
+int sv_cache_compact(sv_kv_cache cache, const int32_t* block_table, int32_t max_blocks, const int32_t* seq_len,
+                     int32_t R, int32_t* block_table_out, int32_t* free_blocks, int32_t* free_count, int32_t* status,
+                     void* workspace, size_t workspace_bytes, sv_stream_t stream)
+{
+    if (R < 0 || max_blocks < 0) return SV_ERR_INVALID_ARG;
+    if (int rc = check_cache(cache, true)) return rc;
+    if (static_cast<int64_t>(max_blocks) * cache.block_size > INT32_MAX || cache.num_blocks > SV_MAX_BLOCKS) return SV_ERR_LIMIT;
+    // the vectors of a block in one layer are counted in 32 bits, with room for a thread block's reach
+    if (static_cast<int64_t>(cache.kv_heads) * (cache.head_dim / 8) > (1ll << 30) / cache.block_size) return SV_ERR_LIMIT;
+    if (free_blocks == nullptr || free_count == nullptr || (R > 0 && seq_len == nullptr) ||
+        (R > 0 && max_blocks > 0 && (block_table == nullptr || block_table_out == nullptr)))
+        return SV_ERR_INVALID_ARG;
+    if (block_table != nullptr && block_table == block_table_out) return SV_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(block_table_out, 4) || !aligned(free_blocks, 4) ||
+        !aligned(free_count, 4) || !aligned(status, 4))
+        return SV_ERR_ALIGN;
+    if (int rc = check_workspace(workspace, workspace_bytes, compact_workspace_bytes(cache.num_blocks))) return rc;
+    if (!have_device()) return SV_ERR_DEVICE;
+    return launched(launch_cache_compact(CompactArgs{cache, block_table, max_blocks, seq_len, R,
+                                                     divisor_of(cache.block_size), block_table_out, free_blocks,
+                                                     free_count, status, workspace},
+                                         stream));
+}
+
+int sv_adjust_logits(sv_rows logits, int32_t R, int32_t k, int32_t branches, const int32_t* draft,
+                     sv_logit_rules rules, sv_rows out, int32_t* status, sv_stream_t stream)
+{
+    if (R < 0 || k < 0 || branches < 1) return SV_ERR_INVALID_ARG;
+    if (k > SV_MAX_K || branches > SV_MAX_BRANCHES) return SV_ERR_LIMIT;
+    if (k == 0 && branches > 1) return SV_ERR_INVALID_ARG;
+    const int64_t rows = static_cast<int64_t>(R) * (1 + branches * k);
+    AdjustArgs a{{}, {}, R, k, branches, draft, rules, status};
+    if (int rc = check_rows(logits, rows, logits.width, &a.in)) return rc;
+    if (int rc = check_rows(out, rows, out.width, &a.out)) return rc;
+    if (out.dtype != logits.dtype) return SV_ERR_DTYPE;
+    if (out.width != logits.width) return SV_ERR_SHAPE;
+    if (rows > 1 && out.data == logits.data && out.row_stride != logits.row_stride) return SV_ERR_SHAPE;
+    const sv_logit_rules& u = rules;
+    if (u.history_width < 0 || u.bias_entries < 0 || u.masks < 0 || u.mask_words < 0) return SV_ERR_INVALID_ARG;
+    if (u.history_width > SV_MAX_HISTORY) return SV_ERR_LIMIT;
+    if (u.mask != nullptr) {
+        if (static_cast<int64_t>(u.mask_words) * 32 < logits.width || u.mask_words > SV_MAX_WIDTH / 32) return SV_ERR_SHAPE;
+        if (u.mask_row == nullptr && u.masks != rows) return SV_ERR_SHAPE;
+    }
+    if (R == 0) return SV_OK;
+    if ((branches * k > 0 && draft == nullptr) || (u.history != nullptr && u.history_len == nullptr) ||
+        (u.bias_entries > 0 && (u.bias_start == nullptr || u.bias_id == nullptr || u.bias_value == nullptr)) ||
+        (u.mask == nullptr && u.mask_row != nullptr))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(draft, 4) || !aligned(u.history, 4) || !aligned(u.history_len, 4) || !aligned(u.prompt_len, 4) ||
+        !aligned(u.repetition, 4) || !aligned(u.presence, 4) || !aligned(u.frequency, 4) || !aligned(u.bias_start, 4) ||
+        !aligned(u.bias_id, 4) || !aligned(u.bias_value, 4) || !aligned(u.mask, 4) || !aligned(u.mask_row, 4) ||
+        !aligned(status, 4))
+        return SV_ERR_ALIGN;
+    if (!have_device()) return SV_ERR_DEVICE;
+    if (!adjust_fits(a)) return SV_ERR_LIMIT;
+    return launched(launch_adjust_logits(a, stream));
 }
 
 }  // extern "C"

@@ -165,6 +165,63 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_cache(const RopeArgs& a, cudaStream_t stream);
 
+struct NormRopeArgs {
+    RopeArgs rope;
+    const void *q_weight, *k_weight;
+    int32_t weight_dtype;
+    float eps;
+};
+cudaError_t launch_norm_rope_cache(const NormRopeArgs& a, cudaStream_t stream);
+
+struct AdjustArgs {
+    Rows in, out;
+    int32_t R, k, branches;
+    const int32_t* draft;
+    sv_logit_rules rules;
+    int32_t* status;
+};
+// false: more thread blocks than a launch can have
+bool adjust_fits(const AdjustArgs& a);
+cudaError_t launch_adjust_logits(const AdjustArgs& a, cudaStream_t stream);
+
+// ---- pages of the cache -----------------------------------------------------
+struct ForkArgs {
+    sv_kv_cache cache;
+    int32_t* block_table;
+    int32_t max_blocks;
+    const int32_t* seq_len;
+    int32_t R;
+    const int32_t *source, *free_blocks, *free_count;
+    Divisor by_block;
+    int32_t *seq_len_out, *free_count_out, *status;
+};
+cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t stream);
+
+struct FreeArgs {
+    const int32_t* block_table;
+    int32_t max_blocks;
+    const int32_t *seq_len, *leave;
+    int32_t R, block_size, num_blocks;
+    Divisor by_block;
+    int32_t* free_blocks;
+    const int32_t* free_count;
+    int32_t *seq_len_out, *free_count_out, *status;
+};
+cudaError_t launch_cache_free(const FreeArgs& a, cudaStream_t stream);
+
+struct CompactArgs {
+    sv_kv_cache cache;
+    const int32_t* block_table;
+    int32_t max_blocks;
+    const int32_t* seq_len;
+    int32_t R;
+    Divisor by_block;
+    int32_t *block_table_out, *free_blocks, *free_count, *status;
+    void* workspace;
+};
+size_t compact_workspace_bytes(int32_t num_blocks);
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t stream);
+
 struct AttnArgs {
     sv_heads q, out;
     sv_kv_cache cache;
@@ -186,5 +243,13 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream);
 
 // number of SMs of the current device
 int device_sm_count();
+
+// Dynamic shared memory above what every kernel may have has to be asked for.
+template <typename Kernel>
+inline cudaError_t allow_shared(Kernel* kernel, int bytes)
+{
+    return bytes <= 48 * 1024 ? cudaSuccess
+                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 
 }  // namespace sv
