@@ -1,12 +1,14 @@
 // sv_adjust_logits: penalties for repeated tokens, biases and grammar masks on the
 // rows of a verify step.
 //
-// A CTA takes a slice of one request's vocabulary for a few of its rows.  Half of its warps
-// stream the rows through as masked copies.  The others meanwhile count the request's tokens
-// that fall into the slice in shared memory (a word an id: seen, times in the output, and
-// the head of a chain of the drafts with that id), list the ids that any rule meets, and
-// compute those ids' entries of every row, which are written over the copies at the end.
-// In place the copy is left out: rows without a mask cost their listed ids alone.
+// A CTA takes a slice of one request's vocabulary for a few of its rows.  It counts the
+// request's tokens that fall into the slice in shared memory (a word an id: seen, times
+// in the output, and the head of a chain of the drafts with that id) and lists the ids that
+// any rule meets, by regions of the slice.  Then each warp takes regions of rows by itself:
+// asynchronous copies bring the next ones into its ring of tiles while it adjusts the listed
+// entries of the present one in shared memory and stores it masked.  The first copies are in
+// flight while the tokens are counted.
+// In place nothing is copied: masked entries are written, listed ones read and written.
 //
 // Counts are whole numbers, so the order in which threads meet the tokens changes nothing.
 #include <algorithm>
@@ -18,13 +20,15 @@
 namespace sv {
 namespace {
 
-constexpr int kAdjThreads = 512;
-constexpr int kAdjBuilders = 256;  // threads that count, list and compute while the others copy
-constexpr int kAdjChunk = 1024;    // ids that a warp copies at a time
-constexpr int kAdjSlice = 8192;    // most ids of a slice
-constexpr int kAdjEdge = 8;        // ids before a slice that a row which starts within a vector needs
-constexpr int kAdjKept = 4096;     // computed entries that wait for the copies
-constexpr int kAdjBatch = 8;       // tokens that a thread loads before it counts them
+constexpr int kAdjThreads = 256;
+constexpr int kAdjWarps = kAdjThreads / 32;
+constexpr int kAdjVecs = 4;                      // 16-byte vectors of a tile that a lane holds
+constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of a row
+constexpr int kAdjStages = 2;                    // tiles of a warp's ring
+constexpr int kAdjSlice = 4096;                  // most ids of a slice
+constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
+constexpr int kAdjBatch = 8;                     // tokens that a thread loads before it counts them
+constexpr int kAdjMaskWords = kAdjTile / 2 / 32 + 1;  // words of a region's mask
 
 // a word of the table: bit 31 seen, bits 19 .. 30 the head of the chain (0: none), bits 0 .. 18 the count
 constexpr uint32_t kAdjSeen = 1u << 31, kAdjHeadShift = 19, kAdjHead = 0xFFFu << kAdjHeadShift,
@@ -34,25 +38,27 @@ static_assert(SV_MAX_BRANCHES * SV_MAX_K < (1 << 12), "a draft's number must fit
 
 struct AdjustGeom {
     int32_t slice, slices;  // ids of a slice (a power of two), slices of a row
+    int32_t region_shift;   // log2 of a slice's regions, at most kAdjWarps
     int32_t rows, groups;   // rows of a request, thread blocks that share them
     int32_t most_rows;      // of a thread block
     int32_t drafts;         // branches * k
 };
 
-// The parts of a CTA's shared memory, in 32-bit words.
+// The parts of a CTA's shared memory, in 32-bit words; the tiles lie first.
 struct AdjustLayout {
-    int32_t bias, bits, kept, mask, list, next, bytes;  // the table lies first; list and next hold 16 bits each
+    int32_t mask, tab, bias, bits, row, list, next, bytes;  // list and next hold 16 bits each
 };
-__host__ __device__ inline AdjustLayout layout_of(const AdjustGeom& g, bool biased, int esize)
+__host__ __device__ inline AdjustLayout layout_of(const AdjustGeom& g, bool biased, bool tiles)
 {
     const int32_t ids = g.slice + kAdjEdge;
     AdjustLayout l;
-    l.bias = ids;
+    l.mask = tiles ? kAdjWarps * kAdjStages * kAdjTile / 4 : 0;
+    l.tab = l.mask + (tiles ? (kAdjWarps * kAdjStages * kAdjMaskWords + 3) / 4 * 4 : 0);
+    l.bias = l.tab + ids;
     l.bits = l.bias + (biased ? ids : 0);
-    l.kept = l.bits + ids / 32 + 1;
-    l.mask = l.kept + kAdjKept * esize / 4;
-    l.list = l.mask + g.most_rows;
-    l.next = l.list + ids / 2;
+    l.row = (l.bits + ids / 32 + 1 + 3) / 4 * 4;
+    l.list = l.row + 2 * g.most_rows;
+    l.next = l.list + (g.slice + (kAdjEdge << g.region_shift)) / 2;
     l.bytes = 4 * (l.next + (g.drafts + 1) / 2);
     return l;
 }
@@ -84,58 +90,72 @@ __device__ __forceinline__ uint32_t narrow<uint32_t>(float v)
 template <typename T>
 constexpr T kNegInf = static_cast<T>(sizeof(T) == 2 ? 0xFF80u : 0xFF800000u);
 
-// Whether each of the N ids from x on is allowed, as bits.  x >= 0; bits behind the mask's end are 0.
-template <int N>
-__device__ __forceinline__ uint32_t allowed(const uint8_t* mask, int32_t mask_bytes, int32_t x)
+__device__ __forceinline__ bool allowed(const uint32_t* mask, int32_t x)
 {
-    const int32_t at = x >> 3, shift = x & 7;
-    uint32_t m = mask[at];
-    if (shift > 8 - N && at + 1 < mask_bytes) m |= static_cast<uint32_t>(mask[at + 1]) << 8;
-    return (m >> shift) & ((1u << N) - 1);
+    return mask == nullptr || ((mask[x >> 5] >> (x & 31)) & 1u);
+}
+
+// The signs of two bytes of `w`, each over two bytes: SIGNS is a selector of PRMT, whose nibbles of 8 and
+// more give a byte's sign eight times.
+template <uint32_t SIGNS>
+__device__ __forceinline__ uint32_t signs(uint32_t w)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(SIGNS));
+    return r;
 }
 
 // A vector's entries, those not allowed set to -inf.
 template <typename T>
 __device__ __forceinline__ uint4 masked(uint4 v, uint32_t m)
 {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (sizeof(T) == 2) {
-            const uint32_t two = (m >> (2 * i)) & 3u;
-            const uint32_t keep = ((two | (two << 15)) & 0x00010001u) * 0xFFFFu;
-            w[i] = (w[i] & keep) | (0xFF80FF80u & ~keep);
-        } else {
-            w[i] = (m >> i) & 1u ? w[i] : 0xFF800000u;
-        }
+    if (sizeof(T) == 4) {
+        return make_uint4(m & 1u ? v.x : 0xFF800000u, m & 2u ? v.y : 0xFF800000u, m & 4u ? v.z : 0xFF800000u,
+                          m & 8u ? v.w : 0xFF800000u);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    // each of four bits to the sign of a byte, then each sign over the bytes of its entry
+    const uint32_t lo = (m & 15u) * 0x10204080u, hi = (m >> 4) * 0x10204080u;
+    const uint32_t k0 = signs<0x9988>(lo), k1 = signs<0xBBAA>(lo), k2 = signs<0x9988>(hi), k3 = signs<0xBBAA>(hi);
+    return make_uint4((v.x & k0) | (0xFF80FF80u & ~k0), (v.y & k1) | (0xFF80FF80u & ~k1), (v.z & k2) | (0xFF80FF80u & ~k2),
+                      (v.w & k3) | (0xFF80FF80u & ~k3));
 }
 
-__device__ __forceinline__ void builders_sync(int threads)
+// ---- asynchronous copies to shared memory --------------------------------------
+__device__ __forceinline__ void copy16(void* dst, const void* src)
 {
-    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// wait until at most `left` of this thread's last groups are under way
+template <int left>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory");
 }
 
-// T: uint16_t for bf16 rows, uint32_t for fp32 rows
-template <typename T>
-__global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const __grid_constant__ AdjustArgs a, const AdjustGeom g)
+// T: uint16_t for bf16 rows, uint32_t for fp32 rows.  COPY: out of place, by tiles; every row of the two
+// matrices starts alike within 16 bytes.
+template <typename T, bool COPY>
+__global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_constant__ AdjustArgs a, const AdjustGeom g)
 {
-    constexpr int kPer = 16 / sizeof(T);                // entries of a vector
-    constexpr int kVecs = kAdjChunk / (32 * kPer);      // vectors that a lane holds
+    constexpr int kPer = 16 / sizeof(T);            // entries of a vector
+    constexpr int kRegion = kAdjTile / sizeof(T);   // ids of a region
     constexpr uint32_t kAll = (1u << kPer) - 1;
     extern __shared__ __align__(16) uint32_t s_mem[];
-    __shared__ int32_t s_listed, s_chunk;
+    __shared__ int32_t s_listed[kAdjWarps];
     const sv_logit_rules& u = a.rules;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t ids = g.slice + kAdjEdge, V = a.in.width;
     const bool biased = u.bias_entries > 0;
-    const AdjustLayout at = layout_of(g, biased, sizeof(T));
-    uint32_t* s_tab = s_mem;
+    const AdjustLayout at = layout_of(g, biased, COPY);
+    uint32_t* s_tab = s_mem + at.tab;
     uint32_t* s_bias = s_mem + at.bias;  // 1 + the last entry of the id's bias, 0 for none
     uint32_t* s_bits = s_mem + at.bits;
-    T* s_kept = reinterpret_cast<T*>(s_mem + at.kept);
-    int32_t* s_mask = reinterpret_cast<int32_t*>(s_mem + at.mask);  // each row's mask, -1 for none
+    int2* s_row = reinterpret_cast<int2*>(s_mem + at.row);  // each row's mask (-1: none), and the drafts before its branch's
     uint16_t* s_list = reinterpret_cast<uint16_t*>(s_mem + at.list);
     uint16_t* s_next = reinterpret_cast<uint16_t*>(s_mem + at.next);
 
@@ -147,69 +167,32 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const __grid_con
     const int32_t row0 = static_cast<int32_t>(static_cast<int64_t>(g.rows) * group / g.groups);
     const int32_t rows = static_cast<int32_t>(static_cast<int64_t>(g.rows) * (group + 1) / g.groups) - row0;
     const int64_t first = static_cast<int64_t>(r) * g.rows + row0;
-    const bool in_place = a.in.data == a.out.data;
-    const bool copies = !in_place || u.mask != nullptr;
-    const int32_t mask_bytes = 4 * u.mask_words;
 
-    for (int i = tid; i < at.kept / 4 + 1; i += kAdjThreads) reinterpret_cast<uint4*>(s_mem)[i] = make_uint4(0, 0, 0, 0);
     for (int j = tid; j < rows; j += kAdjThreads) {
         int64_t i = -1;
         if (u.mask != nullptr) i = u.mask_row != nullptr ? u.mask_row[first + j] : first + j;
-        s_mask[j] = i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1;
+        s_row[j] = make_int2(i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1,
+                             row0 + j > 0 ? (row0 + j - 1) / a.k * a.k : 0);
     }
-    if (tid == 0) s_listed = s_chunk = 0;
-    __syncthreads();
-
-    // a row's entries, its mask (or NULL), and how many entries its start lies behind a 16-byte
-    // boundary (-1: differently so in the two matrices)
-    auto row_of = [&](int32_t j, const T*& in, T*& out, const uint8_t*& mask) -> int32_t {
-        in = reinterpret_cast<const T*>(a.in.data) + (first + j) * a.in.stride;
-        out = reinterpret_cast<T*>(const_cast<char*>(a.out.data)) + (first + j) * a.out.stride;
-        const int32_t i = s_mask[j];
-        mask = i < 0 ? nullptr : reinterpret_cast<const uint8_t*>(u.mask + static_cast<int64_t>(i) * u.mask_words);
-        const uint32_t x = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(in)) & 15u,
-                       y = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out)) & 15u;
-        return x == y ? static_cast<int32_t>(x / sizeof(T)) : -1;
-    };
-    // Entry p of the listed ids' entries, row by row: its id and place, or false where it is another slice's.
-    float rep = 1.0f, pres = 0.0f, freq = 0.0f;
-    auto place_of = [&](int32_t p, int32_t listed, int32_t& j, int32_t& l, const T*& in, T*& out, const uint8_t*& mask) {
-        j = p / listed;
-        l = s_list[p - j * listed];
-        const int32_t shift = max(row_of(j, in, out, mask), 0), x = base + l;
-        return x >= s0 - shift && x < s0 + g.slice - shift;
-    };
-    // The adjusted entry of the table's id l in row j.
-    auto entry_of = [&](int32_t j, int32_t l, const T* in, const uint8_t* mask) -> T {
-        const int32_t x = base + l;
-        const T raw = in[x];
-        if (mask != nullptr && !((mask[x >> 3] >> (x & 7)) & 1)) return kNegInf<T>;
-        // the drafts before the row: the first i + 1 of branch b, for row 1 + b * k + i
-        const int32_t row = row0 + j;
-        int32_t lo = 0, hi = 0;
-        if (row > 0) {
-            lo = (row - 1) / a.k * a.k;
-            hi = row;
-        }
-        const uint32_t word = s_tab[l];
-        uint32_t count = word & kAdjCount;
-        for (uint32_t e = (word & kAdjHead) >> kAdjHeadShift; e != 0; e = s_next[e - 1])
-            count += static_cast<int32_t>(e) > lo && static_cast<int32_t>(e) <= hi;
-        const uint32_t entry = biased ? s_bias[l] : 0u;
-        const bool seen = (word & kAdjSeen) != 0 || count != 0;
-        if (!seen && entry == 0) return raw;
-        float z = widen<T>(raw);
-        if (seen) z = z > 0.0f ? z / rep : z * rep;
-        if (count != 0) z -= pres + freq * static_cast<float>(count);
-        if (entry != 0) z += u.bias_value[entry - 1];
-        return narrow<T>(z);
-    };
-
     // what the request asks for
     uint32_t st = 0;
-    if (u.repetition != nullptr) rep = u.repetition[r];
-    if (u.presence != nullptr) pres = u.presence[r];
-    if (u.frequency != nullptr) freq = u.frequency[r];
+    int32_t len = 0, prompt = 0, b0 = 0, b1 = 0;
+    if (u.history != nullptr) {
+        const int32_t given = u.history_len[r];
+        len = min(max(given, 0), u.history_width);
+        const int32_t p = u.prompt_len != nullptr ? u.prompt_len[r] : 0;
+        prompt = min(max(p, 0), len);
+        if (len != given || prompt != p) st |= SV_ST_BAD_LENGTH;
+    }
+    if (biased) {
+        const int32_t x = u.bias_start[r], y = u.bias_start[r + 1];
+        b0 = min(max(x, 0), u.bias_entries);
+        b1 = min(max(y, b0), u.bias_entries);
+        if (b0 != x || b1 != y) st |= SV_ST_BAD_LENGTH;
+    }
+    float rep = u.repetition != nullptr ? u.repetition[r] : 1.0f;
+    float pres = u.presence != nullptr ? u.presence[r] : 0.0f;
+    float freq = u.frequency != nullptr ? u.frequency[r] : 0.0f;
     if (!(rep > 0.0f) || isinf(rep)) {
         rep = 1.0f;
         st |= SV_ST_BAD_PENALTY;
@@ -222,142 +205,217 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const __grid_con
         freq = 0.0f;
         st |= SV_ST_BAD_PENALTY;
     }
+    for (int i = tid; i < (at.row - at.tab) / 4; i += kAdjThreads)
+        reinterpret_cast<uint4*>(s_tab)[i] = make_uint4(0, 0, 0, 0);
+    if (tid < kAdjWarps) s_listed[tid] = 0;
+    __syncthreads();
 
-    const int builders = copies ? kAdjBuilders : kAdjThreads;
-    if (tid < builders) {
-        int32_t len = 0, prompt = 0, b0 = 0, b1 = 0;
-        if (u.history != nullptr) {
-            const int32_t given = u.history_len[r];
-            len = min(max(given, 0), u.history_width);
-            const int32_t p = u.prompt_len != nullptr ? u.prompt_len[r] : 0;
-            prompt = min(max(p, 0), len);
-            if (len != given || prompt != p) st |= SV_ST_BAD_LENGTH;
-        }
-        if (biased) {
-            const int32_t x = u.bias_start[r], y = u.bias_start[r + 1];
-            b0 = min(max(x, 0), u.bias_entries);
-            b1 = min(max(y, b0), u.bias_entries);
-            if (b0 != x || b1 != y) st |= SV_ST_BAD_LENGTH;
-        }
-        // The slice's entry of a token (-1: outside), noted in the list by the first to meet it.
-        auto meet = [&](int32_t x) -> int32_t {
-            if (static_cast<uint32_t>(x) >= static_cast<uint32_t>(V)) {
-                st |= SV_ST_TOKEN_RANGE;
-                return -1;
-            }
-            const int32_t l = x - base;
-            if (l < 0 || l >= ids) return -1;
-            const uint32_t bit = 1u << (l & 31);
-            if ((atomicOr(&s_bits[l >> 5], bit) & bit) == 0) s_list[atomicAdd(&s_listed, 1)] = static_cast<uint16_t>(l);
-            return l;
-        };
-        const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
-        for (int32_t i0 = tid; i0 < len; i0 += builders * kAdjBatch) {
-            int32_t token[kAdjBatch];
+    // A warp's units: regions of rows, its region the same in each.
+    const int32_t units = rows << g.region_shift, region = warp & ((1 << g.region_shift) - 1);
+    const int32_t unit0 = warp, in_slice = s0 + region * kRegion;
+    struct Row {
+        const T* in;
+        T* out;
+        const uint32_t* mask;  // NULL: none
+        int32_t x0;            // id of the region's first entry
+        int32_t row;
+        int32_t before;        // drafts before those of the row's branch
+    };
+    auto row_of = [&](int32_t unit) {
+        Row w;
+        const int32_t j = unit >> g.region_shift;
+        w.in = reinterpret_cast<const T*>(a.in.data) + (first + j) * a.in.stride;
+        w.out = reinterpret_cast<T*>(const_cast<char*>(a.out.data)) + (first + j) * a.out.stride;
+        const int2 i = s_row[j];
+        w.mask = i.x < 0 ? nullptr : u.mask + static_cast<int64_t>(i.x) * u.mask_words;
+        w.row = row0 + j;
+        w.before = i.y;
+        w.x0 = in_slice;
+        // entries that the row starts behind a 16-byte boundary
+        if (COPY || a.in.data == a.out.data)
+            w.x0 -= (static_cast<int32_t>(reinterpret_cast<uintptr_t>(w.in)) & 15) / static_cast<int32_t>(sizeof(T));
+        return w;
+    };
+    T* tiles = reinterpret_cast<T*>(s_mem) + warp * kAdjStages * kRegion;
+    uint32_t* masks = s_mem + at.mask + warp * kAdjStages * kAdjMaskWords;
+    auto bring = [&](int32_t unit, int stage) {
+        if (unit < units) {
+            const Row w = row_of(unit);
+            T* tile = tiles + stage * kRegion;
 #pragma unroll
-            for (int q = 0; q < kAdjBatch; ++q)
-                if (i0 + q * builders < len) token[q] = history[i0 + q * builders];
-#pragma unroll
-            for (int q = 0; q < kAdjBatch; ++q) {
-                const int32_t i = i0 + q * builders;
-                const int32_t l = i < len ? meet(token[q]) : -1;
-                if (l < 0) continue;
-                if (i >= prompt)
-                    atomicAdd(&s_tab[l], 1u);
-                else
-                    atomicOr(&s_tab[l], kAdjSeen);
+            for (int q = 0; q < kAdjVecs; ++q) {
+                const int32_t o = (q * 32 + lane) * kPer, x = w.x0 + o;
+                if (x >= 0 && x + kPer <= V) {
+                    copy16(tile + o, w.in + x);
+                } else {
+                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y) tile[y - w.x0] = w.in[y];
+                }
+            }
+            if (w.mask != nullptr) {
+                const int32_t word = (w.x0 >> 5) + lane;
+                if (word >= 0 && word < u.mask_words) copy4(masks + stage * kAdjMaskWords + lane, w.mask + word);
+                if (lane == 0 && word + 32 < u.mask_words && kAdjMaskWords > 32)
+                    copy4(masks + stage * kAdjMaskWords + 32, w.mask + word + 32);
             }
         }
-        for (int32_t i = tid; i < g.drafts; i += builders) {
-            const int32_t l = meet(a.draft[static_cast<int64_t>(r) * g.drafts + i]);
-            if (l < 0) continue;
-            uint32_t old = s_tab[l], was;
-            do {
-                was = old;
-                s_next[i] = static_cast<uint16_t>((was & kAdjHead) >> kAdjHeadShift);
-                old = atomicCAS(&s_tab[l], was, (was & ~kAdjHead) | (static_cast<uint32_t>(i + 1) << kAdjHeadShift));
-            } while (old != was);
-        }
-        for (int32_t i = b0 + tid; i < b1; i += builders) {
-            const int32_t l = meet(u.bias_id[i]);
-            if (l >= 0) atomicMax(&s_bias[l], static_cast<uint32_t>(i) + 1);
-        }
-        builders_sync(builders);
-        const int32_t listed = s_listed, kept = min(rows * listed, kAdjKept);
-        for (int32_t p = tid; p < kept; p += builders) {
-            int32_t j, l;
-            const T* in;
-            T* out;
-            const uint8_t* mask;
-            if (place_of(p, listed, j, l, in, out, mask)) s_kept[p] = entry_of(j, l, in, mask);
-        }
+        copies_commit();
+    };
+    if (COPY) {
+#pragma unroll
+        for (int i = 0; i < kAdjStages - 1; ++i) bring(unit0 + i * kAdjWarps, i);
     }
 
-    if (copies) {
-        const int32_t per_row = g.slice / kAdjChunk;
-        for (;;) {
-            int32_t c = 0;
-            if (lane == 0) c = atomicAdd(&s_chunk, 1);
-            c = __shfl_sync(0xFFFFFFFFu, c, 0);
-            if (c >= rows * per_row) break;
-            const T* in;
-            T* out;
-            const uint8_t* mask;
-            const int32_t j = c / per_row, shift = row_of(j, in, out, mask);
-            const int32_t x0 = s0 + (c - j * per_row) * kAdjChunk - max(shift, 0);
-            if (x0 >= V || (in_place && mask == nullptr)) continue;
-            if (shift < 0) {
-                for (int32_t x = x0 + lane; x < min(x0 + kAdjChunk, V); x += 32) {
-                    const bool ok = mask == nullptr || ((mask[x >> 3] >> (x & 7)) & 1);
-                    out[x] = ok ? in[x] : kNegInf<T>;
-                }
-                continue;
-            }
-            uint32_t m[kVecs];
-            uint4 v[kVecs];
-#pragma unroll
-            for (int q = 0; q < kVecs; ++q) {
-                const int32_t x = x0 + (q * 32 + lane) * kPer;
-                const bool whole = x >= 0 && x + kPer <= V;
-                m[q] = whole && mask != nullptr ? allowed<kPer>(mask, mask_bytes, x) : kAll;
-                if (whole && (!in_place || (m[q] != 0u && m[q] != kAll))) v[q] = *reinterpret_cast<const uint4*>(in + x);
-            }
-#pragma unroll
-            for (int q = 0; q < kVecs; ++q) {
-                const int32_t x = x0 + (q * 32 + lane) * kPer;
-                if (x >= 0 && x + kPer <= V) {
-                    if (in_place && m[q] == kAll) continue;
-                    *reinterpret_cast<uint4*>(out + x) = m[q] != kAll ? masked<T>(v[q], m[q]) : v[q];
-                } else {
-                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y) {
-                        const bool ok = mask == nullptr || ((mask[y >> 3] >> (y & 7)) & 1);
-                        if (!in_place || !ok) out[y] = ok ? in[y] : kNegInf<T>;
-                    }
-                }
-            }
+    // The slice's entry of a token (-1: outside).  The first to meet it notes it in its region's list, and
+    // in the next one's where a row that starts within a vector has it there.
+    auto meet = [&](int32_t x) -> int32_t {
+        if (static_cast<uint32_t>(x) >= static_cast<uint32_t>(V)) {
+            st |= SV_ST_TOKEN_RANGE;
+            return -1;
         }
+        const int32_t l = x - base;
+        if (l < 0 || l >= ids) return -1;
+        const uint32_t bit = 1u << (l & 31);
+        if ((atomicOr(&s_bits[l >> 5], bit) & bit) == 0) {
+            const int32_t i = l - kAdjEdge, q = i / kRegion;  // 0 for the entries before the slice, too
+            s_list[q * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q], 1)] = static_cast<uint16_t>(l);
+            if (i >= 0 && (i + kAdjEdge) / kRegion > q && i + kAdjEdge < g.slice)
+                s_list[(q + 1) * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q + 1], 1)] = static_cast<uint16_t>(l);
+        }
+        return l;
+    };
+    const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
+    for (int32_t i0 = tid; i0 < len; i0 += kAdjThreads * kAdjBatch) {
+        int32_t token[kAdjBatch];
+#pragma unroll
+        for (int q = 0; q < kAdjBatch; ++q)
+            if (i0 + q * kAdjThreads < len) token[q] = history[i0 + q * kAdjThreads];
+#pragma unroll
+        for (int q = 0; q < kAdjBatch; ++q) {
+            const int32_t i = i0 + q * kAdjThreads;
+            const int32_t l = i < len ? meet(token[q]) : -1;
+            if (l < 0) continue;
+            if (i >= prompt)
+                atomicAdd(&s_tab[l], 1u);
+            else
+                atomicOr(&s_tab[l], kAdjSeen);
+        }
+    }
+    for (int32_t i = tid; i < g.drafts; i += kAdjThreads) {
+        const int32_t l = meet(a.draft[static_cast<int64_t>(r) * g.drafts + i]);
+        if (l < 0) continue;
+        uint32_t old = s_tab[l], was;
+        do {
+            was = old;
+            s_next[i] = static_cast<uint16_t>((was & kAdjHead) >> kAdjHeadShift);
+            old = atomicCAS(&s_tab[l], was, (was & ~kAdjHead) | (static_cast<uint32_t>(i + 1) << kAdjHeadShift));
+        } while (old != was);
+    }
+    for (int32_t i = b0 + tid; i < b1; i += kAdjThreads) {
+        const int32_t l = meet(u.bias_id[i]);
+        if (l >= 0) atomicMax(&s_bias[l], static_cast<uint32_t>(i) + 1);
     }
     if (s == 0 && group == 0 && a.status != nullptr) {
         if (u.mask != nullptr && u.mask_row != nullptr)
             for (int32_t i = tid; i < g.rows; i += kAdjThreads)
                 if (u.mask_row[static_cast<int64_t>(r) * g.rows + i] >= u.masks) st |= SV_ST_BAD_MASK;
-        // every thread but those that count leaves some bits unset
-        st = (__syncthreads_or(st & SV_ST_TOKEN_RANGE) ? SV_ST_TOKEN_RANGE : 0u) |
-             (__syncthreads_or(st & SV_ST_BAD_MASK) ? SV_ST_BAD_MASK : 0u) | (st & (SV_ST_BAD_LENGTH | SV_ST_BAD_PENALTY));
+        st |= (__syncthreads_or(st & SV_ST_TOKEN_RANGE) ? SV_ST_TOKEN_RANGE : 0u) |
+              (__syncthreads_or(st & SV_ST_BAD_MASK) ? SV_ST_BAD_MASK : 0u);
         if (tid == 0) a.status[r] = static_cast<int32_t>(st);
     }
     __syncthreads();
 
-    // the computed entries over the copies
-    const int32_t listed = s_listed;
-    for (int32_t p = tid; p < rows * listed; p += kAdjThreads) {
-        int32_t j, l;
-        const T* in;
-        T* out;
-        const uint8_t* mask;
-        if (!place_of(p, listed, j, l, in, out, mask)) continue;
-        out[base + l] = p < kAdjKept ? s_kept[p] : entry_of(j, l, in, mask);
+    // The adjusted entry of the table's id l in a row.
+    auto adjusted = [&](const Row& w, int32_t l, T raw) -> T {
+        // the drafts before the row: the first i + 1 of branch b, for row 1 + b * k + i
+        const uint32_t word = s_tab[l];
+        uint32_t count = word & kAdjCount;
+        for (uint32_t e = (word & kAdjHead) >> kAdjHeadShift; e != 0; e = s_next[e - 1])
+            count += static_cast<int32_t>(e) > w.before && static_cast<int32_t>(e) <= w.row;
+        const uint32_t entry = biased ? s_bias[l] : 0u;
+        const bool seen = (word & kAdjSeen) != 0 || count != 0;
+        if (!seen && entry == 0) return raw;
+        float z = widen<T>(raw);
+        if (seen) z = z > 0.0f ? z / rep : z * rep;
+        if (count != 0) z -= pres + freq * static_cast<float>(count);
+        if (entry != 0) z += u.bias_value[entry - 1];
+        return narrow<T>(z);
+    };
+    const uint16_t* list = s_list + region * (kRegion + kAdjEdge);
+    const int32_t listed = s_listed[region];
+
+    if (COPY) {
+        int stage = 0;
+        for (int32_t unit = unit0; unit < units; unit += kAdjWarps) {
+            __syncwarp();  // the tile before is stored
+            bring(unit + (kAdjStages - 1) * kAdjWarps, stage == 0 ? kAdjStages - 1 : stage - 1);
+            copies_wait<kAdjStages - 1>();
+            __syncwarp();
+            const Row w = row_of(unit);
+            T* tile = tiles + stage * kRegion;
+            const uint32_t* words = masks + stage * kAdjMaskWords;
+            for (int32_t i = lane; i < listed; i += 32) {
+                const int32_t l = list[i], o = base + l - w.x0;
+                if (o >= 0 && o < kRegion) tile[o] = adjusted(w, l, tile[o]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < kAdjVecs; ++q) {
+                const int32_t o = (q * 32 + lane) * kPer, x = w.x0 + o;
+                uint4 v = *reinterpret_cast<const uint4*>(tile + o);
+                uint32_t m = kAll;
+                if (w.mask != nullptr) {
+                    const int32_t b = (w.x0 & 31) + o;
+                    m = __funnelshift_r(words[b >> 5], words[min((b >> 5) + 1, kAdjMaskWords - 1)], b & 31) & kAll;
+                    v = masked<T>(v, m);
+                }
+                if (x >= 0 && x + kPer <= V) {
+                    *reinterpret_cast<uint4*>(w.out + x) = v;
+                } else {
+                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y)
+                        w.out[y] = (m >> (y - x)) & 1u ? tile[y - w.x0] : kNegInf<T>;
+                }
+            }
+            stage = stage + 1 == kAdjStages ? 0 : stage + 1;
+        }
+        copies_wait<0>();
+        return;
     }
+
+    const bool in_place = a.in.data == a.out.data;
+    for (int32_t unit = unit0; unit < units; unit += kAdjWarps) {
+        const Row w = row_of(unit);
+        if (in_place && w.mask != nullptr) {
+#pragma unroll
+            for (int q = 0; q < kAdjVecs; ++q) {
+                const int32_t x = w.x0 + (q * 32 + lane) * kPer;
+                if (x >= 0 && x + kPer <= V) {
+                    const uint32_t lo = w.mask[x >> 5], hi = (x & 31) + kPer > 32 ? w.mask[(x >> 5) + 1] : 0u;
+                    const uint32_t m = __funnelshift_r(lo, hi, x & 31) & kAll;
+                    uint4* p = reinterpret_cast<uint4*>(w.out + x);
+                    if (m != kAll) *p = masked<T>(m != 0u ? *p : make_uint4(0, 0, 0, 0), m);
+                } else {
+                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y)
+                        if (!allowed(w.mask, y)) w.out[y] = kNegInf<T>;
+                }
+            }
+        } else if (!in_place) {  // rows that start differently
+#pragma unroll 8
+            for (int32_t x = w.x0 + lane; x < min(w.x0 + kRegion, V); x += 32)
+                w.out[x] = allowed(w.mask, x) ? w.in[x] : kNegInf<T>;
+        }
+        __syncwarp();
+        for (int32_t i = lane; i < listed; i += 32) {
+            const int32_t l = list[i], x = base + l;
+            if (x >= w.x0 && x < w.x0 + kRegion && allowed(w.mask, x)) w.out[x] = adjusted(w, l, w.in[x]);
+        }
+    }
+}
+
+// Whether the rows of the two matrices start alike within 16 bytes, and are not the same ones.
+bool by_tiles(const AdjustArgs& a)
+{
+    return a.in.data != a.out.data && reinterpret_cast<uintptr_t>(a.in.data) % 16 == reinterpret_cast<uintptr_t>(a.out.data) % 16 &&
+           (a.in.stride - a.out.stride) * a.in.esize % 16 == 0;
 }
 
 AdjustGeom geom_of(const AdjustArgs& a)
@@ -366,9 +424,11 @@ AdjustGeom geom_of(const AdjustArgs& a)
     AdjustGeom g{};
     g.drafts = a.branches * a.k;
     g.rows = 1 + g.drafts;
+    const int32_t region = kAdjTile / a.in.esize;
     auto slices = [&](int64_t n) { return (static_cast<int64_t>(a.in.width) + kAdjEdge - 1 + n - 1) / n; };
     g.slice = kAdjSlice;
-    while (g.slice > kAdjChunk && a.R * slices(g.slice) < 2 * sms) g.slice /= 2;
+    while (g.slice > region && a.R * slices(g.slice) < 4 * sms) g.slice /= 2;
+    while ((region << g.region_shift) < g.slice) ++g.region_shift;
     g.slices = static_cast<int32_t>(slices(g.slice));
     const int64_t blocks = static_cast<int64_t>(a.R) * g.slices;
     g.groups = static_cast<int32_t>(std::min<int64_t>(g.rows, std::max<int64_t>(1, 4 * sms / blocks)));
@@ -387,9 +447,11 @@ bool adjust_fits(const AdjustArgs& a)
 cudaError_t launch_adjust_logits(const AdjustArgs& a, cudaStream_t stream)
 {
     const AdjustGeom g = geom_of(a);
-    const int bytes = layout_of(g, a.rules.bias_entries > 0, a.in.esize).bytes;
+    const bool tiles = by_tiles(a), bf16 = a.in.dtype == SV_BF16;
+    const int bytes = layout_of(g, a.rules.bias_entries > 0, tiles).bytes;
     const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.R) * g.slices * g.groups);
-    auto* kernel = a.in.dtype == SV_BF16 ? adjust_kernel<uint16_t> : adjust_kernel<uint32_t>;
+    auto* kernel = tiles ? bf16 ? adjust_kernel<uint16_t, true> : adjust_kernel<uint32_t, true>
+                         : bf16 ? adjust_kernel<uint16_t, false> : adjust_kernel<uint32_t, false>;
     if (cudaError_t e = allow_shared(kernel, bytes)) return e;
     kernel<<<blocks, kAdjThreads, bytes, stream>>>(a, g);
     return cudaGetLastError();
