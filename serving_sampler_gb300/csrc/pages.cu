@@ -1,9 +1,8 @@
 // Pages of the cache: sv_cache_fork, sv_cache_free and sv_cache_compact.
 //
-// Who holds a block is read from the tables each time: sets of blocks are bit maps, laid
-// out over the shared memory of one cluster, whose CTAs set bits in each other's part,
-// meet at the cluster's barriers, and take prefix sums over the bits for an order that
-// does not depend on the threads'.  What moves data (a fork's last blocks, a compaction)
+// Who holds a block is read from the tables each time: sets of blocks are bit maps in the
+// shared memory of one cluster, whose CTAs read the tables together, join their maps, and
+// take prefix sums over the bits for an order that does not depend on the threads'.  What moves data (a fork's last blocks, a compaction)
 // runs over the whole GPU.
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -122,19 +121,90 @@ __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const ForkArgs
 
 // ---- sets of blocks over a cluster --------------------------------------------
 constexpr int kSetThreads = 1024;
-constexpr int kSetCtas = 8;
+constexpr int kSetCtas = 16;
+constexpr int kSetWarps = kSetCtas * kSetThreads / 32;
+constexpr int kSetBatch = 8;                 // entries that a thread loads before it sets their bits
+constexpr int kSetOwnBytes = 200 * 1024;     // largest bit maps of which every CTA has one of its own
 
-// The words of a bit map over [0, num_blocks) lie in kSetCtas equal parts.
+// The words of a bit map over [0, num_blocks) are shared out among the CTAs in equal parts.
 __host__ __device__ inline int32_t set_words(int32_t num_blocks)
 {
     const int32_t words = num_blocks / 32 + (num_blocks % 32 != 0);
     return (words + kSetCtas - 1) / kSetCtas;
 }
 
-__device__ __forceinline__ void set_bit(cg::cluster_group& cluster, uint32_t* part, int32_t words, int32_t id)
+// OWN: every CTA sets bits in a whole map of its own, and the parts are joined afterwards: atomics on
+// another CTA's memory cost far more than those on the CTA's own.  Otherwise (the maps of a pool
+// too large for that) a CTA has its part alone, and bits are set where they belong.
+template <bool OWN>
+__device__ __forceinline__ void set_bit(cg::cluster_group& cluster, uint32_t* map, int32_t words, int32_t id)
 {
-    const int32_t w = id >> 5, rank = w / words;
-    atomicOr(cluster.map_shared_rank(part, rank) + (w - rank * words), 1u << (id & 31));
+    const int32_t w = id >> 5;
+    const uint32_t bit = 1u << (id & 31);
+    if (OWN) {
+        atomicOr(map + w, bit);
+    } else {
+        const int32_t rank = w / words;
+        atomicOr(cluster.map_shared_rank(map, rank) + (w - rank * words), bit);
+    }
+}
+
+// This CTA's part of a map, with the bits that all CTAs have set.
+template <bool OWN>
+__device__ __forceinline__ uint32_t* set_part(cg::cluster_group& cluster, uint32_t* map, int32_t words)
+{
+    if (!OWN) return map;
+    const int rank = static_cast<int>(cluster.block_rank());
+    uint32_t* part = map + rank * words;
+    for (int32_t i = threadIdx.x; i < words; i += kSetThreads) {
+        uint32_t w[kSetCtas];
+#pragma unroll
+        for (int c = 0; c < kSetCtas; ++c) w[c] = cluster.map_shared_rank(part, c)[i];
+        uint32_t all = 0;
+#pragma unroll
+        for (int c = 0; c < kSetCtas; ++c) all |= w[c];
+        part[i] = all;  // no other CTA reads this part
+    }
+    __syncthreads();
+    return part;
+}
+
+// Every row's held entries, one warp a row: begin(r, L, other) gives the entries held, from the row's length and
+// its entry of `more`; bit(r, id) takes an id of the pool; end(r, out) is told whether ids outside of it were among them.
+template <typename Begin, typename Bit, typename End>
+__device__ __forceinline__ void for_rows(cg::cluster_group& cluster, int32_t R, const int32_t* seq_len, const int32_t* more,
+                                         const int32_t* block_table, int32_t max_blocks, int32_t num_blocks, Begin begin,
+                                         Bit bit, End end)
+{
+    const int lane = threadIdx.x & 31;
+    const int32_t w = threadIdx.x / 32 * kSetCtas + static_cast<int32_t>(cluster.block_rank());
+    for (int64_t r0 = w; r0 < R; r0 += 32 * kSetWarps) {
+        // the next 32 rows' lengths at once
+        const int64_t mine = min(r0 + lane * kSetWarps, static_cast<int64_t>(R - 1));
+        const int32_t lengths = seq_len[mine], others = more != nullptr ? more[mine] : 0;
+        for (int i = 0; i < 32; ++i) {
+            const int64_t row = r0 + i * kSetWarps;
+            if (row >= R) break;
+            const int32_t r = static_cast<int32_t>(row);
+            const int32_t held = begin(r, __shfl_sync(0xFFFFFFFFu, lengths, i), __shfl_sync(0xFFFFFFFFu, others, i));
+            const int32_t* table = block_table + row * max_blocks;
+            bool out = false;
+            for (int32_t e0 = lane; e0 < held; e0 += 32 * kSetBatch) {
+                int32_t id[kSetBatch];
+#pragma unroll
+                for (int q = 0; q < kSetBatch; ++q) id[q] = e0 + 32 * q < held ? table[e0 + 32 * q] : 0;
+#pragma unroll
+                for (int q = 0; q < kSetBatch; ++q) {
+                    if (e0 + 32 * q >= held) continue;
+                    if (id[q] >= 0 && id[q] < num_blocks)
+                        bit(r, id[q]);
+                    else
+                        out = true;
+                }
+            }
+            end(r, __any_sync(0xFFFFFFFFu, out));
+        }
+    }
 }
 
 // Exclusive prefix sum of v over the cluster's threads, and its total.  `s_warp` [32], `s_all` [kSetCtas].
@@ -172,48 +242,78 @@ __device__ __forceinline__ int32_t cluster_prefix(cg::cluster_group& cluster, in
     return ahead + before + in - v;
 }
 
+// One cluster of kSetCtas CTAs, more than every device lets a kernel have without asking.
+template <typename Args>
+cudaError_t launch_cluster(void (*kernel)(Args), const Args& a, int bytes, cudaStream_t stream)
+{
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+    if (cudaError_t e = allow_shared(kernel, bytes)) return e;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = kSetCtas;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(kSetCtas);
+    config.blockDim = dim3(kSetThreads);
+    config.dynamicSmemBytes = static_cast<size_t>(bytes);
+    config.stream = stream;
+    config.attrs = &cluster;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, a);
+}
+
 // ---- free -------------------------------------------------------------------
-__global__ void __cluster_dims__(kSetCtas, 1, 1) __launch_bounds__(kSetThreads) cache_free_kernel(const FreeArgs a)
+template <bool OWN>
+__global__ void __launch_bounds__(kSetThreads) cache_free_kernel(const __grid_constant__ FreeArgs a)
 {
     extern __shared__ uint32_t s_set[];
     __shared__ int32_t s_warp[32], s_all[kSetCtas];
     cg::cluster_group cluster = cg::this_cluster();
-    const int32_t words = set_words(a.num_blocks);
-    uint32_t* s_stay = s_set;         // held by a request that stays, or free already
-    uint32_t* s_gone = s_set + words; // held by one that leaves
+    const int32_t words = set_words(a.num_blocks), map = OWN ? words * kSetCtas : words;
+    uint32_t* s_stay = s_set;        // held by a request that stays, or free already
+    uint32_t* s_gone = s_set + map;  // held by one that leaves
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = static_cast<int>(cluster.block_rank());
-    for (int32_t i = tid; i < 2 * words; i += kSetThreads) s_set[i] = 0;
+    for (int32_t i = tid; i < 2 * map; i += kSetThreads) s_set[i] = 0;
     const int32_t count = min(max(a.free_count[0], 0), a.num_blocks);
-    cluster.sync();
+    if (OWN)
+        __syncthreads();
+    else
+        cluster.sync();
 
-    for (int32_t i = rank * kSetThreads + tid; i < count; i += kSetCtas * kSetThreads) {
-        const int32_t id = a.free_blocks[i];
-        if (id >= 0 && id < a.num_blocks) set_bit(cluster, s_stay, words, id);
+    for (int32_t i0 = rank * kSetThreads + tid; i0 < count; i0 += kSetCtas * kSetThreads * kSetBatch) {
+        int32_t id[kSetBatch];
+#pragma unroll
+        for (int q = 0; q < kSetBatch; ++q) {
+            const int64_t i = i0 + static_cast<int64_t>(q) * kSetCtas * kSetThreads;
+            id[q] = i < count ? a.free_blocks[i] : -1;
+        }
+#pragma unroll
+        for (int q = 0; q < kSetBatch; ++q)
+            if (id[q] >= 0 && id[q] < a.num_blocks) set_bit<OWN>(cluster, s_stay, words, id[q]);
     }
     const int64_t room = static_cast<int64_t>(a.max_blocks) * a.block_size;
-    for (int32_t r = rank * (kSetThreads / 32) + tid / 32; r < a.R; r += kSetCtas * (kSetThreads / 32)) {
-        const int32_t L = a.seq_len[r];
-        const bool leaves = a.leave[r] != 0, bad = L < 0 || L > room;
-        const int64_t tokens = bad && (leaves || L < 0) ? 0 : min(static_cast<int64_t>(L), room);
-        const int32_t held = tokens > 0 ? a.by_block.quotient(static_cast<int32_t>(tokens - 1)) + 1 : 0;
-        const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
-        bool out = false;
-        for (int32_t i = lane; i < held; i += 32) {
-            const int32_t id = table[i];
-            if (id >= 0 && id < a.num_blocks)
-                set_bit(cluster, leaves ? s_gone : s_stay, words, id);
-            else
-                out = true;
-        }
-        out = __any_sync(0xFFFFFFFFu, out);
-        if (lane == 0) {
+    bool leaves = false, bad = false;
+    int32_t L = 0;
+    for_rows(
+        cluster, a.R, a.seq_len, a.leave, a.block_table, a.max_blocks, a.num_blocks,
+        [&](int32_t, int32_t length, int32_t leave) {
+            L = length;
+            leaves = leave != 0;
+            bad = L < 0 || L > room;
+            const int64_t tokens = bad && (leaves || L < 0) ? 0 : min(static_cast<int64_t>(L), room);
+            return tokens > 0 ? a.by_block.quotient(static_cast<int32_t>(tokens - 1)) + 1 : 0;
+        },
+        [&](int32_t, int32_t id) { set_bit<OWN>(cluster, leaves ? s_gone : s_stay, words, id); },
+        [&](int32_t r, bool out) {
+            if (lane != 0) return;
             a.seq_len_out[r] = leaves && !bad ? 0 : L;
             if (a.status != nullptr) a.status[r] = (bad ? SV_ST_BAD_LENGTH : 0) | (out ? SV_ST_BAD_BLOCK : 0);
-        }
-    }
+        });
     cluster.sync();
 
+    s_stay = set_part<OWN>(cluster, s_stay, words);
+    s_gone = set_part<OWN>(cluster, s_gone, words);
     const int32_t per = (words + kSetThreads - 1) / kSetThreads;
     const int32_t w0 = min(tid * per, words), w1 = min(w0 + per, words);
     int32_t mine = 0, total;
@@ -241,7 +341,8 @@ __host__ __device__ inline CompactPlan plan_of(const CompactArgs& a)
     return CompactPlan{p, p + 64, p + 64 + n, p + 64 + 2 * n};
 }
 
-__global__ void __cluster_dims__(kSetCtas, 1, 1) __launch_bounds__(kSetThreads) compact_plan_kernel(const CompactArgs a)
+template <bool OWN>
+__global__ void __launch_bounds__(kSetThreads) compact_plan_kernel(const __grid_constant__ CompactArgs a)
 {
     extern __shared__ uint32_t s_set[];
     __shared__ int32_t s_warp[32], s_all[kSetCtas], s_all2[kSetCtas];
@@ -250,45 +351,44 @@ __global__ void __cluster_dims__(kSetCtas, 1, 1) __launch_bounds__(kSetThreads) 
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = static_cast<int>(cluster.block_rank());
     const CompactPlan plan = plan_of(a);
-    for (int32_t i = tid; i < words; i += kSetThreads) s_set[i] = 0;
-    cluster.sync();
+    for (int32_t i = tid; i < (OWN ? words * kSetCtas : words); i += kSetThreads) s_set[i] = 0;
+    if (OWN)
+        __syncthreads();
+    else
+        cluster.sync();
 
     const int64_t room = static_cast<int64_t>(a.max_blocks) * a.cache.block_size;
-    for (int32_t r = rank * (kSetThreads / 32) + tid / 32; r < a.R; r += kSetCtas * (kSetThreads / 32)) {
-        const int32_t L = a.seq_len[r];
-        const int32_t tokens = static_cast<int32_t>(min(static_cast<int64_t>(max(L, 0)), room));
-        const int32_t held = tokens > 0 ? a.by_block.quotient(tokens - 1) + 1 : 0;
-        const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
-        bool out = false;
-        for (int32_t i = lane; i < held; i += 32) {
-            const int32_t id = table[i];
-            if (id >= 0 && id < N)
-                set_bit(cluster, s_set, words, id);
-            else
-                out = true;
-        }
-        out = __any_sync(0xFFFFFFFFu, out);
-        if (lane == 0 && a.status != nullptr)
-            a.status[r] = (L != tokens ? SV_ST_BAD_LENGTH : 0) | (out ? SV_ST_BAD_BLOCK : 0);
-    }
+    bool bad = false;
+    for_rows(
+        cluster, a.R, a.seq_len, nullptr, a.block_table, a.max_blocks, N,
+        [&](int32_t, int32_t L, int32_t) {
+            const int32_t tokens = static_cast<int32_t>(min(static_cast<int64_t>(max(L, 0)), room));
+            bad = L != tokens;
+            return tokens > 0 ? a.by_block.quotient(tokens - 1) + 1 : 0;
+        },
+        [&](int32_t, int32_t id) { set_bit<OWN>(cluster, s_set, words, id); },
+        [&](int32_t r, bool out) {
+            if (lane == 0 && a.status != nullptr) a.status[r] = (bad ? SV_ST_BAD_LENGTH : 0) | (out ? SV_ST_BAD_BLOCK : 0);
+        });
     cluster.sync();
 
+    const uint32_t* part = set_part<OWN>(cluster, s_set, words);
     const int32_t per = (words + kSetThreads - 1) / kSetThreads;
     const int32_t w0 = min(tid * per, words), w1 = min(w0 + per, words);
     int32_t mine = 0, U;
-    for (int32_t w = w0; w < w1; ++w) mine += __popc(s_set[w]);
+    for (int32_t w = w0; w < w1; ++w) mine += __popc(part[w]);
     const int32_t before = cluster_prefix(cluster, mine, s_warp, s_all, U);  // held blocks before word w0
     // Of the ids below U as many are gaps as there are held ones at U or above.  A held id x >= U with h held
     // ids below it is move h - (held ids below U); a gap x < U with h held ids below it is move x - h.
     int32_t low = 0, below;
     for (int32_t w = w0; w < w1; ++w) {
         const int32_t id = (rank * words + w) * 32, left = U - id;
-        low += __popc(left >= 32 ? s_set[w] : left <= 0 ? 0u : s_set[w] & ((1u << left) - 1));
+        low += __popc(left >= 32 ? part[w] : left <= 0 ? 0u : part[w] & ((1u << left) - 1));
     }
     cluster_prefix(cluster, low, s_warp, s_all2, below);
     int32_t h = before;
     for (int32_t w = w0; w < w1; ++w) {
-        const uint32_t bits = s_set[w];
+        const uint32_t bits = part[w];
         const int32_t id = (rank * words + w) * 32;
         for (int32_t i = 0; i < 32 && id + i < N; ++i) {
             const bool held = (bits >> i) & 1u;
@@ -378,20 +478,19 @@ cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t stream)
 
 cudaError_t launch_cache_free(const FreeArgs& a, cudaStream_t stream)
 {
-    const int bytes = 8 * set_words(a.num_blocks);
-    if (cudaError_t e = allow_shared(cache_free_kernel, bytes)) return e;
-    cache_free_kernel<<<kSetCtas, kSetThreads, bytes, stream>>>(a);
-    return cudaGetLastError();
+    const int part = 2 * 4 * set_words(a.num_blocks), whole = part * kSetCtas;
+    return whole <= kSetOwnBytes ? launch_cluster(cache_free_kernel<true>, a, whole, stream)
+                                 : launch_cluster(cache_free_kernel<false>, a, part, stream);
 }
 
 size_t compact_workspace_bytes(int32_t num_blocks) { return 256 + 12 * static_cast<size_t>(num_blocks); }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t stream)
 {
-    const int bytes = 4 * set_words(a.cache.num_blocks);
-    if (cudaError_t e = allow_shared(compact_plan_kernel, bytes)) return e;
-    compact_plan_kernel<<<kSetCtas, kSetThreads, bytes, stream>>>(a);
-    if (cudaError_t e = cudaGetLastError()) return e;
+    const int part = 4 * set_words(a.cache.num_blocks), whole = part * kSetCtas;
+    if (cudaError_t e = whole <= kSetOwnBytes ? launch_cluster(compact_plan_kernel<true>, a, whole, stream)
+                                              : launch_cluster(compact_plan_kernel<false>, a, part, stream))
+        return e;
     PackGeom g{};
     g.vecs = a.cache.head_dim / 8;
     const bool heads_in = a.cache.kv_heads == 1 || a.cache.head_stride <= a.cache.token_stride;
