@@ -3,8 +3,9 @@
 //
 // y = x * (mean(x^2) + eps)^(-1/2) * w, then pairs of y turn as in rope.cu.  The sum of
 // squares needs a whole head before its first entry can be written, so a head belongs to
-// the 1, 2, 4 or 8 lanes that hold its vectors two by two (the same two of every head:
-// the halves of eight pairs, or neighbours), and the sum is taken by exchanges among them.
+// the lanes that hold its vectors two by two (the same two of every head: the halves of
+// eight pairs, or neighbours), and the sum is taken by exchanges among them.  Arithmetic
+// is on pairs of fp32 values.
 #include <algorithm>
 
 #include "sv_internal.h"
@@ -12,6 +13,8 @@
 
 namespace sv {
 namespace {
+
+constexpr int kNormTokens = 4;  // most tokens of a CTA
 
 __device__ __forceinline__ float weight_at(const void* w, int32_t dtype, int i)
 {
@@ -21,149 +24,173 @@ __device__ __forceinline__ float weight_at(const void* w, int32_t dtype, int i)
     return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
 
-// SIDE: as in rope.cu.  LANES: lanes of a head.
-template <bool F16, bool SIDE, int LANES>
+// Two fp32 values times a factor, and the two 16-bit entries of a word as fp32.
+__device__ __forceinline__ uint64_t both(float x) { return pack2(x, x); }
+template <bool F16>
+__device__ __forceinline__ uint64_t wide2(uint32_t w)
+{
+    const float2 v = unpack2<F16>(w);
+    return pack2(v.x, v.y);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t narrow2(uint64_t v)
+{
+    float x, y;
+    unpack2(v, x, y);
+    return pack2<F16>(x, y);
+}
+
+// SIDE: as in rope.cu.  ITEMS: lanes of a head, 32 / ITEMS heads to a warp.
+template <bool F16, bool SIDE, int ITEMS>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs n, const RopeGeom g)
 {
-    constexpr int kGroups = kRopeThreads / LANES;
+    constexpr int kHeads = 32 / ITEMS, kGroups = kRopeThreads / 32 * kHeads;
     const RopeArgs& a = n.rope;
-    __shared__ __align__(16) float2 s_cs[kRopeTokens][SV_MAX_HEAD_DIM / 2 + 8];
-    __shared__ __align__(16) float s_w[2][SV_MAX_HEAD_DIM];
-    __shared__ int64_t s_at[kRopeTokens];
-    const int tid = threadIdx.x, j = tid % LANES;
+    // What a lane reads of the tables lies 16 bytes beside what the next lane reads: [part][lane of the head].
+    __shared__ __align__(16) float4 s_cs[kNormTokens][4][ITEMS];  // cosine and sine of two pairs
+    __shared__ __align__(16) float4 s_w[2][4][ITEMS];             // four entries' weights for q, for k
+    __shared__ int64_t s_at[kNormTokens];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const bool whole = lane < kHeads * ITEMS;  // the last lanes of a warp may have no head
+    const int j = whole ? lane % ITEMS : 0, group = whole ? tid / 32 * kHeads + lane / ITEMS : 0;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * g.tokens;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(g.tokens), a.q.tokens - t0));
     const int Hq = a.q.heads, Hk = a.cache.kv_heads, D = a.cache.head_dim;
-    const uint32_t total = static_cast<uint32_t>(tokens) * g.rows, step = kGroups * gridDim.y;
+    const int step = kGroups * gridDim.y;
 
-    // the two vectors of this lane, and the first of the eight pairs in them
+    // the two vectors of a lane, and whether pairs turn in them
     const int cut = g.half / 8;
-    int va_at = 2 * j, vb_at = 2 * j + 1, pair = -1;
-    if (SIDE) {
-        pair = 8 * j < g.half ? 8 * j : -1;
-    } else if (j < cut) {
-        va_at = j;
-        vb_at = j + cut;
-        pair = 8 * j;
-    }
-    const bool has_a = va_at < g.vecs, has_b = vb_at < g.vecs;
+    auto vectors_of = [&](int j, int& va, int& vb) -> bool {
+        va = 2 * j;
+        vb = 2 * j + 1;
+        if (SIDE) return 8 * j < g.half;
+        if (j >= cut) return false;
+        va = j;
+        vb = j + cut;
+        return true;
+    };
+    int va_at, vb_at;
+    const bool turns = vectors_of(j, va_at, vb_at), has_a = whole && va_at < g.vecs, has_b = whole && vb_at < g.vecs;
 
-    auto place = [&](uint32_t x, int& token, int& row) {
-        uint32_t in = x;
-        token = 0;
-#pragma unroll
-        for (int i = 1; i < kRopeTokens; ++i) {
-            if (in >= static_cast<uint32_t>(g.rows)) {
-                in -= g.rows;
+    struct Head {
+        int token, row;
+        __device__ __forceinline__ void settle(int rows)
+        {
+#pragma unroll 1
+            while (row >= rows) {
+                row -= rows;
                 ++token;
             }
         }
-        row = static_cast<int>(in);
     };
-    auto load = [&](uint32_t x, uint4& va, uint4& vb) {
+    auto load = [&](const Head& h, uint4& va, uint4& vb) {
         va = vb = make_uint4(0, 0, 0, 0);
-        if (x >= total) return;
-        int token, row;
-        place(x, token, row);
-        const sv_heads& h = row < Hq ? a.q : row < Hq + Hk ? a.k : a.v;
-        const int r = row < Hq ? row : row < Hq + Hk ? row - Hq : row - Hq - Hk;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(h.data) +
-                                                          (t0 + token) * h.token_stride + r * h.head_stride);
+        if (h.token >= tokens) return;
+        const sv_heads& m = h.row < Hq ? a.q : h.row < Hq + Hk ? a.k : a.v;
+        const int r = h.row < Hq ? h.row : h.row < Hq + Hk ? h.row - Hq : h.row - Hq - Hk;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.data) +
+                                                          (t0 + h.token) * m.token_stride + r * m.head_stride);
         if (has_a) va = src[va_at];
         if (has_b) vb = src[vb_at];
     };
     uint4 na, nb;  // the next head's vectors, in flight
-    uint32_t x = blockIdx.y * kGroups + tid / LANES;
-    load(x, na, nb);
+    Head next{0, static_cast<int>(blockIdx.y) * kGroups + group};
+    next.settle(g.rows);
+    load(next, na, nb);
     if (tid < tokens) s_at[tid] = slot_offset(a, a.slot[t0 + tid]);
-    for (int i = tid; i < D; i += kRopeThreads) {
-        s_w[0][i] = weight_at(n.q_weight, n.weight_dtype, i);
-        s_w[1][i] = weight_at(n.k_weight, n.weight_dtype, i);
+    for (int i = tid; i < 2 * 4 * ITEMS; i += kRopeThreads) {
+        const int which = i / (4 * ITEMS), part = i / ITEMS % 4, o = i % ITEMS;
+        int x, y;
+        vectors_of(o, x, y);
+        const void* w = which == 0 ? n.q_weight : n.k_weight;
+        const int first = 8 * (part < 2 ? x : y) + 4 * (part & 1);
+        float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+        if (w != nullptr && first < D)
+            f = make_float4(weight_at(w, n.weight_dtype, first), weight_at(w, n.weight_dtype, first + 1),
+                            weight_at(w, n.weight_dtype, first + 2), weight_at(w, n.weight_dtype, first + 3));
+        s_w[which][part][o] = f;
     }
-    for (int y = tid; y < tokens * g.half; y += kRopeThreads) {
-        const int i = y / g.half, p = y - i * g.half;
-        s_cs[i][p] = turn_of(a, a.position[t0 + i], p);
+    for (int y = tid; y < tokens * 8 * ITEMS; y += kRopeThreads) {
+        const int i = y / (8 * ITEMS), p = y - i * (8 * ITEMS);
+        // a lane may hold fewer pairs than eight: the others pass
+        const float2 t = p < g.half ? turn_of(a, a.position[t0 + i], p) : make_float2(1.0f, 0.0f);
+        float* to = &s_cs[i][p / 2 % 4][p / 8].x + p % 2 * (SIDE ? 2 : 1);
+        to[0] = t.x;             // side by side: cosine, sine of each; else the two cosines, then the two sines
+        to[SIDE ? 1 : 2] = t.y;
     }
     __syncthreads();
 
-    // every thread of the CTA takes the same number of rounds: the exchanges need whole warps
-    const uint32_t first = blockIdx.y * kGroups;
-    for (uint32_t base = first; base < total; base += step, x += step) {
+    // every warp takes the same number of rounds: the exchanges need all of its lanes
+    const int total = tokens * g.rows;
+    for (int base = static_cast<int>(blockIdx.y) * kGroups; base < total; base += step) {
         const uint4 va = na, vb = nb;
-        load(x + step, na, nb);
-        float f[16];
+        const Head h = next;
+        next.row += step;
+        next.settle(g.rows);
+        load(next, na, nb);
         const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-        float sum = 0.0f;
+        uint64_t f[8], sums = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float2 v = unpack2<F16>(w[e]);
-            f[2 * e] = v.x;
-            f[2 * e + 1] = v.y;
-            sum = fmaf(v.x, v.x, sum);
-            sum = fmaf(v.y, v.y, sum);
+            f[e] = wide2<F16>(w[e]);
+            sums = fma2(f[e], f[e], sums);
         }
+        float lo, hi;
+        unpack2(sums, lo, hi);
+        float sum = lo + hi;
+        if ((ITEMS & (ITEMS - 1)) == 0) {
 #pragma unroll
-        for (int d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        int token, row;
-        place(x, token, row);
-        uint4 oa = va, ob = vb;
-        if (x < total && row < Hq + Hk) {
-            const float r = rsqrtf(sum * g.by_dim + n.eps);
-            const float* weight = s_w[row < Hq ? 0 : 1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (has_a) {
-                    const float2 u = *reinterpret_cast<const float2*>(weight + 8 * va_at + 2 * e);
-                    f[2 * e] *= r * u.x;
-                    f[2 * e + 1] *= r * u.y;
-                }
-                if (has_b) {
-                    const float2 u = *reinterpret_cast<const float2*>(weight + 8 * vb_at + 2 * e);
-                    f[8 + 2 * e] *= r * u.x;
-                    f[8 + 2 * e + 1] *= r * u.y;
-                }
-            }
-            if (pair >= 0) {
-                const float4* cs = reinterpret_cast<const float4*>(&s_cs[token][pair]);
-                if (SIDE) {
-                    // the last rotated vectors may hold fewer than eight pairs: the others pass
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 f2 = cs[e / 2];
-                        const float c = e & 1 ? f2.z : f2.x, s = e & 1 ? f2.w : f2.y;
-                        const float u = f[2 * e], v = f[2 * e + 1];
-                        if (pair + e < g.half) {
-                            f[2 * e] = fmaf(-v, s, u * c);
-                            f[2 * e + 1] = fmaf(u, s, v * c);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 f2 = cs[e / 2];
-                        const float c = e & 1 ? f2.z : f2.x, s = e & 1 ? f2.w : f2.y;
-                        const float u = f[e], v = f[8 + e];
-                        f[e] = fmaf(-v, s, u * c);
-                        f[8 + e] = fmaf(u, s, v * c);
-                    }
-                }
-            }
-            oa = make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]),
-                            pack2<F16>(f[6], f[7]));
-            ob = make_uint4(pack2<F16>(f[8], f[9]), pack2<F16>(f[10], f[11]), pack2<F16>(f[12], f[13]),
-                            pack2<F16>(f[14], f[15]));
-        }
-        if (x >= total) continue;
-        uint4* dst;
-        if (row < Hq) {
-            dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) +
-                                           (t0 + token) * a.q_out.token_stride + row * a.q_out.head_stride);
+            for (int d = 1; d < ITEMS; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         } else {
-            const int64_t at = s_at[token];
+            // the head's lanes in the same order for each of them
+            float all = 0.0f;
+#pragma unroll
+            for (int d = 0; d < ITEMS; ++d) all += __shfl_sync(0xFFFFFFFFu, sum, lane - j + d);
+            sum = all;
+        }
+        if (!whole || h.token >= tokens) continue;
+        uint4 oa = va, ob = vb;
+        if (h.row < Hq + Hk) {
+            const uint64_t scale = both(rsqrtf(sum * g.by_dim + n.eps));
+            const int which = h.row < Hq ? 0 : 1;
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+                const float4 u = s_w[which][part][j];
+                f[2 * part] = mul2(f[2 * part], mul2(pack2(u.x, u.y), scale));
+                f[2 * part + 1] = mul2(f[2 * part + 1], mul2(pack2(u.z, u.w), scale));
+            }
+            if (turns) {
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {
+                    const float4 t = s_cs[h.token][part][j];
+                    if (SIDE) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float c = e == 0 ? t.x : t.z, sn = e == 0 ? t.y : t.w;
+                            float x, y;
+                            unpack2(f[2 * part + e], x, y);
+                            f[2 * part + e] = fma2(pack2(y, x), pack2(-sn, sn), mul2(f[2 * part + e], both(c)));
+                        }
+                    } else {
+                        const uint64_t c = pack2(t.x, t.y), sn = pack2(t.z, t.w), x = f[part], y = f[4 + part];
+                        f[part] = fma2(y, pack2(-t.z, -t.w), mul2(x, c));
+                        f[4 + part] = fma2(x, sn, mul2(y, c));
+                    }
+                }
+            }
+            oa = make_uint4(narrow2<F16>(f[0]), narrow2<F16>(f[1]), narrow2<F16>(f[2]), narrow2<F16>(f[3]));
+            ob = make_uint4(narrow2<F16>(f[4]), narrow2<F16>(f[5]), narrow2<F16>(f[6]), narrow2<F16>(f[7]));
+        }
+        uint4* dst;
+        if (h.row < Hq) {
+            dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) +
+                                           (t0 + h.token) * a.q_out.token_stride + h.row * a.q_out.head_stride);
+        } else {
+            const int64_t at = s_at[h.token];
             if (at < 0) continue;
-            const bool key = row < Hq + Hk;
+            const bool key = h.row < Hq + Hk;
             dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(key ? a.cache.k : a.cache.v) + at +
-                                           (row - (key ? Hq : Hq + Hk)) * a.cache.head_stride);
+                                           (h.row - (key ? Hq : Hq + Hk)) * a.cache.head_stride);
         }
         if (has_a) dst[va_at] = oa;
         if (has_b) dst[vb_at] = ob;
@@ -235,17 +262,23 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_entries_kernel(const _
     }
 }
 
-template <bool F16, bool SIDE>
-void launch_lanes(const NormRopeArgs& n, const RopeGeom& g, int lanes, dim3 grid, cudaStream_t stream)
+template <bool F16, bool SIDE, int ITEMS>
+void launch_items(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
 {
-    if (lanes == 1)
-        norm_rope_kernel<F16, SIDE, 1><<<grid, kRopeThreads, 0, stream>>>(n, g);
-    else if (lanes == 2)
-        norm_rope_kernel<F16, SIDE, 2><<<grid, kRopeThreads, 0, stream>>>(n, g);
-    else if (lanes == 4)
-        norm_rope_kernel<F16, SIDE, 4><<<grid, kRopeThreads, 0, stream>>>(n, g);
-    else
-        norm_rope_kernel<F16, SIDE, 8><<<grid, kRopeThreads, 0, stream>>>(n, g);
+    if (g.items != ITEMS) {
+        if constexpr (ITEMS > 1) launch_items<F16, SIDE, ITEMS - 1>(n, g, stream);
+        return;
+    }
+    constexpr int kGroups = kRopeThreads / 32 * (32 / ITEMS);
+    const int64_t T = n.rope.q.tokens;
+    const int sms = device_sm_count();
+    auto cdiv = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+    g.tokens = T >= kNormTokens * 4 * sms ? kNormTokens : 1;
+    const int64_t most = cdiv(static_cast<int64_t>(g.tokens) * g.rows, kGroups);
+    const int64_t want = cdiv(2 * sms, T);
+    const dim3 grid(static_cast<unsigned>(cdiv(T, g.tokens)),
+                    static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
+    norm_rope_kernel<F16, SIDE, ITEMS><<<grid, kRopeThreads, 0, stream>>>(n, g);
 }
 
 }  // namespace
@@ -257,6 +290,7 @@ cudaError_t launch_norm_rope_cache(const NormRopeArgs& n, cudaStream_t stream)
     g.vecs = a.cache.head_dim / 8;
     g.half = a.rot_dim / 2;
     g.rows = a.q.heads + 2 * a.cache.kv_heads;
+    g.items = (g.vecs + 1) / 2;
     g.by_dim = 1.0f / a.cache.head_dim;
     const int sms = device_sm_count();
     const bool f16 = a.cache.dtype == SV_F16;
@@ -270,23 +304,17 @@ cudaError_t launch_norm_rope_cache(const NormRopeArgs& n, cudaStream_t stream)
             norm_rope_entries_kernel<false><<<grid, kRopeThreads, 0, stream>>>(n, g);
         return cudaGetLastError();
     }
-    int lanes = 1;
-    while (2 * lanes < g.vecs) lanes *= 2;
-    g.tokens = a.q.tokens >= kRopeTokens * 8 * sms ? kRopeTokens : 1;
-    const int64_t most = cdiv(static_cast<int64_t>(g.tokens) * g.rows, kRopeThreads / lanes);
-    const int64_t want = cdiv(2 * sms, a.q.tokens);
-    const dim3 grid(static_cast<unsigned>(cdiv(a.q.tokens, g.tokens)),
-                    static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
+    constexpr int kMost = SV_MAX_HEAD_DIM / 16;
     if (a.interleaved) {
         if (f16)
-            launch_lanes<true, true>(n, g, lanes, grid, stream);
+            launch_items<true, true, kMost>(n, g, stream);
         else
-            launch_lanes<false, true>(n, g, lanes, grid, stream);
+            launch_items<false, true, kMost>(n, g, stream);
     } else {
         if (f16)
-            launch_lanes<true, false>(n, g, lanes, grid, stream);
+            launch_items<true, false, kMost>(n, g, stream);
         else
-            launch_lanes<false, false>(n, g, lanes, grid, stream);
+            launch_items<false, false, kMost>(n, g, stream);
     }
     return cudaGetLastError();
 }
