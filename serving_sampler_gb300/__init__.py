@@ -485,6 +485,23 @@ def _new_ints(like, stream, *sizes):
     return torch.unsafe_split_with_sizes(_empty(sum(sizes), torch.int32, like.device, stream), sizes)
 
 
+def _like(t, stream):
+    """An output with the shape and type of an input, which costs less to ask for than its size and type."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        out = torch.empty_like(t)
+    out.record_stream(torch.cuda.current_stream(t.device))
+    return out
+
+
+def _table_width(block_table, R) -> int:
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != R:
+        raise ValueError("block_table must be [R, max_blocks]")
+    return shape[1]
+
+
 def step_tables(seq_len, new_len, block_table, free_blocks, free_count, block_size: int, T: int, parent=None,
                 mask_words: int = 0, out: dict | None = None, stream=None) -> dict:
     """Lay a step's tokens out in the paged cache.  seq_len, new_len int32 [R]; block_table int32
@@ -578,10 +595,11 @@ def norm_rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, q_weight=N
     """rope_cache with an RMS norm over the D entries of every head of q and k ahead of the rotation, in the same pass.
     q_weight, k_weight [D]: weights in the heads' dtype or float32 (one dtype for both), or None for ones.  The other
     arguments are those of rope_cache.  Returns the normed and rotated q (q_out may be q)."""
-    lib = load()
-    T, _, D = q.shape
+    lib = _lib or load()
+    x, cache = heads_of(q), cache_of(k_cache, v_cache)
+    T, D = x.tokens, x.head_dim
     if q_out is None:
-        q_out = _empty(q.shape, q.dtype, q.device, stream)
+        q_out = _like(q, stream)
     if slot.dtype is not torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != T:
         raise ValueError("slot must be a contiguous int64 CUDA tensor with an entry for each token")
     if freqs.dtype not in (torch.int64, torch.uint64) or not freqs.is_cuda or not freqs.is_contiguous():
@@ -590,10 +608,10 @@ def norm_rope_cache(q, k, v, position, slot, freqs, k_cache, v_cache, q_weight=N
     if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
         raise TypeError("q_weight and k_weight must have one dtype")
     w_type = SV_F32 if w is None or w.dtype is torch.float32 else _half_type(w)
-    rc = lib.sv_norm_rope_cache(heads_of(q), heads_of(k), heads_of(v), _ints(position, "position", T), slot.data_ptr(),
+    rc = lib.sv_norm_rope_cache(x, heads_of(k), heads_of(v), _ints(position, "position", T), slot.data_ptr(),
                                 freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, mscale,
                                 _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D), w_type, eps,
-                                heads_of(q_out), cache_of(k_cache, v_cache), _raw_stream(stream, q))
+                                x if q_out is q else heads_of(q_out), cache, _raw_stream(stream, q))
     if rc:
         _check(rc)
     return q_out
@@ -680,23 +698,21 @@ def cache_fork(k_cache, v_cache, block_table, seq_len, source, free_blocks, free
     tokens of a last block that is not full are copied, in every layer of the caches ([layers, ] num_blocks,
     block_size, kv_heads, head_dim), into a block from free_blocks int32 [num_blocks], of which free_count int32 [1]
     are free.  The forks' rows are written in place.  Returns seq_len [R], free_count [1] and status [R]."""
-    lib = load()
+    lib = _lib or load()
     R = seq_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("block_table must be [R, max_blocks]")
-    a_seq = _ints(seq_len, "seq_len")
+    most, a_seq, a_count = _table_width(block_table, R), _ints(seq_len, "seq_len"), _ints(free_count, "free_count", 1)
     if out is None:
-        out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, stream, R, 1, R)))
+        out = dict(seq_len=_like(seq_len, stream), free_count=_like(free_count, stream), status=_like(seq_len, stream))
     else:
         _check_out(out, seq_len=(torch.int32, R), free_count=(torch.int32, 1), status=(torch.int32, R))
     if R == 0:
         with torch.cuda.stream(stream):
             out["free_count"].copy_(free_count)
         return out
-    rc = lib.sv_cache_fork(cache_of(k_cache, v_cache), _ints(block_table, "block_table"), block_table.shape[1], a_seq, R,
-                           _ints(source, "source", R), _ints(free_blocks, "free_blocks", k_cache.shape[-4]),
-                           _ints(free_count, "free_count", 1), out["seq_len"].data_ptr(), out["free_count"].data_ptr(),
-                           _at(out.get("status")), _raw_stream(stream, seq_len))
+    cache = cache_of(k_cache, v_cache)
+    rc = lib.sv_cache_fork(cache, _ints(block_table, "block_table"), most, a_seq, R, _ints(source, "source", R),
+                           _ints(free_blocks, "free_blocks", cache.num_blocks), a_count, out["seq_len"].data_ptr(),
+                           out["free_count"].data_ptr(), _at(out.get("status")), _raw_stream(stream, seq_len))
     if rc:
         _check(rc)
     return out
@@ -707,23 +723,20 @@ def cache_free(block_table, seq_len, leave, free_blocks, free_count, block_size:
     """Requests that leave (leave int32 [R], nonzero): the blocks that they hold and no other request does are pushed on
     free_blocks int32 [num_blocks] by rising id.  Returns seq_len [R] (0 for those that left), free_count [1] and
     status [R]."""
-    lib = load()
+    lib = _lib or load()
     R = seq_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("block_table must be [R, max_blocks]")
-    a_seq = _ints(seq_len, "seq_len")
+    most, a_seq, a_count = _table_width(block_table, R), _ints(seq_len, "seq_len"), _ints(free_count, "free_count", 1)
     if out is None:
-        out = dict(zip(("seq_len", "free_count", "status"), _new_ints(seq_len, stream, R, 1, R)))
+        out = dict(seq_len=_like(seq_len, stream), free_count=_like(free_count, stream), status=_like(seq_len, stream))
     else:
         _check_out(out, seq_len=(torch.int32, R), free_count=(torch.int32, 1), status=(torch.int32, R))
     if R == 0:
         with torch.cuda.stream(stream):
             out["free_count"].copy_(free_count)
         return out
-    rc = lib.sv_cache_free(_ints(block_table, "block_table"), block_table.shape[1], a_seq, _ints(leave, "leave", R), R,
-                           block_size, _ints(free_blocks, "free_blocks"), _ints(free_count, "free_count", 1),
-                           free_blocks.numel(), out["seq_len"].data_ptr(), out["free_count"].data_ptr(),
-                           _at(out.get("status")), _raw_stream(stream, seq_len))
+    rc = lib.sv_cache_free(_ints(block_table, "block_table"), most, a_seq, _ints(leave, "leave", R), R, block_size,
+                           _ints(free_blocks, "free_blocks"), a_count, free_blocks.numel(), out["seq_len"].data_ptr(),
+                           out["free_count"].data_ptr(), _at(out.get("status")), _raw_stream(stream, seq_len))
     if rc:
         _check(rc)
     return out
@@ -738,15 +751,15 @@ def cache_compact(k_cache, v_cache, block_table, seq_len, out: dict | None = Non
     caches ([layers, ] num_blocks, block_size, kv_heads, head_dim).  Returns the new block_table [R, max_blocks] (-1
     behind a request's blocks), free_blocks [num_blocks] (the lowest id on top, -1 behind them), free_count [1] and
     status [R].  Blocks that no request holds lose their contents."""
-    lib = load()
+    lib = _lib or load()
     R = seq_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("block_table must be [R, max_blocks]")
+    most, a_seq, a_table = _table_width(block_table, R), _ints(seq_len, "seq_len"), _ints(block_table, "block_table")
     cache = cache_of(k_cache, v_cache)
-    n, most = cache.num_blocks, block_table.shape[1]
+    n = cache.num_blocks
     if out is None:
-        table, free, count, status = _new_ints(seq_len, stream, R * most, n, 1, R)
-        out = dict(block_table=table.view(R, most), free_blocks=free, free_count=count, status=status)
+        device = seq_len.device
+        out = dict(block_table=_like(block_table, stream), free_blocks=_empty(n, torch.int32, device, stream),
+                   free_count=_empty(1, torch.int32, device, stream), status=_like(seq_len, stream))
     else:
         i32 = torch.int32
         _check_out(out, block_table=(i32, R * most), free_blocks=(i32, n), free_count=(i32, 1), status=(i32, R))
@@ -754,10 +767,9 @@ def cache_compact(k_cache, v_cache, block_table, seq_len, out: dict | None = Non
         workspace = _workspace(lib.sv_cache_compact_workspace(n), seq_len.device, None, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    rc = lib.sv_cache_compact(cache, _ints(block_table, "block_table"), most, _ints(seq_len, "seq_len"), R,
-                              out["block_table"].data_ptr(), out["free_blocks"].data_ptr(),
-                              out["free_count"].data_ptr(), _at(out.get("status")), workspace.data_ptr(),
-                              _nbytes(workspace), _raw_stream(stream, seq_len))
+    rc = lib.sv_cache_compact(cache, a_table, most, a_seq, R, out["block_table"].data_ptr(),
+                              out["free_blocks"].data_ptr(), out["free_count"].data_ptr(), _at(out.get("status")),
+                              workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, seq_len))
     if rc:
         _check(rc)
     return out
@@ -765,11 +777,23 @@ def cache_compact(k_cache, v_cache, block_table, seq_len, out: dict | None = Non
 
 def _floats(t, name, n):
     """The address of a float32 CUDA tensor that is passed as it lies."""
-    if t is None:
-        return None
     if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} entries")
     return t.data_ptr()
+
+
+def _logit_rows(t, rows, name) -> SvRows:
+    """A matrix of logits of which the first `rows` rows count; its rows may be strided."""
+    shape, strides = t.shape, t.stride()
+    if not t.is_cuda or len(shape) != 2 or shape[0] < rows:
+        raise ValueError(f"{name} must be a CUDA tensor [{rows}, V]")
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError("entries of a logit row must be contiguous")
+    dtype = t.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"logits must be bfloat16 or float32, got {dtype}")
+    return SvRows(t.data_ptr(), SV_BF16 if dtype is torch.bfloat16 else SV_F32, shape[1],
+                  strides[0] if rows > 1 else shape[1])
 
 
 def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=None, history_len=None, prompt_len=None,
@@ -784,42 +808,47 @@ def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=Non
     mask int32 [masks, words] of allowed ids as bits with mask_row int32 [rows] (negative: none), or a mask for each row
     without mask_row.  A row's drafts count as said before it.  Returns logits (out=dict(logits=logits) works in
     place) and status [R]."""
-    lib = load()
+    lib = _lib or load()
     rows = R * (1 + branches * k)
-    if logits.dim() != 2 or logits.shape[0] < rows:
-        raise ValueError(f"logits must be [{rows}, V]")
-    V = logits.shape[1]
+    x = _logit_rows(logits, rows, "logits")
     if out is None:
-        out = dict(logits=_empty((rows, V), logits.dtype, logits.device, stream),
-                   status=_empty(R, torch.int32, logits.device, stream))
+        alike = rows == len(logits) and logits.is_contiguous()
+        y = _like(logits, stream) if alike else _empty((rows, x.width), logits.dtype, logits.device, stream)
+        out = dict(logits=y, status=_empty(R, torch.int32, logits.device, stream))
     else:
         _check_out(out, status=(torch.int32, R))
-        if out["logits"].dim() != 2 or out["logits"].shape[0] < rows:
-            raise ValueError(f"out['logits'] must be [{rows}, V]")
-    if V > 1 and (logits.stride(1) != 1 or out["logits"].stride(1) != 1):
-        raise ValueError("entries of a logit row must be contiguous")
+        y = out["logits"]
     if draft is None and branches * k > 0:
         raise ValueError("draft must be [R, branches, k]")
-    if history is not None and (history.dim() != 2 or history.shape[0] != R or history_len is None):
-        raise ValueError("history must be [R, width], with history_len")
-    if mask is not None and mask.dim() != 2:
-        raise ValueError("mask must be [masks, words]")
-    start, ids, values = bias if bias is not None else (None, None, None)
-    n = 0 if bias is None else ids.numel()
-    rules = SvLogitRules(
-        None if history is None else _ints(history, "history"),
-        None if history is None else _ints(history_len, "history_len", R),
-        None if history is None or prompt_len is None else _ints(prompt_len, "prompt_len", R),
-        0 if history is None else history.shape[1], _floats(repetition, "repetition", R),
-        _floats(presence, "presence", R), _floats(frequency, "frequency", R),
-        None if bias is None else _ints(start, "the biases' start", R + 1),
-        None if bias is None else _ints(ids, "the biases' ids"), _floats(values, "the biases' values", n), n,
-        None if mask is None else _ints(mask, "mask"), 0 if mask is None else mask.shape[0],
-        0 if mask is None else mask.shape[1],
-        None if mask is None or mask_row is None else _ints(mask_row, "mask_row", rows))
-    rc = lib.sv_adjust_logits(rows_of(logits), R, k, branches,
-                              None if branches * k == 0 else _ints(draft, "draft", R * branches * k), rules,
-                              rows_of(out["logits"]), _at(out.get("status")), _raw_stream(stream, logits))
+    rules = SvLogitRules()
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != R or history_len is None:
+            raise ValueError("history must be [R, width], with history_len")
+        rules.history, rules.history_width = _ints(history, "history"), history.shape[1]
+        rules.history_len = _ints(history_len, "history_len", R)
+        if prompt_len is not None:
+            rules.prompt_len = _ints(prompt_len, "prompt_len", R)
+    if repetition is not None:
+        rules.repetition = _floats(repetition, "repetition", R)
+    if presence is not None:
+        rules.presence = _floats(presence, "presence", R)
+    if frequency is not None:
+        rules.frequency = _floats(frequency, "frequency", R)
+    if bias is not None:
+        start, ids, values = bias
+        rules.bias_start, rules.bias_id = _ints(start, "the biases' start", R + 1), _ints(ids, "the biases' ids")
+        rules.bias_entries = n = ids.numel()
+        rules.bias_value = _floats(values, "the biases' values", n)
+    if mask is not None:
+        if mask.dim() != 2:
+            raise ValueError("mask must be [masks, words]")
+        rules.mask = _ints(mask, "mask")
+        rules.masks, rules.mask_words = mask.shape
+        if mask_row is not None:
+            rules.mask_row = _ints(mask_row, "mask_row", rows)
+    rc = lib.sv_adjust_logits(x, R, k, branches, None if branches * k == 0 else _ints(draft, "draft", R * branches * k),
+                              rules, x if y is logits else _logit_rows(y, rows, "out['logits']"),
+                              _at(out.get("status")), _raw_stream(stream, logits))
     if rc:
         _check(rc)
     return out
