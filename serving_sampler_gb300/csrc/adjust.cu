@@ -27,7 +27,7 @@ constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of
 constexpr int kAdjStages = 2;                    // tiles of a warp's ring
 constexpr int kAdjSlice = 4096;                  // most ids of a slice
 constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
-constexpr int kAdjBatch = 8;                     // tokens that a thread loads before it counts them
+constexpr int kAdjBatch = 12;                    // tokens that a thread loads before it counts them
 constexpr int kAdjMaskWords = kAdjTile / 2 / 32 + 1;  // words of a region's mask
 
 // a word of the table: bit 31 seen, bits 19 .. 30 the head of the chain (0: none), bits 0 .. 18 the count
@@ -42,20 +42,21 @@ struct AdjustGeom {
     int32_t rows, groups;   // rows of a request, thread blocks that share them
     int32_t most_rows;      // of a thread block
     int32_t drafts;         // branches * k
+    int32_t bias_bits;      // of an id's word in the table of biases: 0 without biases, 16 where their numbers fit, else 32
 };
 
 // The parts of a CTA's shared memory, in 32-bit words; the tiles lie first.
 struct AdjustLayout {
     int32_t mask, tab, bias, bits, row, list, next, bytes;  // list and next hold 16 bits each
 };
-__host__ __device__ inline AdjustLayout layout_of(const AdjustGeom& g, bool biased, bool tiles)
+__host__ __device__ inline AdjustLayout layout_of(const AdjustGeom& g, bool tiles)
 {
     const int32_t ids = g.slice + kAdjEdge;
     AdjustLayout l;
     l.mask = tiles ? kAdjWarps * kAdjStages * kAdjTile / 4 : 0;
     l.tab = l.mask + (tiles ? (kAdjWarps * kAdjStages * kAdjMaskWords + 3) / 4 * 4 : 0);
     l.bias = l.tab + ids;
-    l.bits = l.bias + (biased ? ids : 0);
+    l.bits = l.bias + ids * g.bias_bits / 32;
     l.row = (l.bits + ids / 32 + 1 + 3) / 4 * 4;
     l.list = l.row + 2 * g.most_rows;
     l.next = l.list + (g.slice + (kAdjEdge << g.region_shift)) / 2;
@@ -150,10 +151,10 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     const sv_logit_rules& u = a.rules;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t ids = g.slice + kAdjEdge, V = a.in.width;
-    const bool biased = u.bias_entries > 0;
-    const AdjustLayout at = layout_of(g, biased, COPY);
+    const bool biased = g.bias_bits != 0;
+    const AdjustLayout at = layout_of(g, COPY);
     uint32_t* s_tab = s_mem + at.tab;
-    uint32_t* s_bias = s_mem + at.bias;  // 1 + the last entry of the id's bias, 0 for none
+    uint32_t* s_bias = s_mem + at.bias;  // an id's last bias: 1 + its number, 0 for none
     uint32_t* s_bits = s_mem + at.bits;
     int2* s_row = reinterpret_cast<int2*>(s_mem + at.row);  // each row's mask (-1: none), and the drafts before its branch's
     uint16_t* s_list = reinterpret_cast<uint16_t*>(s_mem + at.list);
@@ -174,6 +175,15 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
         s_row[j] = make_int2(i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1,
                              row0 + j > 0 ? (row0 + j - 1) / a.k * a.k : 0);
     }
+    // The first tokens are on their way before their number is known: all of the row may be read.
+    const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
+    int32_t token[kAdjBatch];
+    auto fetch = [&](int32_t i0, int32_t end) {
+#pragma unroll
+        for (int q = 0; q < kAdjBatch; ++q)
+            if (i0 + q * kAdjThreads < end) token[q] = history[i0 + q * kAdjThreads];
+    };
+    if (u.history != nullptr) fetch(tid, u.history_width);
     // what the request asks for
     uint32_t st = 0;
     int32_t len = 0, prompt = 0, b0 = 0, b1 = 0;
@@ -283,12 +293,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
         }
         return l;
     };
-    const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
-    for (int32_t i0 = tid; i0 < len; i0 += kAdjThreads * kAdjBatch) {
-        int32_t token[kAdjBatch];
-#pragma unroll
-        for (int q = 0; q < kAdjBatch; ++q)
-            if (i0 + q * kAdjThreads < len) token[q] = history[i0 + q * kAdjThreads];
+    for (int32_t i0 = tid; i0 < len;) {
 #pragma unroll
         for (int q = 0; q < kAdjBatch; ++q) {
             const int32_t i = i0 + q * kAdjThreads;
@@ -299,6 +304,8 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
             else
                 atomicOr(&s_tab[l], kAdjSeen);
         }
+        i0 += kAdjThreads * kAdjBatch;
+        fetch(i0, len);
     }
     for (int32_t i = tid; i < g.drafts; i += kAdjThreads) {
         const int32_t l = meet(a.draft[static_cast<int64_t>(r) * g.drafts + i]);
@@ -312,7 +319,20 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     }
     for (int32_t i = b0 + tid; i < b1; i += kAdjThreads) {
         const int32_t l = meet(u.bias_id[i]);
-        if (l >= 0) atomicMax(&s_bias[l], static_cast<uint32_t>(i) + 1);
+        if (l < 0) continue;
+        const uint32_t entry = static_cast<uint32_t>(i) + 1;
+        if (g.bias_bits == 32) {
+            atomicMax(&s_bias[l], entry);
+        } else {
+            uint32_t* word = &s_bias[l >> 1];
+            const int half = (l & 1) * 16;
+            uint32_t old = *word, was;
+            do {
+                was = old;
+                if (((was >> half) & 0xFFFFu) >= entry) break;
+                old = atomicCAS(word, was, (was & ~(0xFFFFu << half)) | (entry << half));
+            } while (old != was);
+        }
     }
     if (s == 0 && group == 0 && a.status != nullptr) {
         if (u.mask != nullptr && u.mask_row != nullptr)
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
         uint32_t count = word & kAdjCount;
         for (uint32_t e = (word & kAdjHead) >> kAdjHeadShift; e != 0; e = s_next[e - 1])
             count += static_cast<int32_t>(e) > w.before && static_cast<int32_t>(e) <= w.row;
-        const uint32_t entry = biased ? s_bias[l] : 0u;
+        const uint32_t entry = !biased ? 0u : g.bias_bits == 32 ? s_bias[l] : (s_bias[l >> 1] >> ((l & 1) * 16)) & 0xFFFFu;
         const bool seen = (word & kAdjSeen) != 0 || count != 0;
         if (!seen && entry == 0) return raw;
         float z = widen<T>(raw);
@@ -424,6 +444,7 @@ AdjustGeom geom_of(const AdjustArgs& a)
     AdjustGeom g{};
     g.drafts = a.branches * a.k;
     g.rows = 1 + g.drafts;
+    g.bias_bits = a.rules.bias_entries == 0 ? 0 : a.rules.bias_entries <= 0xFFFF ? 16 : 32;
     const int32_t region = kAdjTile / a.in.esize;
     auto slices = [&](int64_t n) { return (static_cast<int64_t>(a.in.width) + kAdjEdge - 1 + n - 1) / n; };
     g.slice = kAdjSlice;
@@ -448,7 +469,7 @@ cudaError_t launch_adjust_logits(const AdjustArgs& a, cudaStream_t stream)
 {
     const AdjustGeom g = geom_of(a);
     const bool tiles = by_tiles(a), bf16 = a.in.dtype == SV_BF16;
-    const int bytes = layout_of(g, a.rules.bias_entries > 0, tiles).bytes;
+    const int bytes = layout_of(g, tiles).bytes;
     const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.R) * g.slices * g.groups);
     auto* kernel = tiles ? bf16 ? adjust_kernel<uint16_t, true> : adjust_kernel<uint32_t, true>
                          : bf16 ? adjust_kernel<uint16_t, false> : adjust_kernel<uint32_t, false>;
