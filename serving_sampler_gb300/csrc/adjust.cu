@@ -27,7 +27,7 @@ constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of
 constexpr int kAdjStages = 2;                    // tiles of a warp's ring
 constexpr int kAdjSlice = 4096;                  // most ids of a slice
 constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
-constexpr int kAdjBatch = 12;                    // tokens that a thread loads before it counts them
+constexpr int kAdjBatch = 8;                     // tokens that a thread loads before it counts them
 constexpr int kAdjMaskWords = kAdjTile / 2 / 32 + 1;  // words of a region's mask
 
 // a word of the table: bit 31 seen, bits 19 .. 30 the head of the chain (0: none), bits 0 .. 18 the count
@@ -35,6 +35,8 @@ constexpr uint32_t kAdjSeen = 1u << 31, kAdjHeadShift = 19, kAdjHead = 0xFFFu <<
                    kAdjCount = (1u << kAdjHeadShift) - 1;
 static_assert(SV_MAX_HISTORY <= (1 << kAdjHeadShift) - 1, "a count must not reach the chain's head");
 static_assert(SV_MAX_BRANCHES * SV_MAX_K < (1 << 12), "a draft's number must fit the head");
+static_assert(kAdjSlice / (kAdjTile / 4) <= kAdjWarps, "a warp keeps to one region, and a region has a warp");
+static_assert(kAdjMaskWords >= 33, "a warp brings 33 words of a mask");
 
 struct AdjustGeom {
     int32_t slice, slices;  // ids of a slice (a power of two), slices of a row
@@ -47,7 +49,7 @@ struct AdjustGeom {
 
 // The parts of a CTA's shared memory, in 32-bit words; the tiles lie first.
 struct AdjustLayout {
-    int32_t mask, tab, bias, bits, row, list, next, bytes;  // list and next hold 16 bits each
+    int32_t mask, tab, bias, row, list, next, bytes;  // list and next hold 16 bits each
 };
 __host__ __device__ inline AdjustLayout layout_of(const AdjustGeom& g, bool tiles)
 {
@@ -56,8 +58,7 @@ __host__ __device__ inline AdjustLayout layout_of(const AdjustGeom& g, bool tile
     l.mask = tiles ? kAdjWarps * kAdjStages * kAdjTile / 4 : 0;
     l.tab = l.mask + (tiles ? (kAdjWarps * kAdjStages * kAdjMaskWords + 3) / 4 * 4 : 0);
     l.bias = l.tab + ids;
-    l.bits = l.bias + ids * g.bias_bits / 32;
-    l.row = (l.bits + ids / 32 + 1 + 3) / 4 * 4;
+    l.row = l.bias + ids * g.bias_bits / 32;
     l.list = l.row + 2 * g.most_rows;
     l.next = l.list + (g.slice + (kAdjEdge << g.region_shift)) / 2;
     l.bytes = 4 * (l.next + (g.drafts + 1) / 2);
@@ -155,7 +156,6 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     const AdjustLayout at = layout_of(g, COPY);
     uint32_t* s_tab = s_mem + at.tab;
     uint32_t* s_bias = s_mem + at.bias;  // an id's last bias: 1 + its number, 0 for none
-    uint32_t* s_bits = s_mem + at.bits;
     int2* s_row = reinterpret_cast<int2*>(s_mem + at.row);  // each row's mask (-1: none), and the drafts before its branch's
     uint16_t* s_list = reinterpret_cast<uint16_t*>(s_mem + at.list);
     uint16_t* s_next = reinterpret_cast<uint16_t*>(s_mem + at.next);
@@ -177,13 +177,15 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     }
     // The first tokens are on their way before their number is known: all of the row may be read.
     const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
-    int32_t token[kAdjBatch];
-    auto fetch = [&](int32_t i0, int32_t end) {
+    const int32_t* draft = a.draft + static_cast<int64_t>(r) * g.drafts;
+    int32_t token[kAdjBatch], first_draft = 0, first_bias = 0;
+    auto fetch = [&](int32_t (&to)[kAdjBatch], int32_t i0, int32_t end) {
 #pragma unroll
         for (int q = 0; q < kAdjBatch; ++q)
-            if (i0 + q * kAdjThreads < end) token[q] = history[i0 + q * kAdjThreads];
+            if (i0 + q * kAdjThreads < end) to[q] = history[i0 + q * kAdjThreads];
     };
-    if (u.history != nullptr) fetch(tid, u.history_width);
+    if (u.history != nullptr) fetch(token, tid, u.history_width);
+    if (tid < g.drafts) first_draft = draft[tid];
     // what the request asks for
     uint32_t st = 0;
     int32_t len = 0, prompt = 0, b0 = 0, b1 = 0;
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
         b0 = min(max(x, 0), u.bias_entries);
         b1 = min(max(y, b0), u.bias_entries);
         if (b0 != x || b1 != y) st |= SV_ST_BAD_LENGTH;
+        if (b0 + tid < b1) first_bias = u.bias_id[b0 + tid];
     }
     float rep = u.repetition != nullptr ? u.repetition[r] : 1.0f;
     float pres = u.presence != nullptr ? u.presence[r] : 0.0f;
@@ -275,40 +278,31 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
         for (int i = 0; i < kAdjStages - 1; ++i) bring(unit0 + i * kAdjWarps, i);
     }
 
-    // The slice's entry of a token (-1: outside).  The first to meet it notes it in its region's list, and
-    // in the next one's where a row that starts within a vector has it there.
+    // The slice's entry of a token, -1 for none.
     auto meet = [&](int32_t x) -> int32_t {
         if (static_cast<uint32_t>(x) >= static_cast<uint32_t>(V)) {
             st |= SV_ST_TOKEN_RANGE;
             return -1;
         }
-        const int32_t l = x - base;
-        if (l < 0 || l >= ids) return -1;
-        const uint32_t bit = 1u << (l & 31);
-        if ((atomicOr(&s_bits[l >> 5], bit) & bit) == 0) {
-            const int32_t i = l - kAdjEdge, q = i / kRegion;  // 0 for the entries before the slice, too
-            s_list[q * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q], 1)] = static_cast<uint16_t>(l);
-            if (i >= 0 && (i + kAdjEdge) / kRegion > q && i + kAdjEdge < g.slice)
-                s_list[(q + 1) * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q + 1], 1)] = static_cast<uint16_t>(l);
-        }
-        return l;
+        return static_cast<uint32_t>(x - base) < static_cast<uint32_t>(ids) ? x - base : -1;
     };
-    for (int32_t i0 = tid; i0 < len;) {
+    for (int32_t i0 = tid; i0 < len; i0 += kAdjThreads * kAdjBatch) {
+        int32_t next[kAdjBatch];
+        fetch(next, i0 + kAdjThreads * kAdjBatch, len);
 #pragma unroll
         for (int q = 0; q < kAdjBatch; ++q) {
             const int32_t i = i0 + q * kAdjThreads;
             const int32_t l = i < len ? meet(token[q]) : -1;
+            token[q] = next[q];
             if (l < 0) continue;
             if (i >= prompt)
                 atomicAdd(&s_tab[l], 1u);
             else
                 atomicOr(&s_tab[l], kAdjSeen);
         }
-        i0 += kAdjThreads * kAdjBatch;
-        fetch(i0, len);
     }
     for (int32_t i = tid; i < g.drafts; i += kAdjThreads) {
-        const int32_t l = meet(a.draft[static_cast<int64_t>(r) * g.drafts + i]);
+        const int32_t l = meet(i == tid ? first_draft : draft[i]);
         if (l < 0) continue;
         uint32_t old = s_tab[l], was;
         do {
@@ -318,7 +312,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
         } while (old != was);
     }
     for (int32_t i = b0 + tid; i < b1; i += kAdjThreads) {
-        const int32_t l = meet(u.bias_id[i]);
+        const int32_t l = meet(i == b0 + tid ? first_bias : u.bias_id[i]);
         if (l < 0) continue;
         const uint32_t entry = static_cast<uint32_t>(i) + 1;
         if (g.bias_bits == 32) {
@@ -344,6 +338,25 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     }
     __syncthreads();
 
+    // The ids that a rule meets, by regions; the last ones of a region stand in the next one's list, too, for
+    // the rows that start within a vector and have them there.
+    auto bias_of = [&](int32_t l) -> uint32_t {
+        return !biased ? 0u : g.bias_bits == 32 ? s_bias[l] : (s_bias[l >> 1] >> ((l & 1) * 16)) & 0xFFFFu;
+    };
+    for (int32_t l0 = 4 * tid; l0 < ids; l0 += 4 * kAdjThreads) {
+        const uint4 four = *reinterpret_cast<const uint4*>(s_tab + l0);
+        uint32_t met = (four.x != 0) | (four.y != 0) << 1 | (four.z != 0) << 2 | (four.w != 0) << 3;
+        if (biased)
+            for (int e = 0; e < 4; ++e) met |= (bias_of(l0 + e) != 0) << e;
+        for (; met != 0; met &= met - 1) {
+            const int32_t l = l0 + __ffs(met) - 1, i = l - kAdjEdge, q = i / kRegion;  // 0 for those before the slice, too
+            s_list[q * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q], 1)] = static_cast<uint16_t>(l);
+            if (i >= 0 && (i + kAdjEdge) / kRegion > q && i + kAdjEdge < g.slice)
+                s_list[(q + 1) * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q + 1], 1)] = static_cast<uint16_t>(l);
+        }
+    }
+    __syncthreads();
+
     // The adjusted entry of the table's id l in a row.
     auto adjusted = [&](const Row& w, int32_t l, T raw) -> T {
         // the drafts before the row: the first i + 1 of branch b, for row 1 + b * k + i
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
         uint32_t count = word & kAdjCount;
         for (uint32_t e = (word & kAdjHead) >> kAdjHeadShift; e != 0; e = s_next[e - 1])
             count += static_cast<int32_t>(e) > w.before && static_cast<int32_t>(e) <= w.row;
-        const uint32_t entry = !biased ? 0u : g.bias_bits == 32 ? s_bias[l] : (s_bias[l >> 1] >> ((l & 1) * 16)) & 0xFFFFu;
+        const uint32_t entry = bias_of(l);
         const bool seen = (word & kAdjSeen) != 0 || count != 0;
         if (!seen && entry == 0) return raw;
         float z = widen<T>(raw);
