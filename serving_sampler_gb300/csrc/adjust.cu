@@ -24,7 +24,7 @@ constexpr int kAdjThreads = 256;
 constexpr int kAdjWarps = kAdjThreads / 32;
 constexpr int kAdjVecs = 4;                      // 16-byte vectors of a tile that a lane holds
 constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of a row
-constexpr int kAdjStages = 2;                    // tiles of a warp's ring
+constexpr int kAdjStages = 2;                    // tiles of a warp's ring: one on its way, one in hand
 constexpr int kAdjSlice = 4096;                  // most ids of a slice
 constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
 constexpr int kAdjBatch = 8;                     // tokens that a thread loads before it counts them
@@ -142,7 +142,7 @@ __device__ __forceinline__ void copies_wait()
 // T: uint16_t for bf16 rows, uint32_t for fp32 rows.  COPY: out of place, by tiles; every row of the two
 // matrices starts alike within 16 bytes.
 template <typename T, bool COPY>
-__global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_constant__ AdjustArgs a, const AdjustGeom g)
+__global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const __grid_constant__ AdjustArgs a, const AdjustGeom g)
 {
     constexpr int kPer = 16 / sizeof(T);            // entries of a vector
     constexpr int kRegion = kAdjTile / sizeof(T);   // ids of a region
@@ -223,68 +223,67 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     if (tid < kAdjWarps) s_listed[tid] = 0;
     __syncthreads();
 
-    // A warp's units: regions of rows, its region the same in each.
-    const int32_t units = rows << g.region_shift, region = warp & ((1 << g.region_shift) - 1);
-    const int32_t unit0 = warp, in_slice = s0 + region * kRegion;
-    struct Row {
-        const T* in;
-        T* out;
-        const uint32_t* mask;  // NULL: none
-        int32_t x0;            // id of the region's first entry
-        int32_t row;
-        int32_t before;        // drafts before those of the row's branch
+    // A warp takes one region, in every kAdjWarps / regions-th row from row j0 on.
+    const int32_t region = warp & ((1 << g.region_shift) - 1), in_slice = s0 + region * kRegion;
+    const int32_t j0 = warp >> g.region_shift, j_step = kAdjWarps >> g.region_shift;
+    const bool in_place = a.in.data == a.out.data;
+    const T* in = reinterpret_cast<const T*>(a.in.data) + (first + j0) * a.in.stride;
+    T* out = reinterpret_cast<T*>(const_cast<char*>(a.out.data)) + (first + j0) * a.out.stride;
+    const int64_t in_step = j_step * a.in.stride, out_step = j_step * a.out.stride;
+    // The id of a row's first entry of the region: rows may start within 16 bytes.
+    auto region_of = [&](const T* row) -> int32_t {
+        return COPY || in_place ? in_slice - (static_cast<int32_t>(reinterpret_cast<uintptr_t>(row)) & 15) / static_cast<int32_t>(sizeof(T))
+                                : in_slice;
     };
-    auto row_of = [&](int32_t unit) {
-        Row w;
-        const int32_t j = unit >> g.region_shift;
-        w.in = reinterpret_cast<const T*>(a.in.data) + (first + j) * a.in.stride;
-        w.out = reinterpret_cast<T*>(const_cast<char*>(a.out.data)) + (first + j) * a.out.stride;
-        const int2 i = s_row[j];
-        w.mask = i.x < 0 ? nullptr : u.mask + static_cast<int64_t>(i.x) * u.mask_words;
-        w.row = row0 + j;
-        w.before = i.y;
-        w.x0 = in_slice;
-        // entries that the row starts behind a 16-byte boundary
-        if (COPY || a.in.data == a.out.data)
-            w.x0 -= (static_cast<int32_t>(reinterpret_cast<uintptr_t>(w.in)) & 15) / static_cast<int32_t>(sizeof(T));
-        return w;
+    auto mask_of = [&](int32_t j) -> const uint32_t* {
+        const int32_t i = s_row[j].x;
+        return i < 0 ? nullptr : u.mask + static_cast<int64_t>(i) * u.mask_words;
     };
-    T* tiles = reinterpret_cast<T*>(s_mem) + warp * kAdjStages * kRegion;
+    uint8_t* tiles = reinterpret_cast<uint8_t*>(s_mem) + warp * kAdjStages * kAdjTile;
     uint32_t* masks = s_mem + at.mask + warp * kAdjStages * kAdjMaskWords;
-    auto bring = [&](int32_t unit, int stage) {
-        if (unit < units) {
-            const Row w = row_of(unit);
-            T* tile = tiles + stage * kRegion;
+    // row j's region on its way to a tile
+    auto bring = [&](const T* row, int32_t j, int stage) {
+        if (j < rows) {
+            const int32_t x0 = region_of(row);
+            uint8_t* tile = tiles + stage * kAdjTile;
+            if (x0 >= 0 && x0 + kRegion <= V) {
+                const uint4* src = reinterpret_cast<const uint4*>(row + x0) + lane;
 #pragma unroll
-            for (int q = 0; q < kAdjVecs; ++q) {
-                const int32_t o = (q * 32 + lane) * kPer, x = w.x0 + o;
-                if (x >= 0 && x + kPer <= V) {
-                    copy16(tile + o, w.in + x);
-                } else {
-                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y) tile[y - w.x0] = w.in[y];
+                for (int q = 0; q < kAdjVecs; ++q) copy16(tile + (q * 32 + lane) * 16, src + q * 32);
+            } else {
+#pragma unroll 1
+                for (int q = 0; q < kAdjVecs; ++q) {
+                    const int32_t o = (q * 32 + lane) * kPer, x = x0 + o;
+                    if (x >= 0 && x + kPer <= V) {
+                        copy16(tile + o * sizeof(T), row + x);
+                    } else {
+#pragma unroll 1
+                        for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y) reinterpret_cast<T*>(tile)[y - x0] = row[y];
+                    }
                 }
             }
-            if (w.mask != nullptr) {
-                const int32_t word = (w.x0 >> 5) + lane;
-                if (word >= 0 && word < u.mask_words) copy4(masks + stage * kAdjMaskWords + lane, w.mask + word);
-                if (lane == 0 && word + 32 < u.mask_words && kAdjMaskWords > 32)
-                    copy4(masks + stage * kAdjMaskWords + 32, w.mask + word + 32);
+            if (const uint32_t* mask = mask_of(j)) {
+                const int32_t word = (x0 >> 5) + lane;
+                if (word >= 0 && word < u.mask_words) copy4(masks + stage * kAdjMaskWords + lane, mask + word);
+                if (lane == 0 && word + 32 < u.mask_words) copy4(masks + stage * kAdjMaskWords + 32, mask + word + 32);
             }
         }
         copies_commit();
     };
+    const T* coming = in;
     if (COPY) {
-#pragma unroll
-        for (int i = 0; i < kAdjStages - 1; ++i) bring(unit0 + i * kAdjWarps, i);
+        bring(coming, j0, 0);
+        coming += in_step;
     }
 
-    // The slice's entry of a token, -1 for none.
-    auto meet = [&](int32_t x) -> int32_t {
-        if (static_cast<uint32_t>(x) >= static_cast<uint32_t>(V)) {
-            st |= SV_ST_TOKEN_RANGE;
-            return -1;
-        }
-        return static_cast<uint32_t>(x - base) < static_cast<uint32_t>(ids) ? x - base : -1;
+    // Tokens of the vocabulary that are the slice's: low .. low + span - 1.
+    const bool tells = s == 0 && group == 0 && a.status != nullptr;
+    const int32_t low = max(base, 0);
+    const uint32_t span = static_cast<uint32_t>(max(min(base + ids, V) - low, 0));
+    bool outside = false;
+    auto meets = [&](int32_t x) -> bool {
+        if (tells) outside = outside || static_cast<uint32_t>(x) >= static_cast<uint32_t>(V);
+        return static_cast<uint32_t>(x - low) < span;
     };
     for (int32_t i0 = tid; i0 < len; i0 += kAdjThreads * kAdjBatch) {
         int32_t next[kAdjBatch];
@@ -292,28 +291,30 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
 #pragma unroll
         for (int q = 0; q < kAdjBatch; ++q) {
             const int32_t i = i0 + q * kAdjThreads;
-            const int32_t l = i < len ? meet(token[q]) : -1;
+            if (i < len && meets(token[q])) {
+                if (i >= prompt)
+                    atomicAdd(&s_tab[token[q] - base], 1u);
+                else
+                    atomicOr(&s_tab[token[q] - base], kAdjSeen);
+            }
             token[q] = next[q];
-            if (l < 0) continue;
-            if (i >= prompt)
-                atomicAdd(&s_tab[l], 1u);
-            else
-                atomicOr(&s_tab[l], kAdjSeen);
         }
     }
     for (int32_t i = tid; i < g.drafts; i += kAdjThreads) {
-        const int32_t l = meet(i == tid ? first_draft : draft[i]);
-        if (l < 0) continue;
-        uint32_t old = s_tab[l], was;
+        const int32_t x = i == tid ? first_draft : draft[i];
+        if (!meets(x)) continue;
+        uint32_t* word = &s_tab[x - base];
+        uint32_t old = *word, was;
         do {
             was = old;
             s_next[i] = static_cast<uint16_t>((was & kAdjHead) >> kAdjHeadShift);
-            old = atomicCAS(&s_tab[l], was, (was & ~kAdjHead) | (static_cast<uint32_t>(i + 1) << kAdjHeadShift));
+            old = atomicCAS(word, was, (was & ~kAdjHead) | (static_cast<uint32_t>(i + 1) << kAdjHeadShift));
         } while (old != was);
     }
     for (int32_t i = b0 + tid; i < b1; i += kAdjThreads) {
-        const int32_t l = meet(i == b0 + tid ? first_bias : u.bias_id[i]);
-        if (l < 0) continue;
+        const int32_t x = i == b0 + tid ? first_bias : u.bias_id[i];
+        if (!meets(x)) continue;
+        const int32_t l = x - base;
         const uint32_t entry = static_cast<uint32_t>(i) + 1;
         if (g.bias_bits == 32) {
             atomicMax(&s_bias[l], entry);
@@ -328,12 +329,13 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
             } while (old != was);
         }
     }
-    if (s == 0 && group == 0 && a.status != nullptr) {
+    if (tells) {
+        bool over = false;
         if (u.mask != nullptr && u.mask_row != nullptr)
             for (int32_t i = tid; i < g.rows; i += kAdjThreads)
-                if (u.mask_row[static_cast<int64_t>(r) * g.rows + i] >= u.masks) st |= SV_ST_BAD_MASK;
-        st |= (__syncthreads_or(st & SV_ST_TOKEN_RANGE) ? SV_ST_TOKEN_RANGE : 0u) |
-              (__syncthreads_or(st & SV_ST_BAD_MASK) ? SV_ST_BAD_MASK : 0u);
+                over = over || u.mask_row[static_cast<int64_t>(r) * g.rows + i] >= u.masks;
+        if (__syncthreads_or(outside)) st |= SV_ST_TOKEN_RANGE;
+        if (__syncthreads_or(over)) st |= SV_ST_BAD_MASK;
         if (tid == 0) a.status[r] = static_cast<int32_t>(st);
     }
     __syncthreads();
@@ -346,8 +348,13 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     for (int32_t l0 = 4 * tid; l0 < ids; l0 += 4 * kAdjThreads) {
         const uint4 four = *reinterpret_cast<const uint4*>(s_tab + l0);
         uint32_t met = (four.x != 0) | (four.y != 0) << 1 | (four.z != 0) << 2 | (four.w != 0) << 3;
-        if (biased)
-            for (int e = 0; e < 4; ++e) met |= (bias_of(l0 + e) != 0) << e;
+        if (g.bias_bits == 16) {
+            const uint2 w = *reinterpret_cast<const uint2*>(s_bias + l0 / 2);
+            met |= ((w.x & 0xFFFFu) != 0) | (w.x >> 16 != 0) << 1 | ((w.y & 0xFFFFu) != 0) << 2 | (w.y >> 16 != 0) << 3;
+        } else if (g.bias_bits == 32) {
+            const uint4 w = *reinterpret_cast<const uint4*>(s_bias + l0);
+            met |= (w.x != 0) | (w.y != 0) << 1 | (w.z != 0) << 2 | (w.w != 0) << 3;
+        }
         for (; met != 0; met &= met - 1) {
             const int32_t l = l0 + __ffs(met) - 1, i = l - kAdjEdge, q = i / kRegion;  // 0 for those before the slice, too
             s_list[q * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q], 1)] = static_cast<uint16_t>(l);
@@ -357,13 +364,13 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
     }
     __syncthreads();
 
-    // The adjusted entry of the table's id l in a row.
-    auto adjusted = [&](const Row& w, int32_t l, T raw) -> T {
+    // The adjusted entry of the table's id l in row j.
+    auto adjusted = [&](int32_t j, int32_t l, T raw) -> T {
         // the drafts before the row: the first i + 1 of branch b, for row 1 + b * k + i
         const uint32_t word = s_tab[l];
         uint32_t count = word & kAdjCount;
         for (uint32_t e = (word & kAdjHead) >> kAdjHeadShift; e != 0; e = s_next[e - 1])
-            count += static_cast<int32_t>(e) > w.before && static_cast<int32_t>(e) <= w.row;
+            count += static_cast<int32_t>(e) > s_row[j].y && static_cast<int32_t>(e) <= row0 + j;
         const uint32_t entry = bias_of(l);
         const bool seen = (word & kAdjSeen) != 0 || count != 0;
         if (!seen && entry == 0) return raw;
@@ -378,68 +385,126 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const __grid_consta
 
     if (COPY) {
         int stage = 0;
-        for (int32_t unit = unit0; unit < units; unit += kAdjWarps) {
+        for (int32_t j = j0; j < rows; j += j_step, out += out_step) {
             __syncwarp();  // the tile before is stored
-            bring(unit + (kAdjStages - 1) * kAdjWarps, stage == 0 ? kAdjStages - 1 : stage - 1);
-            copies_wait<kAdjStages - 1>();
+            bring(coming, j + j_step, stage ^ 1);
+            coming += in_step;
+            copies_wait<1>();
             __syncwarp();
-            const Row w = row_of(unit);
-            T* tile = tiles + stage * kRegion;
+            const int32_t x0 = region_of(out);
+            T* tile = reinterpret_cast<T*>(tiles + stage * kAdjTile);
             const uint32_t* words = masks + stage * kAdjMaskWords;
             for (int32_t i = lane; i < listed; i += 32) {
-                const int32_t l = list[i], o = base + l - w.x0;
-                if (o >= 0 && o < kRegion) tile[o] = adjusted(w, l, tile[o]);
+                const int32_t l = list[i], o = base + l - x0;
+                if (static_cast<uint32_t>(o) < static_cast<uint32_t>(kRegion)) tile[o] = adjusted(j, l, tile[o]);
             }
             __syncwarp();
+            const bool has_mask = s_row[j].x >= 0;
+            auto bits_of = [&](int32_t o) -> uint32_t {
+                const int32_t b = (x0 & 31) + o;
+                return __funnelshift_r(words[b >> 5], words[min((b >> 5) + 1, kAdjMaskWords - 1)], b & 31) & kAll;
+            };
+            const uint4* from = reinterpret_cast<const uint4*>(tile) + lane;
+            if (x0 >= 0 && x0 + kRegion <= V) {
+                uint4* to = reinterpret_cast<uint4*>(out + x0) + lane;
+                if (has_mask) {
 #pragma unroll
-            for (int q = 0; q < kAdjVecs; ++q) {
-                const int32_t o = (q * 32 + lane) * kPer, x = w.x0 + o;
-                uint4 v = *reinterpret_cast<const uint4*>(tile + o);
-                uint32_t m = kAll;
-                if (w.mask != nullptr) {
-                    const int32_t b = (w.x0 & 31) + o;
-                    m = __funnelshift_r(words[b >> 5], words[min((b >> 5) + 1, kAdjMaskWords - 1)], b & 31) & kAll;
-                    v = masked<T>(v, m);
-                }
-                if (x >= 0 && x + kPer <= V) {
-                    *reinterpret_cast<uint4*>(w.out + x) = v;
+                    for (int q = 0; q < kAdjVecs; ++q) to[q * 32] = masked<T>(from[q * 32], bits_of((q * 32 + lane) * kPer));
                 } else {
-                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y)
-                        w.out[y] = (m >> (y - x)) & 1u ? tile[y - w.x0] : kNegInf<T>;
+#pragma unroll
+                    for (int q = 0; q < kAdjVecs; ++q) to[q * 32] = from[q * 32];
+                }
+            } else {
+#pragma unroll 1
+                for (int q = 0; q < kAdjVecs; ++q) {
+                    const int32_t o = (q * 32 + lane) * kPer, x = x0 + o;
+                    const uint32_t m = has_mask ? bits_of(o) : kAll;
+                    if (x >= 0 && x + kPer <= V) {
+                        *reinterpret_cast<uint4*>(out + x) = masked<T>(from[q * 32], m);
+                    } else {
+#pragma unroll 1
+                        for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y)
+                            out[y] = (m >> (y - x)) & 1u ? tile[y - x0] : kNegInf<T>;
+                    }
                 }
             }
-            stage = stage + 1 == kAdjStages ? 0 : stage + 1;
+            stage ^= 1;
         }
         copies_wait<0>();
         return;
     }
 
-    const bool in_place = a.in.data == a.out.data;
-    for (int32_t unit = unit0; unit < units; unit += kAdjWarps) {
-        const Row w = row_of(unit);
-        if (in_place && w.mask != nullptr) {
+    if (!in_place) {  // rows that start differently
+        for (int32_t j = j0; j < rows; j += j_step, in += in_step, out += out_step) {
+            const uint32_t* mask = mask_of(j);
+#pragma unroll 8
+            for (int32_t x = in_slice + lane; x < min(in_slice + kRegion, V); x += 32)
+                out[x] = allowed(mask, x) ? in[x] : kNegInf<T>;
+            __syncwarp();
+            for (int32_t i = lane; i < listed; i += 32) {
+                const int32_t l = list[i], x = base + l;
+                if (x >= in_slice && x < in_slice + kRegion && allowed(mask, x)) out[x] = adjusted(j, l, in[x]);
+            }
+        }
+        return;
+    }
+
+    // In place: a lane has 32 ids' bits of the row's mask, brought while the row before was written, and the
+    // first listed entries are read while the masked ones are written.
+    uint32_t lo = 0, hi = 0;
+    auto bring_mask = [&](const T* row, int32_t j) {
+        lo = hi = 0xFFFFFFFFu;
+        const uint32_t* mask = j < rows ? mask_of(j) : nullptr;
+        if (mask == nullptr) return;
+        const int32_t word = (region_of(row) >> 5) + lane;
+        if (word >= 0 && word < u.mask_words) lo = mask[word];
+        if (word + 1 < u.mask_words) hi = mask[word + 1];
+    };
+    bring_mask(out, j0);
+    for (int32_t j = j0; j < rows; j += j_step, out += out_step) {
+        const int32_t x0 = region_of(out);
+        const bool has_mask = s_row[j].x >= 0;
+        const uint32_t bits = __funnelshift_r(lo, hi, x0 & 31);  // of ids x0 + 32 * lane on
+        bring_mask(out + out_step, j + j_step);
+        auto entry = [&](int32_t i, int32_t& l) -> int32_t {  // listed id i's place in the region, -1 for none
+            l = i < listed ? list[i] : 0;
+            const int32_t o = base + l - x0;
+            const bool here = i < listed && static_cast<uint32_t>(o) < static_cast<uint32_t>(kRegion);
+            const uint32_t word = __shfl_sync(0xFFFFFFFFu, bits, (o >> 5) & 31);
+            return here && ((word >> (o & 31)) & 1u) ? o : -1;
+        };
+        int32_t l;
+        const int32_t o = entry(lane, l);
+        T raw = 0;
+        if (o >= 0) raw = out[x0 + o];
+        if (has_mask) {
+            uint32_t m[kAdjVecs];
+            uint4 v[kAdjVecs];
 #pragma unroll
             for (int q = 0; q < kAdjVecs; ++q) {
-                const int32_t x = w.x0 + (q * 32 + lane) * kPer;
+                const int word = q * kPer;  // of the warp's, plus lane * kPer / 32
+                m[q] = (__shfl_sync(0xFFFFFFFFu, bits, word + lane * kPer / 32) >> (lane * kPer % 32)) & kAll;
+                const int32_t x = x0 + (q * 32 + lane) * kPer;
+                // what is masked need not be read
+                if (x >= 0 && x + kPer <= V && m[q] != 0u && m[q] != kAll) v[q] = *reinterpret_cast<const uint4*>(out + x);
+            }
+#pragma unroll
+            for (int q = 0; q < kAdjVecs; ++q) {
+                const int32_t x = x0 + (q * 32 + lane) * kPer;
                 if (x >= 0 && x + kPer <= V) {
-                    const uint32_t lo = w.mask[x >> 5], hi = (x & 31) + kPer > 32 ? w.mask[(x >> 5) + 1] : 0u;
-                    const uint32_t m = __funnelshift_r(lo, hi, x & 31) & kAll;
-                    uint4* p = reinterpret_cast<uint4*>(w.out + x);
-                    if (m != kAll) *p = masked<T>(m != 0u ? *p : make_uint4(0, 0, 0, 0), m);
+                    if (m[q] != kAll) *reinterpret_cast<uint4*>(out + x) = masked<T>(v[q], m[q]);
                 } else {
+#pragma unroll 1
                     for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y)
-                        if (!allowed(w.mask, y)) w.out[y] = kNegInf<T>;
+                        if (!((m[q] >> (y - x)) & 1u)) out[y] = kNegInf<T>;
                 }
             }
-        } else if (!in_place) {  // rows that start differently
-#pragma unroll 8
-            for (int32_t x = w.x0 + lane; x < min(w.x0 + kRegion, V); x += 32)
-                w.out[x] = allowed(w.mask, x) ? w.in[x] : kNegInf<T>;
+            __syncwarp();
         }
-        __syncwarp();
-        for (int32_t i = lane; i < listed; i += 32) {
-            const int32_t l = list[i], x = base + l;
-            if (x >= w.x0 && x < w.x0 + kRegion && allowed(w.mask, x)) w.out[x] = adjusted(w, l, w.in[x]);
+        if (o >= 0) out[x0 + o] = adjusted(j, l, raw);
+        for (int32_t i = 32; i < listed; i += 32) {
+            const int32_t p = entry(i + lane, l);
+            if (p >= 0) out[x0 + p] = adjusted(j, l, out[x0 + p]);
         }
     }
 }
