@@ -47,15 +47,15 @@ __device__ __forceinline__ Fork fork_of(const ForkArgs& a, int32_t r)
     return f;
 }
 
-// Grid: x = rows, y = 128 16-byte columns of the heads of all layers, K and V.  A thread owns
-// a column and walks the tokens of the source's last block, eight loads before their stores.
+// Grid: x = rows, y = 128 16-byte columns of the heads of all layers, K and V, z = shares of the tokens.  A
+// thread owns a column and walks its share of the source's last block, eight loads before their stores.
 __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const ForkArgs a)
 {
     const int tid = threadIdx.x;
     const int32_t r = blockIdx.x;
-    const bool teller = r + 1 == a.R && blockIdx.y == 0;  // it tells how many blocks are left
+    const bool first = blockIdx.y == 0 && blockIdx.z == 0, teller = r + 1 == a.R && first;  // it tells how many blocks are left
     const Fork f = fork_of(a, r);
-    if (blockIdx.y != 0 && !f.needs) return;
+    if (!first && !f.needs) return;
 
     int32_t before = 0;  // blocks taken by the rows before
     if (f.needs || teller) {
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const ForkArgs
     const int32_t full = a.by_block.quotient(f.tokens), tail = f.tokens - full * a.cache.block_size;
     const int32_t* from = a.block_table + static_cast<int64_t>(done ? f.source : 0) * a.max_blocks;
     const int32_t last = takes ? from[full] : -1;
-    if (blockIdx.y == 0) {
+    if (first) {
         bool out = takes && (fresh < 0 || fresh >= a.cache.num_blocks || last < 0 || last >= a.cache.num_blocks);
         if (done) {
             int32_t* to = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const ForkArgs
     const uint16_t* src = p + last * a.cache.block_stride;
     uint16_t* dst = p + fresh * a.cache.block_stride;
     if (src == dst) return;  // a stack that holds a block in use
-    for (int32_t i0 = 0; i0 < tail; i0 += kMoveBatch) {
+    for (int32_t i0 = blockIdx.z * kMoveBatch; i0 < tail; i0 += gridDim.z * kMoveBatch) {
         uint4 val[kMoveBatch];
 #pragma unroll
         for (int u = 0; u < kMoveBatch; ++u)
@@ -471,7 +471,11 @@ __global__ void __launch_bounds__(kPackThreads) compact_move_kernel(const Compac
 cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t stream)
 {
     const int64_t columns = 2ll * a.cache.layers * a.cache.kv_heads * (a.cache.head_dim / 8);
-    const dim3 grid(static_cast<unsigned>(a.R), static_cast<unsigned>((columns + kForkThreads - 1) / kForkThreads));
+    const int64_t rows = (columns + kForkThreads - 1) / kForkThreads;
+    // few rows leave room for several thread blocks to a last block's tokens; those of rows that fork nothing cost, too
+    const int64_t shares = std::min<int64_t>((a.cache.block_size + kMoveBatch - 1) / kMoveBatch,
+                                             std::max<int64_t>(1, 64ll * std::max(1, device_sm_count()) / (a.R * rows)));
+    const dim3 grid(static_cast<unsigned>(a.R), static_cast<unsigned>(rows), static_cast<unsigned>(std::min<int64_t>(shares, 65535)));
     cache_fork_kernel<<<grid, kForkThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
