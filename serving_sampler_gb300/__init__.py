@@ -419,34 +419,39 @@ def _half_type(t) -> int:
 
 def heads_of(t) -> SvHeads:
     """Describe a CUDA tensor of heads [tokens, heads, head_dim] (tokens and heads may be strided)."""
-    load()
-    if not t.is_cuda or t.dim() != 3:
+    if _lib is None:
+        load()
+    shape = t.shape
+    if len(shape) != 3 or not t.is_cuda:
         raise ValueError("heads must be a 3-D CUDA tensor [tokens, heads, head_dim]")
-    T, H, D = t.shape
+    T, H, D = shape
     st, sh, sd = t.stride()
     if sd != 1 and D > 1:
         raise ValueError("entries of a head must be contiguous")
-    return SvHeads(t.data_ptr(), _half_type(t), T, H, D, st, sh)
+    return SvHeads(t.data_ptr(), SV_BF16 if t.dtype is torch.bfloat16 else _half_type(t), T, H, D, st, sh)
 
 
 def cache_of(k, v) -> SvKvCache:
     """Describe a paged cache: K and V tensors [num_blocks, block_size, kv_heads, head_dim], or with the layers in
     front, of one dtype and the same strides (any order of the axes but the last)."""
-    load()
-    shape, strides = k.shape, k.stride()
+    if _lib is None:
+        load()
+    shape, strides, dtype = k.shape, k.stride(), k.dtype
     n = len(shape)
-    if not k.is_cuda or not v.is_cuda or n not in (4, 5) or shape != v.shape:
+    if n != 4 and n != 5 or shape != v.shape or not k.is_cuda or not v.is_cuda:
         raise ValueError("caches must be 4-D or 5-D CUDA tensors of one shape")
-    if k.dtype is not v.dtype:
+    if dtype is not v.dtype:
         raise TypeError("K and V caches must have one dtype")
     if strides != v.stride():
         raise ValueError("K and V caches must have the same strides")
     if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError("entries of a head must be contiguous")
-    layers, layer_stride = (1, 0) if n == 4 else (shape[0], strides[0])
-    nb, bs, H, D = shape[-4:]
-    sb, st, sh, _ = strides[-4:]
-    return SvKvCache(k.data_ptr(), v.data_ptr(), _half_type(k), nb, bs, H, D, layers, sb, st, sh, layer_stride)
+    if n == 4:
+        (nb, bs, H, D), (sb, st, sh, _), layers, sl = shape, strides, 1, 0
+    else:
+        (layers, nb, bs, H, D), (sl, sb, st, sh, _) = shape, strides
+    code = SV_BF16 if dtype is torch.bfloat16 else _half_type(k)
+    return SvKvCache(k.data_ptr(), v.data_ptr(), code, nb, bs, H, D, layers, sb, st, sh, sl)
 
 
 def _ints(t, name, n=-1) -> int:
