@@ -397,8 +397,9 @@ int sv_suffix_append(int32_t* suffix, int32_t N, int32_t R, const int32_t* token
  *   draft       int32 [R, branches, k]; NULL only where branches * k is 0.
  *   rules       below.
  *   out         rows of the adjusted logits, logits' dtype and width; may be logits
- *               itself (same data and row_stride: only what changes is written), and
- *               must not overlap it otherwise.
+ *               itself (same data and row_stride: only what changes is written), or
+ *               other columns of a wider matrix; no entry of the two may be the same
+ *               otherwise (SV_ERR_INVALID_ARG).
  *   status      int32 [R] out or NULL.
  * For token x in a row, z its logit in fp32:
  *   seen   x is among the request's history or the drafts before the row;
@@ -563,7 +564,8 @@ int sv_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, c
  *   eps         >= 0 and finite.
  * Every head x of q and k becomes y = x * (mean(x^2) + eps)^(-1/2) * weight over its
  * head_dim entries (Zhang and Sennrich 2019), then is rotated as by sv_rope_cache; v is
- * not normed.  All in fp32, rounded once.  The other arguments, their limits and what
+ * not normed.  All in fp32, rounded once; the sum of a head's squares must lie within
+ * fp32's range.  The other arguments, their limits and what
  * is written where are those of sv_rope_cache.
  * ---------------------------------------------------------------------- */
 int sv_norm_rope_cache(sv_heads q, sv_heads k, sv_heads v, const int32_t* position, const int64_t* slot,

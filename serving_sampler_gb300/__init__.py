@@ -491,11 +491,11 @@ def _new_ints(like, stream, *sizes):
 
 
 def _like(t, stream):
-    """An output with the shape and type of an input, which costs less to ask for than its size and type."""
+    """A contiguous output with the shape and type of an input, which costs less to ask for than its size and type."""
     if stream is None:
-        return torch.empty_like(t)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
-        out = torch.empty_like(t)
+        out = torch.empty_like(t, memory_format=torch.contiguous_format)
     out.record_stream(torch.cuda.current_stream(t.device))
     return out
 
@@ -817,8 +817,7 @@ def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=Non
     rows = R * (1 + branches * k)
     x = _logit_rows(logits, rows, "logits")
     if out is None:
-        alike = rows == len(logits) and logits.is_contiguous()
-        y = _like(logits, stream) if alike else _empty((rows, x.width), logits.dtype, logits.device, stream)
+        y = _like(logits, stream) if rows == len(logits) else _empty((rows, x.width), logits.dtype, logits.device, stream)
         out = dict(logits=y, status=_empty(R, torch.int32, logits.device, stream))
     else:
         _check_out(out, status=(torch.int32, R))

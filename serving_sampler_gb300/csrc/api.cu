@@ -90,6 +90,18 @@ static int check_heads(const sv_heads& h, int32_t dtype, int32_t head_dim, int32
     return SV_OK;
 }
 
+// Whether two matrices of `rows` rows share an entry and are not the same one.
+static bool overlap(const Rows& a, const Rows& b, int64_t rows)
+{
+    if (rows == 0 || a.data == b.data) return false;
+    const int64_t wide = static_cast<int64_t>(a.width) * a.esize, step = a.stride * a.esize;
+    const char *ae = a.data + (rows - 1) * step + wide, *be = b.data + (rows - 1) * b.stride * b.esize + wide;
+    if (a.data >= be || b.data >= ae) return false;
+    if (rows == 1 || a.stride != b.stride) return true;
+    const int64_t apart = ((b.data - a.data) % step + step) % step;  // columns of one wider matrix
+    return apart < wide || apart + wide > step;
+}
+
 static bool have_device()
 {
     int dev = 0;
@@ -681,6 +693,7 @@ int sv_adjust_logits(sv_rows logits, int32_t R, int32_t k, int32_t branches, con
     if (out.dtype != logits.dtype) return SV_ERR_DTYPE;
     if (out.width != logits.width) return SV_ERR_SHAPE;
     if (rows > 1 && out.data == logits.data && out.row_stride != logits.row_stride) return SV_ERR_SHAPE;
+    if (overlap(a.in, a.out, rows)) return SV_ERR_INVALID_ARG;
     const sv_logit_rules& u = rules;
     if (u.history_width < 0 || u.bias_entries < 0 || u.masks < 0 || u.mask_words < 0) return SV_ERR_INVALID_ARG;
     if (u.history_width > SV_MAX_HISTORY) return SV_ERR_LIMIT;

@@ -216,6 +216,39 @@ def test_results_do_not_depend_on_the_batch(sv):
         assert torch.equal(alone.view(torch.int16), many[5 * r:5 * r + 5].view(torch.int16))
 
 
+def test_rows_past_32_bits(sv):
+    """Offsets of rows past 2^32 bytes and 2^32 entries, in place and to columns beside them."""
+    for dtype, stride in ((torch.bfloat16, 2 ** 31 + 24), (torch.float32, 2 ** 30 + 12)):
+        c = Case(1, 2, 1, 700, dtype, seed=20)
+        room = torch.empty(2 * stride + 2000, dtype=dtype, device="cuda")
+        x, y = (room[o:].as_strided((3, 700), (stride, 1)) for o in (0, 1000))
+        x.copy_(torch.from_numpy(c.z))
+        raw = x.double().cpu().numpy()
+        want, err, status = plain.adjust(raw, 1, 2, 1, c.draft, c.history, c.history_len, c.prompt_len, c.repetition,
+                                         c.presence, c.frequency, c.bias, c.mask)
+        for out in (y, x):
+            got = sv.adjust_logits(x, 1, 2, 1, _i32(c.draft), out=dict(logits=out, status=_i32([7])), **c.kwargs())
+            torch.cuda.synchronize()
+            c.compare(got, want, err, status)
+        del room, x, y
+        torch.cuda.empty_cache()
+
+
+def test_outputs_that_meet_the_rows_are_refused(sv):
+    c = Case(2, 1, 1, 100, torch.float32, seed=21)
+    room = torch.zeros((6, 300), device="cuda")
+    x, draft, kw = room[:4, :100], _i32(c.draft), c.kwargs()
+    x.copy_(torch.from_numpy(c.z))
+    want = sv.adjust_logits(x, 2, 1, 1, draft, **kw)["logits"]
+    for bad in (room[:4, 50:150], room[1:5, :100], room[1:5, 250:], room.view(-1)[100:].as_strided((4, 100), (100, 1))):
+        if bad.shape[1] == 100:
+            with pytest.raises(sv.SpecVerifyError):
+                sv.adjust_logits(x, 2, 1, 1, draft, out=dict(logits=bad), **kw)
+    for good in (room[:4, 100:200], room[2:, 200:]):
+        got = sv.adjust_logits(x, 2, 1, 1, draft, out=dict(logits=good), **kw)["logits"]
+        assert torch.equal(got, want)
+
+
 def test_rows_behind_the_last_stay(sv):
     c = Case(2, 1, 1, 100, torch.float32, seed=17)
     x, _ = c.logits()

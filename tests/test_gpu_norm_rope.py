@@ -108,6 +108,15 @@ def test_zeros_and_no_numbers(sv):
         assert bad[4, 1].all() and bad.sum() == D
 
 
+def test_heads_in_another_order(sv):
+    """q with the heads in front: the result has the tokens in front, and the same values."""
+    q, k, v, kc, vc, slot = _rope_case(30, 4, 2, 64, torch.bfloat16)
+    args = (k, v, _i32(range(30)), slot, sv.rope_freqs(64), kc, vc)
+    want = sv.norm_rope_cache(q, *args)
+    got = sv.norm_rope_cache(q.transpose(0, 1).contiguous().transpose(0, 1), *args)
+    assert got.is_contiguous() and torch.equal(got, want)
+
+
 def test_the_norm_is_of_each_head_alone(sv):
     """Heads that differ by powers of two come out the same."""
     q, k, v, kc, vc, slot = _rope_case(40, 4, 2, 128, torch.bfloat16)

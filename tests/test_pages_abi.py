@@ -36,6 +36,12 @@ def test_adjust_checks(m):  # noqa: F811
     assert call(rows=_rows(m, stride=32)) == -3 and call(rows=_rows(m, data=None)) == -1
     assert call(rows=_rows(m, data=0x10001)) == -7
     assert call(out=_rows(m, stride=128)) == -3                      # in place, but not row by row
+    # 14 rows of 64 entries of 2 bytes: the other matrix may be the columns beside them, and nothing that meets them
+    wide = lambda data: _rows(m, data=data, stride=128)  # noqa: E731
+    for data in (0x10000 + 2, 0x10000 + 126, 0x10000 + 256 + 130, 0x10000 - 256 * 13 - 126):
+        assert call(rows=wide(0x10000), out=wide(data)) == -1, data
+    assert call(rows=wide(0x10000), out=_rows(m, data=0x10000 + 128)) == -1
+    assert call(R=1, k=0, branches=1, out=_rows(m, data=0x10000 + 126)) == -1
     assert call(history=BUF.value, history_width=8) == -1            # no lengths
     assert call(history=BUF.value, history_len=BUF.value, history_width=-1) == -1
     assert call(history=BUF.value, history_len=BUF.value, history_width=524288) == -4
@@ -129,6 +135,9 @@ def test_valid_calls_without_a_device(m):  # noqa: F811
     lib = m.load()
     q, k, rows = _heads(m), _heads(m, heads=2), _rows(m)
     assert lib.sv_adjust_logits(rows, 2, 3, 2, BUF, m.SvLogitRules(), rows, None, None) == -8
+    wide = lambda data: _rows(m, data=data, stride=128)  # noqa: E731
+    for data in (0x10000 + 128, 0x10000 - 128, 0x10000 + 256 * 14, 0x10000 - 256 * 14, 0x10000 + 256 * 5 + 128):
+        assert lib.sv_adjust_logits(wide(0x10000), 2, 3, 2, BUF, m.SvLogitRules(), wide(data), None, None) == -8, data
     assert lib.sv_norm_rope_cache(q, k, k, BUF, BUF, BUF, 64, 0, 1.0, None, None, 7, 1e-6, q, _cache(m), None) == -8
     assert lib.sv_cache_fork(_cache(m), BUF, 4, BUF, 2, BUF, BUF, BUF, BUF, BUF, None, None) == -8
     assert lib.sv_cache_free(BUF, 4, BUF, BUF, 2, 16, BUF, BUF, 8, BUF, BUF, None, None) == -8
