@@ -11,6 +11,14 @@
 // In place nothing is copied: masked entries are written, listed ones read and written.
 //
 // Counts are whole numbers, so the order in which threads meet the tokens changes nothing.
+//
+// Bound by bytes less than by what stands before them: 72 us for 576 rows of 151,936 bf16 logits (359 MB, 5.0 TB/s,
+// 0.73 of a copy's rate) with 500 to 8,000 tokens a request, biases and two masks in three rows, of which 55 are the
+// copy alone, 4 the scan of every request's tokens in each of its 38 slices, 5 the listed entries, 4 biases and lists,
+// 3 the masks; 33 us for 561 rows of 32,003 fp32 logits (146 MB, 4.5 TB/s).  In place 69 and 28 us, and 47 and 18
+// without masks.  One row of 151,936 takes 4.6 us: a launch, the tokens, a tile.
+// A tile in shared memory costs less than computing over the copies afterwards (93 and 41 us), two tiles a warp less
+// than three (81 against 103: the third costs a thread block per SM), slices of 4,096 ids less than 8,192 or 2,048.
 #include <algorithm>
 #include <cuda_bf16.h>
 
@@ -27,7 +35,7 @@ constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of
 constexpr int kAdjStages = 2;                    // tiles of a warp's ring: one on its way, one in hand
 constexpr int kAdjSlice = 4096;                  // most ids of a slice
 constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
-constexpr int kAdjBatch = 8;                     // tokens that a thread loads before it counts them
+constexpr int kAdjBatch = 8;                     // tokens that a thread loads at a time (4: 76 us, 12: 73 and 36)
 constexpr int kAdjMaskWords = kAdjTile / 2 / 32 + 1;  // words of a region's mask
 
 // a word of the table: bit 31 seen, bits 19 .. 30 the head of the chain (0: none), bits 0 .. 18 the count
