@@ -35,7 +35,7 @@ constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of
 constexpr int kAdjStages = 2;                    // tiles of a warp's ring: one on its way, one in hand
 constexpr int kAdjSlice = 4096;                  // most ids of a slice
 constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
-constexpr int kAdjBatch = 8;                     // tokens that a thread loads at a time (4: 76 us, 12: 73 and 36)
+constexpr int kAdjTokens = 16;                   // tokens of a thread that are brought at a time
 constexpr int kAdjMaskWords = kAdjTile / 2 / 32 + 1;  // words of a region's mask
 
 // a word of the table: bit 31 seen, bits 19 .. 30 the head of the chain (0: none), bits 0 .. 18 the count
@@ -44,6 +44,9 @@ constexpr uint32_t kAdjSeen = 1u << 31, kAdjHeadShift = 19, kAdjHead = 0xFFFu <<
 static_assert(SV_MAX_HISTORY <= (1 << kAdjHeadShift) - 1, "a count must not reach the chain's head");
 static_assert(SV_MAX_BRANCHES * SV_MAX_K < (1 << 12), "a draft's number must fit the head");
 static_assert(kAdjSlice / (kAdjTile / 4) <= kAdjWarps, "a warp keeps to one region, and a region has a warp");
+static_assert(kAdjSlice < kAdjThreads * 32, "a thread lists 32 ids, and one is left for those before the slice");
+static_assert(kAdjTokens == 16, "a thread reads its tokens four at a time, and 16 bits say which are the slice's");
+static_assert(kAdjTokens * 32 * 4 <= kAdjTile, "a warp's tokens wait in a tile");
 static_assert(kAdjMaskWords >= 33, "a warp brings 33 words of a mask");
 
 struct AdjustGeom {
@@ -55,18 +58,19 @@ struct AdjustGeom {
     int32_t bias_bits;      // of an id's word in the table of biases: 0 without biases, 16 where their numbers fit, else 32
 };
 
-// The parts of a CTA's shared memory, in 32-bit words; the tiles lie first.
+// The parts of a CTA's shared memory, in 32-bit words; the tiles lie first (in place: one a warp, for tokens).
 struct AdjustLayout {
-    int32_t mask, tab, bias, row, list, next, bytes;  // list and next hold 16 bits each
+    int32_t mask, tab, bias, bits, row, list, next, bytes;  // list and next hold 16 bits each
 };
 __host__ __device__ inline AdjustLayout layout_of(const AdjustGeom& g, bool tiles)
 {
     const int32_t ids = g.slice + kAdjEdge;
     AdjustLayout l;
-    l.mask = tiles ? kAdjWarps * kAdjStages * kAdjTile / 4 : 0;
+    l.mask = kAdjWarps * (tiles ? kAdjStages : 1) * kAdjTile / 4;
     l.tab = l.mask + (tiles ? (kAdjWarps * kAdjStages * kAdjMaskWords + 3) / 4 * 4 : 0);
     l.bias = l.tab + ids;
-    l.row = l.bias + ids * g.bias_bits / 32;
+    l.bits = l.bias + ids * g.bias_bits / 32;
+    l.row = l.bits + g.slice / 32 + 4;
     l.list = l.row + 2 * g.most_rows;
     l.next = l.list + (g.slice + (kAdjEdge << g.region_shift)) / 2;
     l.bytes = 4 * (l.next + (g.drafts + 1) / 2);
@@ -150,7 +154,7 @@ __device__ __forceinline__ void copies_wait()
 // T: uint16_t for bf16 rows, uint32_t for fp32 rows.  COPY: out of place, by tiles; every row of the two
 // matrices starts alike within 16 bytes.
 template <typename T, bool COPY>
-__global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const __grid_constant__ AdjustArgs a, const AdjustGeom g)
+__global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_constant__ AdjustArgs a, const AdjustGeom g)
 {
     constexpr int kPer = 16 / sizeof(T);            // entries of a vector
     constexpr int kRegion = kAdjTile / sizeof(T);   // ids of a region
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
     const AdjustLayout at = layout_of(g, COPY);
     uint32_t* s_tab = s_mem + at.tab;
     uint32_t* s_bias = s_mem + at.bias;  // an id's last bias: 1 + its number, 0 for none
+    uint32_t* s_bits = s_mem + at.bits;  // the slice's ids that a rule meets, then those before it
     int2* s_row = reinterpret_cast<int2*>(s_mem + at.row);  // each row's mask (-1: none), and the drafts before its branch's
     uint16_t* s_list = reinterpret_cast<uint16_t*>(s_mem + at.list);
     uint16_t* s_next = reinterpret_cast<uint16_t*>(s_mem + at.next);
@@ -177,60 +182,6 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
     const int32_t rows = static_cast<int32_t>(static_cast<int64_t>(g.rows) * (group + 1) / g.groups) - row0;
     const int64_t first = static_cast<int64_t>(r) * g.rows + row0;
 
-    for (int j = tid; j < rows; j += kAdjThreads) {
-        int64_t i = -1;
-        if (u.mask != nullptr) i = u.mask_row != nullptr ? u.mask_row[first + j] : first + j;
-        s_row[j] = make_int2(i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1,
-                             row0 + j > 0 ? (row0 + j - 1) / a.k * a.k : 0);
-    }
-    // The first tokens are on their way before their number is known: all of the row may be read.
-    const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
-    const int32_t* draft = a.draft + static_cast<int64_t>(r) * g.drafts;
-    int32_t token[kAdjBatch], first_draft = 0, first_bias = 0;
-    auto fetch = [&](int32_t (&to)[kAdjBatch], int32_t i0, int32_t end) {
-#pragma unroll
-        for (int q = 0; q < kAdjBatch; ++q)
-            if (i0 + q * kAdjThreads < end) to[q] = history[i0 + q * kAdjThreads];
-    };
-    if (u.history != nullptr) fetch(token, tid, u.history_width);
-    if (tid < g.drafts) first_draft = draft[tid];
-    // what the request asks for
-    uint32_t st = 0;
-    int32_t len = 0, prompt = 0, b0 = 0, b1 = 0;
-    if (u.history != nullptr) {
-        const int32_t given = u.history_len[r];
-        len = min(max(given, 0), u.history_width);
-        const int32_t p = u.prompt_len != nullptr ? u.prompt_len[r] : 0;
-        prompt = min(max(p, 0), len);
-        if (len != given || prompt != p) st |= SV_ST_BAD_LENGTH;
-    }
-    if (biased) {
-        const int32_t x = u.bias_start[r], y = u.bias_start[r + 1];
-        b0 = min(max(x, 0), u.bias_entries);
-        b1 = min(max(y, b0), u.bias_entries);
-        if (b0 != x || b1 != y) st |= SV_ST_BAD_LENGTH;
-        if (b0 + tid < b1) first_bias = u.bias_id[b0 + tid];
-    }
-    float rep = u.repetition != nullptr ? u.repetition[r] : 1.0f;
-    float pres = u.presence != nullptr ? u.presence[r] : 0.0f;
-    float freq = u.frequency != nullptr ? u.frequency[r] : 0.0f;
-    if (!(rep > 0.0f) || isinf(rep)) {
-        rep = 1.0f;
-        st |= SV_ST_BAD_PENALTY;
-    }
-    if (!isfinite(pres)) {
-        pres = 0.0f;
-        st |= SV_ST_BAD_PENALTY;
-    }
-    if (!isfinite(freq)) {
-        freq = 0.0f;
-        st |= SV_ST_BAD_PENALTY;
-    }
-    for (int i = tid; i < (at.row - at.tab) / 4; i += kAdjThreads)
-        reinterpret_cast<uint4*>(s_tab)[i] = make_uint4(0, 0, 0, 0);
-    if (tid < kAdjWarps) s_listed[tid] = 0;
-    __syncthreads();
-
     // A warp takes one region, in every kAdjWarps / regions-th row from row j0 on.
     const int32_t region = warp & ((1 << g.region_shift) - 1), in_slice = s0 + region * kRegion;
     const int32_t j0 = warp >> g.region_shift, j_step = kAdjWarps >> g.region_shift;
@@ -243,45 +194,103 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
         return COPY || in_place ? in_slice - (static_cast<int32_t>(reinterpret_cast<uintptr_t>(row)) & 15) / static_cast<int32_t>(sizeof(T))
                                 : in_slice;
     };
-    auto mask_of = [&](int32_t j) -> const uint32_t* {
-        const int32_t i = s_row[j].x;
+    uint8_t* tiles = reinterpret_cast<uint8_t*>(s_mem) + warp * (COPY ? kAdjStages : 1) * kAdjTile;
+    uint32_t* masks = s_mem + at.mask + warp * kAdjStages * kAdjMaskWords;
+    auto mask_at = [&](int32_t i) -> const uint32_t* {
         return i < 0 ? nullptr : u.mask + static_cast<int64_t>(i) * u.mask_words;
     };
-    uint8_t* tiles = reinterpret_cast<uint8_t*>(s_mem) + warp * kAdjStages * kAdjTile;
-    uint32_t* masks = s_mem + at.mask + warp * kAdjStages * kAdjMaskWords;
-    // row j's region on its way to a tile
-    auto bring = [&](const T* row, int32_t j, int stage) {
-        if (j < rows) {
-            const int32_t x0 = region_of(row);
-            uint8_t* tile = tiles + stage * kAdjTile;
-            if (x0 >= 0 && x0 + kRegion <= V) {
-                const uint4* src = reinterpret_cast<const uint4*>(row + x0) + lane;
+    // a row's region on its way to a tile
+    auto bring = [&](const T* row, int stage) {
+        const int32_t x0 = region_of(row);
+        uint8_t* tile = tiles + stage * kAdjTile;
+        if (x0 >= 0 && x0 + kRegion <= V) {
+            const uint4* src = reinterpret_cast<const uint4*>(row + x0) + lane;
 #pragma unroll
-                for (int q = 0; q < kAdjVecs; ++q) copy16(tile + (q * 32 + lane) * 16, src + q * 32);
-            } else {
+            for (int q = 0; q < kAdjVecs; ++q) copy16(tile + (q * 32 + lane) * 16, src + q * 32);
+        } else {
 #pragma unroll 1
-                for (int q = 0; q < kAdjVecs; ++q) {
-                    const int32_t o = (q * 32 + lane) * kPer, x = x0 + o;
-                    if (x >= 0 && x + kPer <= V) {
-                        copy16(tile + o * sizeof(T), row + x);
-                    } else {
+            for (int q = 0; q < kAdjVecs; ++q) {
+                const int32_t o = (q * 32 + lane) * kPer, x = x0 + o;
+                if (x >= 0 && x + kPer <= V) {
+                    copy16(tile + o * sizeof(T), row + x);
+                } else {
 #pragma unroll 1
-                        for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y) reinterpret_cast<T*>(tile)[y - x0] = row[y];
-                    }
+                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y) reinterpret_cast<T*>(tile)[y - x0] = row[y];
                 }
             }
-            if (const uint32_t* mask = mask_of(j)) {
-                const int32_t word = (x0 >> 5) + lane;
-                if (word >= 0 && word < u.mask_words) copy4(masks + stage * kAdjMaskWords + lane, mask + word);
-                if (lane == 0 && word + 32 < u.mask_words) copy4(masks + stage * kAdjMaskWords + 32, mask + word + 32);
+        }
+    };
+    // its mask's words: those of a region that does not begin with a word reach into one more
+    auto bring_mask = [&](const T* row, int32_t i, int stage) {
+        if (i < 0) return;
+        const int32_t x0 = region_of(row), word = (x0 >> 5) + lane;
+        const uint32_t* from = mask_at(i) + word;
+        uint32_t* to = masks + stage * kAdjMaskWords + lane;
+        if (static_cast<uint32_t>(word) < static_cast<uint32_t>(u.mask_words)) copy4(to, from);
+        if ((x0 & 31) != 0 && lane == 0 && word + 32 < u.mask_words) copy4(to + 32, from + 32);
+    };
+    auto mask_row_of = [&](int32_t j) -> int32_t {
+        int64_t i = -1;
+        if (u.mask != nullptr) i = u.mask_row != nullptr ? u.mask_row[first + j] : first + j;
+        return i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1;
+    };
+
+    // The first tile and the first tokens are on their way before anything is known of the request: all of a row of
+    // the history may be read.  The tokens wait in the tile that comes into use last.
+    const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
+    int32_t* tokens = reinterpret_cast<int32_t*>(tiles + (COPY ? kAdjStages - 1 : 0) * kAdjTile) + 4 * lane;
+    const bool by_four = (reinterpret_cast<uintptr_t>(history) & 15) == 0;
+    // Of the tokens i0 .. end - 1 four in 1,024 are this thread's; it alone reads them.
+    auto bring_tokens = [&](int32_t i0, int32_t end) {
+#pragma unroll
+        for (int q = 0; q < kAdjTokens / 4; ++q) {
+            const int32_t i = i0 + 4 * (q * kAdjThreads + tid);
+            if (by_four && i + 4 <= end) {
+                copy16(tokens + q * 128, history + i);
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < 4 && i + e < end; ++e) copy4(tokens + q * 128 + e, history + i + e);
             }
         }
-        copies_commit();
     };
-    const T* coming = in;
-    if (COPY) {
-        bring(coming, j0, 0);
-        coming += in_step;
+    if (COPY && j0 < rows) bring(in, 0);
+    if (u.history != nullptr) bring_tokens(0, u.history_width);
+    copies_commit();
+    const int32_t* draft = a.draft + static_cast<int64_t>(r) * g.drafts;
+    const int32_t first_draft = tid < g.drafts ? draft[tid] : 0;
+    const int32_t first_mask = COPY && j0 < rows ? mask_row_of(j0) : -1;
+    const int32_t asked_len = u.history != nullptr ? u.history_len[r] : 0;
+    const int32_t asked_prompt = u.history != nullptr && u.prompt_len != nullptr ? u.prompt_len[r] : 0;
+    const int32_t asked_b0 = biased ? u.bias_start[r] : 0, asked_b1 = biased ? u.bias_start[r + 1] : 0;
+    float rep = u.repetition != nullptr ? u.repetition[r] : 1.0f;
+    float pres = u.presence != nullptr ? u.presence[r] : 0.0f;
+    float freq = u.frequency != nullptr ? u.frequency[r] : 0.0f;
+    for (int i = tid; i < (at.row - at.tab) / 4; i += kAdjThreads)
+        reinterpret_cast<uint4*>(s_tab)[i] = make_uint4(0, 0, 0, 0);
+    if (tid < kAdjWarps) s_listed[tid] = 0;
+    for (int j = tid; j < rows; j += kAdjThreads)
+        s_row[j] = make_int2(mask_row_of(j), row0 + j > 0 ? (row0 + j - 1) / a.k * a.k : 0);
+    bring_mask(in, first_mask, 0);
+    copies_commit();
+    __syncthreads();
+
+    // what cannot be asked for is left out or cut
+    uint32_t st = 0;
+    const int32_t b0 = min(max(asked_b0, 0), u.bias_entries), b1 = min(max(asked_b1, b0), u.bias_entries);
+    const int32_t first_bias = b0 + tid < b1 ? u.bias_id[b0 + tid] : 0;
+    const int32_t len = min(max(asked_len, 0), u.history_width), prompt = min(max(asked_prompt, 0), len);
+    if (len != asked_len || prompt != asked_prompt || b0 != asked_b0 || b1 != asked_b1) st |= SV_ST_BAD_LENGTH;
+    if (!(rep > 0.0f) || isinf(rep)) {
+        rep = 1.0f;
+        st |= SV_ST_BAD_PENALTY;
+    }
+    if (!isfinite(pres)) {
+        pres = 0.0f;
+        st |= SV_ST_BAD_PENALTY;
+    }
+    if (!isfinite(freq)) {
+        freq = 0.0f;
+        st |= SV_ST_BAD_PENALTY;
     }
 
     // Tokens of the vocabulary that are the slice's: low .. low + span - 1.
@@ -293,25 +302,47 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
         if (tells) outside = outside || static_cast<uint32_t>(x) >= static_cast<uint32_t>(V);
         return static_cast<uint32_t>(x - low) < span;
     };
-    for (int32_t i0 = tid; i0 < len; i0 += kAdjThreads * kAdjBatch) {
-        int32_t next[kAdjBatch];
-        fetch(next, i0 + kAdjThreads * kAdjBatch, len);
+    // Notes that a rule meets an id, and gives the id's place in the table.
+    auto place = [&](int32_t x) -> int32_t {
+        const int32_t i = x - s0;
+        atomicOr(i >= 0 ? &s_bits[i >> 5] : &s_bits[g.slice / 32], 1u << (i >= 0 ? i & 31 : i + kAdjEdge));
+        return x - base;
+    };
+    copies_wait<1>();  // the tokens
+    for (int32_t i0 = 0; i0 < len;) {
+        uint32_t hits = 0, wrong = 0;  // which of this thread's tokens are the slice's (most have none), or nobody's
 #pragma unroll
-        for (int q = 0; q < kAdjBatch; ++q) {
-            const int32_t i = i0 + q * kAdjThreads;
-            if (i < len && meets(token[q])) {
-                if (i >= prompt)
-                    atomicAdd(&s_tab[token[q] - base], 1u);
-                else
-                    atomicOr(&s_tab[token[q] - base], kAdjSeen);
-            }
-            token[q] = next[q];
+        for (int q = 0; q < kAdjTokens / 4; ++q) {
+            if (i0 + 4 * q * kAdjThreads >= len) break;
+            const int4 x = *reinterpret_cast<const int4*>(tokens + q * 128);
+            const uint32_t brought = (1u << min(max(len - (i0 + 4 * (q * kAdjThreads + tid)), 0), 4)) - 1;
+            auto below = [&](int32_t from, uint32_t n) -> uint32_t {  // which are from .. from + n - 1
+                return (static_cast<uint32_t>(x.x - from) < n) | (static_cast<uint32_t>(x.y - from) < n) << 1 |
+                       (static_cast<uint32_t>(x.z - from) < n) << 2 | (static_cast<uint32_t>(x.w - from) < n) << 3;
+            };
+            hits |= (below(low, span) & brought) << (4 * q);
+            if (tells) wrong |= ~below(0, static_cast<uint32_t>(V)) & brought;
+        }
+        outside = outside || wrong != 0;
+        for (; hits != 0; hits &= hits - 1) {
+            const int q = __ffs(hits) - 1;
+            const int32_t l = place(tokens[q / 4 * 128 + q % 4]);
+            if (i0 + 4 * (q / 4 * kAdjThreads + tid) + q % 4 >= prompt)
+                atomicAdd(&s_tab[l], 1u);
+            else
+                atomicOr(&s_tab[l], kAdjSeen);
+        }
+        i0 += kAdjThreads * kAdjTokens;
+        if (i0 < len) {
+            bring_tokens(i0, len);
+            copies_commit();
+            copies_wait<0>();
         }
     }
     for (int32_t i = tid; i < g.drafts; i += kAdjThreads) {
         const int32_t x = i == tid ? first_draft : draft[i];
         if (!meets(x)) continue;
-        uint32_t* word = &s_tab[x - base];
+        uint32_t* word = &s_tab[place(x)];
         uint32_t old = *word, was;
         do {
             was = old;
@@ -322,7 +353,7 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
     for (int32_t i = b0 + tid; i < b1; i += kAdjThreads) {
         const int32_t x = i == b0 + tid ? first_bias : u.bias_id[i];
         if (!meets(x)) continue;
-        const int32_t l = x - base;
+        const int32_t l = place(x);
         const uint32_t entry = static_cast<uint32_t>(i) + 1;
         if (g.bias_bits == 32) {
             atomicMax(&s_bias[l], entry);
@@ -348,27 +379,24 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
     }
     __syncthreads();
 
-    // The ids that a rule meets, by regions; the last ones of a region stand in the next one's list, too, for
-    // the rows that start within a vector and have them there.
+    // The ids that a rule meets, by regions.  The last ones before a region stand in its list, too, for the rows that
+    // start within a vector and have them there.
     auto bias_of = [&](int32_t l) -> uint32_t {
         return !biased ? 0u : g.bias_bits == 32 ? s_bias[l] : (s_bias[l >> 1] >> ((l & 1) * 16)) & 0xFFFFu;
     };
-    for (int32_t l0 = 4 * tid; l0 < ids; l0 += 4 * kAdjThreads) {
-        const uint4 four = *reinterpret_cast<const uint4*>(s_tab + l0);
-        uint32_t met = (four.x != 0) | (four.y != 0) << 1 | (four.z != 0) << 2 | (four.w != 0) << 3;
-        if (g.bias_bits == 16) {
-            const uint2 w = *reinterpret_cast<const uint2*>(s_bias + l0 / 2);
-            met |= ((w.x & 0xFFFFu) != 0) | (w.x >> 16 != 0) << 1 | ((w.y & 0xFFFFu) != 0) << 2 | (w.y >> 16 != 0) << 3;
-        } else if (g.bias_bits == 32) {
-            const uint4 w = *reinterpret_cast<const uint4*>(s_bias + l0);
-            met |= (w.x != 0) | (w.y != 0) << 1 | (w.z != 0) << 2 | (w.w != 0) << 3;
-        }
-        for (; met != 0; met &= met - 1) {
-            const int32_t l = l0 + __ffs(met) - 1, i = l - kAdjEdge, q = i / kRegion;  // 0 for those before the slice, too
-            s_list[q * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q], 1)] = static_cast<uint16_t>(l);
-            if (i >= 0 && (i + kAdjEdge) / kRegion > q && i + kAdjEdge < g.slice)
-                s_list[(q + 1) * (kRegion + kAdjEdge) + atomicAdd(&s_listed[q + 1], 1)] = static_cast<uint16_t>(l);
-        }
+    auto note = [&](int32_t p, int32_t l0, uint32_t met) {
+        if (met == 0) return;
+        uint16_t* to = s_list + p * (kRegion + kAdjEdge) + atomicAdd(&s_listed[p], __popc(met));
+        for (; met != 0; met &= met - 1) *to++ = static_cast<uint16_t>(l0 + __ffs(met) - 1);
+    };
+    if (32 * tid < g.slice) {
+        const uint32_t met = s_bits[tid];
+        note(32 * tid / kRegion, kAdjEdge + 32 * tid, met);
+        const int32_t after = (32 * tid + 32) / kRegion;  // the region that begins behind these ids
+        if ((32 * tid + 32) % kRegion == 0 && after < 1 << g.region_shift)
+            note(after, kAdjEdge + 32 * tid + 24, met >> 24);
+    } else if (tid == kAdjThreads - 1) {
+        note(0, 0, s_bits[g.slice / 32]);
     }
     __syncthreads();
 
@@ -395,8 +423,12 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
         int stage = 0;
         for (int32_t j = j0; j < rows; j += j_step, out += out_step) {
             __syncwarp();  // the tile before is stored
-            bring(coming, j + j_step, stage ^ 1);
-            coming += in_step;
+            in += in_step;
+            if (j + j_step < rows) {
+                bring(in, stage ^ 1);
+                bring_mask(in, s_row[j + j_step].x, stage ^ 1);
+            }
+            copies_commit();
             copies_wait<1>();
             __syncwarp();
             const int32_t x0 = region_of(out);
@@ -415,12 +447,17 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
             const uint4* from = reinterpret_cast<const uint4*>(tile) + lane;
             if (x0 >= 0 && x0 + kRegion <= V) {
                 uint4* to = reinterpret_cast<uint4*>(out + x0) + lane;
-                if (has_mask) {
-#pragma unroll
-                    for (int q = 0; q < kAdjVecs; ++q) to[q * 32] = masked<T>(from[q * 32], bits_of((q * 32 + lane) * kPer));
-                } else {
+                if (!has_mask) {
 #pragma unroll
                     for (int q = 0; q < kAdjVecs; ++q) to[q * 32] = from[q * 32];
+                } else if (x0 % 8 == 0) {  // a vector's bits lie in one byte
+                    const uint8_t* bits = reinterpret_cast<const uint8_t*>(words) + ((x0 & 31) + lane * kPer) / 8;
+#pragma unroll
+                    for (int q = 0; q < kAdjVecs; ++q)
+                        to[q * 32] = masked<T>(from[q * 32], kPer == 8 ? bits[q * 4 * kPer] : (bits[q * 4 * kPer] >> (lane * kPer % 8)) & kAll);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kAdjVecs; ++q) to[q * 32] = masked<T>(from[q * 32], bits_of((q * 32 + lane) * kPer));
                 }
             } else {
 #pragma unroll 1
@@ -444,7 +481,7 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
 
     if (!in_place) {  // rows that start differently
         for (int32_t j = j0; j < rows; j += j_step, in += in_step, out += out_step) {
-            const uint32_t* mask = mask_of(j);
+            const uint32_t* mask = mask_at(s_row[j].x);
 #pragma unroll 8
             for (int32_t x = in_slice + lane; x < min(in_slice + kRegion, V); x += 32)
                 out[x] = allowed(mask, x) ? in[x] : kNegInf<T>;
@@ -460,20 +497,20 @@ __global__ void __launch_bounds__(kAdjThreads, COPY ? 3 : 4) adjust_kernel(const
     // In place: a lane has 32 ids' bits of the row's mask, brought while the row before was written, and the
     // first listed entries are read while the masked ones are written.
     uint32_t lo = 0, hi = 0;
-    auto bring_mask = [&](const T* row, int32_t j) {
+    auto read_mask = [&](const T* row, int32_t j) {
         lo = hi = 0xFFFFFFFFu;
-        const uint32_t* mask = j < rows ? mask_of(j) : nullptr;
+        const uint32_t* mask = j < rows ? mask_at(s_row[j].x) : nullptr;
         if (mask == nullptr) return;
         const int32_t word = (region_of(row) >> 5) + lane;
         if (word >= 0 && word < u.mask_words) lo = mask[word];
         if (word + 1 < u.mask_words) hi = mask[word + 1];
     };
-    bring_mask(out, j0);
+    read_mask(out, j0);
     for (int32_t j = j0; j < rows; j += j_step, out += out_step) {
         const int32_t x0 = region_of(out);
         const bool has_mask = s_row[j].x >= 0;
         const uint32_t bits = __funnelshift_r(lo, hi, x0 & 31);  // of ids x0 + 32 * lane on
-        bring_mask(out + out_step, j + j_step);
+        read_mask(out + out_step, j + j_step);
         auto entry = [&](int32_t i, int32_t& l) -> int32_t {  // listed id i's place in the region, -1 for none
             l = i < listed ? list[i] : 0;
             const int32_t o = base + l - x0;
