@@ -622,6 +622,8 @@ int sv_cache_fork(sv_kv_cache cache, int32_t* block_table, int32_t max_blocks, c
     if (seq_len == nullptr || source == nullptr || free_blocks == nullptr || free_count == nullptr ||
         seq_len_out == nullptr || free_count_out == nullptr || (max_blocks > 0 && block_table == nullptr))
         return SV_ERR_INVALID_ARG;
+    // other rows read what one row would write over
+    if (seq_len_out == seq_len || seq_len_out == source || free_count_out == free_count) return SV_ERR_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(source, 4) || !aligned(free_blocks, 4) ||
         !aligned(free_count, 4) || !aligned(seq_len_out, 4) || !aligned(free_count_out, 4) || !aligned(status, 4))
         return SV_ERR_ALIGN;
@@ -641,6 +643,7 @@ int sv_cache_free(const int32_t* block_table, int32_t max_blocks, const int32_t*
     if (seq_len == nullptr || leave == nullptr || free_count == nullptr || seq_len_out == nullptr ||
         free_count_out == nullptr || (max_blocks > 0 && block_table == nullptr) || (num_blocks > 0 && free_blocks == nullptr))
         return SV_ERR_INVALID_ARG;
+    if (seq_len_out == seq_len || seq_len_out == leave || free_count_out == free_count) return SV_ERR_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(leave, 4) || !aligned(free_blocks, 4) ||
         !aligned(free_count, 4) || !aligned(seq_len_out, 4) || !aligned(free_count_out, 4) || !aligned(status, 4))
         return SV_ERR_ALIGN;

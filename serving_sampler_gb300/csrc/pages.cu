@@ -127,6 +127,7 @@ constexpr int kSetCtas = 16;
 constexpr int kSetWarps = kSetCtas * kSetThreads / 32;
 constexpr int kSetBatch = 8;                 // entries that a thread loads before it sets their bits
 constexpr int kSetOwnBytes = 200 * 1024;     // largest bit maps of which every CTA has one of its own
+static_assert(kSetOwnBytes <= kMostShared && 2 * (SV_MAX_BLOCKS / 8 / kSetCtas) <= kMostShared, "the largest pool's maps must fit");
 
 // The words of a bit map over [0, num_blocks) are shared out among the CTAs in equal parts.
 __host__ __device__ inline int32_t set_words(int32_t num_blocks)

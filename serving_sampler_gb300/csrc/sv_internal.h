@@ -244,12 +244,14 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream);
 // number of SMs of the current device
 int device_sm_count();
 
-// Dynamic shared memory above what every kernel may have has to be asked for.
+// Dynamic shared memory above what every kernel may have has to be asked for.  Always the same size is: two
+// threads that launch a kernel with different ones must not take each other's back.
+constexpr int kMostShared = 220 * 1024;
 template <typename Kernel>
 inline cudaError_t allow_shared(Kernel* kernel, int bytes)
 {
     return bytes <= 48 * 1024 ? cudaSuccess
-                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
 }
 
 }  // namespace sv

@@ -279,6 +279,60 @@ def test_captured_and_replayed(sv):
     assert torch.equal(got["logits"].view(torch.int16), want["logits"].view(torch.int16))
 
 
+def test_a_replayed_graph_takes_new_rules(sv):
+    c, d = (Case(5, 3, 2, 3001, torch.bfloat16, seed=x) for x in (22, 23))
+    x, _ = c.logits()
+    kw, draft = c.kwargs(), _i32(c.draft)
+    call = lambda: sv.adjust_logits(x, 5, 3, 2, draft, **kw)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call()
+    d.bias = None
+    c.bias = None
+    for name, t in d.kwargs().items():
+        if name != "bias" and t is not None:
+            kw[name].copy_(t)
+    kw["bias"][0].zero_()
+    draft.copy_(_i32(d.draft)), x.copy_(d.logits()[0])
+    g.replay()
+    torch.cuda.synchronize()
+    want, err, status = plain.adjust(x.double().cpu().numpy(), 5, 3, 2, d.draft, d.history, d.history_len, d.prompt_len,
+                                     d.repetition, d.presence, d.frequency, None, d.mask)
+    d.compare(got, want, err, status)
+
+
+def test_threads_with_slices_of_other_sizes(sv):
+    """Calls from two threads at once, which need different amounts of shared memory."""
+    import threading
+
+    cases = [Case(1, 2, 1, 700, torch.bfloat16, seed=24), Case(64, 2, 1, 32003, torch.bfloat16, seed=25)]
+    args, wants, wrong = [], [], []
+    for c in cases:
+        args.append((c.logits()[0].contiguous(), _i32(c.draft), c.kwargs()))
+        wants.append(sv.adjust_logits(args[-1][0], c.R, 2, 1, args[-1][1], **args[-1][2])["logits"])
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    got = sv.adjust_logits(args[i][0], cases[i].R, 2, 1, args[i][1], **args[i][2])["logits"]
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(got.view(torch.int16), wants[i].view(torch.int16)):
+                    wrong.append(i)
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_refusals(sv):
     c = Case(2, 3, 1, 100, torch.float32, seed=19)
     x, _ = c.logits()

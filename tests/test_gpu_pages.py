@@ -280,6 +280,37 @@ def test_captured_and_replayed(sv):
         assert all(torch.equal(got[name], want[name]) for name in want)
 
 
+def test_a_replayed_graph_takes_new_tables(sv):
+    """The lengths, tables and the stack of a captured call may change between its replays."""
+    p, q = (Pool([40, 23, 0, 9, x, 0], 8, 60, layers=2, seed=x, most=9) for x in (17, 64))
+    table, seq, free, count = _i32(p.table), _i32(p.seq), _i32(p.free), _i32([p.count])
+    source, leave = _i32([-1, -1, 1, -1, -1, 0]), _i32([1, 0, 0, 1, 0, 0])
+    graphs, outs = [], []
+    for call in (lambda: sv.cache_fork(p.k, p.v, table, seq, source, free, count),
+                 lambda: sv.cache_free(table, seq, leave, free, count, 8), lambda: sv.cache_compact(p.k, p.v, table, seq)):
+        call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call())
+    new_source, new_leave = [-1, -1, 4, -1, -1, 2], [0, 1, 0, 0, 1, 0]
+    wants = [plain.fork(q.host(q.k), q.host(q.v), q.table, q.seq, new_source, q.free, q.count),
+             plain.free_rows(q.table, q.seq, np.array(new_leave), q.free, q.count, 8, 60),
+             plain.compact(q.host(q.k), q.host(q.v), q.table, q.seq)]
+    for g, got, want in zip(graphs, outs, wants):
+        for mine, other in ((table, q.table), (seq, q.seq), (free, q.free), (count, [q.count]), (source, new_source),
+                            (leave, new_leave)):
+            mine.copy_(_i32(other))
+        p.k.copy_(q.k), p.v.copy_(q.v)
+        g.replay()
+        torch.cuda.synchronize()
+        for name in got:
+            _same(got[name], want[name], name)
+        if "k" in want:
+            np.testing.assert_array_equal(p.host(p.k), want["k"])
+            np.testing.assert_array_equal(p.host(p.v), want["v"])
+
+
 def test_two_streams_at_once(sv):
     """Calls that share nothing, side by side."""
     pools = [Pool(np.random.default_rng(i).integers(0, 900, 50), 8, 6000, layers=2, seed=i) for i in range(2)]
@@ -293,6 +324,18 @@ def test_two_streams_at_once(sv):
     for p, g, w in zip(pools, got, wants):
         _same(g["block_table"], w["block_table"], "block_table")
         np.testing.assert_array_equal(p.host(p.k), w["k"])
+
+
+def test_outputs_over_inputs_are_refused(sv):
+    p = Pool([40, 0], 8, 30)
+    table, seq, free, count = _i32(p.table), _i32(p.seq), _i32(p.free), _i32([p.count])
+    two, other = _i32([-1, 0]), _i32([0, 0])
+    for out in (dict(seq_len=seq, free_count=_i32([0])), dict(seq_len=two, free_count=_i32([0])),
+                dict(seq_len=other, free_count=count)):
+        with pytest.raises(sv.SpecVerifyError):
+            sv.cache_fork(p.k, p.v, table, seq, two, free, count, out=out)
+        with pytest.raises(sv.SpecVerifyError):
+            sv.cache_free(table, seq, two, free, count, 8, out=out)
 
 
 def test_no_requests(sv):

@@ -5,7 +5,7 @@ import pytest
 
 from tests.test_cache_abi import BUF, WS, P, _cache, _heads, m  # noqa: F401
 
-ODD, MISALIGNED = P(0x10002), P(0x10001)
+ODD, MISALIGNED, OUT = P(0x10002), P(0x10001), P(0x30000)
 
 
 def _rows(m, width=64, dtype=0, data=0x10000, stride=None):  # noqa: F811
@@ -81,13 +81,14 @@ def test_norm_rope_checks(m):  # noqa: F811
 def test_fork_checks(m):  # noqa: F811
     f = m.load().sv_cache_fork
 
-    def call(R=2, mb=4, cache=None, table=BUF, seq=BUF, source=BUF, free=BUF, count=BUF, seq_out=BUF, count_out=BUF,
+    def call(R=2, mb=4, cache=None, table=BUF, seq=BUF, source=BUF, free=BUF, count=BUF, seq_out=OUT, count_out=OUT,
              status=None):
         return f(cache or _cache(m), table, mb, seq, R, source, free, count, seq_out, count_out, status, None)
 
     assert call(R=0) == 0
     assert call(R=-1) == -1 and call(mb=-1) == -1 and call(mb=1 << 28) == -4
     assert call(cache=_cache(m, layers=600000)) == -4 and call(cache=_cache(m, dtype=1)) == -2
+    assert call(seq_out=BUF) == -1 and call(count_out=BUF) == -1     # in place
     for name in ("table", "seq", "source", "free", "count", "seq_out", "count_out"):
         assert call(**{name: None}) == -1 and call(**{name: ODD}) == -7
     assert call(status=ODD) == -7
@@ -96,13 +97,14 @@ def test_fork_checks(m):  # noqa: F811
 def test_free_checks(m):  # noqa: F811
     f = m.load().sv_cache_free
 
-    def call(R=2, bs=16, mb=4, nb=8, table=BUF, seq=BUF, leave=BUF, free=BUF, count=BUF, seq_out=BUF, count_out=BUF,
+    def call(R=2, bs=16, mb=4, nb=8, table=BUF, seq=BUF, leave=BUF, free=BUF, count=BUF, seq_out=OUT, count_out=OUT,
              status=None):
         return f(table, mb, seq, leave, R, bs, free, count, nb, seq_out, count_out, status, None)
 
     assert call(R=0) == 0
     assert call(R=-1) == -1 and call(mb=-1) == -1 and call(bs=0) == -1 and call(nb=-1) == -1
     assert call(mb=1 << 28) == -4 and call(nb=(1 << 22) + 1) == -4
+    assert call(seq_out=BUF) == -1 and call(count_out=BUF) == -1     # in place
     for name in ("table", "seq", "leave", "free", "count", "seq_out", "count_out"):
         assert call(**{name: None}) == -1 and call(**{name: ODD}) == -7
     assert call(status=ODD) == -7
@@ -139,6 +141,6 @@ def test_valid_calls_without_a_device(m):  # noqa: F811
     for data in (0x10000 + 128, 0x10000 - 128, 0x10000 + 256 * 14, 0x10000 - 256 * 14, 0x10000 + 256 * 5 + 128):
         assert lib.sv_adjust_logits(wide(0x10000), 2, 3, 2, BUF, m.SvLogitRules(), wide(data), None, None) == -8, data
     assert lib.sv_norm_rope_cache(q, k, k, BUF, BUF, BUF, 64, 0, 1.0, None, None, 7, 1e-6, q, _cache(m), None) == -8
-    assert lib.sv_cache_fork(_cache(m), BUF, 4, BUF, 2, BUF, BUF, BUF, BUF, BUF, None, None) == -8
-    assert lib.sv_cache_free(BUF, 4, BUF, BUF, 2, 16, BUF, BUF, 8, BUF, BUF, None, None) == -8
+    assert lib.sv_cache_fork(_cache(m), BUF, 4, BUF, 2, BUF, BUF, BUF, OUT, OUT, None, None) == -8
+    assert lib.sv_cache_free(BUF, 4, BUF, BUF, 2, 16, BUF, BUF, 8, OUT, OUT, None, None) == -8
     assert lib.sv_cache_compact(_cache(m), BUF, 4, BUF, 2, P(0x30000), BUF, BUF, None, WS, 1 << 20, None) == -8
