@@ -233,10 +233,12 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
         if (static_cast<uint32_t>(word) < static_cast<uint32_t>(u.mask_words)) copy4(to, from);
         if ((x0 & 31) != 0 && lane == 0 && word + 32 < u.mask_words) copy4(to + 32, from + 32);
     };
-    auto mask_row_of = [&](int32_t j) -> int32_t {
-        int64_t i = -1;
-        if (u.mask != nullptr) i = u.mask_row != nullptr ? u.mask_row[first + j] : first + j;
-        return i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1;
+    // row j's mask as it was asked for, and as an index (-1: none)
+    const bool rows_ask = u.mask != nullptr && u.mask_row != nullptr;
+    auto asked_mask = [&](int32_t j) -> int32_t { return rows_ask && j < rows ? u.mask_row[first + j] : 0; };
+    auto mask_index = [&](int32_t asked, int32_t j) -> int32_t {
+        const int64_t i = rows_ask ? asked : first + j;
+        return u.mask != nullptr && i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1;
     };
 
     // The first tile and the first tokens are on their way before anything is known of the request: all of a row of
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
     copies_commit();
     const int32_t* draft = a.draft + static_cast<int64_t>(r) * g.drafts;
     const int32_t first_draft = tid < g.drafts ? draft[tid] : 0;
-    const int32_t first_mask = COPY && j0 < rows ? mask_row_of(j0) : -1;
+    const int32_t first_mask = COPY ? asked_mask(j0) : 0, row_mask = asked_mask(tid);
     const int32_t asked_len = u.history != nullptr ? u.history_len[r] : 0;
     const int32_t asked_prompt = u.history != nullptr && u.prompt_len != nullptr ? u.prompt_len[r] : 0;
     const int32_t asked_b0 = biased ? u.bias_start[r] : 0, asked_b1 = biased ? u.bias_start[r + 1] : 0;
@@ -273,8 +275,9 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
         reinterpret_cast<uint4*>(s_tab)[i] = make_uint4(0, 0, 0, 0);
     if (tid < kAdjWarps) s_listed[tid] = 0;
     for (int j = tid; j < rows; j += kAdjThreads)
-        s_row[j] = make_int2(mask_row_of(j), row0 + j > 0 ? (row0 + j - 1) / a.k * a.k : 0);
-    bring_mask(in, first_mask, 0);
+        s_row[j] = make_int2(mask_index(j == tid ? row_mask : asked_mask(j), j),
+                             row0 + j > 0 ? (row0 + j - 1) / a.k * a.k : 0);
+    if (COPY && j0 < rows) bring_mask(in, mask_index(first_mask, j0), 0);
     copies_commit();
     __syncthreads();
 
