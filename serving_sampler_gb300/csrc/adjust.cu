@@ -12,10 +12,10 @@
 //
 // Counts are whole numbers, so the order in which threads meet the tokens changes nothing.
 //
-// Bound by bytes less than by what stands before them: 68 us for 576 rows of 151,936 bf16 logits (359 MB, 5.3 TB/s,
-// 0.78 of a copy's rate) with 500 to 8,000 tokens a request, 16 biases and masks on two rows of three, of which 55 are
+// Bound by bytes less than by what stands before them: 67 us for 576 rows of 151,936 bf16 logits (359 MB, 5.4 TB/s,
+// 0.79 of a copy's rate) with 500 to 8,000 tokens a request, 16 biases and masks on two rows of three, of which 55 are
 // the copy alone, 2 the scan of every request's tokens in each of its 38 slices, 5 the listed entries, 3 biases and
-// drafts, 3 the masks; 34 us for 561 rows of 32,003 fp32 logits (146 MB, 4.3 TB/s).  In place 65 and 27 us, and 41 and
+// drafts, 2 the masks; 33 us for 561 rows of 32,003 fp32 logits (146 MB, 4.4 TB/s).  In place 64 and 27 us, and 41 and
 // 18 without masks.  One row of 151,936 takes 4.4 us: a launch, the tokens, a tile.  24 warps share an SM there, so an
 // instruction costs a warp about ten cycles, and those that stand before the rows count most.
 // A tile in shared memory costs less than computing over the copies afterwards (93 and 41 us at the time), two tiles a
