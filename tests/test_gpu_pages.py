@@ -199,8 +199,10 @@ def test_free_with_bad_lengths_and_blocks(sv):
     p.check_free(sv, [1] * 6, count=1000)          # more than the stack holds: a full one
 
 
-def test_free_the_largest_pool(sv):
-    N = sv.MAX_BLOCKS
+# the largest pool there may be, and those on both sides of where a thread block's shared memory holds all of its bits
+@pytest.mark.parametrize("N", [812000, 828000, 1 << 22])
+def test_free_the_largest_pools(sv, N):
+    assert sv.MAX_BLOCKS == 1 << 22
     table = torch.arange(N, dtype=torch.int32, device="cuda").flip(0).view(4, N // 4).contiguous()
     free = torch.empty(N, dtype=torch.int32, device="cuda")
     got = sv.cache_free(table, _i32([N // 4 * 8] * 4), _i32([0, 1, 0, 1]), free, _i32([0]), 8)
@@ -208,7 +210,7 @@ def test_free_the_largest_pool(sv):
     want = torch.cat([table[3].flip(0), table[1].flip(0)])
     assert torch.equal(free[: N // 2], want)
     with pytest.raises(sv.SpecVerifyError):
-        sv.cache_free(table, _i32([8] * 4), _i32([0] * 4), torch.empty(N + 1, dtype=torch.int32, device="cuda"), _i32([0]), 8)
+        sv.cache_free(table, _i32([8] * 4), _i32([0] * 4), torch.empty(sv.MAX_BLOCKS + 1, dtype=torch.int32, device="cuda"), _i32([0]), 8)
 
 
 # --- compact -----------------------------------------------------------------------------------------------------
@@ -246,9 +248,8 @@ def test_compact_with_bad_lengths_and_blocks(sv):
     assert p.check_compact(sv)["status"].tolist() == [1024, 1024, 2048, 2048]
 
 
-def test_compact_the_largest_pool(sv):
-    """A pool of the most blocks there may be, all of it held or none."""
-    N = sv.MAX_BLOCKS
+@pytest.mark.parametrize("N", [1628000, 1648000, 1 << 22])
+def test_compact_the_largest_pools(sv, N):
     k = torch.zeros((N, 8, 1, 8), dtype=torch.bfloat16, device="cuda")
     v = torch.zeros_like(k)
     table = torch.arange(N - 1, N - 2049, -1, dtype=torch.int32, device="cuda").view(8, 256)
