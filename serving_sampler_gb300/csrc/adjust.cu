@@ -38,6 +38,7 @@ constexpr int kAdjVecs = 4;                      // 16-byte vectors of a tile th
 constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of a row
 constexpr int kAdjStages = 2;                    // tiles of a warp's ring: one on its way, one in hand
 constexpr int kAdjSlice = 4096;                  // most ids of a slice
+constexpr int kAdjFewSlice = 8192, kAdjFewRows = 2;  // of one with few rows behind it, and how many those are
 constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
 constexpr int kAdjTokens = 16;                   // tokens of a thread that are brought at a time
 constexpr int kAdjMaskWords = kAdjTile / 2 / 32 + 1;  // words of a region's mask
@@ -47,8 +48,9 @@ constexpr uint32_t kAdjSeen = 1u << 31, kAdjHeadShift = 19, kAdjHead = 0xFFFu <<
                    kAdjCount = (1u << kAdjHeadShift) - 1;
 static_assert(SV_MAX_HISTORY <= (1 << kAdjHeadShift) - 1, "a count must not reach the chain's head");
 static_assert(SV_MAX_BRANCHES * SV_MAX_K < (1 << 12), "a draft's number must fit the head");
-static_assert(kAdjSlice / (kAdjTile / 4) <= kAdjWarps, "a warp keeps to one region, and a region has a warp");
-static_assert(kAdjSlice < kAdjThreads * 32, "a thread lists 32 ids, and one is left for those before the slice");
+static_assert(kAdjSlice / (kAdjTile / 4) <= kAdjWarps && kAdjFewSlice / (kAdjTile / 2) <= kAdjWarps,
+              "a warp keeps to one region, and a region has a warp");
+static_assert(kAdjFewSlice <= kAdjThreads * 32, "a thread lists 32 ids");
 static_assert(kAdjTokens == 16, "a thread reads its tokens four at a time, and 16 bits say which are the slice's");
 static_assert(kAdjTokens * 32 * 4 <= kAdjTile, "a warp's tokens wait in a tile");
 static_assert(kAdjMaskWords >= 33, "a warp brings 33 words of a mask");
@@ -402,9 +404,8 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
         const int32_t after = (32 * tid + 32) / kRegion;  // the region that begins behind these ids
         if ((32 * tid + 32) % kRegion == 0 && after < 1 << g.region_shift)
             note(after, kAdjEdge + 32 * tid + 24, met >> 24);
-    } else if (tid == kAdjThreads - 1) {
-        note(0, 0, s_bits[g.slice / 32]);
     }
+    if (tid == 0) note(0, 0, s_bits[g.slice / 32]);
     __syncthreads();
 
     // The adjusted entry of the table's id l in row j.
@@ -577,7 +578,9 @@ AdjustGeom geom_of(const AdjustArgs& a)
     g.bias_bits = a.rules.bias_entries == 0 ? 0 : a.rules.bias_entries <= 0xFFFF ? 16 : 32;
     const int32_t region = kAdjTile / a.in.esize;
     auto slices = [&](int64_t n) { return (static_cast<int64_t>(a.in.width) + kAdjEdge - 1 + n - 1) / n; };
-    g.slice = kAdjSlice;
+    // a row or two are little work behind a table, and the request's tokens are looked through for every slice: 256 rows
+    // of 256 requests take 88 us with slices of 8,192 bf16 entries and 103 with 4,096; four rows each 36 and 39
+    g.slice = g.rows <= kAdjFewRows ? std::min(kAdjFewSlice, kAdjWarps * region) : kAdjSlice;
     while (g.slice > region && a.R * slices(g.slice) < 4 * sms) g.slice /= 2;
     while ((region << g.region_shift) < g.slice) ++g.region_shift;
     g.slices = static_cast<int32_t>(slices(g.slice));
