@@ -281,6 +281,24 @@ def test_captured_and_replayed(sv):
         assert all(torch.equal(got[name], want[name]) for name in want)
 
 
+def test_layer_by_layer(sv):
+    """A call for each layer on the same inputs does what one call does for all of them."""
+    p = Pool([40, 23, 0, 9], 8, 30, layers=3)
+    table, seq, free, count, source = _i32(p.table), _i32(p.seq), _i32(p.free), _i32([p.count]), _i32([-1, -1, 1, -1])
+    k, v = [x.clone() for x in p.k], [x.clone() for x in p.v]
+    one = sv.cache_fork(p.k, p.v, table, seq, source, free, count)
+    forked = table.clone()
+    for layer in range(3):
+        each = sv.cache_fork(k[layer], v[layer], table, seq, source, free, count)
+        assert torch.equal(table, forked) and all(torch.equal(each[name], one[name]) for name in one)
+    seq_len = one["seq_len"]
+    one = sv.cache_compact(p.k, p.v, table, seq_len)
+    for layer in range(3):
+        each = sv.cache_compact(k[layer], v[layer], table, seq_len)
+        assert all(torch.equal(each[name], one[name]) for name in one)
+        assert torch.equal(k[layer], p.k[layer]) and torch.equal(v[layer], p.v[layer])
+
+
 def test_a_replayed_graph_takes_new_tables(sv):
     """The lengths, tables and the stack of a captured call may change between its replays."""
     p, q = (Pool([40, 23, 0, 9, x, 0], 8, 60, layers=2, seed=x, most=9) for x in (17, 64))
