@@ -49,15 +49,38 @@ __device__ __forceinline__ Fork fork_of(const ForkArgs& a, int32_t r)
 
 // Grid: x = rows, y = 128 16-byte columns of the heads of all layers, K and V, z = shares of the tokens.  A
 // thread owns a column and walks its share of the source's last block, eight loads before their stores.
-// Bound by bytes behind a chain of loads (source, length, blocks taken before, block ids): 23.7 us for 64 forks of
-// 16 layers, 134 MB, 5.6 TB/s, 0.83 of a copy's rate (25.1 with one share); 3.9 us for 7 forks of 4 layers.
+// Bound by bytes behind a chain of loads (source, length, blocks taken before, block ids), of which the first
+// loads wait for no more than the source's: 23.0 us for 64 forks of 16 layers, 134 MB, 5.8 TB/s, 0.86 of a copy's rate
+// (25.1 with one share, 23.9 with loads behind the chain); 3.6 us for 7 forks of 4 layers.
 __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const ForkArgs a)
 {
     const int tid = threadIdx.x;
     const int32_t r = blockIdx.x;
     const bool first = blockIdx.y == 0 && blockIdx.z == 0, teller = r + 1 == a.R && first;  // it tells how many blocks are left
     const Fork f = fork_of(a, r);
-    if (!first && !f.needs) return;
+    const int32_t full = a.by_block.quotient(max(f.tokens, 0)), tail = f.tokens - full * a.cache.block_size;
+    if (!first && (!f.needs || static_cast<int64_t>(blockIdx.z) * kMoveBatch >= tail)) return;
+    const int32_t N = a.cache.num_blocks, given = a.free_count[0];
+    const int32_t* from = a.block_table + static_cast<int64_t>(f.makes ? f.source : 0) * a.max_blocks;
+    const int32_t last = f.needs ? from[full] : -1;
+
+    // the first tokens are on their way while the block they go to is found
+    const int32_t vecs = a.cache.head_dim / 8, columns = a.cache.kv_heads * vecs;
+    const int64_t column = static_cast<int64_t>(blockIdx.y) * kForkThreads + tid;
+    const int32_t plane = static_cast<int32_t>(column / columns),
+                  col = static_cast<int32_t>(column - static_cast<int64_t>(plane) * columns), h = col / vecs;
+    const bool moves = f.needs && last >= 0 && last < N && plane < 2 * a.cache.layers;
+    uint16_t* p = static_cast<uint16_t*>((plane & 1) ? a.cache.v : a.cache.k) + (plane >> 1) * a.cache.layer_stride +
+                  h * a.cache.head_stride + (col - h * vecs) * 8;
+    const uint16_t* src = p + last * a.cache.block_stride;
+    uint4 val[kMoveBatch];
+    auto load = [&](int32_t i0) {
+#pragma unroll
+        for (int u = 0; u < kMoveBatch; ++u)
+            if (i0 + u < tail) val[u] = *reinterpret_cast<const uint4*>(src + (i0 + u) * a.cache.token_stride);
+    };
+    int32_t i0 = blockIdx.z * kMoveBatch;
+    if (moves) load(i0);
 
     int32_t before = 0;  // blocks taken by the rows before
     if (f.needs || teller) {
@@ -70,20 +93,17 @@ __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const ForkArgs
 #pragma unroll
         for (int i = 0; i < kForkThreads / 32; ++i) before += s_sum[i];
     }
-    const int32_t count = min(max(a.free_count[0], 0), a.cache.num_blocks);
+    const int32_t count = min(max(given, 0), N);
     const bool takes = f.needs && before < count;
     const int32_t fresh = takes ? a.free_blocks[count - 1 - before] : -1;
     const bool done = f.makes && (takes || !f.needs);
-    const int32_t full = a.by_block.quotient(f.tokens), tail = f.tokens - full * a.cache.block_size;
-    const int32_t* from = a.block_table + static_cast<int64_t>(done ? f.source : 0) * a.max_blocks;
-    const int32_t last = takes ? from[full] : -1;
     if (first) {
-        bool out = takes && (fresh < 0 || fresh >= a.cache.num_blocks || last < 0 || last >= a.cache.num_blocks);
+        bool out = takes && (fresh < 0 || fresh >= N || last < 0 || last >= N);
         if (done) {
             int32_t* to = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
             for (int32_t i = tid; i < full; i += kForkThreads) {
                 const int32_t id = from[i];
-                out = out || id < 0 || id >= a.cache.num_blocks;
+                out = out || id < 0 || id >= N;
                 to[i] = id;
             }
             if (takes && tid == 0) to[full] = fresh;
@@ -97,27 +117,16 @@ __global__ void __launch_bounds__(kForkThreads) cache_fork_kernel(const ForkArgs
             if (teller) a.free_count_out[0] = max(count - before - (f.needs ? 1 : 0), 0);
         }
     }
-    if (!takes || fresh < 0 || fresh >= a.cache.num_blocks || last < 0 || last >= a.cache.num_blocks) return;
-
-    const int32_t vecs = a.cache.head_dim / 8, columns = a.cache.kv_heads * vecs;
-    const int64_t column = static_cast<int64_t>(blockIdx.y) * kForkThreads + tid;
-    const int32_t plane = static_cast<int32_t>(column / columns),
-                  col = static_cast<int32_t>(column - static_cast<int64_t>(plane) * columns);
-    if (plane >= 2 * a.cache.layers) return;
-    const int32_t h = col / vecs;
-    uint16_t* p = static_cast<uint16_t*>((plane & 1) ? a.cache.v : a.cache.k) + (plane >> 1) * a.cache.layer_stride +
-                  h * a.cache.head_stride + (col - h * vecs) * 8;
-    const uint16_t* src = p + last * a.cache.block_stride;
+    // a stack that holds the source's own block leaves it as it is
+    if (!takes || !moves || fresh < 0 || fresh >= N || fresh == last) return;
     uint16_t* dst = p + fresh * a.cache.block_stride;
-    if (src == dst) return;  // a stack that holds a block in use
-    for (int32_t i0 = blockIdx.z * kMoveBatch; i0 < tail; i0 += gridDim.z * kMoveBatch) {
-        uint4 val[kMoveBatch];
-#pragma unroll
-        for (int u = 0; u < kMoveBatch; ++u)
-            if (i0 + u < tail) val[u] = *reinterpret_cast<const uint4*>(src + (i0 + u) * a.cache.token_stride);
+    while (true) {
 #pragma unroll
         for (int u = 0; u < kMoveBatch; ++u)
             if (i0 + u < tail) *reinterpret_cast<uint4*>(dst + (i0 + u) * a.cache.token_stride) = val[u];
+        i0 += gridDim.z * kMoveBatch;
+        if (i0 >= tail) break;
+        load(i0);
     }
 }
 
