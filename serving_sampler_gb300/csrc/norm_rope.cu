@@ -46,15 +46,47 @@ __device__ __forceinline__ uint32_t narrow2(uint64_t v)
     return pack2<F16>(x, y);
 }
 
-// SIDE: as in rope.cu.  ITEMS: lanes of a head, 32 / ITEMS heads to a warp.
-template <bool F16, bool SIDE, int ITEMS>
+// A vector of E 16-bit entries.
+template <int E>
+struct Packed {
+    uint32_t w[E / 2];
+};
+template <int E>
+__device__ __forceinline__ Packed<E> load_packed(const void* p)
+{
+    Packed<E> v;
+    if constexpr (E == 8) {
+        const uint4 x = *static_cast<const uint4*>(p);
+        v.w[0] = x.x, v.w[1] = x.y, v.w[2] = x.z, v.w[3] = x.w;
+    } else if constexpr (E == 4) {
+        const uint2 x = *static_cast<const uint2*>(p);
+        v.w[0] = x.x, v.w[1] = x.y;
+    } else {
+        v.w[0] = *static_cast<const uint32_t*>(p);
+    }
+    return v;
+}
+template <int E>
+__device__ __forceinline__ void store_packed(void* p, const Packed<E>& v)
+{
+    if constexpr (E == 8)
+        *static_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    else if constexpr (E == 4)
+        *static_cast<uint2*>(p) = make_uint2(v.w[0], v.w[1]);
+    else
+        *static_cast<uint32_t*>(p) = v.w[0];
+}
+
+// SIDE: as in rope.cu.  ITEMS: lanes of a head, 32 / ITEMS heads to a warp.  E: entries of a vector, of which the
+// distance between a pair's halves is a multiple (8 where pairs lie side by side).
+template <bool F16, bool SIDE, int ITEMS, int E>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs n, const RopeGeom g)
 {
-    constexpr int kHeads = 32 / ITEMS, kGroups = kRopeThreads / 32 * kHeads;
+    constexpr int kHeads = 32 / ITEMS, kGroups = kRopeThreads / 32 * kHeads, kParts = E / 2;
     const RopeArgs& a = n.rope;
     // What a lane reads of the tables lies 16 bytes beside what the next lane reads: [part][lane of the head].
-    __shared__ __align__(16) float4 s_cs[kNormTokens][4][ITEMS];  // cosine and sine of two pairs
-    __shared__ __align__(16) float4 s_w[2][4][ITEMS];             // four entries' weights for q, for k
+    __shared__ __align__(16) float4 s_cs[kNormTokens][kParts][ITEMS];  // cosine and sine of two pairs
+    __shared__ __align__(16) float4 s_w[2][kParts][ITEMS];             // four entries' weights for q, for k
     __shared__ int64_t s_at[kNormTokens];
     const int tid = threadIdx.x, lane = tid & 31;
     const bool whole = lane < kHeads * ITEMS;  // the last lanes of a warp may have no head
@@ -65,7 +97,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
     const int step = kGroups * gridDim.y;
 
     // the two vectors of a lane, and whether pairs turn in them
-    const int cut = g.half / 8;
+    const int cut = g.half / E, vecs = D / E;
     auto vectors_of = [&](int j, int& va, int& vb) -> bool {
         va = 2 * j;
         vb = 2 * j + 1;
@@ -76,7 +108,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
         return true;
     };
     int va_at, vb_at;
-    const bool turns = vectors_of(j, va_at, vb_at), has_a = whole && va_at < g.vecs, has_b = whole && vb_at < g.vecs;
+    const bool turns = vectors_of(j, va_at, vb_at), has_a = whole && va_at < vecs, has_b = whole && vb_at < vecs;
 
     struct Head {
         int token, row;
@@ -89,38 +121,38 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
             }
         }
     };
-    auto load = [&](const Head& h, uint4& va, uint4& vb) {
-        va = vb = make_uint4(0, 0, 0, 0);
+    auto load = [&](const Head& h, Packed<E>& va, Packed<E>& vb) {
+        va = vb = Packed<E>{};
         if (h.token >= tokens) return;
         const sv_heads& m = h.row < Hq ? a.q : h.row < Hq + Hk ? a.k : a.v;
         const int r = h.row < Hq ? h.row : h.row < Hq + Hk ? h.row - Hq : h.row - Hq - Hk;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.data) +
-                                                          (t0 + h.token) * m.token_stride + r * m.head_stride);
-        if (has_a) va = src[va_at];
-        if (has_b) vb = src[vb_at];
+        const uint16_t* src = static_cast<const uint16_t*>(m.data) + (t0 + h.token) * m.token_stride + r * m.head_stride;
+        if (has_a) va = load_packed<E>(src + va_at * E);
+        if (has_b) vb = load_packed<E>(src + vb_at * E);
     };
-    uint4 na, nb;  // the next head's vectors, in flight
+    Packed<E> na, nb;  // the next head's vectors, in flight
     Head next{0, static_cast<int>(blockIdx.y) * kGroups + group};
     next.settle(g.rows);
     load(next, na, nb);
     if (tid < tokens) s_at[tid] = slot_offset(a, a.slot[t0 + tid]);
-    for (int i = tid; i < 2 * 4 * ITEMS; i += kRopeThreads) {
-        const int which = i / (4 * ITEMS), part = i / ITEMS % 4, o = i % ITEMS;
+    for (int i = tid; i < 2 * kParts * ITEMS; i += kRopeThreads) {
+        const int which = i / (kParts * ITEMS), part = i / ITEMS % kParts, o = i % ITEMS;
         int x, y;
         vectors_of(o, x, y);
         const void* w = which == 0 ? n.q_weight : n.k_weight;
-        const int first = 8 * (part < 2 ? x : y) + 4 * (part & 1);
-        float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-        if (w != nullptr && first < D)
-            f = make_float4(weight_at(w, n.weight_dtype, first), weight_at(w, n.weight_dtype, first + 1),
-                            weight_at(w, n.weight_dtype, first + 2), weight_at(w, n.weight_dtype, first + 3));
-        s_w[which][part][o] = f;
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int at = 4 * part + e, entry = at < E ? E * x + at : E * y + at - E;  // of the lane's 2 E
+            f[e] = w != nullptr && entry < D ? weight_at(w, n.weight_dtype, entry) : 1.0f;
+        }
+        s_w[which][part][o] = make_float4(f[0], f[1], f[2], f[3]);
     }
-    for (int y = tid; y < tokens * 8 * ITEMS; y += kRopeThreads) {
-        const int i = y / (8 * ITEMS), p = y - i * (8 * ITEMS);
-        // a lane may hold fewer pairs than eight: the others pass
+    for (int y = tid; y < tokens * E * ITEMS; y += kRopeThreads) {
+        const int i = y / (E * ITEMS), p = y - i * (E * ITEMS);
+        // a lane may hold fewer pairs than E: the others pass
         const float2 t = p < g.half ? turn_of(a, a.position[t0 + i], p) : make_float2(1.0f, 0.0f);
-        float* to = &s_cs[i][p / 2 % 4][p / 8].x + p % 2 * (SIDE ? 2 : 1);
+        float* to = &s_cs[i][p / 2 % kParts][p / E].x + p % 2 * (SIDE ? 2 : 1);
         to[0] = t.x;             // side by side: cosine, sine of each; else the two cosines, then the two sines
         to[SIDE ? 1 : 2] = t.y;
     }
@@ -129,16 +161,15 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
     // every warp takes the same number of rounds: the exchanges need all of its lanes
     const int total = tokens * g.rows;
     for (int base = static_cast<int>(blockIdx.y) * kGroups; base < total; base += step) {
-        const uint4 va = na, vb = nb;
+        Packed<E> va = na, vb = nb;
         const Head h = next;
         next.row += step;
         next.settle(g.rows);
         load(next, na, nb);
-        const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-        uint64_t f[8], sums = 0;
+        uint64_t f[E], sums = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f[e] = wide2<F16>(w[e]);
+        for (int e = 0; e < E; ++e) {
+            f[e] = wide2<F16>(e < kParts ? va.w[e % kParts] : vb.w[e % kParts]);
             sums = fma2(f[e], f[e], sums);
         }
         float lo, hi;
@@ -155,19 +186,18 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
             sum = all;
         }
         if (!whole || h.token >= tokens) continue;
-        uint4 oa = va, ob = vb;
         if (h.row < Hq + Hk) {
             const uint64_t scale = both(rsqrtf(sum * g.by_dim + n.eps));
             const int which = h.row < Hq ? 0 : 1;
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
+            for (int part = 0; part < kParts; ++part) {
                 const float4 u = s_w[which][part][j];
                 f[2 * part] = mul2(f[2 * part], mul2(pack2(u.x, u.y), scale));
                 f[2 * part + 1] = mul2(f[2 * part + 1], mul2(pack2(u.z, u.w), scale));
             }
             if (turns) {
 #pragma unroll
-                for (int part = 0; part < 4; ++part) {
+                for (int part = 0; part < kParts; ++part) {
                     const float4 t = s_cs[h.token][part][j];
                     if (SIDE) {
 #pragma unroll
@@ -178,32 +208,34 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
                             f[2 * part + e] = fma2(pack2(y, x), pack2(-sn, sn), mul2(f[2 * part + e], both(c)));
                         }
                     } else {
-                        const uint64_t c = pack2(t.x, t.y), sn = pack2(t.z, t.w), x = f[part], y = f[4 + part];
+                        const uint64_t c = pack2(t.x, t.y), sn = pack2(t.z, t.w), x = f[part], y = f[kParts + part];
                         f[part] = fma2(y, pack2(-t.z, -t.w), mul2(x, c));
-                        f[4 + part] = fma2(x, sn, mul2(y, c));
+                        f[kParts + part] = fma2(x, sn, mul2(y, c));
                     }
                 }
             }
-            oa = make_uint4(narrow2<F16>(f[0]), narrow2<F16>(f[1]), narrow2<F16>(f[2]), narrow2<F16>(f[3]));
-            ob = make_uint4(narrow2<F16>(f[4]), narrow2<F16>(f[5]), narrow2<F16>(f[6]), narrow2<F16>(f[7]));
+#pragma unroll
+            for (int e = 0; e < kParts; ++e) {
+                va.w[e] = narrow2<F16>(f[e]);
+                vb.w[e] = narrow2<F16>(f[kParts + e]);
+            }
         }
-        uint4* dst;
+        uint16_t* dst;
         if (h.row < Hq) {
-            dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) +
-                                           (t0 + h.token) * a.q_out.token_stride + h.row * a.q_out.head_stride);
+            dst = static_cast<uint16_t*>(const_cast<void*>(a.q_out.data)) + (t0 + h.token) * a.q_out.token_stride +
+                  h.row * a.q_out.head_stride;
         } else {
             const int64_t at = s_at[h.token];
             if (at < 0) continue;
             const bool key = h.row < Hq + Hk;
-            dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(key ? a.cache.k : a.cache.v) + at +
-                                           (h.row - (key ? Hq : Hq + Hk)) * a.cache.head_stride);
+            dst = static_cast<uint16_t*>(key ? a.cache.k : a.cache.v) + at + (h.row - (key ? Hq : Hq + Hk)) * a.cache.head_stride;
         }
-        if (has_a) dst[va_at] = oa;
-        if (has_b) dst[vb_at] = ob;
+        if (has_a) store_packed<E>(dst + va_at * E, va);
+        if (has_b) store_packed<E>(dst + vb_at * E, vb);
     }
 }
 
-// Halves that lie apart by no multiple of 8 entries: a warp takes a head, entry by entry, and
+// Halves that lie apart by an odd number of entries: a warp takes a head, entry by entry, and
 // gets the partners' values by a second read of them; it has read all before it writes any.
 template <bool F16>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_entries_kernel(const __grid_constant__ NormRopeArgs n,
@@ -268,13 +300,9 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_entries_kernel(const _
     }
 }
 
-template <bool F16, bool SIDE, int ITEMS>
+template <bool F16, bool SIDE, int ITEMS, int E>
 void launch_items(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
 {
-    if (g.items != ITEMS) {
-        if constexpr (ITEMS > 1) launch_items<F16, SIDE, ITEMS - 1>(n, g, stream);
-        return;
-    }
     constexpr int kGroups = kRopeThreads / 32 * (32 / ITEMS);
     const int64_t T = n.rope.q.tokens;
     const int sms = device_sm_count();
@@ -285,7 +313,33 @@ void launch_items(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
     const int64_t want = cdiv(2 * sms, T);
     const dim3 grid(static_cast<unsigned>(cdiv(T, g.tokens)),
                     static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
-    norm_rope_kernel<F16, SIDE, ITEMS><<<grid, kRopeThreads, 0, stream>>>(n, g);
+    norm_rope_kernel<F16, SIDE, ITEMS, E><<<grid, kRopeThreads, 0, stream>>>(n, g);
+}
+
+// The lanes that a head's vectors fill, for vectors of 8 entries.
+template <bool F16, bool SIDE, int ITEMS>
+void launch_eights(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
+{
+    if (g.items == ITEMS)
+        launch_items<F16, SIDE, ITEMS, 8>(n, g, stream);
+    else if constexpr (ITEMS > 1)
+        launch_eights<F16, SIDE, ITEMS - 1>(n, g, stream);
+}
+
+// Halves that lie apart by a multiple of 4 or of 2 entries: a power of two of lanes.  4,160 tokens, 28 + 4 heads of 96
+// with 24 rotated take 20 us, of 80 with 20 rotated 28, where an entry at a time takes 37 for either.
+template <bool F16>
+void launch_shorter(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
+{
+    const bool fours = g.half % 4 == 0, small = n.rope.cache.head_dim <= SV_MAX_HEAD_DIM / 2;
+    if (fours && small)
+        launch_items<F16, false, SV_MAX_HEAD_DIM / 16, 4>(n, g, stream);
+    else if (fours)
+        launch_items<F16, false, SV_MAX_HEAD_DIM / 8, 4>(n, g, stream);
+    else if (small)
+        launch_items<F16, false, SV_MAX_HEAD_DIM / 8, 2>(n, g, stream);
+    else
+        launch_items<F16, false, SV_MAX_HEAD_DIM / 4, 2>(n, g, stream);
 }
 
 }  // namespace
@@ -302,7 +356,7 @@ cudaError_t launch_norm_rope_cache(const NormRopeArgs& n, cudaStream_t stream)
     const int sms = device_sm_count();
     const bool f16 = a.cache.dtype == SV_F16;
     auto cdiv = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-    if (!a.interleaved && g.half % 8 != 0) {
+    if (!a.interleaved && g.half % 2 != 0) {
         const int64_t most = cdiv(g.rows, kRopeThreads / 32), want = cdiv(8 * sms, a.q.tokens);
         const dim3 grid(static_cast<unsigned>(a.q.tokens), static_cast<unsigned>(std::max<int64_t>(1, std::min(want, most))));
         if (f16)
@@ -314,14 +368,19 @@ cudaError_t launch_norm_rope_cache(const NormRopeArgs& n, cudaStream_t stream)
     constexpr int kMost = SV_MAX_HEAD_DIM / 16;
     if (a.interleaved) {
         if (f16)
-            launch_items<true, true, kMost>(n, g, stream);
+            launch_eights<true, true, kMost>(n, g, stream);
         else
-            launch_items<false, true, kMost>(n, g, stream);
+            launch_eights<false, true, kMost>(n, g, stream);
+    } else if (g.half % 8 == 0) {
+        if (f16)
+            launch_eights<true, false, kMost>(n, g, stream);
+        else
+            launch_eights<false, false, kMost>(n, g, stream);
     } else {
         if (f16)
-            launch_items<true, false, kMost>(n, g, stream);
+            launch_shorter<true>(n, g, stream);
         else
-            launch_items<false, false, kMost>(n, g, stream);
+            launch_shorter<false>(n, g, stream);
     }
     return cudaGetLastError();
 }

@@ -73,7 +73,9 @@ def _check(sv, T, Hq, Hk, D, rot, interleaved, dtype, kind="own", eps=1e-6, fuse
 @pytest.mark.parametrize("T,Hq,Hk,D,rot", [
     (1, 1, 1, 8, 8), (1, 32, 8, 128, 128), (9, 28, 4, 128, 64), (65, 6, 3, 96, 96), (33, 5, 5, 80, 20),
     (17, 4, 2, 64, 0), (40, 8, 1, 72, 36), (300, 3, 3, 16, 2), (5, 64, 2, 128, 48), (7, 2, 1, 24, 24), (5000, 3, 1, 40, 32),
-    (6, 1, 1, 16, 16), (6, 2, 2, 32, 32), (20000, 1, 1, 8, 0), (4863, 2, 1, 104, 64), (4864, 1, 2, 48, 48)])
+    (6, 1, 1, 16, 16), (6, 2, 2, 32, 32), (20000, 1, 1, 8, 0), (4863, 2, 1, 104, 64), (4864, 1, 2, 48, 48),
+    (50, 4, 2, 128, 88), (50, 4, 2, 64, 40), (50, 4, 2, 120, 60), (50, 4, 2, 56, 44), (3000, 3, 1, 72, 72), (3000, 3, 1, 88, 46),
+    (31, 2, 1, 8, 4), (31, 2, 1, 128, 4)])
 def test_norm_rope(sv, T, Hq, Hk, D, rot, interleaved, dtype):
     _check(sv, T, Hq, Hk, D, rot, interleaved, dtype, kind=("own", "float", "none")[T % 3], fused=T != 65,
            head_major=T == 33, mscale=1.0 if T != 9 else 1.2772588722239782)
