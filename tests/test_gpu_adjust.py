@@ -107,7 +107,11 @@ class Case:
     (1, 0, 1, 1, 3, 1, "own"), (1, 0, 1, 151936, 777, 0, None), (3, 1, 1, 31, 9, 4, "own"), (5, 8, 1, 4096, 300, 16, "few"),
     (2, 16, 2, 32003, 500, 100, "own"), (7, 4, 8, 1000, 60, 3, "few"), (40, 3, 1, 8191, 40, 0, "own"),
     (3, 256, 8, 257, 1500, 7, "few"), (200, 0, 1, 5000, 20, 5, None), (2, 3, 1, 1023, 0, 0, "own"),
-    (1, 5, 1, 200001, 4000, 300, "few"), (30, 2, 1, 16385, 100, 2000, None)])
+    (1, 5, 1, 200001, 4000, 300, "few"), (30, 2, 1, 16385, 100, 2000, None),
+    (40, 1, 1, 5000, 60, 5000, "few"),      # more biases than 16 bits count
+    (3, 2, 1, 9001, 8195, 9, "own"),        # long rows of history that start anywhere
+    (40, 1, 1, 140001, 600, 20, "few"),     # the wide slices of one or two rows
+    (160, 0, 1, 40008, 4100, 3, "own")])
 def test_adjust(sv, R, k, branches, V, width, biases, masks, dtype):
     Case(R, k, branches, V, dtype, width, biases, masks, seed=V + R).check(sv)
 
