@@ -843,6 +843,8 @@ def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=Non
         rules.bias_start, rules.bias_id = _ints(start, "the biases' start", R + 1), _ints(ids, "the biases' ids")
         rules.bias_entries = n = ids.numel()
         rules.bias_value = _floats(values, "the biases' values", n)
+    if mask is None and mask_row is not None:
+        raise ValueError("mask_row says which mask a row has: there are none")
     if mask is not None:
         if mask.dim() != 2:
             raise ValueError("mask must be [masks, words]")

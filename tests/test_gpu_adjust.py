@@ -189,6 +189,10 @@ def test_rules_one_at_a_time(sv):
         c = Case(3, 2, 2, 2050, torch.bfloat16, seed=13)
         setattr(c, name, None)
         c.check(sv)
+        c = Case(3, 2, 2, 2050, torch.bfloat16, masks="few", seed=13)
+        if name != "mask":
+            setattr(c, name, None)
+        c.check(sv)
         c = Case(3, 2, 2, 2050, torch.bfloat16, seed=14)
         for other in ("prompt_len", "repetition", "presence", "frequency", "bias", "mask"):
             if other != name:
@@ -367,6 +371,8 @@ def test_refusals(sv):
         call(mask=kw["mask"][:5].contiguous())     # neither a mask for each row nor their numbers
     with pytest.raises(ValueError, match="mask_row"):
         call(mask_row=_i32([0]))
+    with pytest.raises(ValueError, match="mask_row"):
+        call(mask=None, mask_row=_i32([0] * 8))
     status = torch.empty(2, dtype=torch.int32, device="cuda")
     with pytest.raises(sv.SpecVerifyError):
         call(out=dict(logits=torch.empty_like(x, dtype=torch.bfloat16), status=status))
