@@ -38,7 +38,6 @@ constexpr int kAdjVecs = 4;                      // 16-byte vectors of a tile th
 constexpr int kAdjTile = kAdjVecs * 32 * 16;     // bytes of a tile: a region of a row
 constexpr int kAdjStages = 2;                    // tiles of a warp's ring: one on its way, one in hand
 constexpr int kAdjSlice = 4096;                  // most ids of a slice
-constexpr int kAdjFewSlice = 8192, kAdjFewRows = 2;  // of one with few rows behind it, and how many those are
 constexpr int kAdjEdge = 8;                      // ids before a slice that a row which starts within a vector needs
 constexpr int kAdjTokens = 16;                   // tokens of a thread that are brought at a time
 constexpr int kAdjMaskWords = kAdjTile / 2 / 32 + 1;  // words of a region's mask
@@ -48,9 +47,8 @@ constexpr uint32_t kAdjSeen = 1u << 31, kAdjHeadShift = 19, kAdjHead = 0xFFFu <<
                    kAdjCount = (1u << kAdjHeadShift) - 1;
 static_assert(SV_MAX_HISTORY <= (1 << kAdjHeadShift) - 1, "a count must not reach the chain's head");
 static_assert(SV_MAX_BRANCHES * SV_MAX_K < (1 << 12), "a draft's number must fit the head");
-static_assert(kAdjSlice / (kAdjTile / 4) <= kAdjWarps && kAdjFewSlice / (kAdjTile / 2) <= kAdjWarps,
-              "a warp keeps to one region, and a region has a warp");
-static_assert(kAdjFewSlice <= kAdjThreads * 32, "a thread lists 32 ids");
+static_assert(kAdjSlice / (kAdjTile / 4) <= kAdjWarps, "a warp keeps to one region, and a region has a warp");
+static_assert(kAdjSlice <= kAdjThreads * 32, "a thread lists 32 ids");
 static_assert(kAdjTokens == 16, "a thread reads its tokens four at a time, and 16 bits say which are the slice's");
 static_assert(kAdjTokens * 32 * 4 <= kAdjTile, "a warp's tokens wait in a tile");
 static_assert(kAdjMaskWords >= 33, "a warp brings 33 words of a mask");
@@ -138,6 +136,54 @@ __device__ __forceinline__ uint4 masked(uint4 v, uint32_t m)
     const uint32_t k0 = signs<0x9988>(lo), k1 = signs<0xBBAA>(lo), k2 = signs<0x9988>(hi), k3 = signs<0xBBAA>(hi);
     return make_uint4((v.x & k0) | (0xFF80FF80u & ~k0), (v.y & k1) | (0xFF80FF80u & ~k1), (v.z & k2) | (0xFF80FF80u & ~k2),
                       (v.w & k3) | (0xFF80FF80u & ~k3));
+}
+
+// What a request asks for, and what of it is done: what cannot be asked for is left out or cut.
+struct Rules {
+    int32_t len, prompt, b0, b1;
+    float rep, pres, freq;
+};
+__device__ __forceinline__ Rules asked_of(const AdjustArgs& a, int32_t r)
+{
+    const sv_logit_rules& u = a.rules;
+    Rules q;
+    q.len = u.history != nullptr ? u.history_len[r] : 0;
+    q.prompt = u.history != nullptr && u.prompt_len != nullptr ? u.prompt_len[r] : 0;
+    q.b0 = u.bias_entries != 0 ? u.bias_start[r] : 0;
+    q.b1 = u.bias_entries != 0 ? u.bias_start[r + 1] : 0;
+    q.rep = u.repetition != nullptr ? u.repetition[r] : 1.0f;
+    q.pres = u.presence != nullptr ? u.presence[r] : 0.0f;
+    q.freq = u.frequency != nullptr ? u.frequency[r] : 0.0f;
+    return q;
+}
+__device__ __forceinline__ Rules rules_of(const AdjustArgs& a, const Rules& q, uint32_t& st)
+{
+    const sv_logit_rules& u = a.rules;
+    Rules o;
+    o.b0 = min(max(q.b0, 0), u.bias_entries);
+    o.b1 = min(max(q.b1, o.b0), u.bias_entries);
+    o.len = min(max(q.len, 0), u.history_width);
+    o.prompt = min(max(q.prompt, 0), o.len);
+    if (o.len != q.len || o.prompt != q.prompt || o.b0 != q.b0 || o.b1 != q.b1) st |= SV_ST_BAD_LENGTH;
+    const bool rep_ok = q.rep > 0.0f && !isinf(q.rep), pres_ok = isfinite(q.pres), freq_ok = isfinite(q.freq);
+    o.rep = rep_ok ? q.rep : 1.0f;
+    o.pres = pres_ok ? q.pres : 0.0f;
+    o.freq = freq_ok ? q.freq : 0.0f;
+    if (!rep_ok || !pres_ok || !freq_ok) st |= SV_ST_BAD_PENALTY;
+    return o;
+}
+
+// An entry whose id stands `count` times in the output and, if `seen`, in the prompt; `bias` may be null.
+template <typename T>
+__device__ __forceinline__ T adjust(T raw, bool seen, uint32_t count, const float* bias, const Rules& ru)
+{
+    seen = seen || count != 0;
+    if (!seen && bias == nullptr) return raw;
+    float z = widen<T>(raw);
+    if (seen) z = z > 0.0f ? z / ru.rep : z * ru.rep;
+    if (count != 0) z -= ru.pres + ru.freq * static_cast<float>(count);
+    if (bias != nullptr) z += *bias;
+    return narrow<T>(z);
 }
 
 // ---- asynchronous copies to shared memory --------------------------------------
@@ -267,12 +313,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
     const int32_t* draft = a.draft + static_cast<int64_t>(r) * g.drafts;
     const int32_t first_draft = tid < g.drafts ? draft[tid] : 0;
     const int32_t first_mask = COPY ? asked_mask(j0) : 0, row_mask = asked_mask(tid);
-    const int32_t asked_len = u.history != nullptr ? u.history_len[r] : 0;
-    const int32_t asked_prompt = u.history != nullptr && u.prompt_len != nullptr ? u.prompt_len[r] : 0;
-    const int32_t asked_b0 = biased ? u.bias_start[r] : 0, asked_b1 = biased ? u.bias_start[r + 1] : 0;
-    float rep = u.repetition != nullptr ? u.repetition[r] : 1.0f;
-    float pres = u.presence != nullptr ? u.presence[r] : 0.0f;
-    float freq = u.frequency != nullptr ? u.frequency[r] : 0.0f;
+    const Rules asked = asked_of(a, r);
     for (int i = tid; i < (at.row - at.tab) / 4; i += kAdjThreads)
         reinterpret_cast<uint4*>(s_tab)[i] = make_uint4(0, 0, 0, 0);
     if (tid < kAdjWarps) s_listed[tid] = 0;
@@ -283,24 +324,10 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
     copies_commit();
     __syncthreads();
 
-    // what cannot be asked for is left out or cut
     uint32_t st = 0;
-    const int32_t b0 = min(max(asked_b0, 0), u.bias_entries), b1 = min(max(asked_b1, b0), u.bias_entries);
+    const Rules ru = rules_of(a, asked, st);
+    const int32_t b0 = ru.b0, b1 = ru.b1, len = ru.len, prompt = ru.prompt;
     const int32_t first_bias = b0 + tid < b1 ? u.bias_id[b0 + tid] : 0;
-    const int32_t len = min(max(asked_len, 0), u.history_width), prompt = min(max(asked_prompt, 0), len);
-    if (len != asked_len || prompt != asked_prompt || b0 != asked_b0 || b1 != asked_b1) st |= SV_ST_BAD_LENGTH;
-    if (!(rep > 0.0f) || isinf(rep)) {
-        rep = 1.0f;
-        st |= SV_ST_BAD_PENALTY;
-    }
-    if (!isfinite(pres)) {
-        pres = 0.0f;
-        st |= SV_ST_BAD_PENALTY;
-    }
-    if (!isfinite(freq)) {
-        freq = 0.0f;
-        st |= SV_ST_BAD_PENALTY;
-    }
 
     // Tokens of the vocabulary that are the slice's: low .. low + span - 1.
     const bool tells = s == 0 && group == 0 && a.status != nullptr;
@@ -416,13 +443,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
         for (uint32_t e = (word & kAdjHead) >> kAdjHeadShift; e != 0; e = s_next[e - 1])
             count += static_cast<int32_t>(e) > s_row[j].y && static_cast<int32_t>(e) <= row0 + j;
         const uint32_t entry = bias_of(l);
-        const bool seen = (word & kAdjSeen) != 0 || count != 0;
-        if (!seen && entry == 0) return raw;
-        float z = widen<T>(raw);
-        if (seen) z = z > 0.0f ? z / rep : z * rep;
-        if (count != 0) z -= pres + freq * static_cast<float>(count);
-        if (entry != 0) z += u.bias_value[entry - 1];
-        return narrow<T>(z);
+        return adjust<T>(raw, (word & kAdjSeen) != 0, count, entry != 0 ? &u.bias_value[entry - 1] : nullptr, ru);
     };
     const uint16_t* list = s_list + region * (kRegion + kAdjEdge);
     const int32_t listed = s_listed[region];
@@ -562,6 +583,304 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
     }
 }
 
+// ---- requests of few rows -------------------------------------------------------
+// A table that has a word for every id of a slice costs more than a row or two behind it.  Here a thread block takes a
+// long slice, and its table has words only for the ids that a rule meets: they are marked in a bit map first, and an
+// id's place is the number of marks before it, from the marks before its word and those of its word.  Then the tokens
+// are counted, the rows are copied and masked, and the marked entries are written once more from what they were.  Where
+// more ids are marked than the table has words, they are taken in windows, with the tokens gone through for each.
+//
+// 256 requests of one row of 151,936 bf16 logits with 500 to 8,000 tokens take 42 us so, 31 in place and 20 without
+// masks, and 88, 86 and 75 with a word for every id of 8,192 (the copy's bytes alone: 24).  A call of up to 100 tokens a
+// request takes 35, 22 and 9.  What is left: 256 blocks do not fill 152 SMs evenly, and a block's steps wait for one
+// another.  512 threads, two blocks an SM, each with as much of a row as lets all
+// blocks be resident at once: with 1,024 and one block 47, 256 and four 65, three blocks an SM 54, slices of which four
+// times as many blocks would be resident 57.  Entries met and tokens brought two or four at a time spill or save nothing
+// (43 and 46).
+constexpr int kFewThreads = 512;
+constexpr int kFewBlocks = 2;      // an SM
+constexpr int kFewSlice = 262144;  // most ids of a slice, and the least where there are few
+constexpr int kFewLeast = 8192;
+constexpr int kFewTable = 4096;    // most words of a table
+constexpr int kFewVecs = 4;        // vectors of a row that a thread moves at a time
+// Most rows of a request, out of place and in place: 256 requests of three rows take 107 us so and 119 with the other
+// kernel, 64 of four 48 and 42; in place 64 of four 29 and 36, of eight 55 and 58, and 64 of 33 rows of 32,000 79 and 53.
+constexpr int kFewRows = 3, kFewRowsInPlace = 8;
+
+struct FewGeom {
+    int32_t slice, slices;
+    int32_t rows, drafts;
+    int32_t table;  // words
+};
+
+struct FewLayout {
+    int32_t tab, bias, rank, list, next, row, bytes;  // next holds 16 bits each; the bits lie first
+};
+__host__ __device__ inline FewLayout few_layout(const FewGeom& g, bool biased)
+{
+    const int32_t words = g.slice / 32 + 1;
+    FewLayout l;
+    l.tab = (words + 3) / 4 * 4;
+    l.bias = l.tab + g.table;
+    l.rank = l.bias + (biased ? g.table : 0);
+    l.list = l.rank + words;
+    l.next = l.list + g.table;
+    l.row = l.next + (g.drafts + 1) / 2;
+    l.bytes = 4 * (l.row + g.rows);
+    return l;
+}
+
+enum class Lie { InPlace, Alike, Apart };  // Apart: they start differently within 16 bytes
+
+template <typename T, Lie HOW>
+__global__ void __launch_bounds__(kFewThreads, kFewBlocks) adjust_few_kernel(const __grid_constant__ AdjustArgs a, const FewGeom g)
+{
+    constexpr int kPer = 16 / sizeof(T);
+    constexpr uint32_t kAll = (1u << kPer) - 1;
+    extern __shared__ __align__(16) uint32_t s_mem[];
+    __shared__ int32_t s_warp[kFewThreads / 32];
+    const sv_logit_rules& u = a.rules;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t V = a.in.width, words = g.slice / 32 + 1;
+    const bool biased = u.bias_entries != 0;
+    const FewLayout at = few_layout(g, biased);
+    uint32_t* s_bits = s_mem;
+    uint32_t* s_tab = s_mem + at.tab;
+    uint32_t* s_bias = s_mem + at.bias;
+    int32_t* s_rank = reinterpret_cast<int32_t*>(s_mem + at.rank);
+    int32_t* s_list = reinterpret_cast<int32_t*>(s_mem + at.list);
+    uint16_t* s_next = reinterpret_cast<uint16_t*>(s_mem + at.next);
+    int32_t* s_row = reinterpret_cast<int32_t*>(s_mem + at.row);  // each row's mask, -1 for none
+
+    const int32_t s = static_cast<int32_t>(blockIdx.x % g.slices), r = static_cast<int32_t>(blockIdx.x / g.slices);
+    const int32_t s0 = s * g.slice, base = s0 - 32;  // id of the first bit
+    const int64_t first = static_cast<int64_t>(r) * g.rows;
+    const T* in = reinterpret_cast<const T*>(a.in.data) + first * a.in.stride;
+    T* out = reinterpret_cast<T*>(const_cast<char*>(a.out.data)) + first * a.out.stride;
+    // The id of a row's first entry of the slice: rows may start within 16 bytes.
+    auto start_of = [&](const T* row) -> int32_t {
+        return HOW == Lie::Apart ? s0 : s0 - (static_cast<int32_t>(reinterpret_cast<uintptr_t>(row)) & 15) / static_cast<int32_t>(sizeof(T));
+    };
+    auto mask_at = [&](int32_t i) -> const uint32_t* {
+        return i < 0 ? nullptr : u.mask + static_cast<int64_t>(i) * u.mask_words;
+    };
+    const int32_t* history = u.history + static_cast<int64_t>(r) * u.history_width;
+    const bool by_four = (reinterpret_cast<uintptr_t>(history) & 15) == 0;
+    const int32_t* draft = a.draft + static_cast<int64_t>(r) * g.drafts;
+    const Rules asked = asked_of(a, r);
+    for (int32_t i = tid; i < words; i += kFewThreads) s_bits[i] = 0;
+    bool over = false;
+    for (int32_t j = tid; j < g.rows; j += kFewThreads) {
+        const int64_t i = u.mask == nullptr ? -1 : u.mask_row != nullptr ? u.mask_row[first + j] : first + j;
+        over = over || (u.mask != nullptr && u.mask_row != nullptr && i >= u.masks);
+        s_row[j] = i >= 0 && i < u.masks ? static_cast<int32_t>(i) : -1;
+    }
+    __syncthreads();
+
+    // The rows, masked.
+    auto stream = [&]() {
+        for (int32_t j = 0; j < g.rows; ++j) {
+            const T* src = in + j * a.in.stride;
+            T* dst = out + j * a.out.stride;
+            const uint32_t* mask = mask_at(s_row[j]);
+            if (HOW == Lie::InPlace && mask == nullptr) continue;
+            if (HOW == Lie::Apart) {
+#pragma unroll 8
+                for (int32_t x = s0 + tid; x < min(s0 + g.slice, V); x += kFewThreads)
+                    dst[x] = allowed(mask, x) ? src[x] : kNegInf<T>;
+                continue;
+            }
+            const int32_t x0 = start_of(dst);
+            // a warp's vectors lie side by side, and each lane has 32 of their ids' bits
+            constexpr int kSpan = kFewVecs * 32 * kPer;
+            for (int32_t n = warp * kSpan; n < g.slice; n += kFewThreads / 32 * kSpan) {
+                const int32_t x0 = start_of(dst) + n;
+                const bool inside = x0 >= 0 && x0 + kSpan <= V;
+                uint4 v[kFewVecs];
+                uint32_t m[kFewVecs];
+                const T* from = src + x0 + lane * kPer;
+                T* to = dst + x0 + lane * kPer;
+                if (HOW == Lie::Alike && inside) {
+#pragma unroll
+                    for (int q = 0; q < kFewVecs; ++q) v[q] = *reinterpret_cast<const uint4*>(from + q * 32 * kPer);
+                }
+                uint32_t bits = 0xFFFFFFFFu;
+                if (mask != nullptr) {
+                    const int32_t word = (x0 >> 5) + lane;
+                    uint32_t lo = 0, hi = 0;
+                    if (word >= 0 && word < u.mask_words) lo = mask[word];
+                    if ((x0 & 31) != 0 && word + 1 < u.mask_words) hi = mask[word + 1];
+                    bits = __funnelshift_r(lo, hi, x0 & 31);
+                }
+#pragma unroll
+                for (int q = 0; q < kFewVecs; ++q)
+                    m[q] = (__shfl_sync(0xFFFFFFFFu, bits, q * kPer + lane * kPer / 32) >> (lane * kPer % 32)) & kAll;
+                if (inside) {
+                    if (HOW == Lie::InPlace) {  // what is masked or stays need not be read
+#pragma unroll
+                        for (int q = 0; q < kFewVecs; ++q)
+                            if (m[q] != 0u && m[q] != kAll) v[q] = *reinterpret_cast<const uint4*>(from + q * 32 * kPer);
+                    }
+#pragma unroll
+                    for (int q = 0; q < kFewVecs; ++q)
+                        if (HOW == Lie::Alike || m[q] != kAll) *reinterpret_cast<uint4*>(to + q * 32 * kPer) = masked<T>(v[q], m[q]);
+                    continue;
+                }
+#pragma unroll
+                for (int q = 0; q < kFewVecs; ++q) {
+                    const int32_t x = x0 + (q * 32 + lane) * kPer;
+#pragma unroll 1
+                    for (int32_t y = max(x, 0); y < min(x + kPer, V); ++y) {
+                        if (!((m[q] >> (y - x)) & 1u))
+                            dst[y] = kNegInf<T>;
+                        else if (HOW == Lie::Alike)
+                            dst[y] = src[y];
+                    }
+                }
+            }
+        }
+    };
+    // Half of the blocks copy first, so that some copy while others count: 256 rows take 42 us so, 44 where all copy first or
+    // last.  In place little is copied: 31 and 20 us where all begin with it, 32 and 21 where half do.
+    const bool early = HOW == Lie::InPlace || blockIdx.x < gridDim.x / 2;
+    if (early) stream();
+
+    uint32_t st = 0;
+    const Rules ru = rules_of(a, asked, st);
+    const bool tells = s == 0 && a.status != nullptr;
+    const int32_t low = max(s0 - kAdjEdge, 0);
+    const uint32_t span = static_cast<uint32_t>(max(min(s0 + g.slice, V) - low, 0));
+    bool outside = false;
+    auto each_token = [&](auto&& f) {
+        if (by_four) {
+            const int32_t fours = ru.len / 4;
+            for (int32_t i = tid; i < fours; i += kFewThreads) {
+                const int4 x = reinterpret_cast<const int4*>(history)[i];
+                f(4 * i, x.x);
+                f(4 * i + 1, x.y);
+                f(4 * i + 2, x.z);
+                f(4 * i + 3, x.w);
+            }
+            const int32_t i = 4 * fours + tid;
+            if (i < ru.len) f(i, history[i]);
+        } else {
+            for (int32_t i = tid; i < ru.len; i += kFewThreads) f(i, history[i]);
+        }
+    };
+    auto mark = [&](int32_t x) {
+        if (static_cast<uint32_t>(x - low) < span) atomicOr(&s_bits[(x - base) >> 5], 1u << (x & 31));
+    };
+    each_token([&](int32_t, int32_t x) {
+        outside = outside || static_cast<uint32_t>(x) >= static_cast<uint32_t>(V);
+        mark(x);
+    });
+    for (int32_t i = tid; i < g.drafts; i += kFewThreads) {
+        const int32_t x = draft[i];
+        outside = outside || static_cast<uint32_t>(x) >= static_cast<uint32_t>(V);
+        mark(x);
+    }
+    for (int32_t i = ru.b0 + tid; i < ru.b1; i += kFewThreads) {
+        const int32_t x = u.bias_id[i];
+        outside = outside || static_cast<uint32_t>(x) >= static_cast<uint32_t>(V);
+        mark(x);
+    }
+    if (tells) {
+        if (__syncthreads_or(outside)) st |= SV_ST_TOKEN_RANGE;
+        if (__syncthreads_or(over)) st |= SV_ST_BAD_MASK;
+        if (tid == 0) a.status[r] = static_cast<int32_t>(st);
+    }
+    __syncthreads();
+
+    // how many ids are marked before each word
+    const int32_t share = (words + kFewThreads - 1) / kFewThreads, w0 = min(tid * share, words), w1 = min(w0 + share, words);
+    int32_t mine = 0;
+    for (int32_t w = w0; w < w1; ++w) mine += __popc(s_bits[w]);
+    int32_t before = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int32_t o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        if (lane >= d) before += o;
+    }
+    if (lane == 31) s_warp[warp] = before;
+    __syncthreads();
+    int32_t ids = 0;
+    before -= mine;
+    for (int w = 0; w < kFewThreads / 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        ids += s_warp[w];
+    }
+    for (int32_t w = w0; w < w1; ++w) {
+        s_rank[w] = before;
+        before += __popc(s_bits[w]);
+    }
+
+    bool streamed = early;
+    for (int32_t from = 0; from < ids || !streamed; from += g.table) {
+        const int32_t n = max(min(ids - from, g.table), 0);
+        for (int32_t i = tid; i < n; i += kFewThreads) {
+            s_tab[i] = 0;
+            if (biased) s_bias[i] = 0;
+        }
+        __syncthreads();
+        // an id's place in the window, at least n for none
+        auto place = [&](int32_t x) -> uint32_t {
+            if (static_cast<uint32_t>(x - low) >= span) return 0xFFFFFFFFu;
+            const int32_t w = (x - base) >> 5;
+            return static_cast<uint32_t>(s_rank[w] + __popc(s_bits[w] & ((1u << (x & 31)) - 1)) - from);
+        };
+        const uint32_t limit = static_cast<uint32_t>(n);
+        for (int32_t w = tid; w < words; w += kFewThreads) {
+            uint32_t p = static_cast<uint32_t>(s_rank[w] - from);
+            for (uint32_t b = s_bits[w]; b != 0; b &= b - 1, ++p)
+                if (p < limit) s_list[p] = 32 * w + __ffs(b) - 1;
+        }
+        each_token([&](int32_t i, int32_t x) {
+            const uint32_t p = place(x);
+            if (p >= limit) return;
+            if (i >= ru.prompt)
+                atomicAdd(&s_tab[p], 1u);
+            else
+                atomicOr(&s_tab[p], kAdjSeen);
+        });
+        for (int32_t i = tid; i < g.drafts; i += kFewThreads) {
+            const uint32_t p = place(draft[i]);
+            if (p >= limit) continue;
+            uint32_t old = s_tab[p], was;
+            do {
+                was = old;
+                s_next[i] = static_cast<uint16_t>((was & kAdjHead) >> kAdjHeadShift);
+                old = atomicCAS(&s_tab[p], was, (was & ~kAdjHead) | (static_cast<uint32_t>(i + 1) << kAdjHeadShift));
+            } while (old != was);
+        }
+        for (int32_t i = ru.b0 + tid; i < ru.b1; i += kFewThreads) {
+            const uint32_t p = place(u.bias_id[i]);
+            if (p < limit) atomicMax(&s_bias[p], static_cast<uint32_t>(i) + 1);
+        }
+        if (!streamed) stream();
+        streamed = true;
+        __syncthreads();
+        for (int32_t j = 0; j < g.rows; ++j) {
+            const T* src = in + j * a.in.stride;
+            T* dst = out + j * a.out.stride;
+            const uint32_t* mask = mask_at(s_row[j]);
+            const int32_t start = start_of(dst), end = min(start + g.slice, V);
+            const int32_t before_branch = j > 0 ? (j - 1) / a.k * a.k : 0;
+            for (int32_t i = tid; i < n; i += kFewThreads) {
+                const int32_t x = base + s_list[i];
+                if (x < start || x >= end) continue;
+                const T raw = src[x];  // on its way while the mask's word is
+                if (!allowed(mask, x)) continue;
+                const uint32_t word = s_tab[i], entry = biased ? s_bias[i] : 0u;
+                uint32_t count = word & kAdjCount;
+                for (uint32_t e = (word & kAdjHead) >> kAdjHeadShift; e != 0; e = s_next[e - 1])
+                    count += static_cast<int32_t>(e) > before_branch && static_cast<int32_t>(e) <= j;
+                dst[x] = adjust<T>(raw, (word & kAdjSeen) != 0, count, entry != 0 ? &u.bias_value[entry - 1] : nullptr, ru);
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // Whether the rows of the two matrices start alike within 16 bytes, and are not the same ones.
 bool by_tiles(const AdjustArgs& a)
 {
@@ -578,9 +897,7 @@ AdjustGeom geom_of(const AdjustArgs& a)
     g.bias_bits = a.rules.bias_entries == 0 ? 0 : a.rules.bias_entries <= 0xFFFF ? 16 : 32;
     const int32_t region = kAdjTile / a.in.esize;
     auto slices = [&](int64_t n) { return (static_cast<int64_t>(a.in.width) + kAdjEdge - 1 + n - 1) / n; };
-    // a row or two are little work behind a table, and the request's tokens are looked through for every slice: 256 rows
-    // of 256 requests take 88 us with slices of 8,192 bf16 entries and 103 with 4,096; four rows each 36 and 39
-    g.slice = g.rows <= kAdjFewRows ? std::min(kAdjFewSlice, kAdjWarps * region) : kAdjSlice;
+    g.slice = kAdjSlice;
     while (g.slice > region && a.R * slices(g.slice) < 4 * sms) g.slice /= 2;
     while ((region << g.region_shift) < g.slice) ++g.region_shift;
     g.slices = static_cast<int32_t>(slices(g.slice));
@@ -590,18 +907,55 @@ AdjustGeom geom_of(const AdjustArgs& a)
     return g;
 }
 
+// Whether a call's requests have few rows, and are so many that the other kernel's blocks would not all be resident at
+// once: 16 requests of one row take 9.0 us with that one and 9.6 with this (in place 7.2 and 8.7), 24 take 10.1 and 10.2 (10.7
+// and 8.7), 64 26 and 18 (25 and 16).
+bool few_rows(const AdjustArgs& a, const AdjustGeom& g)
+{
+    return g.rows <= (a.in.data == a.out.data ? kFewRowsInPlace : kFewRows) &&
+           static_cast<int64_t>(a.R) * g.slices > 4 * std::max(1, device_sm_count());
+}
+
+FewGeom few_geom_of(const AdjustArgs& a)
+{
+    const int sms = std::max(1, device_sm_count());
+    FewGeom g{};
+    g.drafts = a.branches * a.k;
+    g.rows = 1 + g.drafts;
+    const int64_t ids = static_cast<int64_t>(a.in.width) + kAdjEdge - 1, span = kFewVecs * 32 * 8;  // a warp's vectors of bf16
+    const int64_t resident = std::max<int64_t>(1, kFewBlocks * sms / a.R);  // slices of a row
+    const int64_t slices = std::max((ids + kFewSlice - 1) / kFewSlice, std::min(resident, (ids + kFewLeast - 1) / kFewLeast));
+    g.slice = static_cast<int32_t>(((ids + slices - 1) / slices + span - 1) / span * span);
+    g.slices = static_cast<int32_t>((ids + g.slice - 1) / g.slice);
+    const int64_t met = static_cast<int64_t>(a.rules.history != nullptr ? a.rules.history_width : 0) + g.drafts + a.rules.bias_entries;
+    g.table = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({met, g.slice + kAdjEdge, kFewTable})));
+    return g;
+}
+
 }  // namespace
 
 bool adjust_fits(const AdjustArgs& a)
 {
     const AdjustGeom g = geom_of(a);
+    if (few_rows(a, g)) return static_cast<int64_t>(a.R) * few_geom_of(a).slices <= INT32_MAX;
     return static_cast<int64_t>(a.R) * g.slices * g.groups <= INT32_MAX;
 }
 
 cudaError_t launch_adjust_logits(const AdjustArgs& a, cudaStream_t stream)
 {
-    const AdjustGeom g = geom_of(a);
     const bool tiles = by_tiles(a), bf16 = a.in.dtype == SV_BF16;
+    const AdjustGeom g = geom_of(a);
+    if (few_rows(a, g)) {
+        const FewGeom f = few_geom_of(a);
+        const int bytes = few_layout(f, a.rules.bias_entries != 0).bytes;
+        const bool in_place = a.in.data == a.out.data;
+        auto* kernel = in_place ? bf16 ? adjust_few_kernel<uint16_t, Lie::InPlace> : adjust_few_kernel<uint32_t, Lie::InPlace>
+                       : tiles  ? bf16 ? adjust_few_kernel<uint16_t, Lie::Alike> : adjust_few_kernel<uint32_t, Lie::Alike>
+                                : bf16 ? adjust_few_kernel<uint16_t, Lie::Apart> : adjust_few_kernel<uint32_t, Lie::Apart>;
+        if (cudaError_t e = allow_shared(kernel, bytes)) return e;
+        kernel<<<static_cast<unsigned>(static_cast<int64_t>(a.R) * f.slices), kFewThreads, bytes, stream>>>(a, f);
+        return cudaGetLastError();
+    }
     const int bytes = layout_of(g, tiles).bytes;
     const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.R) * g.slices * g.groups);
     auto* kernel = tiles ? bf16 ? adjust_kernel<uint16_t, true> : adjust_kernel<uint32_t, true>
