@@ -244,14 +244,15 @@ cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t stream);
 // number of SMs of the current device
 int device_sm_count();
 
-// Dynamic shared memory above what every kernel may have has to be asked for.  Always the same size is: two
-// threads that launch a kernel with different ones must not take each other's back.
-constexpr int kMostShared = 220 * 1024;
+// Dynamic shared memory above what every kernel may have has to be asked for.  That is 48 KB less the kernel's static
+// shared memory, of which none that asks here has more than 1 KB.  Always the same size is: two threads that launch a
+// kernel with different ones must not take each other's back.
+constexpr int kFreeShared = 47 * 1024, kMostShared = 220 * 1024;
 template <typename Kernel>
 inline cudaError_t allow_shared(Kernel* kernel, int bytes)
 {
-    return bytes <= 48 * 1024 ? cudaSuccess
-                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    return bytes <= kFreeShared ? cudaSuccess
+                                : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
 }
 
 }  // namespace sv
