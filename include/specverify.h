@@ -663,9 +663,10 @@ int sv_cache_commit(sv_kv_cache cache, const int32_t* block_table, int32_t max_b
  *
  * In all three calls a seq_len outside [0, max_blocks * block_size] sets
  * SV_ST_BAD_LENGTH, and a held block id outside [0, num_blocks) SV_ST_BAD_BLOCK; that
- * entry is passed over.  The outputs must not overlap the inputs (one that is the other
- * is refused, SV_ERR_INVALID_ARG).  A call repeated on the same inputs writes the same
- * values, so caches that lie layer by layer in memory of their own take a call each.
+ * entry is passed over.  No array that is written may share a byte with another array of
+ * the call (SV_ERR_INVALID_ARG; the caches are not looked at).  A call repeated on the same
+ * inputs writes the same values, so caches that lie layer by layer in memory of their own
+ * take a call each.
  * Within a step (between sv_step_tables and sv_cache_commit) a request holds the blocks of
  * the larger of seq_len and kv_len: freeing and compacting then take that one.
  * ---------------------------------------------------------------------- */

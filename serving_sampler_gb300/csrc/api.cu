@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "specverify.h"
 #include "sv_internal.h"
@@ -100,6 +101,36 @@ static bool overlap(const Rows& a, const Rows& b, int64_t rows)
     if (rows == 1 || a.stride != b.stride) return true;
     const int64_t apart = ((b.data - a.data) % step + step) % step;  // columns of one wider matrix
     return apart < wide || apart + wide > step;
+}
+
+// An array of a call.
+struct Span {
+    const void* data;
+    int64_t bytes;
+};
+static Span ints(const void* p, int64_t n) { return Span{p, 4 * n}; }
+
+static bool meet(const Span& a, const Span& b)
+{
+    if (a.data == nullptr || b.data == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+    const char *x = static_cast<const char*>(a.data), *y = static_cast<const char*>(b.data);
+    return x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether one of `written` shares a byte with one of `read`, or two of `written` do.
+static bool over(std::initializer_list<Span> written, std::initializer_list<Span> read)
+{
+    for (const Span& w : written)
+        for (const Span& r : read)
+            if (meet(w, r)) return true;
+    return false;
+}
+static bool among(std::initializer_list<Span> written)
+{
+    for (const Span* a = written.begin(); a != written.end(); ++a)
+        for (const Span* b = a + 1; b != written.end(); ++b)
+            if (meet(*a, *b)) return true;
+    return false;
 }
 
 static bool have_device()
@@ -622,12 +653,16 @@ int sv_cache_fork(sv_kv_cache cache, int32_t* block_table, int32_t max_blocks, c
     if (seq_len == nullptr || source == nullptr || free_blocks == nullptr || free_count == nullptr ||
         seq_len_out == nullptr || free_count_out == nullptr || (max_blocks > 0 && block_table == nullptr))
         return SV_ERR_INVALID_ARG;
-    // other rows read what one row would write over
-    if (seq_len_out == seq_len || seq_len_out == source || free_count_out == free_count) return SV_ERR_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(source, 4) || !aligned(free_blocks, 4) ||
         !aligned(free_count, 4) || !aligned(seq_len_out, 4) || !aligned(free_count_out, 4) || !aligned(status, 4))
         return SV_ERR_ALIGN;
+    // other rows read what one row would write over
+    const Span table = ints(block_table, static_cast<int64_t>(R) * max_blocks), seq = ints(seq_len, R), from = ints(source, R),
+               stack = ints(free_blocks, cache.num_blocks), count = ints(free_count, 1), seq_out = ints(seq_len_out, R),
+               count_out = ints(free_count_out, 1), told = ints(status, R);
+    if (over({seq_out, count_out, told}, {table, seq, from, stack, count})) return SV_ERR_INVALID_ARG;
     if (!have_device()) return SV_ERR_DEVICE;
+    if (over({table}, {seq, from, stack, count}) || among({seq_out, count_out, told})) return SV_ERR_INVALID_ARG;
     return launched(launch_cache_fork(ForkArgs{cache, block_table, max_blocks, seq_len, R, source, free_blocks, free_count,
                                                divisor_of(cache.block_size), seq_len_out, free_count_out, status},
                                       stream));
@@ -643,11 +678,15 @@ int sv_cache_free(const int32_t* block_table, int32_t max_blocks, const int32_t*
     if (seq_len == nullptr || leave == nullptr || free_count == nullptr || seq_len_out == nullptr ||
         free_count_out == nullptr || (max_blocks > 0 && block_table == nullptr) || (num_blocks > 0 && free_blocks == nullptr))
         return SV_ERR_INVALID_ARG;
-    if (seq_len_out == seq_len || seq_len_out == leave || free_count_out == free_count) return SV_ERR_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(leave, 4) || !aligned(free_blocks, 4) ||
         !aligned(free_count, 4) || !aligned(seq_len_out, 4) || !aligned(free_count_out, 4) || !aligned(status, 4))
         return SV_ERR_ALIGN;
+    const Span table = ints(block_table, static_cast<int64_t>(R) * max_blocks), seq = ints(seq_len, R), gone = ints(leave, R),
+               stack = ints(free_blocks, num_blocks), count = ints(free_count, 1), seq_out = ints(seq_len_out, R),
+               count_out = ints(free_count_out, 1), told = ints(status, R);
+    if (over({seq_out, count_out, told}, {table, seq, gone, stack, count})) return SV_ERR_INVALID_ARG;
     if (!have_device()) return SV_ERR_DEVICE;
+    if (over({stack}, {table, seq, gone, count}) || among({seq_out, count_out, told})) return SV_ERR_INVALID_ARG;
     return launched(launch_cache_free(FreeArgs{block_table, max_blocks, seq_len, leave, R, block_size, num_blocks,
                                                divisor_of(block_size), free_blocks, free_count, seq_len_out,
                                                free_count_out, status},
@@ -671,12 +710,19 @@ int sv_cache_compact(sv_kv_cache cache, const int32_t* block_table, int32_t max_
     if (free_blocks == nullptr || free_count == nullptr || (R > 0 && seq_len == nullptr) ||
         (R > 0 && max_blocks > 0 && (block_table == nullptr || block_table_out == nullptr)))
         return SV_ERR_INVALID_ARG;
-    if (block_table != nullptr && block_table == block_table_out) return SV_ERR_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(block_table_out, 4) || !aligned(free_blocks, 4) ||
         !aligned(free_count, 4) || !aligned(status, 4))
         return SV_ERR_ALIGN;
-    if (int rc = check_workspace(workspace, workspace_bytes, compact_workspace_bytes(cache.num_blocks))) return rc;
+    const size_t need = compact_workspace_bytes(cache.num_blocks);
+    if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
+    // the second launch reads tables and lengths again, beside what it writes
+    const int64_t entries = static_cast<int64_t>(R) * max_blocks;
+    const Span table = ints(block_table, entries), seq = ints(seq_len, R), table_out = ints(block_table_out, entries),
+               stack = ints(free_blocks, cache.num_blocks), count = ints(free_count, 1), told = ints(status, R),
+               plan{workspace, static_cast<int64_t>(need)};
+    if (over({table_out, told, plan}, {table, seq})) return SV_ERR_INVALID_ARG;
     if (!have_device()) return SV_ERR_DEVICE;
+    if (over({stack, count}, {table, seq}) || among({table_out, stack, count, told, plan})) return SV_ERR_INVALID_ARG;
     return launched(launch_cache_compact(CompactArgs{cache, block_table, max_blocks, seq_len, R,
                                                      divisor_of(cache.block_size), block_table_out, free_blocks,
                                                      free_count, status, workspace},
