@@ -400,7 +400,7 @@ int sv_suffix_append(int32_t* suffix, int32_t N, int32_t R, const int32_t* token
  *               itself (same data and row_stride: only what changes is written), or
  *               other columns of a wider matrix; no entry of the two may be the same
  *               otherwise (SV_ERR_INVALID_ARG).
- *   status      int32 [R] out or NULL.
+ *   status      int32 [R] out or NULL; over none of the call's other arrays (SV_ERR_INVALID_ARG).
  * For token x in a row, z its logit in fp32:
  *   seen   x is among the request's history or the drafts before the row;
  *   count  times x occurs in the history behind the prompt and in those drafts;

@@ -133,6 +133,15 @@ static bool among(std::initializer_list<Span> written)
     return false;
 }
 
+// Whether an array shares a byte with one of the matrix's rows; between two rows there may be room for it.
+static bool over_rows(const Span& a, const Rows& m, int64_t rows)
+{
+    const int64_t wide = static_cast<int64_t>(m.width) * m.esize, step = m.stride * m.esize;
+    if (!meet(a, Span{m.data, (rows - 1) * step + wide})) return false;
+    const int64_t in = static_cast<const char*>(a.data) - m.data;
+    return in < 0 || in % step < wide || in % step + a.bytes > step;
+}
+
 static bool have_device()
 {
     int dev = 0;
@@ -760,6 +769,15 @@ int sv_adjust_logits(sv_rows logits, int32_t R, int32_t k, int32_t branches, con
         !aligned(u.bias_id, 4) || !aligned(u.bias_value, 4) || !aligned(u.mask, 4) || !aligned(u.mask_row, 4) ||
         !aligned(status, 4))
         return SV_ERR_ALIGN;
+    // thread blocks of a request read its rules while one of them tells its status
+    const Span told = ints(status, R);
+    if (over({told}, {ints(draft, static_cast<int64_t>(R) * branches * k), ints(u.history, static_cast<int64_t>(R) * u.history_width),
+                      ints(u.history_len, R), ints(u.prompt_len, R), ints(u.repetition, R), ints(u.presence, R),
+                      ints(u.frequency, R), ints(u.bias_start, static_cast<int64_t>(R) + 1), ints(u.bias_id, u.bias_entries),
+                      ints(u.bias_value, u.bias_entries), ints(u.mask, static_cast<int64_t>(u.masks) * u.mask_words),
+                      ints(u.mask_row, rows)}) ||
+        over_rows(told, a.in, rows) || over_rows(told, a.out, rows))
+        return SV_ERR_INVALID_ARG;
     if (!have_device()) return SV_ERR_DEVICE;
     if (!adjust_fits(a)) return SV_ERR_LIMIT;
     return launched(launch_adjust_logits(a, stream));
