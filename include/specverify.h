@@ -426,7 +426,7 @@ typedef struct sv_logit_rules {
     const float* bias_value;    /* [bias_entries]; -inf bans a token */
     int32_t bias_entries;       /* 0: no biases (bias_start may be NULL) */
     const uint32_t* mask;       /* [masks, mask_words]: bit x % 32 of word x / 32 allows token x; NULL: no masks */
-    int32_t masks, mask_words;  /* mask_words * 32 >= V */
+    int32_t masks, mask_words;  /* mask_words * 32 >= V; masks 0: none to choose from, and mask is not read */
     const int32_t* mask_row;    /* one for each row of logits: its mask, negative for none; NULL: row i has mask i */
 } sv_logit_rules;
 int sv_adjust_logits(sv_rows logits, int32_t R, int32_t k, int32_t branches, const int32_t* draft,

@@ -780,6 +780,9 @@ def cache_compact(k_cache, v_cache, block_table, seq_len, out: dict | None = Non
     return out
 
 
+_NOWHERE = 256  # the address of an array without entries, which has none in torch: such a one is not read, but it is given
+
+
 def _floats(t, name, n):
     """The address of a float32 CUDA tensor that is passed as it lies."""
     if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
@@ -810,8 +813,8 @@ def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=Non
     draft int32 [R, branches, k]; history int32 [R, width], of which history_len int32 [R] are the request's tokens so
     far and prompt_len int32 [R] (or None) of those its prompt; repetition, presence, frequency float32 [R] or None;
     bias (start int32 [R + 1], ids int32 [n], values float32 [n]) or None: request r's are start[r] .. start[r + 1] - 1;
-    mask int32 [masks, words] of allowed ids as bits with mask_row int32 [rows] (negative: none), or a mask for each row
-    without mask_row.  A row's drafts count as said before it.  Returns logits (out=dict(logits=logits) works in
+    mask int32 [masks, words] of allowed ids as bits (masks may be 0) with mask_row int32 [rows] (negative: none), or a
+    mask for each row without mask_row.  A row's drafts count as said before it.  Returns logits (out=dict(logits=logits) works in
     place) and status [R]."""
     lib = _lib or load()
     rows = R * (1 + branches * k)
@@ -828,7 +831,7 @@ def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=Non
     if history is not None:
         if history.dim() != 2 or history.shape[0] != R or history_len is None:
             raise ValueError("history must be [R, width], with history_len")
-        rules.history, rules.history_width = _ints(history, "history"), history.shape[1]
+        rules.history, rules.history_width = _ints(history, "history") or _NOWHERE, history.shape[1]
         rules.history_len = _ints(history_len, "history_len", R)
         if prompt_len is not None:
             rules.prompt_len = _ints(prompt_len, "prompt_len", R)
@@ -848,7 +851,7 @@ def adjust_logits(logits, R: int, k: int, branches: int, draft=None, history=Non
     if mask is not None:
         if mask.dim() != 2:
             raise ValueError("mask must be [masks, words]")
-        rules.mask = _ints(mask, "mask")
+        rules.mask = _ints(mask, "mask") or _NOWHERE
         rules.masks, rules.mask_words = mask.shape
         if mask_row is not None:
             rules.mask_row = _ints(mask_row, "mask_row", rows)
