@@ -690,7 +690,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) adjust_few_kernel(con
                     dst[x] = allowed(mask, x) ? src[x] : kNegInf<T>;
                 continue;
             }
-            const int32_t x0 = start_of(dst);
             // a warp's vectors lie side by side, and each lane has 32 of their ids' bits
             constexpr int kSpan = kFewVecs * 32 * kPer;
             for (int32_t n = warp * kSpan; n < g.slice; n += kFewThreads / 32 * kSpan) {

@@ -22,6 +22,14 @@ namespace {
 
 constexpr int kNormTokens = 4;  // most tokens of a CTA
 
+struct NormGeom {
+    int32_t half;    // rotated pairs
+    int32_t rows;    // q heads, then k heads, then v heads
+    int32_t items;   // lanes that a head's vectors of 8 entries fill, two each
+    int32_t tokens;  // of a CTA
+    float by_dim;    // 1 / head_dim
+};
+
 __device__ __forceinline__ float weight_at(const void* w, int32_t dtype, int i)
 {
     if (w == nullptr) return 1.0f;
@@ -80,7 +88,7 @@ __device__ __forceinline__ void store_packed(void* p, const Packed<E>& v)
 // SIDE: as in rope.cu.  ITEMS: lanes of a head, 32 / ITEMS heads to a warp.  E: entries of a vector, of which the
 // distance between a pair's halves is a multiple (8 where pairs lie side by side).
 template <bool F16, bool SIDE, int ITEMS, int E>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs n, const RopeGeom g)
+__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs n, const NormGeom g)
 {
     constexpr int kHeads = 32 / ITEMS, kGroups = kRopeThreads / 32 * kHeads, kParts = E / 2;
     const RopeArgs& a = n.rope;
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
 // gets the partners' values by a second read of them; it has read all before it writes any.
 template <bool F16>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_entries_kernel(const __grid_constant__ NormRopeArgs n,
-                                                                         const RopeGeom g)
+                                                                         const NormGeom g)
 {
     constexpr int kMost = SV_MAX_HEAD_DIM / 32;
     const RopeArgs& a = n.rope;
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_entries_kernel(const _
 }
 
 template <bool F16, bool SIDE, int ITEMS, int E>
-void launch_items(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
+void launch_items(const NormRopeArgs& n, NormGeom& g, cudaStream_t stream)
 {
     constexpr int kGroups = kRopeThreads / 32 * (32 / ITEMS);
     const int64_t T = n.rope.q.tokens;
@@ -318,7 +326,7 @@ void launch_items(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
 
 // The lanes that a head's vectors fill, for vectors of 8 entries.
 template <bool F16, bool SIDE, int ITEMS>
-void launch_eights(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
+void launch_eights(const NormRopeArgs& n, NormGeom& g, cudaStream_t stream)
 {
     if (g.items == ITEMS)
         launch_items<F16, SIDE, ITEMS, 8>(n, g, stream);
@@ -329,7 +337,7 @@ void launch_eights(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
 // Halves that lie apart by a multiple of 4 or of 2 entries: a power of two of lanes.  4,160 tokens, 28 + 4 heads of 96
 // with 24 rotated take 20 us, of 80 with 20 rotated 28, where an entry at a time takes 37 for either.
 template <bool F16>
-void launch_shorter(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
+void launch_shorter(const NormRopeArgs& n, NormGeom& g, cudaStream_t stream)
 {
     const bool fours = g.half % 4 == 0, small = n.rope.cache.head_dim <= SV_MAX_HEAD_DIM / 2;
     if (fours && small)
@@ -347,11 +355,10 @@ void launch_shorter(const NormRopeArgs& n, RopeGeom& g, cudaStream_t stream)
 cudaError_t launch_norm_rope_cache(const NormRopeArgs& n, cudaStream_t stream)
 {
     const RopeArgs& a = n.rope;
-    RopeGeom g{};
-    g.vecs = a.cache.head_dim / 8;
+    NormGeom g{};
     g.half = a.rot_dim / 2;
     g.rows = a.q.heads + 2 * a.cache.kv_heads;
-    g.items = (g.vecs + 1) / 2;
+    g.items = (a.cache.head_dim / 8 + 1) / 2;
     g.by_dim = 1.0f / a.cache.head_dim;
     const int sms = device_sm_count();
     const bool f16 = a.cache.dtype == SV_F16;

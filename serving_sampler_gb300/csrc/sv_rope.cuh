@@ -1,5 +1,5 @@
-// What the rotary cache writes share: the angle of a pair, the place of a slot, packed
-// 16-bit entries, and which vectors of a head make an item.
+// What the rotary cache writes share: the angle of a pair, the place of a slot and packed
+// 16-bit entries.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -11,7 +11,6 @@
 namespace sv {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeTokens = 4;  // most tokens of a CTA
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w)
@@ -46,50 +45,6 @@ __device__ __forceinline__ int64_t slot_offset(const RopeArgs& a, int64_t slot)
     const int64_t block = slot >= 0 ? slot / a.cache.block_size : -1;
     if (block < 0 || block >= a.cache.num_blocks) return -1;
     return block * a.cache.block_stride + (slot - block * a.cache.block_size) * a.cache.token_stride;
-}
-
-struct RopeGeom {
-    int32_t vecs;               // 16-byte vectors of a head
-    int32_t half;               // rotated pairs
-    int32_t rows;               // q heads, then k heads, then v heads
-    int32_t items, line;        // items of a head, of a token
-    uint32_t by_items;          // ceil(2^32 / items), for division by multiplication (0 for one item)
-    int32_t tokens;             // of a CTA
-    float by_dim;               // 1 / head_dim
-};
-
-// Items of a head: their two vectors, and the first of the eight pairs they hold (-1: they pass).
-struct RopeItem {
-    int32_t token, row, a, b, pair;
-};
-template <bool SIDE>
-__device__ __forceinline__ RopeItem item_of(const RopeArgs& a, const RopeGeom& g, uint32_t x)
-{
-    RopeItem m;
-    uint32_t in = x;
-    m.token = 0;
-#pragma unroll
-    for (int i = 1; i < kRopeTokens; ++i) {
-        if (in >= static_cast<uint32_t>(g.line)) {
-            in -= g.line;
-            ++m.token;
-        }
-    }
-    m.row = static_cast<int32_t>(g.by_items != 0 ? __umulhi(in, g.by_items) : in);
-    const int32_t j = static_cast<int32_t>(in - m.row * g.items);
-    const bool turns = m.row < a.q.heads + a.cache.kv_heads;
-    const int32_t cut = g.half / 8;  // rotated items when the halves lie apart
-    m.a = 2 * j;
-    m.b = 2 * j + 1;
-    m.pair = -1;
-    if (turns && SIDE) {
-        m.pair = 8 * j;
-    } else if (turns && j < cut) {
-        m.a = j;
-        m.b = j + cut;
-        m.pair = 8 * j;
-    }
-    return m;
 }
 
 }  // namespace sv
