@@ -15,8 +15,9 @@
 // Bound by bytes less than by what stands before them: 67 us for 576 rows of 151,936 bf16 logits (359 MB, 5.4 TB/s,
 // 0.79 of a copy's rate) with 500 to 8,000 tokens a request, 16 biases and masks on two rows of three, of which 55 are
 // the copy alone, 2 the scan of every request's tokens in each of its 38 slices, 5 the listed entries, 3 biases and
-// drafts, 2 the masks; 33 us for 561 rows of 32,003 fp32 logits (146 MB, 4.4 TB/s).  In place 64 and 27 us, and 41 and
-// 18 without masks.  One row of 151,936 takes 4.4 us: a launch, the tokens, a tile.  24 warps share an SM there, so an
+// drafts, 2 the masks; 33 us for 561 rows of 32,003 fp32 logits (146 MB, 4.4 TB/s).  In place 66 and 36 us, and 48 and
+// 20 without masks.  Rows of the two matrices that start differently within 16 bytes go entry by entry: 576 rows of 151,935
+// whose output has no room between its rows take 303 us, and 71 where both have the same.  One row of 151,936 takes 4.4 us: a launch, the tokens, a tile.  24 warps share an SM there, so an
 // instruction costs a warp about ten cycles, and those that stand before the rows count most.
 // A tile in shared memory costs less than computing over the copies afterwards (93 and 41 us at the time), two tiles a
 // warp less than three (81 against 103: the third costs a thread block per SM), slices of 4,096 ids less than 8,192 or
@@ -597,6 +598,12 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
 // blocks be resident at once: with 1,024 and one block 47, 256 and four 65, three blocks an SM 54, slices of which four
 // times as many blocks would be resident 57.  Entries met and tokens brought two or four at a time spill or save nothing
 // (43 and 46).
+// Every window of 4,096 marks goes through all of a request's tokens once more, so long histories cost most where ids
+// hardly repeat: 256 requests of 32,000 such tokens take 230 us (the other kernel: 443), of 100,000 1,220 (1,357), and with
+// ids by a power of their rank 150 and 686 (377 and 1,097).  The other kernel spreads a request over 38 blocks, so it is the
+// faster one where a few requests of many are far longer than the rest, which the host does not know: 4 of 256 with 100,000
+// tokens take 852 us here and 136 there, with 500,000 5,800 and 374.  Shorter slices wherever histories may be long (32,768
+// ids: 218 and 1,450) cost batches of even lengths: 64 of 100,000 tokens 365 us for 262.
 constexpr int kFewThreads = 512;
 constexpr int kFewBlocks = 2;      // an SM
 constexpr int kFewSlice = 262144;  // most ids of a slice, and the least where there are few
@@ -604,7 +611,7 @@ constexpr int kFewLeast = 8192;
 constexpr int kFewTable = 4096;    // most words of a table
 constexpr int kFewVecs = 4;        // vectors of a row that a thread moves at a time
 // Most rows of a request, out of place and in place: 256 requests of three rows take 107 us so and 119 with the other
-// kernel, 64 of four 48 and 42; in place 64 of four 29 and 36, of eight 55 and 58, and 64 of 33 rows of 32,000 79 and 53.
+// kernel (205 of three whose ids hardly repeat 134 and 107), 64 of four 48 and 42; in place 64 of four 29 and 36, of eight 55 and 58, and 64 of 33 rows of 32,000 79 and 53.
 constexpr int kFewRows = 3, kFewRowsInPlace = 8;
 
 struct FewGeom {

@@ -433,8 +433,8 @@ struct PackGeom {
     uint32_t planes;
 };
 
-// Bound by bytes: 237 us for both kernels where 730 MB move, 6.4 TB/s, 0.95 of a copy's rate, of which the plan takes
-// 10 (the moves alone run at the copy's rate); 11 us for a small pool.
+// Bound by bytes: 238 us for both kernels where 751 MB move (1,502 MB read and written), 6.3 TB/s, 0.93 of a copy's rate,
+// of which the plan takes 10 (the moves alone run at the copy's rate); 11 us for a small pool.
 __global__ void __launch_bounds__(kPackThreads) compact_move_kernel(const CompactArgs a, const PackGeom g)
 {
     const CompactPlan plan = plan_of(a);
