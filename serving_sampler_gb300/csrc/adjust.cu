@@ -591,8 +591,9 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const __grid_con
 // are counted, the rows are copied and masked, and the marked entries are written once more from what they were.  Where
 // more ids are marked than the table has words, they are taken in windows, with the tokens gone through for each.
 //
-// 256 requests of one row of 151,936 bf16 logits with 500 to 8,000 tokens take 42 us so, 31 in place and 20 without
-// masks, and 88, 86 and 75 with a word for every id of 8,192 (the copy's bytes alone: 24).  A call of up to 100 tokens a
+// 256 requests of one row of 151,936 bf16 logits with 500 to 8,000 tokens take 44 us so, 37 in place and 22 without
+// masks, and 103, 95 and 81 with a word for every id (the copy's bytes alone: 24); 512 of them with up to 2,000 tokens 71, 53
+// and 26, and 160, 151 and 122.  A call of up to 100 tokens a
 // request takes 35, 22 and 9.  What is left: 256 blocks do not fill 152 SMs evenly, and a block's steps wait for one
 // another.  512 threads, two blocks an SM, each with as much of a row as lets all
 // blocks be resident at once: with 1,024 and one block 47, 256 and four 65, three blocks an SM 54, slices of which four
@@ -611,7 +612,7 @@ constexpr int kFewLeast = 8192;
 constexpr int kFewTable = 4096;    // most words of a table
 constexpr int kFewVecs = 4;        // vectors of a row that a thread moves at a time
 // Most rows of a request, out of place and in place: 256 requests of three rows take 107 us so and 119 with the other
-// kernel (205 of three whose ids hardly repeat 134 and 107), 64 of four 48 and 42; in place 64 of four 29 and 36, of eight 55 and 58, and 64 of 33 rows of 32,000 79 and 53.
+// kernel (205 of three whose ids hardly repeat 134 and 107), 64 of four 48 and 41; in place 64 of four 35 and 41, of eight 55 and 58, and 64 of 33 rows of 32,000 79 and 53.
 constexpr int kFewRows = 3, kFewRowsInPlace = 8;
 
 struct FewGeom {
@@ -915,7 +916,7 @@ AdjustGeom geom_of(const AdjustArgs& a)
 
 // Whether a call's requests have few rows, and are so many that the other kernel's blocks would not all be resident at
 // once: 16 requests of one row take 9.0 us with that one and 9.6 with this (in place 7.2 and 8.7), 24 take 10.1 and 10.2 (10.7
-// and 8.7), 64 26 and 18 (25 and 16).
+// and 8.7), 64 30 and 20 (25 and 15).
 bool few_rows(const AdjustArgs& a, const AdjustGeom& g)
 {
     return g.rows <= (a.in.data == a.out.data ? kFewRowsInPlace : kFewRows) &&
