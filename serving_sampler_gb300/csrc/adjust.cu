@@ -612,7 +612,8 @@ constexpr int kFewLeast = 8192;
 constexpr int kFewTable = 4096;    // most words of a table
 constexpr int kFewVecs = 4;        // vectors of a row that a thread moves at a time
 // Most rows of a request, out of place and in place: 256 requests of three rows take 107 us so and 119 with the other
-// kernel (205 of three whose ids hardly repeat 134 and 107), 64 of four 48 and 41; in place 64 of four 35 and 41, of eight 55 and 58, and 64 of 33 rows of 32,000 79 and 53.
+// kernel (205 of three whose ids hardly repeat 134 and 107), 64 of four 48 and 41; in place 64 of four 35 and 41, of eight
+// 55 and 58, and 64 of 33 rows of 32,000 79 and 53.
 constexpr int kFewRows = 3, kFewRowsInPlace = 8;
 
 struct FewGeom {
